@@ -1,9 +1,11 @@
-"""GB300-native decode-step front of a Gated DeltaNet layer.
+"""GB300-native decode-step front and prompt side of a Gated DeltaNet layer.
 
 `GdnDecode` wraps the C ABI of libgdn_decode.so (include/gdn_decode.h) for
 torch CUDA tensors: it allocates the workspace with torch, marshals pointers
 and streams, and launches one persistent CUDA kernel per step. It computes
 nothing itself and has no fallback: without the built library it raises.
+`GdnPrefill`, `linear` and `slot_map` (prefill.py) wrap the prompt side
+(include/gdn_prefill.h) in the same way.
 """
 from __future__ import annotations
 
@@ -15,7 +17,7 @@ from ._native import (GDN_ENGINE_AUTO, GDN_ENGINE_CUDA_CORE, GDN_ENGINE_TCGEN05,
 
 _FORMATS = {"bf16": GDN_W_BF16, "mxfp4": GDN_W_MXFP4, "mxfp6": GDN_W_MXFP6}
 
-__all__ = ["GdnDecode", "GdnError", "ENGINES", "step_static"]
+__all__ = ["GdnDecode", "GdnError", "GdnPrefill", "SlotMap", "ENGINES", "linear", "slot_map", "step_static"]
 
 ENGINES = {"auto": GDN_ENGINE_AUTO, "cuda_core": GDN_ENGINE_CUDA_CORE, "tcgen05": GDN_ENGINE_TCGEN05}
 _WEIGHT_KEYS = ("input_norm_w", "qkvz", "qkvz_scales", "ba", "conv_w", "A_log", "dt_bias", "gated_norm_w",
@@ -208,3 +210,6 @@ def step_static(shape, x, residual, weights, state_indices, conv_state, ssm_stat
     if st != GDN_OK:
         raise GdnError("gdn_decode_step_static", st)
     return None
+
+
+from .prefill import GdnPrefill, SlotMap, linear, slot_map  # noqa: E402

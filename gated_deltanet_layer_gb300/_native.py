@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/gdn_decode.h (argument marshalling only).
+"""ctypes binding of the C ABI in include/gdn_decode.h and include/gdn_prefill.h
+(argument marshalling only).
 
 Every step of the decode path runs in the CUDA library libgdn_decode.so. If the
 library is missing this module raises; there is no other implementation.
@@ -20,13 +21,17 @@ GDN_DEBUG_TIMELINE = 0x2
 GDN_LAUNCH_COOPERATIVE = 0x1
 GDN_LAUNCH_NO_EARLY_WEIGHTS = 0x2
 
-# Every symbol the headers declare (include/gdn_decode.h and the diagnostics
-# in include/gdn_decode_diag.h).
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU_TANH = 0, 1, 2
+
+# Every symbol the headers declare (include/gdn_decode.h, the diagnostics in
+# include/gdn_decode_diag.h and the prompt side in include/gdn_prefill.h).
 EXPORTS = (
     "gdn_decode_workspace_bytes", "gdn_decode_create", "gdn_decode_step", "gdn_decode_check",
     "gdn_decode_reset", "gdn_decode_destroy", "gdn_status_string", "gdn_decode_launch_info",
     "gdn_decode_plan", "gdn_decode_debug_timeline", "gdn_decode_step_static", "gdn_decode_verify",
     "gdn_decode_step_out",
+    "gdn_prefill_workspace_bytes", "gdn_prefill_create", "gdn_prefill_conv", "gdn_prefill_delta",
+    "gdn_prefill_check", "gdn_prefill_reset", "gdn_prefill_destroy", "gdn_linear", "gdn_slot_map",
 )
 
 # Size of the library's fixed device scratch (gdn_decode_step_static).
@@ -42,6 +47,15 @@ class Config(ctypes.Structure):
         ("norm_eps", ctypes.c_float), ("gated_norm_eps", ctypes.c_float), ("l2_eps", ctypes.c_float),
         ("q_scale", ctypes.c_float), ("deadline_us", ctypes.c_uint32), ("num_ctas", ctypes.c_int32),
         ("debug_flags", ctypes.c_int32), ("launch_flags", ctypes.c_int32),
+    ]
+
+
+class PrefillConfig(ctypes.Structure):
+    _fields_ = [
+        ("num_k_heads", ctypes.c_int32), ("num_v_heads", ctypes.c_int32), ("head_k_dim", ctypes.c_int32),
+        ("head_v_dim", ctypes.c_int32), ("conv_kernel", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+        ("max_tokens", ctypes.c_int32), ("max_seqs", ctypes.c_int32), ("ssm_dtype", ctypes.c_int32),
+        ("gated_norm_eps", ctypes.c_float), ("l2_eps", ctypes.c_float), ("q_scale", ctypes.c_float),
     ]
 
 
@@ -98,6 +112,26 @@ def lib() -> ctypes.CDLL:
     L.gdn_decode_step_static.argtypes = [cfgp, i32, vp, vp, ctypes.POINTER(Weights), vp, vp, vp, vp, vp, vp,
                                          u32p]
     L.gdn_decode_step_static.restype = ctypes.c_int
+    pcfgp, i64 = ctypes.POINTER(PrefillConfig), ctypes.c_int64
+    L.gdn_prefill_workspace_bytes.argtypes = [pcfgp]
+    L.gdn_prefill_workspace_bytes.restype = ctypes.c_size_t
+    L.gdn_prefill_create.argtypes = [pcfgp, vp, ctypes.c_size_t, vp, ctypes.POINTER(vp)]
+    L.gdn_prefill_create.restype = ctypes.c_int
+    L.gdn_prefill_conv.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.gdn_prefill_conv.restype = ctypes.c_int
+    L.gdn_prefill_delta.argtypes = [vp, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64,
+                                    vp]
+    L.gdn_prefill_delta.restype = ctypes.c_int
+    L.gdn_prefill_check.argtypes = [vp, vp, u32p]
+    L.gdn_prefill_check.restype = ctypes.c_int
+    L.gdn_prefill_reset.argtypes = [vp, vp]
+    L.gdn_prefill_reset.restype = ctypes.c_int
+    L.gdn_prefill_destroy.argtypes = [vp]
+    L.gdn_prefill_destroy.restype = None
+    L.gdn_linear.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, vp]
+    L.gdn_linear.restype = ctypes.c_int
+    L.gdn_slot_map.argtypes = [i32, i32, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.gdn_slot_map.restype = ctypes.c_int
     _lib = L
     return L
 

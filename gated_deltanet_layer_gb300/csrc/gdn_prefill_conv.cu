@@ -1,0 +1,145 @@
+// Causal depthwise conv1d (kernel 4) + SiLU over ragged prompts, with the conv
+// state in and out (gdn_prefill_conv).
+//
+//   out[t][c] = silu(sum_j w[c][j] x[t-3+j][c])
+//
+// Bound by bandwidth: every input row is read once and every output row written
+// once (4 bytes a value), 12 flops each. A CTA takes one chunk of 64 tokens of
+// one sequence and 8 channels a thread (16-byte loads and stores), and walks the
+// chunk with the three older taps in registers, so a row is read once but for
+// the three rows before the chunk.
+#include "gdn_prefill.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kConvThreads = 128;
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) {
+  const int place = blockIdx.x;
+  const int s = chunk_seq(p.r, place);
+  int b, e, in = 0, out = 0;
+  seq_rows(p.r, s, &b, &e);
+  const int j = place - chunk_first_place(p.r, s);
+  const bool live = seq_slots(p.r, s, j == 0 && blockIdx.y == 0 && threadIdx.x == 0, &in, &out);
+  const int t0 = b + j * kChunk, t1 = min(t0 + kChunk, e);
+  const int c = (blockIdx.y * kConvThreads + threadIdx.x) * 8;
+  // A place past the sequence's last chunk has no rows, and none before it to
+  // take taps from; the first one is always there, for the state.
+  if (c >= p.C || (j > 0 && t0 >= e)) return;
+  if (!live) {
+    for (int t = t0; t < t1; ++t)
+      *reinterpret_cast<uint4*>(p.out + (long long)t * p.ldo + c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  float w[4][8];
+  {
+    const uint4* wp = reinterpret_cast<const uint4*>(p.w + (size_t)c * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[8];
+      unpack8(__ldg(wp + i), f);  // two channels' four taps
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k][2 * i] = f[k];
+        w[k][2 * i + 1] = f[4 + k];
+      }
+    }
+  }
+  // the three taps before the chunk: rows of the sequence, or the old state
+  uint4 h[3] = {};  // packed bf16, oldest first
+  const __nv_bfloat16* x = p.x + c;
+  if (j > 0) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) h[k] = __ldg(reinterpret_cast<const uint4*>(x + (long long)(t0 - 3 + k) * p.ldx));
+  } else if (in > 0) {
+    const uint4* sp = reinterpret_cast<const uint4*>(p.state + ((size_t)in * p.C + c) * 3);
+    __align__(16) uint16_t raw[24];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) reinterpret_cast<uint4*>(raw)[i] = sp[i];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = raw[6 * i + k] | ((uint32_t)raw[6 * i + 3 + k] << 16);
+      h[k] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  if (j == 0) {
+    // The sequence's new state: its last three inputs. This thread alone reads
+    // and writes these channels of the slots, and it has read the old taps, so
+    // state_in may be state_out.
+    const int n = e - b;
+    uint4 l[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int at = n - 3 + k;  // offset in the sequence; before it, the old taps
+      l[k] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(x + (long long)(b + at) * p.ldx))
+                     : at == -1 ? h[2] : at == -2 ? h[1] : h[0];
+    }
+    __align__(16) uint16_t raw[24];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t v[4] = {l[k].x, l[k].y, l[k].z, l[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        raw[6 * i + k] = (uint16_t)v[i];
+        raw[6 * i + 3 + k] = (uint16_t)(v[i] >> 16);
+      }
+    }
+    uint4* sp = reinterpret_cast<uint4*>(p.state + ((size_t)out * p.C + c) * 3);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) sp[i] = reinterpret_cast<const uint4*>(raw)[i];
+  }
+  float x0[8], x1[8], x2[8];
+  unpack8(h[0], x0);
+  unpack8(h[1], x1);
+  unpack8(h[2], x2);
+  constexpr int kAhead = 8;  // rows in flight
+  uint4 q[kAhead];
+  for (int t = t0; t < t1; t += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (t + i < t1) q[i] = __ldg(reinterpret_cast<const uint4*>(x + (long long)(t + i) * p.ldx));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (t + i >= t1) break;
+      float f[8];
+      unpack8(q[i], f);
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float a = fmaf(w[3][k], f[k], fmaf(w[2][k], x2[k], fmaf(w[1][k], x1[k], w[0][k] * x0[k])));
+        const float d = fmaf(w[3][k + 1], f[k + 1],
+                             fmaf(w[2][k + 1], x2[k + 1], fmaf(w[1][k + 1], x1[k + 1], w[0][k + 1] * x0[k + 1])));
+        o[k / 2] = pack_bf16x2(silu_f(a), silu_f(d));
+      }
+      *reinterpret_cast<uint4*>(p.out + (long long)(t + i) * p.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x0[k] = x1[k];
+        x1[k] = x2[k];
+        x2[k] = f[k];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_conv(const ConvParams& p, cudaStream_t s) {
+  const dim3 grid(chunk_places(p.r.tokens, p.r.seqs), (p.C / 8 + kConvThreads - 1) / kConvThreads);
+  conv_kernel<<<grid, kConvThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace gdn
