@@ -17,7 +17,8 @@ from ._native import (GDN_ENGINE_AUTO, GDN_ENGINE_CUDA_CORE, GDN_ENGINE_TCGEN05,
 
 _FORMATS = {"bf16": GDN_W_BF16, "mxfp4": GDN_W_MXFP4, "mxfp6": GDN_W_MXFP6}
 
-__all__ = ["GdnDecode", "GdnError", "GdnPrefill", "SlotMap", "ENGINES", "linear", "slot_map", "step_static"]
+__all__ = ["GdnDecode", "GdnError", "GdnPrefill", "SlotMap", "ENGINES", "linear", "linear_check", "slot_map",
+           "step_static"]
 
 ENGINES = {"auto": GDN_ENGINE_AUTO, "cuda_core": GDN_ENGINE_CUDA_CORE, "tcgen05": GDN_ENGINE_TCGEN05}
 _WEIGHT_KEYS = ("input_norm_w", "qkvz", "qkvz_scales", "ba", "conv_w", "A_log", "dt_bias", "gated_norm_w",
@@ -212,4 +213,4 @@ def step_static(shape, x, residual, weights, state_indices, conv_state, ssm_stat
     return None
 
 
-from .prefill import GdnPrefill, SlotMap, linear, slot_map  # noqa: E402
+from .prefill import GdnPrefill, SlotMap, linear, linear_check, slot_map  # noqa: E402

@@ -31,7 +31,8 @@ EXPORTS = (
     "gdn_decode_plan", "gdn_decode_debug_timeline", "gdn_decode_step_static", "gdn_decode_verify",
     "gdn_decode_step_out",
     "gdn_prefill_workspace_bytes", "gdn_prefill_create", "gdn_prefill_conv", "gdn_prefill_delta",
-    "gdn_prefill_check", "gdn_prefill_reset", "gdn_prefill_destroy", "gdn_linear", "gdn_slot_map",
+    "gdn_prefill_check", "gdn_prefill_reset", "gdn_prefill_destroy", "gdn_linear",
+    "gdn_linear_check", "gdn_slot_map",
 )
 
 # Size of the library's fixed device scratch (gdn_decode_step_static).
@@ -130,6 +131,8 @@ def lib() -> ctypes.CDLL:
     L.gdn_prefill_destroy.restype = None
     L.gdn_linear.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, vp]
     L.gdn_linear.restype = ctypes.c_int
+    L.gdn_linear_check.argtypes = [vp, u32p]
+    L.gdn_linear_check.restype = ctypes.c_int
     L.gdn_slot_map.argtypes = [i32, i32, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     L.gdn_slot_map.restype = ctypes.c_int
     _lib = L

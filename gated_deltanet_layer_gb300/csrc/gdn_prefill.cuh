@@ -132,6 +132,8 @@ struct SlotParams {
 cudaError_t launch_conv(const ConvParams& p, cudaStream_t s);
 cudaError_t launch_delta(const DeltaParams& p, int d, bool state_bf16, cudaStream_t s);
 cudaError_t launch_linear(const LinearParams& p, cudaStream_t s);
+// Waits for the stream, reads the linear kernels' error word and clears it.
+cudaError_t linear_error(unsigned int* word, cudaStream_t s);
 cudaError_t launch_slot_map(const SlotParams& p, cudaStream_t s);
 
 __device__ __forceinline__ float sigmoid_f(float t) { return 1.0f / (1.0f + expf(-t)); }

@@ -217,6 +217,13 @@ extern "C" gdn_status gdn_linear(int32_t rows, int32_t cols, int32_t inner, cons
   return cuda_status(launch_linear(p, (cudaStream_t)stream));
 }
 
+extern "C" gdn_status gdn_linear_check(void* stream, uint32_t* detail) {
+  uint32_t word = 0;
+  if (linear_error(&word, (cudaStream_t)stream) != cudaSuccess) return GDN_ERR_CUDA;
+  if (detail) *detail = word;
+  return word ? GDN_ERR_DEADLINE : GDN_OK;
+}
+
 extern "C" gdn_status gdn_slot_map(int32_t requests, int32_t tokens, const int32_t* new_lens, const int32_t* context_lens,
                                    int32_t block_size, int32_t max_blocks, int32_t* block_table, const int32_t* free_list,
                                    int32_t free_cap, const int32_t* free_count, int32_t* free_count_out,

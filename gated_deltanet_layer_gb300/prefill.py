@@ -16,7 +16,7 @@ import torch
 from . import _native
 from ._native import (GDN_ACT_GELU_TANH, GDN_ACT_NONE, GDN_ACT_SILU, GDN_OK, GDN_STATE_BF16, GDN_STATE_F32, GdnError)
 
-__all__ = ["GdnPrefill", "SlotMap", "linear", "slot_map"]
+__all__ = ["GdnPrefill", "SlotMap", "linear", "linear_check", "slot_map"]
 
 ACTIVATIONS = {None: GDN_ACT_NONE, "none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "gelu": GDN_ACT_GELU_TANH}
 
@@ -76,6 +76,14 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, stream=Non
     if st != GDN_OK:
         raise GdnError("gdn_linear", st)
     return out
+
+
+def linear_check(stream=None):
+    """(status, detail word) of the device's gdn_linear calls; synchronises
+    and clears the word."""
+    d = ctypes.c_uint32()
+    st = _native.lib().gdn_linear_check(_stream(stream, None), ctypes.byref(d))
+    return st, d.value
 
 
 def slot_map(new_lens, context_lens, block_size, block_table, free_list, free_count, tokens, *, out=None, error=None,

@@ -135,6 +135,12 @@ gdn_status gdn_linear(int32_t rows, int32_t cols, int32_t inner, const void* x, 
                       int64_t ldw, const void* bias, int32_t activation, const void* residual, int64_t ldr,
                       void* out, int64_t ldo, void* stream);
 
+/* Synchronise `stream`, read the error word of this device's gdn_linear calls
+ * and clear it: GDN_OK, or GDN_ERR_DEADLINE when a wait inside a kernel passed
+ * its limit (the call's outputs are then not all written). *detail (optional)
+ * receives the raw word, as for gdn_prefill_check. */
+gdn_status gdn_linear_check(void* stream, uint32_t* detail);
+
 /* Offsets, block tables and slots of a ragged step from its request lengths.
  * Request r holds context_lens[r] tokens in blocks of block_size slots (its
  * first ceil(context / block_size) table entries) and brings new_lens[r] more.

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from gated_deltanet_layer_gb300 import GdnDecode, GdnError, GdnPrefill, _native, linear, slot_map, workloads as WL
+from gated_deltanet_layer_gb300 import (GdnDecode, GdnError, GdnPrefill, _native, linear, linear_check, slot_map,
+                                        workloads as WL)
 import prefill_harness as P
 
 pytestmark = pytest.mark.gpu
@@ -268,6 +269,7 @@ def _linear_case(M, N, K, act=None, bias=False, residual=False, stride=0, seed=1
     want, scale = _linear_reference(x, w, b, act, r)
     off = np.abs(P.f64(got) - want) - (2.0 ** -8 * np.abs(want) + 1.2 * (K / 16 + 16) * 2.0 ** -23 * scale)
     assert off.max() <= 0, off.max()
+    assert linear_check() == (0, 0)
 
 
 @pytest.mark.parametrize("M", [1, 2, 5, 16, 17, 64, 65, 128, 129, 300])
