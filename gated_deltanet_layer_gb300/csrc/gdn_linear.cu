@@ -33,16 +33,21 @@ __device__ __forceinline__ float act_f(float y, int act) {
 
 // ------------------------------------------------------------- many rows
 
-constexpr int kPairStages = 6;
+// Stages of the ring: what the 227 KB hold beside the epilogue's staging.
+template <int BN>
+constexpr int pair_stages() {
+  return BN == 256 ? 5 : BN == 128 ? 7 : 8;
+}
 constexpr int kPairThreads = 256;
-constexpr int kStageStride = 66;  // floats a staged row takes: 64 and two, against bank conflicts
+constexpr int kStageStride = 68;  // floats a staged row takes: 64 and four, against bank conflicts
 
 template <int BN>
 struct alignas(1024) PairSmem {
-  unsigned char a[kPairStages][128 * 128];
-  unsigned char b[kPairStages][BN / 2 * 128];
+  static constexpr int kStages = pair_stages<BN>();
+  unsigned char a[kStages][128 * 128];
+  unsigned char b[kStages][BN / 2 * 128];
   float stage[4][32 * kStageStride];
-  uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2];
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   uint32_t tmem;
 };
 
@@ -58,7 +63,19 @@ __device__ __forceinline__ void tile_at(const PairTiles& t, int i, int* m, int* 
   *n = r / rows;
 }
 
-// Two columns of one output row.
+// Eight columns of one output row, 16 bytes of residual in and of output out.
+__device__ __forceinline__ void put8(const LinearParams& p, long long m, int n, const float* v, const float (&bias)[8],
+                                     const uint4& res) {
+  const uint32_t r[4] = {res.x, res.y, res.z, res.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = pack_bf16x2(act_f(v[2 * j] + bias[2 * j], p.act) + bf16_lo(r[j]),
+                       act_f(v[2 * j + 1] + bias[2 * j + 1], p.act) + bf16_hi(r[j]));
+  *reinterpret_cast<uint4*>(p.out + m * p.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Two columns of one output row (any alignment).
 __device__ __forceinline__ void put2(const LinearParams& p, long long m, int n, float a, float b, float bias_a, float bias_b,
                                      bool wide) {
   const bool two = n + 1 < p.N;
@@ -88,12 +105,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const LinearParams p,
                 const PairTiles tiles) {
   extern __shared__ unsigned char raw[];
+  constexpr int kStages = pair_stages<BN>();
+  static_assert(sizeof(PairSmem<BN>) + 1024 <= 232448, "227 KB of shared memory a CTA");
   PairSmem<BN>& s = *reinterpret_cast<PairSmem<BN>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   constexpr uint32_t kBytes = 128 * 128 + BN / 2 * 128;  // one CTA's share of a stage
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kPairStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
     }
@@ -130,13 +149,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t bar = map_rank(&s.full[st], 0);
         tma_load_2d_pair(s.a[st], &xmap, k * kBK, m0, bar);
         tma_load_2d_pair(s.b[st], &wmap, k * kBK, n0, bar);
-        if (++st == kPairStages) st = 0, ph ^= 1;
+        if (++st == kStages) st = 0, ph ^= 1;
       }
     }
     // every stage consumed: no copy is in flight when the CTAs leave
-    for (int k = 0; k < kPairStages && ok; ++k) {
+    for (int k = 0; k < kStages && ok; ++k) {
       ok = mbar_wait(&s.empty[st], ph ^ 1);
-      if (++st == kPairStages) st = 0, ph ^= 1;
+      if (++st == kStages) st = 0, ph ^= 1;
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     constexpr uint32_t idesc = idesc_bf16_f32(256, BN);
@@ -153,7 +172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int j = 0; j < kBK / 16; ++j) mma_bf16_pair(d, a + 2 * j, b + 2 * j, idesc, (k | j) != 0);
         mma_commit_pair(&s.empty[st]);
-        if (++st == kPairStages) st = 0, ph ^= 1;
+        if (++st == kStages) st = 0, ph ^= 1;
       }
       mma_commit_pair(&s.acc_full[buf]);
       if (++buf == 2) buf = 0, aph ^= 1;
@@ -163,42 +182,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     float* sm = s.stage[q];
     const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0 &&
                       p.ldo % 2 == 0 && (!p.residual || p.ldr % 2 == 0);
+    // rows of 16 bytes throughout: a lane takes 8 columns of every fourth row
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 15) == 0 &&
+                     p.N % 8 == 0 && p.ldo % 8 == 0 && (!p.residual || p.ldr % 8 == 0);
     int buf = 0;
     uint32_t aph = 0;
     for (int i = pair; i < tiles.total && ok; i += pairs) {
       int tm, tn;
       tile_at(tiles, i, &tm, &tn);
-      ok = mbar_wait(&s.acc_full[buf], aph);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
       const int m0 = tm * 256 + (int)rank * 128 + q * 32;
       const int rows = min(32, p.M - m0);
-      constexpr int kCols = BN < 64 ? BN : 64;
-      for (int c = 0; c < BN; c += kCols) {
+      for (int c = 0; c < BN; c += 64) {
+        // the residual's loads are in flight while the tile is multiplied
+        const int n8 = tn * BN + c + (lane & 7) * 8;
+        const bool mine = vec && n8 < p.N;
+        uint4 res[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          res[r] = make_uint4(0, 0, 0, 0);
+          const int row = 4 * r + (lane >> 3);
+          if (mine && p.residual && row < rows)
+            res[r] = *reinterpret_cast<const uint4*>(p.residual + (long long)(m0 + row) * p.ldr + n8);
+        }
+        if (c == 0) {
+          ok = mbar_wait(&s.acc_full[buf], aph);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
         const uint32_t t = tmem + buf * 256 + c + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-        for (int h = 0; h < kCols; h += 32) {
+        for (int h = 0; h < 64; h += 32) {
           float v[32];
           tmem_ld32(t + h, v);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            *reinterpret_cast<float2*>(sm + lane * kStageStride + h + j) = make_float2(v[j], v[j + 1]);
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(sm + lane * kStageStride + h + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
-        if (c + kCols == BN) {
+        if (c + 64 == BN) {
           // the accumulator is out: the next tile but one may take it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_rank(&s.acc_empty[buf], 0));
         }
         __syncwarp();
-        const int n = tn * BN + c + 2 * lane;
-        if (n < p.N) {
-          const float ba = p.bias ? bf16_to_f(p.bias[n]) : 0.f, bb = p.bias && n + 1 < p.N ? bf16_to_f(p.bias[n + 1]) : 0.f;
+        if (vec) {
+          if (mine) {
+            float bias[8] = {};
+            if (p.bias) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) bias[j] = bf16_to_f(p.bias[n8 + j]);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const int row = 4 * r + (lane >> 3);
+              if (row < rows) put8(p, m0 + row, n8, sm + row * kStageStride + (lane & 7) * 8, bias, res[r]);
+            }
+          }
+        } else {
+          const int n = tn * BN + c + 2 * lane;
+          if (n < p.N) {
+            const float ba = p.bias ? bf16_to_f(p.bias[n]) : 0.f, bb = p.bias && n + 1 < p.N ? bf16_to_f(p.bias[n + 1]) : 0.f;
 #pragma unroll 4
-          for (int r = 0; r < rows; ++r) {
-            const float2 v = *reinterpret_cast<const float2*>(sm + r * kStageStride + 2 * lane);
-            put2(p, m0 + r, n, v.x, v.y, ba, bb, wide);
+            for (int r = 0; r < rows; ++r) {
+              const float2 v = *reinterpret_cast<const float2*>(sm + r * kStageStride + 2 * lane);
+              put2(p, m0 + r, n, v.x, v.y, ba, bb, wide);
+            }
           }
         }
         __syncwarp();
