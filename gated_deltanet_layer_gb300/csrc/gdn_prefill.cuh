@@ -7,6 +7,8 @@
 namespace gdn {
 
 constexpr int kChunk = 64;  // tokens of one chunk of a sequence
+// Longest sequence that the delta rule takes token by token.
+constexpr int kRecurrentMax = 8;
 
 // What of an index error (bits 23..16 of the error word).
 constexpr uint32_t kWhatSlot = 1, kWhatOffsets = 2, kWhatLength = 3, kWhatWait = 4;
@@ -130,7 +132,10 @@ struct SlotParams {
 
 // Launchers, one for each operator's translation unit.
 cudaError_t launch_conv(const ConvParams& p, cudaStream_t s);
-cudaError_t launch_delta(const DeltaParams& p, int d, bool state_bf16, cudaStream_t s);
+// ws: delta_chunk_bytes() of device memory, 256-byte aligned.
+cudaError_t launch_delta(const DeltaParams& p, int d, bool state_bf16, unsigned char* ws, cudaStream_t s);
+cudaError_t launch_delta_chunks(const DeltaParams& p, int d, bool state_bf16, unsigned char* ws, cudaStream_t s);
+size_t delta_chunk_bytes(long long tokens, long long seqs, int Hk, int Hv, int d);
 cudaError_t launch_linear(const LinearParams& p, cudaStream_t s);
 // Waits for the stream, reads the linear kernels' error word and clears it.
 cudaError_t linear_error(unsigned int* word, cudaStream_t s);

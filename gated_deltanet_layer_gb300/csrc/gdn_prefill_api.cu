@@ -74,7 +74,8 @@ Ragged ragged(const gdn_prefill* h, int32_t seqs, int32_t tokens, int32_t max_le
 }  // namespace
 
 extern "C" size_t gdn_prefill_workspace_bytes(const gdn_prefill_config* cfg) {
-  return validate(cfg) == GDN_OK ? kErrorBytes : 0;
+  if (validate(cfg) != GDN_OK) return 0;
+  return kErrorBytes + delta_chunk_bytes(cfg->max_tokens, cfg->max_seqs, cfg->num_k_heads, cfg->num_v_heads, cfg->head_k_dim);
 }
 
 extern "C" gdn_status gdn_prefill_create(const gdn_prefill_config* cfg, void* workspace, size_t workspace_bytes,
@@ -104,7 +105,8 @@ extern "C" gdn_status gdn_prefill_conv(gdn_prefill_t* h, int32_t seqs, int32_t t
   if (ldx < C || ldo < C || ldx % 8 || ldo % 8) return GDN_ERR_ARG;
   const Span o{out, extent(tokens, ldo, C)}, state{conv_state, (size_t)h->cfg.num_slots * C * 6};
   const Span in[] = {{x, extent(tokens, ldx, C)}, {conv_w, (size_t)C * 8}, {cu_seqlens, (size_t)(seqs + 1) * 4},
-                     {state_in, (size_t)seqs * 4}, {state_out, (size_t)seqs * 4}, {h->ws, kErrorBytes}};
+                     {state_in, (size_t)seqs * 4}, {state_out, (size_t)seqs * 4},
+                     {h->ws, gdn_prefill_workspace_bytes(&h->cfg)}};
   if (overlaps_any(o, in) || overlap(o, state) || overlaps_any(state, in)) return GDN_ERR_ARG;
   if (seqs == 0 && tokens == 0) return GDN_OK;
   ConvParams p{};
@@ -164,7 +166,8 @@ extern "C" gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t 
   p.gnorm_eps = c.gated_norm_eps;
   p.l2_eps = c.l2_eps;
   p.q_scale = c.q_scale;
-  return cuda_status(launch_delta(p, c.head_k_dim, c.ssm_dtype == GDN_STATE_BF16, (cudaStream_t)stream));
+  return cuda_status(launch_delta(p, c.head_k_dim, c.ssm_dtype == GDN_STATE_BF16, h->ws + kErrorBytes,
+                                  (cudaStream_t)stream));
 }
 
 extern "C" gdn_status gdn_prefill_check(gdn_prefill_t* h, void* stream, uint32_t* detail) {

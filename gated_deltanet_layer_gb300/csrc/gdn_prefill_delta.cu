@@ -1,5 +1,6 @@
 // The gated delta rule over ragged prompts (gdn_prefill_delta): the recurrent
-// form, one token after the other.
+// form, one token after the other, for sequences of up to kRecurrentMax tokens;
+// it also writes the rows of padding.
 //
 // One CTA for each (sequence, value head). A warp keeps 32 rows of the state
 // S[dv][dk] in registers, a lane the columns lane*E .. lane*E + E - 1 of all of
@@ -8,6 +9,8 @@
 // leaves row i's sum in lane i, which forms u_i = beta (v_i - (S k)_i); u is
 // broadcast back, S += u k^T, and o = S q the same way. All f32.
 // One token is bound by the state's read and write.
+#include <algorithm>
+
 #include "gdn_prefill.cuh"
 
 namespace gdn {
@@ -89,6 +92,7 @@ __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
   int b, e, in = 0, out = 0;
   seq_rows(p.r, s, &b, &e);
   const bool live = seq_slots(p.r, s, h == 0 && threadIdx.x == 0, &in, &out);
+  if (live && e - b > kRecurrentMax) return;  // the chunked form's
   const int row = threadIdx.x;  // the dv row this lane finishes
   if (!live) {
     for (int t = b; t < e; ++t) p.out[(long long)t * p.ldo + h * D + row] = __float2bfloat16_rn(0.f);
@@ -169,8 +173,10 @@ cudaError_t launch_d(const DeltaParams& p, bool state_bf16, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_delta(const DeltaParams& p, int d, bool state_bf16, cudaStream_t s) {
-  return d == 128 ? launch_d<128>(p, state_bf16, s) : launch_d<64>(p, state_bf16, s);
+cudaError_t launch_delta(const DeltaParams& p, int d, bool state_bf16, unsigned char* ws, cudaStream_t s) {
+  const cudaError_t e = d == 128 ? launch_d<128>(p, state_bf16, s) : launch_d<64>(p, state_bf16, s);
+  if (e != cudaSuccess || p.r.seqs == 0 || std::min(p.r.max_len, p.r.tokens) <= kRecurrentMax) return e;
+  return launch_delta_chunks(p, d, state_bf16, ws, s);
 }
 
 }  // namespace gdn
