@@ -473,6 +473,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
 
 // ------------------------------------------------------------------ the chunks of a sequence
 
+// silu(z) before a rounding to bf16: the fast exponential and division (a few 2^-22)
+// are far below it.
+__device__ __forceinline__ float gate(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
 constexpr int kChainThreads = 384;  // producer, MMA, TMEM, -; four warps of state rows; four of outputs
 
 // TMEM columns
@@ -676,42 +680,62 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       const uint32_t ph = n & 1;
       ChainStage<D>& g = s.st[st];
       if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      const auto value = [&](int i) { return real ? bf16_to_f(g.v[i][row]) : 0.f; };
-      // of this row's v over the chunk: sums of beta |v| and of e^(G_C-G) beta |v|, the
-      // largest |v|
+      // This row's v over the chunk, zero past the sequence's end. (The lanes past D
+      // = 64 rows do as those of the first 64, from a zero state; nobody reads them.)
+      uint32_t v[32];
+      {
+        const __nv_bfloat16* vr = &g.v[0][row & (D - 1)];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          v[i] = __bfloat16_as_ushort(vr[2 * i * D]) | ((uint32_t)__bfloat16_as_ushort(vr[(2 * i + 1) * D]) << 16);
+      }
+      if (toks < kChunk) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] &= 2 * i + 1 < toks ? 0xffffffffu : 2 * i < toks ? 0xffffu : 0u;
+      }
+      // sums of beta |v| and of e^(G_C-G) beta |v|, the largest |v|
       int first_bad = __float_as_int(g.scal[S_END][1]);
       float sb, sw, mv;
-      const auto sums = [&](int until) {
-        sb = sw = mv = 0.f;
-#pragma unroll 1
-        for (int i = 0; i < until; i += 8) {
+      const auto sums = [&]() {
+        float2 b2 = make_float2(0.f, 0.f), w2 = b2;
+        float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; k += 4) {
-            const float4 be = *reinterpret_cast<const float4*>(&g.scal[S_BETA][i + k]);
-            const float4 w = *reinterpret_cast<const float4*>(&g.scal[S_W][i + k]);
-            const float bs[4] = {be.x, be.y, be.z, be.w}, ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float a = i + k + u < until ? fabsf(value(i + k + u)) : 0.f;
-              sb = fmaf(bs[u], a, sb);
-              sw = fmaf(ws[u], a, sw);
-              mv = fmaxf(mv, a);
-            }
-          }
+        for (int i = 0; i < 64; i += 4) {
+          const float4 be = *reinterpret_cast<const float4*>(&g.scal[S_BETA][i]);
+          const float4 w = *reinterpret_cast<const float4*>(&g.scal[S_W][i]);
+          const uint32_t p0 = v[i / 2] & 0x7fff7fffu, p1 = v[i / 2 + 1] & 0x7fff7fffu;
+          const float2 a0 = make_float2(bf16_lo(p0), bf16_hi(p0)), a1 = make_float2(bf16_lo(p1), bf16_hi(p1));
+          b2 = __ffma2_rn(make_float2(be.x, be.y), a0, b2);
+          w2 = __ffma2_rn(make_float2(w.x, w.y), a0, w2);
+          b2 = __ffma2_rn(make_float2(be.z, be.w), a1, b2);
+          w2 = __ffma2_rn(make_float2(w.z, w.w), a1, w2);
+          m0 = fmaxf(m0, fmaxf(a0.x, a0.y));
+          m1 = fmaxf(m1, fmaxf(a1.x, a1.y));
         }
+        sb = b2.x + b2.y, sw = w2.x + w2.y, mv = fmaxf(m0, m1);
       };
-      sums(toks);
+      sums();
       float gam_end = g.scal[S_END][0];
       if (first_bad < 64 || !finite(sb)) {
         // a row that stops being finite: zeros from there on
-        for (int i = toks - 1; i >= 0; --i)
-          if (!finite(value(i))) first_bad = min(first_bad, i);
-        sums(min(first_bad, toks));
+#pragma unroll
+        for (int i = 31; i >= 0; --i) {
+          if (!finite(bf16_hi(v[i]))) first_bad = min(first_bad, 2 * i + 1);
+          if (!finite(bf16_lo(v[i]))) first_bad = min(first_bad, 2 * i);
+        }
+        sb = mv = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          v[i] &= 2 * i + 1 < first_bad ? 0xffffffffu : 2 * i < first_bad ? 0xffffu : 0u;
+          const float a = fmaxf(fabsf(bf16_lo(v[i])), fabsf(bf16_hi(v[i])));
+          sb += 2.f * a;  // beta <= 1
+          mv = fmaxf(mv, a);
+        }
         gam_end = sw = 0.f;
       }
       if (dead) first_bad = 0;
       // scales: of U, and of the state after this chunk
-      const float fu = row_scale(g.scal[S_END][2] * (mv + bound + sb));
+      const float fu = row_scale((first_bad < 64 ? 1.f : g.scal[S_END][2]) * (mv + bound + sb));
       bound = fmaf(gam_end, fminf(bound, near), sw) * 1.01f;
       const float fs_next = row_scale(bound);
       const float shrink = gam_end * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
@@ -760,7 +784,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       tc_fence_after();
       // zeros from the first token on that is past the end or not finite
       const int until = min(first_bad, toks);
-#pragma unroll 1
+#pragma unroll
       for (int half = 0; half < 2; ++half) {
         float x[32];
         uint32_t hi[16], lo[16];
@@ -770,10 +794,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
           const int i = half * 32 + j;
           const float4 be = *reinterpret_cast<const float4*>(&g.scal[S_BETA][i]);
           const float4 c1 = *reinterpret_cast<const float4*>(&g.scal[S_C1][i]);
-          float2 r0 = make_float2(be.x * fmaf(-c1.x, x[j] * p_scale, fu * value(i)),
-                                  be.y * fmaf(-c1.y, x[j + 1] * p_scale, fu * value(i + 1)));
-          float2 r1 = make_float2(be.z * fmaf(-c1.z, x[j + 2] * p_scale, fu * value(i + 2)),
-                                  be.w * fmaf(-c1.w, x[j + 3] * p_scale, fu * value(i + 3)));
+          const float2 f2 = make_float2(fu, fu), p2 = make_float2(-p_scale, -p_scale);
+          const float2 v0 = make_float2(bf16_lo(v[i / 2]), bf16_hi(v[i / 2]));
+          const float2 v1 = make_float2(bf16_lo(v[i / 2 + 1]), bf16_hi(v[i / 2 + 1]));
+          const float2 q0 = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), make_float2(c1.x, c1.y));
+          const float2 q1 = __fmul2_rn(__fmul2_rn(make_float2(x[j + 2], x[j + 3]), p2), make_float2(c1.z, c1.w));
+          float2 r0 = __fmul2_rn(make_float2(be.x, be.y), __ffma2_rn(f2, v0, q0));
+          float2 r1 = __fmul2_rn(make_float2(be.z, be.w), __ffma2_rn(f2, v1, q1));
           if (until < 64) {
             if (i >= until) r0.x = 0.f;
             if (i + 1 >= until) r0.y = 0.f;
@@ -865,27 +892,31 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     // ---- the outputs
     const int row = tid - 256, w = warp - 8;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    // On the way out eight lanes take a row, four columns in every 32 each; a warp
+    // the rows 16 w .. 16 w + 15, four at a time.
     constexpr int E = D / 32;
-    float gw[E] = {};
+    const int sub = lane >> 3, l8 = (lane & 7) * 4;
+    float gw[E][4] = {};
     if (p.z) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) gw[j] = bf16_to_f(p.gnorm_w[lane * E + j]);
+      for (int k = 0; k < E; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gw[k][j] = bf16_to_f(p.gnorm_w[32 * k + l8 + j]);
     }
     for (int n = 0; n < chunks; ++n) {
       const int st = n & 1, t0 = b + n * kChunk, toks = min(kChunk, e - t0);
       const uint32_t ph = n & 1;
       ChainStage<D>& g = s.st[st];
       // this warp's rows of z, in flight while the chunk is finished
-      uint32_t zw[16][E / 2];
+      uint2 z[4][E];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (!p.z || 4 * i + w >= toks) continue;
-        const __nv_bfloat16* z = p.z + (long long)(t0 + 4 * i + w) * p.ldz + h * D + lane * E;
-        if constexpr (E == 4) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(z));
-          zw[i][0] = v.x, zw[i][1] = v.y;
-        } else {
-          zw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(z));
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * w + 4 * i + sub;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          z[i][k] = make_uint2(0, 0);
+          if (p.z && t < toks)
+            z[i][k] = __ldg(reinterpret_cast<const uint2*>(p.z + (long long)(t0 + t) * p.ldz + h * D + 32 * k + l8));
         }
       }
       if (ok) ok = mbar_wait(&s.row_ready, ph);
@@ -900,13 +931,17 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         tmem_ld32(tmem + kQS + half * 32 + lanes, x);
         tmem_ld32(tmem + kAU + half * 32 + lanes, y);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < 32; j += 4) {
           const int i = half * 32 + j;
-          float o = fmaf(g.scal[S_CQG][i], x[j] * inv_s, g.scal[S_CQ][i] * (y[j] * inv_u));
-          if (i >= first_bad) o = __int_as_float(0x7fffffff);
-          s.o[i][row] = o;
+          const float4 cg = *reinterpret_cast<const float4*>(&g.scal[S_CQG][i]);
+          const float4 cq = *reinterpret_cast<const float4*>(&g.scal[S_CQ][i]);
+          s.o[i][row] = fmaf(cg.x, x[j] * inv_s, cq.x * (y[j] * inv_u));
+          s.o[i + 1][row] = fmaf(cg.y, x[j + 1] * inv_s, cq.y * (y[j + 1] * inv_u));
+          s.o[i + 2][row] = fmaf(cg.z, x[j + 2] * inv_s, cq.z * (y[j + 2] * inv_u));
+          s.o[i + 3][row] = fmaf(cg.w, x[j + 3] * inv_s, cq.w * (y[j + 3] * inv_u));
         }
       }
+      for (int i = first_bad; i < kChunk; ++i) s.o[i][row] = __int_as_float(0x7fffffff);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -915,28 +950,34 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");  // the output warps: every row is staged
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int t = 4 * i + w;
-        if (t >= toks) break;
-        float o[E];
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * w + 4 * i + sub;
+        float4 o[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) o[j] = s.o[t][lane * E + j];
+        for (int k = 0; k < E; ++k) o[k] = *reinterpret_cast<const float4*>(&s.o[t][32 * k + l8]);
         if (p.z) {
           float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < E; ++j) sum = fmaf(o[j], o[j], sum);
-          const float r = 1.0f / sqrtf(warp_sum(sum) * (1.0f / D) + p.gnorm_eps);
+          for (int k = 0; k < E; ++k)
+            sum = fmaf(o[k].x, o[k].x, fmaf(o[k].y, o[k].y, fmaf(o[k].z, o[k].z, fmaf(o[k].w, o[k].w, sum))));
 #pragma unroll
-          for (int j = 0; j < E; j += 2) {
-            o[j] = o[j] * r * gw[j] * silu_f(bf16_lo(zw[i][j / 2]));
-            o[j + 1] = o[j + 1] * r * gw[j + 1] * silu_f(bf16_hi(zw[i][j / 2]));
+          for (int m = 4; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          const float r = rsqrtf(sum * (1.0f / D) + p.gnorm_eps);
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            const float zf[4] = {bf16_lo(z[i][k].x), bf16_hi(z[i][k].x), bf16_lo(z[i][k].y), bf16_hi(z[i][k].y)};
+            o[k].x *= r * gw[k][0] * gate(zf[0]);
+            o[k].y *= r * gw[k][1] * gate(zf[1]);
+            o[k].z *= r * gw[k][2] * gate(zf[2]);
+            o[k].w *= r * gw[k][3] * gate(zf[3]);
           }
         }
-        __nv_bfloat16* dst = p.out + (long long)(t0 + t) * p.ldo + h * D + lane * E;
-        if constexpr (E == 4)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-        else
-          *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0], o[1]);
+        if (t < toks) {
+          __nv_bfloat16* dst = p.out + (long long)(t0 + t) * p.ldo + h * D + l8;
+#pragma unroll
+          for (int k = 0; k < E; ++k)
+            *reinterpret_cast<uint2*>(dst + 32 * k) = make_uint2(pack_bf16x2(o[k].x, o[k].y), pack_bf16x2(o[k].z, o[k].w));
+        }
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");  // before the next chunk is staged
     }
