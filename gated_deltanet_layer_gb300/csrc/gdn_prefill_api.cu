@@ -133,7 +133,7 @@ extern "C" gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t 
   if (max_len < 0 || !A_log || !dt_bias || !ssm_state || (z && !gated_norm_w)) return GDN_ERR_ARG;
   if (tokens > 0 && (!qkv || !ba || !core_out)) return GDN_ERR_ARG;
   if (!aligned(qkv, 16) || !aligned(z, 16) || !aligned(core_out, 16) || !aligned(ssm_state, 16)) return GDN_ERR_ARG;
-  if (!aligned(ba, 2) || !aligned(A_log, 4) || !aligned(dt_bias, 2) || !aligned(gated_norm_w, 2)) return GDN_ERR_ARG;
+  if (!aligned(ba, 2) || !aligned(A_log, 4) || !aligned(dt_bias, 2) || !aligned(gated_norm_w, 16)) return GDN_ERR_ARG;
   if (ldqkv < C || ldba < 2 * Hv || ldcore < cols || (z && ldz < cols)) return GDN_ERR_ARG;
   if (ldqkv % 8 || ldcore % 8 || (z && ldz % 8)) return GDN_ERR_ARG;
   const size_t sdt = c.ssm_dtype == GDN_STATE_BF16 ? 2 : 4;

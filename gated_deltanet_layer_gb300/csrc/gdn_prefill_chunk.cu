@@ -45,14 +45,18 @@ namespace {
 using namespace tc;
 
 constexpr float kScaleT = 4096.f;   // of T's f16 images
-constexpr int kImg = 4 * 8192;      // T hi, T lo, causal products hi, lo: 64 x 64 f16 each
-enum { S_BETA, S_C1, S_CU, S_W, S_CQG, S_CQ, S_END, S_COUNT };  // arrays of 64 floats beside them
-constexpr int kHeadBytes = kImg + S_COUNT * 256;
+// A chunk's images and scalars of a value head, arrays of 64 floats: what the state's
+// chain needs (T hi, T lo) and what the outputs need (causal products hi, lo).
+enum { S_BETA, S_C1, S_CU, S_W, S_END, S_COUNT };
+enum { O_CQG, O_CQ, O_COUNT };
+constexpr int kImg = 2 * 8192;  // two images of 64 x 64 f16
+constexpr int kChainBytes = kImg + S_COUNT * 256, kOutBytes = kImg + O_COUNT * 256;
+constexpr int kHeadBytes = kChainBytes + kOutBytes;
 // S_END: [0] e^(G_C), [1] (an int) the first token whose k or gates are not finite,
 // else 64, [2] the largest beta
 
 template <int D>
-constexpr int kq_bytes() { return 2 * kChunk * D * 2; }
+constexpr int kq_bytes() { return 2 * kChunk * D * 2; }  // the k image, then q's
 
 struct ChunkParams {
   DeltaParams p;
@@ -106,14 +110,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const float (&v)[32]) {
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16f(uint32_t t, const float (&v)[16]) {
   uint32_t r[16];
 #pragma unroll
-  for (int h = 0; h < 32; h += 16) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[h + i]);
-    tmem_st16(t + h, r);
-  }
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  tmem_st16(t, r);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -154,7 +160,7 @@ struct alignas(1024) PrepSmem {
   };
   unsigned char a[2][2][8192];  // causal products of two heads, hi and lo
   float m[2][64 * kLStride];    // L, then T in its place
-  float scal[2][S_COUNT][64];
+  float scal[2][S_COUNT][64], oscal[2][O_COUNT][64];
   float ghi[2][64], glo[2][64];  // running sums of the log2 gates
   float bj[2][64];               // 2^(G of the 16-block's end - G_j) / norm of k_j
   float top[2][64];              // of a row of the causal products, by column halves
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
         s.scal[warp][S_C1][tok] = gam * s.rn[tok];
         s.scal[warp][S_CU][tok] = left * s.rn[tok];
         s.scal[warp][S_W][tok] = left * beta[k];
-        s.scal[warp][S_CQG][tok] = p.q_scale * s.rn[64 + tok] * gam;
+        s.oscal[warp][O_CQG][tok] = p.q_scale * s.rn[64 + tok] * gam;
       }
       if (lane == 0) {
         s.scal[warp][S_END][0] = exp2f(ehi + elo);
@@ -361,9 +367,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       }
       __syncthreads();
       if (!lower) {
-        // a row of the causal products takes a power of two of its own (S_CQ undoes it)
+        // a row of the causal products takes a power of two of its own (O_CQ undoes it)
         const float f = row_scale(fmaxf(s.top[0][i], s.top[1][i]));
-        if (half == 0) s.scal[h][S_CQ][i] = p.q_scale * s.rn[64 + i] * inverse_pow2(f);
+        if (half == 0) s.oscal[h][O_CQ][i] = p.q_scale * s.rn[64 + i] * inverse_pow2(f);
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           uint32_t w[4], wl[4];
@@ -457,8 +463,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       for (int h = 0; h < heads; ++h) {
         unsigned char* img = c.head + ((size_t)place * p.Hv + kh * p.group + g0 + h) * kHeadBytes;
         bulk_store(img, s.t[h][0], 16384);
-        bulk_store(img + 16384, s.a[h][0], 16384);
         bulk_store(img + kImg, s.scal[h], S_COUNT * 256);
+        bulk_store(img + kChainBytes, s.a[h][0], 16384);
+        bulk_store(img + kChainBytes + kImg, s.oscal[h], O_COUNT * 256);
       }
       bulk_commit();
       if (g0 + 2 < p.group) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -473,11 +480,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
 
 // ------------------------------------------------------------------ the chunks of a sequence
 
-// silu(z) before a rounding to bf16: the fast exponential and division (a few 2^-22)
-// are far below it.
-__device__ __forceinline__ float gate(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-
-constexpr int kChainThreads = 384;  // producer, MMA, TMEM, -; four warps of state rows; four of outputs
+// Warps: 0 loads, 1 issues MMAs, 2 holds the TMEM; 4 to 11 keep the state's rows (a
+// thread is a row of S^T and half of its columns, or of the chunk's tokens); 12 to 15
+// write the outputs, and sum up the next chunk's v on the side.
+// The loops over columns and tokens are rolled, 16 at a time: one warp a scheduler in
+// code that runs straight through waits for its instructions (unrolled, a chunk took 4
+// times as long).
+constexpr int kChainThreads = 512;
 
 // TMEM columns
 constexpr uint32_t kS = 0, kShi = 128, kSlo = 192, kPU = 256, kRhi = 320, kRlo = 352, kQS = 384, kAU = 448;
@@ -486,22 +495,56 @@ constexpr uint32_t kS = 0, kShi = 128, kSlo = 192, kPU = 256, kRhi = 320, kRlo =
 constexpr uint32_t kUhi = kSlo + 32, kUlo = kShi + 32;
 
 template <int D>
-struct alignas(1024) ChainStage {
-  unsigned char k[64 * D * 2], q[64 * D * 2];  // f16 images
-  unsigned char thi[8192], tlo[8192], ahi[8192], alo[8192];
+struct alignas(1024) ChainIn {
+  unsigned char k[64 * D * 2];  // f16 image
+  unsigned char thi[8192], tlo[8192];
   float scal[S_COUNT][64];
   __nv_bfloat16 v[64][D];
+};
+template <int D>
+struct alignas(1024) OutIn {
+  unsigned char q[64 * D * 2];
+  unsigned char ahi[8192], alo[8192];
+  float scal[O_COUNT][64];
 };
 
 template <int D>
 struct ChainSmem {
-  ChainStage<D> st[2];
+  ChainIn<D> in[2];
+  OutIn<D> oin[2];
   float o[64][132];
+  float4 sums[2][128];  // of a row's v: sum beta |v|, sum e^(G_C-G) beta |v|, max |v|, first token not finite
+  float part[2][128];   // of a row's squares, by halves of its columns
   float inv_s[2][128], inv_u[2][128];
   int first_bad[2][128];
-  uint64_t full[2], empty[2], s_ready[2], p_done, r_ready, u_done, u_ready, s_done[2], o_done, o_free, row_ready;
+  uint64_t full[2], empty[2], ofull[2], oempty[2], s_ready[2], s_done[2];
+  uint64_t p_done, r_ready, u_done, u_ready, o_done, o_free, row_ready, sums_ready;
   uint32_t tmem;
 };
+
+// silu(z) before a rounding to bf16: the fast exponential and division (a few 2^-22)
+// are far below it.
+__device__ __forceinline__ float gate(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// 16 columns of a row of a state.
+template <bool BF16>
+__device__ __forceinline__ void state16(const void* base, size_t at, float (&x)[16]) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at + 8 * j);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[8 * j + 2 * k] = bf16_lo(w[k]), x[8 * j + 2 * k + 1] = bf16_hi(w[k]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + 4 * j);
+      x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
+    }
+  }
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkParams c) {
@@ -517,17 +560,20 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 5);  // the MMA's commit and four output warps
+      mbar_init(&s.empty[i], 5);  // the MMAs' commit, and the output warps' sums
+      mbar_init(&s.ofull[i], 1);
+      mbar_init(&s.oempty[i], 5);  // the MMAs' commit, and the output warps
       mbar_init(&s.s_ready[i], 4);
       mbar_init(&s.s_done[i], 1);
     }
     mbar_init(&s.p_done, 1);
-    mbar_init(&s.r_ready, 4);
+    mbar_init(&s.r_ready, 8);
     mbar_init(&s.u_done, 1);
-    mbar_init(&s.u_ready, 4);
+    mbar_init(&s.u_ready, 8);
     mbar_init(&s.o_done, 1);
     mbar_init(&s.o_free, 4);
     mbar_init(&s.row_ready, 4);
+    mbar_init(&s.sums_ready, 4);
     fence_mbar_init();
   }
   if (warp == 2) tmem_alloc(&s.tmem, 512);
@@ -540,31 +586,47 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   if (warp == 0) {
     for (int n = 0; n < chunks; ++n) {
       const int t0 = b + n * kChunk, toks = min(kChunk, e - t0), st = n & 1;
-      ChainStage<D>& g = s.st[st];
-      ok = ok && mbar_wait(&s.empty[st], ((n >> 1) & 1) ^ 1);
+      const uint32_t ph = ((n >> 1) & 1) ^ 1;
+      const size_t place = place0 + n;
+      const unsigned char* kq = c.kq + (place * p.Hk + kh) * kq_bytes<D>();
+      const unsigned char* img = c.head + (place * p.Hv + h) * kHeadBytes;
+      ChainIn<D>& g = s.in[st];
+      ok = ok && mbar_wait(&s.empty[st], ph);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const size_t place = place0 + n;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&s.full[st], kq_bytes<D>() + kHeadBytes + toks * D * 2);
-        bulk_load(g.k, c.kq + (place * p.Hk + kh) * kq_bytes<D>(), kq_bytes<D>(), &s.full[st]);
-        bulk_load(g.thi, c.head + (place * p.Hv + h) * kHeadBytes, kHeadBytes, &s.full[st]);
+        mbar_arrive_expect_tx(&s.full[st], kq_bytes<D>() / 2 + kChainBytes + toks * D * 2);
+        bulk_load(g.thi, img, kChainBytes, &s.full[st]);
       }
       __syncwarp();
       for (int t = lane; t < toks; t += 32)
         bulk_load(g.v[t], p.qkv + (long long)(t0 + t) * p.ldqkv + 2 * p.Hk * D + h * D, D * 2, &s.full[st]);
+      if (lane == 0) bulk_load(g.k, kq, kq_bytes<D>() / 2, &s.full[st]);
+      ok = mbar_wait(&s.oempty[st], ph);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        OutIn<D>& y = s.oin[st];
+        mbar_arrive_expect_tx(&s.ofull[st], kq_bytes<D>() / 2 + kOutBytes);
+        bulk_load(y.q, kq + kq_bytes<D>() / 2, kq_bytes<D>() / 2, &s.ofull[st]);
+        bulk_load(y.ahi, img + kChainBytes, kOutBytes, &s.ofull[st]);
+      }
+      __syncwarp();
     }
     // no copy is in flight when the CTA leaves
-    for (int n = max(0, chunks - 2); n < chunks; ++n)
+    for (int n = max(0, chunks - 2); n < chunks; ++n) {
       if (ok) ok = mbar_wait(&s.full[n & 1], (n >> 1) & 1);
+      if (ok) ok = mbar_wait(&s.ofull[n & 1], (n >> 1) & 1);
+    }
   } else if (warp == 1 && lane == 0) {
     constexpr uint32_t idesc = idesc_f16(128, 64, false), idesc_s = idesc_f16(128, 64, true);
     for (int n = 0; n < chunks && ok; ++n) {
       const int st = n & 1;
       const uint32_t ph = n & 1;
-      ChainStage<D>& g = s.st[st];
+      ChainIn<D>& g = s.in[st];
+      OutIn<D>& y = s.oin[st];
       ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      const uint32_t k = smem_u32(g.k), q = smem_u32(g.q);
+      const uint32_t k = smem_u32(g.k), q = smem_u32(y.q);
       // P = S k, in halves of dk as they are ready
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -581,6 +643,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       if (!ok) break;
       mma_commit(&s.p_done);
       // the state's part of the outputs, under the chain
+      if (!(ok = mbar_wait(&s.ofull[st], (n >> 1) & 1))) break;
       if (!(ok = mbar_wait(&s.o_free, ph ^ 1))) break;
       tc_fence_after();
 #pragma unroll
@@ -614,7 +677,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         mma_commit(&s.s_done[a]);
       }
       if (D == 64) mma_commit(&s.s_done[1]);
-      const uint64_t ah = sdesc_k_sw128(smem_u32(g.ahi)), al = sdesc_k_sw128(smem_u32(g.alo));
+      mma_commit(&s.empty[st]);
+      const uint64_t ah = sdesc_k_sw128(smem_u32(y.ahi)), al = sdesc_k_sw128(smem_u32(y.alo));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, ah + 2 * j, idesc, j > 0);
@@ -622,234 +686,176 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, al + 2 * j, idesc, true);
       }
       mma_commit(&s.o_done);
-      mma_commit(&s.empty[st]);
+      mma_commit(&s.oempty[st]);
     }
     // no MMA is in flight when the TMEM is freed
     if (ok) ok = mbar_wait(&s.o_done, (chunks - 1) & 1);
-  } else if (warp >= 4 && warp < 8) {
-    // ---- the state's rows: thread = dv row
-    const int row = tid - 128;
+  } else if (warp >= 4 && warp < 12) {
+    // ---- the state's rows
+    const int row = tid & 127, half = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int col0 = half * (D / 2), tok0 = half * 32;
     const bool real = row < D;
-    // bound: of the row's 2-norm at the chunk's start, which fs is the scale of;
-    // near: the same from the last measured norm
-    float bound = 0.f, fs = 1.f;
-    bool dead = false;  // the row holds a value that is not finite
-    for (int pass = 0; pass < 2; ++pass) {
-      // the starting state: its largest value, then the scaled accumulator
-      float ss = 0.f, mx = 0.f;
-      for (int col = 0; col < D; col += 32) {
-        float x[32] = {};
-        if (real && in > 0) {
-          const size_t at = (((size_t)in * p.Hv + h) * D + row) * D + col;
-          if constexpr (BF16) {
+    // The lanes past D = 64 rows do as the first 64 do, from a zero state; nobody
+    // reads them.
+    const int vrow = row & (D - 1);
+    // bound: of the row's 2-norm at the chunk's start, which fs is the scale of
+    float bound, fs;
+    bool dead;  // the row holds a value that is not finite
+    {
+      const size_t at = (((size_t)max(in, 0) * p.Hv + h) * D + vrow) * D + col0;
+      float zero = 0.f, mx = 0.f;
+      if (real && in > 0) {
+#pragma unroll 2
+        for (int col = 0; col < D / 2; col += 16) {
+          float x[16];
+          state16<BF16>(p.state, at + col, x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.state) + at + 8 * j);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[8 * j + 2 * k] = bf16_lo(w[k]), x[8 * j + 2 * k + 1] = bf16_hi(w[k]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.state) + at + 4 * j);
-              x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
-            }
-          }
-        }
-        if (pass == 0) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fabsf(x[j])), ss += x[j] * 0.f;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = dead ? 0.f : x[j] * fs;
-          tmem_st32(tmem + kS + col + lanes, x);
+          for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(x[j])), zero += x[j] * 0.f;
         }
       }
-      if (pass == 0) {
-        dead = !(ss == 0.f);
-        bound = dead ? 0.f : 12.f * mx;  // at least the 2-norm of 128 values
-        fs = row_scale(bound);
+      s.part[half][row] = zero == 0.f ? mx : __int_as_float(0x7fffffff);
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      const float a = s.part[0][row], o = s.part[1][row];
+      dead = !(finite(a) && finite(o));
+      bound = dead ? 0.f : 12.f * fmaxf(a, o);  // at least the 2-norm of 128 values
+      fs = row_scale(bound);
+#pragma unroll 1
+      for (int col = 0; col < D / 2; col += 16) {
+        float x[16] = {};
+        if (real && in > 0 && !dead) state16<BF16>(p.state, at + col, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= fs;
+        tmem_st16f(tmem + kS + col0 + col + lanes, x);
       }
+      tmem_wait_st();
     }
-    tmem_wait_st();
-    float near = bound;
+    float near = 0.f, near_mul = 0.f;  // of the last chunk: sum of v's part, factor of the norm before it
     for (int n = 0; n < chunks; ++n) {
       const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
       const uint32_t ph = n & 1;
-      ChainStage<D>& g = s.st[st];
+      ChainIn<D>& g = s.in[st];
       if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      // This row's v over the chunk, zero past the sequence's end. (The lanes past D
-      // = 64 rows do as those of the first 64, from a zero state; nobody reads them.)
-      uint32_t v[32];
-      {
-        const __nv_bfloat16* vr = &g.v[0][row & (D - 1)];
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          v[i] = __bfloat16_as_ushort(vr[2 * i * D]) | ((uint32_t)__bfloat16_as_ushort(vr[(2 * i + 1) * D]) << 16);
-      }
-      if (toks < kChunk) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] &= 2 * i + 1 < toks ? 0xffffffffu : 2 * i < toks ? 0xffffu : 0u;
-      }
-      // sums of beta |v| and of e^(G_C-G) beta |v|, the largest |v|
-      int first_bad = __float_as_int(g.scal[S_END][1]);
-      float sb, sw, mv;
-      const auto sums = [&]() {
-        float2 b2 = make_float2(0.f, 0.f), w2 = b2;
-        float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 be = *reinterpret_cast<const float4*>(&g.scal[S_BETA][i]);
-          const float4 w = *reinterpret_cast<const float4*>(&g.scal[S_W][i]);
-          const uint32_t p0 = v[i / 2] & 0x7fff7fffu, p1 = v[i / 2 + 1] & 0x7fff7fffu;
-          const float2 a0 = make_float2(bf16_lo(p0), bf16_hi(p0)), a1 = make_float2(bf16_lo(p1), bf16_hi(p1));
-          b2 = __ffma2_rn(make_float2(be.x, be.y), a0, b2);
-          w2 = __ffma2_rn(make_float2(w.x, w.y), a0, w2);
-          b2 = __ffma2_rn(make_float2(be.z, be.w), a1, b2);
-          w2 = __ffma2_rn(make_float2(w.z, w.w), a1, w2);
-          m0 = fmaxf(m0, fmaxf(a0.x, a0.y));
-          m1 = fmaxf(m1, fmaxf(a1.x, a1.y));
-        }
-        sb = b2.x + b2.y, sw = w2.x + w2.y, mv = fmaxf(m0, m1);
-      };
-      sums();
-      float gam_end = g.scal[S_END][0];
-      if (first_bad < 64 || !finite(sb)) {
-        // a row that stops being finite: zeros from there on
-#pragma unroll
-        for (int i = 31; i >= 0; --i) {
-          if (!finite(bf16_hi(v[i]))) first_bad = min(first_bad, 2 * i + 1);
-          if (!finite(bf16_lo(v[i]))) first_bad = min(first_bad, 2 * i);
-        }
-        sb = mv = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          v[i] &= 2 * i + 1 < first_bad ? 0xffffffffu : 2 * i < first_bad ? 0xffffu : 0u;
-          const float a = fmaxf(fabsf(bf16_lo(v[i])), fabsf(bf16_hi(v[i])));
-          sb += 2.f * a;  // beta <= 1
-          mv = fmaxf(mv, a);
-        }
-        gam_end = sw = 0.f;
-      }
-      if (dead) first_bad = 0;
+      if (ok) ok = mbar_wait(&s.sums_ready, ph);
+      // both halves of the last chunk's squares are written
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      const float4 sum = s.sums[st][row];
+      if (n > 0) bound = fminf(bound, fmaf(near_mul, sqrtf(s.part[0][row] + s.part[1][row]), near) * 1.01f);
+      const int first_bad = dead ? 0 : __float_as_int(sum.w);
+      const float gam_end = first_bad < kChunk ? 0.f : g.scal[S_END][0], sw = first_bad < kChunk ? 0.f : sum.y;
       // scales: of U, and of the state after this chunk
-      const float fu = row_scale((first_bad < 64 ? 1.f : g.scal[S_END][2]) * (mv + bound + sb));
-      bound = fmaf(gam_end, fminf(bound, near), sw) * 1.01f;
+      const float fu = row_scale((first_bad < kChunk ? 1.f : g.scal[S_END][2]) * (sum.z + bound + sum.x));
+      bound = fmaf(gam_end, bound, sw) * 1.01f;
       const float fs_next = row_scale(bound);
       const float shrink = gam_end * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
+      const float inv_s = inverse_pow2(fs), p_scale = fminf(fu * inv_s, 0x1p126f);
+      const float u_scale = fminf(fs_next * inverse_pow2(fu), 0x1p126f);
+      near = sw;
+      near_mul = gam_end * inv_s;
+      if (half == 0) {
+        s.inv_s[st][row] = inv_s;
+        s.inv_u[st][row] = inverse_pow2(fu);
+        s.first_bad[st][row] = first_bad;
+      }
+      if (n > 0) {
+        if (ok) ok = mbar_wait(&s.s_done[half], ph ^ 1);
+        if (half == 1 && ok) ok = mbar_wait(&s.o_done, ph ^ 1);  // U stood in the upper halves
+        tc_fence_after();
+      }
+      // S hi, lo for this chunk's products, and S shrunk for what is added to it
       float2 ss2 = make_float2(0.f, 0.f);
       const float2 shrink2 = make_float2(shrink, shrink);
 #pragma unroll 1
-      for (int col = 0; col < D; col += 32) {
-        const int hh = col >= D / 2;
-        if (n > 0 && (col & (D / 2 - 1)) == 0) {
-          if (ok) ok = mbar_wait(&s.s_done[hh], ph ^ 1);
-          if (hh == 1 && ok) ok = mbar_wait(&s.o_done, ph ^ 1);  // U stood in the upper halves
-          tc_fence_after();
-        }
-        float x[32];
-        uint32_t hi[16], lo[16];
-        tmem_ld32(tmem + kS + col + lanes, x);
+      for (int col = col0; col < col0 + D / 2; col += 16) {
+        float x[16];
+        uint32_t hi[8], lo[8];
+        tmem_ld16(tmem + kS + col + lanes, x);
         if (dead) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = 0.f;
+          for (int j = 0; j < 16; ++j) x[j] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = 0; j < 16; j += 2) {
           const float2 y = make_float2(x[j], x[j + 1]);
           ss2 = __ffma2_rn(y, y, ss2);
           split2(y, &hi[j / 2], &lo[j / 2]);
           const float2 z = __fmul2_rn(y, shrink2);
           x[j] = z.x, x[j + 1] = z.y;
         }
-        tmem_st16(tmem + kShi + col / 2 + lanes, hi);
-        tmem_st16(tmem + kSlo + col / 2 + lanes, lo);
-        tmem_st32(tmem + kS + col + lanes, x);
-        if ((col & (D / 2 - 1)) == D / 2 - 32) {
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.s_ready[hh]);
-        }
+        tmem_st8(tmem + kShi + col / 2 + lanes, hi);
+        tmem_st8(tmem + kSlo + col / 2 + lanes, lo);
+        tmem_st16f(tmem + kS + col + lanes, x);
       }
-      const float ss = ss2.x + ss2.y;
-      const float inv_s = inverse_pow2(fs), p_scale = fminf(fu * inv_s, 0x1p126f);
-      near = fmaf(gam_end, sqrtf(ss) * inv_s, sw) * 1.01f;
-      s.inv_s[st][row] = inv_s;
-      s.inv_u[st][row] = inverse_pow2(fu);
-      s.first_bad[st][row] = first_bad;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.s_ready[half]);
+      // R: zeros from the first token on that is past the end or not finite
+      const int until = min(first_bad, toks);
+      const float2 f2 = make_float2(fu, fu), p2 = make_float2(-p_scale, -p_scale);
       if (ok) ok = mbar_wait(&s.p_done, ph);
       tc_fence_after();
-      // zeros from the first token on that is past the end or not finite
-      const int until = min(first_bad, toks);
+      // the two halves' squares: both have read the last chunk's (P waited for both)
+      s.part[half][row] = ss2.x + ss2.y;
+#pragma unroll 1
+      for (int i = tok0; i < tok0 + 32; i += 16) {
+        float x[16];
+        uint32_t v[16], hi[8], lo[8];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x[32];
-        uint32_t hi[16], lo[16];
-        tmem_ld32(tmem + kPU + half * 32 + lanes, x);
+        for (int j = 0; j < 16; ++j) v[j] = __bfloat16_as_ushort(g.v[i + j][vrow]);
+        tmem_ld16(tmem + kPU + i + lanes, x);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const int i = half * 32 + j;
-          const float4 be = *reinterpret_cast<const float4*>(&g.scal[S_BETA][i]);
-          const float4 c1 = *reinterpret_cast<const float4*>(&g.scal[S_C1][i]);
-          const float2 f2 = make_float2(fu, fu), p2 = make_float2(-p_scale, -p_scale);
-          const float2 v0 = make_float2(bf16_lo(v[i / 2]), bf16_hi(v[i / 2]));
-          const float2 v1 = make_float2(bf16_lo(v[i / 2 + 1]), bf16_hi(v[i / 2 + 1]));
-          const float2 q0 = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), make_float2(c1.x, c1.y));
-          const float2 q1 = __fmul2_rn(__fmul2_rn(make_float2(x[j + 2], x[j + 3]), p2), make_float2(c1.z, c1.w));
-          float2 r0 = __fmul2_rn(make_float2(be.x, be.y), __ffma2_rn(f2, v0, q0));
-          float2 r1 = __fmul2_rn(make_float2(be.z, be.w), __ffma2_rn(f2, v1, q1));
-          if (until < 64) {
-            if (i >= until) r0.x = 0.f;
-            if (i + 1 >= until) r0.y = 0.f;
-            if (i + 2 >= until) r1.x = 0.f;
-            if (i + 3 >= until) r1.y = 0.f;
-          }
-          split2(r0, &hi[j / 2], &lo[j / 2]);
-          split2(r1, &hi[j / 2 + 1], &lo[j / 2 + 1]);
+        for (int j = 0; j < 16; j += 2) {
+          const float2 be = *reinterpret_cast<const float2*>(&g.scal[S_BETA][i + j]);
+          const float2 c1 = *reinterpret_cast<const float2*>(&g.scal[S_C1][i + j]);
+          const float2 vv = make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j + 1] << 16));
+          const float2 q = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), c1);
+          const float2 r = __fmul2_rn(be, __ffma2_rn(f2, vv, q));
+          x[j] = r.x, x[j + 1] = r.y;
         }
-        tmem_st16(tmem + kRhi + half * 16 + lanes, hi);
-        tmem_st16(tmem + kRlo + half * 16 + lanes, lo);
+        if (until < kChunk) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (i + j >= until) x[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) split2(make_float2(x[j], x[j + 1]), &hi[j / 2], &lo[j / 2]);
+        tmem_st8(tmem + kRhi + i / 2 + lanes, hi);
+        tmem_st8(tmem + kRlo + i / 2 + lanes, lo);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.r_ready);
-      const float u_scale = fminf(fs_next * inverse_pow2(fu), 0x1p126f);
+      // U for the outputs, and e^(G_C-G) U at the state's scale
+      const float2 us2 = make_float2(u_scale, u_scale), t2 = make_float2(1.0f / kScaleT, 1.0f / kScaleT);
       if (ok) ok = mbar_wait(&s.u_done, ph);
       tc_fence_after();
-      const float2 us2 = make_float2(u_scale, u_scale), t2 = make_float2(1.0f / kScaleT, 1.0f / kScaleT);
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        float u[32];
-        uint32_t hi[16], lo[16], ohi[16], olo[16];
-        tmem_ld32(tmem + kPU + half * 32 + lanes, u);
-        if (first_bad < 64) {
+      for (int i = tok0; i < tok0 + 32; i += 16) {
+        float u[16];
+        uint32_t hi[8], lo[8], ohi[8], olo[8];
+        tmem_ld16(tmem + kPU + i + lanes, u);
+        if (first_bad < kChunk) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (half * 32 + j >= first_bad) u[j] = 0.f;
+          for (int j = 0; j < 16; ++j)
+            if (i + j >= first_bad) u[j] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 cu = *reinterpret_cast<const float4*>(&g.scal[S_CU][half * 32 + j]);
-          const float2 cs[2] = {make_float2(cu.x, cu.y), make_float2(cu.z, cu.w)};
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 y = __fmul2_rn(make_float2(u[j + 2 * k], u[j + 2 * k + 1]), t2);
-            split2(y, &ohi[j / 2 + k], &olo[j / 2 + k]);
-            float2 w = __fmul2_rn(__fmul2_rn(y, us2), cs[k]);
-            if (first_bad < 64) w = make_float2(0.f, 0.f);
-            split2(w, &hi[j / 2 + k], &lo[j / 2 + k]);
-          }
+        for (int j = 0; j < 16; j += 2) {
+          const float2 cu = *reinterpret_cast<const float2*>(&g.scal[S_CU][i + j]);
+          const float2 y = __fmul2_rn(make_float2(u[j], u[j + 1]), t2);
+          split2(y, &ohi[j / 2], &olo[j / 2]);
+          float2 w = __fmul2_rn(__fmul2_rn(y, us2), cu);
+          if (first_bad < kChunk) w = make_float2(0.f, 0.f);
+          split2(w, &hi[j / 2], &lo[j / 2]);
         }
-        tmem_st16(tmem + kRhi + half * 16 + lanes, hi);
-        tmem_st16(tmem + kRlo + half * 16 + lanes, lo);
-        tmem_st16(tmem + kUhi + half * 16 + lanes, ohi);
-        tmem_st16(tmem + kUlo + half * 16 + lanes, olo);
+        tmem_st8(tmem + kRhi + i / 2 + lanes, hi);
+        tmem_st8(tmem + kRlo + i / 2 + lanes, lo);
+        tmem_st8(tmem + kUhi + i / 2 + lanes, ohi);
+        tmem_st8(tmem + kUlo + i / 2 + lanes, olo);
       }
-      if (first_bad < 64) dead = true;
+      if (first_bad < kChunk) dead = true;  // from now on
       fs = fs_next;
       tmem_wait_st();
       tc_fence_before();
@@ -859,54 +865,96 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       // ahead of the output warps
       if (lane == 0) {
         mbar_arrive(&s.u_ready);
-        mbar_arrive(&s.row_ready);
+        if (half == 0) mbar_arrive(&s.row_ready);
       }
     }
     // the state after the last chunk
-    const uint32_t ph = (chunks - 1) & 1;
-    if (ok) ok = mbar_wait(&s.s_done[0], ph);
-    if (ok) ok = mbar_wait(&s.s_done[1], ph);
+    if (ok) ok = mbar_wait(&s.s_done[half], (chunks - 1) & 1);
     tc_fence_after();
     const float nan = __int_as_float(0x7fffffff), inv = inverse_pow2(fs);
-    for (int col = 0; col < D; col += 32) {
-      float x[32];
-      tmem_ld32(tmem + kS + col + lanes, x);
+#pragma unroll 1
+    for (int col = col0; col < col0 + D / 2; col += 16) {
+      float x[16];
+      tmem_ld16(tmem + kS + col + lanes, x);
       if (!real || !ok) continue;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = dead ? nan : x[j] * inv;
+      for (int j = 0; j < 16; ++j) x[j] = dead ? nan : x[j] * inv;
       const size_t at = (((size_t)out * p.Hv + h) * D + row) * D + col;
       if constexpr (BF16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.state) + at + 8 * j) =
               make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
                          pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7]));
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
           *reinterpret_cast<float4*>(static_cast<float*>(p.state) + at + 4 * j) =
               make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ---- the outputs
-    const int row = tid - 256, w = warp - 8;
+    const int row = tid & 127, w = warp - 12;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    // Sums of this row's v over chunk n: see ChainSmem::sums.
+    const auto sum_up = [&](int n) {
+      const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
+      ChainIn<D>& g = s.in[st];
+      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
+      const __nv_bfloat16* v = &g.v[0][row & (D - 1)];
+      float2 b2 = make_float2(0.f, 0.f), w2 = b2;
+      float m = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < toks; i += 16) {
+        float a[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] = fabsf(bf16_to_f(v[(i + j) * D]));
+        if (i + 16 > toks) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (i + j >= toks) a[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 y = make_float2(a[j], a[j + 1]);
+          b2 = __ffma2_rn(*reinterpret_cast<const float2*>(&g.scal[S_BETA][i + j]), y, b2);
+          w2 = __ffma2_rn(*reinterpret_cast<const float2*>(&g.scal[S_W][i + j]), y, w2);
+          m = fmaxf(m, fmaxf(y.x, y.y));
+        }
+      }
+      int bad = __float_as_int(g.scal[S_END][1]);
+      float4 sum = make_float4(b2.x + b2.y, w2.x + w2.y, m, 0.f);
+      if (bad < kChunk || !finite(sum.x)) {
+        // up to the first token whose v, k or gates are not finite (beta <= 1)
+        sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < min(toks, bad); ++i) {
+          const float a = fabsf(bf16_to_f(v[i * D]));
+          if (!finite(a)) {
+            bad = i;
+            break;
+          }
+          sum.x += a;
+          sum.z = fmaxf(sum.z, a);
+        }
+      }
+      sum.w = __int_as_float(bad);
+      s.sums[st][row] = sum;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s.sums_ready);
+        mbar_arrive(&s.empty[st]);
+      }
+    };
+    sum_up(0);
     // On the way out eight lanes take a row, four columns in every 32 each; a warp
     // the rows 16 w .. 16 w + 15, four at a time.
     constexpr int E = D / 32;
     const int sub = lane >> 3, l8 = (lane & 7) * 4;
-    float gw[E][4] = {};
-    if (p.z) {
-#pragma unroll
-      for (int k = 0; k < E; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) gw[k][j] = bf16_to_f(p.gnorm_w[32 * k + l8 + j]);
-    }
     for (int n = 0; n < chunks; ++n) {
       const int st = n & 1, t0 = b + n * kChunk, toks = min(kChunk, e - t0);
       const uint32_t ph = n & 1;
-      ChainStage<D>& g = s.st[st];
+      OutIn<D>& y = s.oin[st];
       // this warp's rows of z, in flight while the chunk is finished
       uint2 z[4][E];
 #pragma unroll
@@ -919,26 +967,31 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
             z[i][k] = __ldg(reinterpret_cast<const uint2*>(p.z + (long long)(t0 + t) * p.ldz + h * D + 32 * k + l8));
         }
       }
+      if (n + 1 < chunks) {
+        // P of this chunk says that its sums are read, so sums_ready never runs two
+        // phases ahead of the state's rows
+        if (ok) ok = mbar_wait(&s.p_done, ph);
+        sum_up(n + 1);
+      }
       if (ok) ok = mbar_wait(&s.row_ready, ph);
-      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
+      if (ok) ok = mbar_wait(&s.ofull[st], (n >> 1) & 1);
       const float inv_s = s.inv_s[st][row], inv_u = s.inv_u[st][row];
       const int first_bad = s.first_bad[st][row];
       if (ok) ok = mbar_wait(&s.o_done, ph);
       tc_fence_after();
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        float x[32], y[32];
-        tmem_ld32(tmem + kQS + half * 32 + lanes, x);
-        tmem_ld32(tmem + kAU + half * 32 + lanes, y);
+      for (int i = 0; i < kChunk; i += 16) {
+        float x[16], u[16];
+        tmem_ld16(tmem + kQS + i + lanes, x);
+        tmem_ld16(tmem + kAU + i + lanes, u);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const int i = half * 32 + j;
-          const float4 cg = *reinterpret_cast<const float4*>(&g.scal[S_CQG][i]);
-          const float4 cq = *reinterpret_cast<const float4*>(&g.scal[S_CQ][i]);
-          s.o[i][row] = fmaf(cg.x, x[j] * inv_s, cq.x * (y[j] * inv_u));
-          s.o[i + 1][row] = fmaf(cg.y, x[j + 1] * inv_s, cq.y * (y[j + 1] * inv_u));
-          s.o[i + 2][row] = fmaf(cg.z, x[j + 2] * inv_s, cq.z * (y[j + 2] * inv_u));
-          s.o[i + 3][row] = fmaf(cg.w, x[j + 3] * inv_s, cq.w * (y[j + 3] * inv_u));
+        for (int j = 0; j < 16; j += 4) {
+          const float4 cg = *reinterpret_cast<const float4*>(&y.scal[O_CQG][i + j]);
+          const float4 cq = *reinterpret_cast<const float4*>(&y.scal[O_CQ][i + j]);
+          s.o[i + j][row] = fmaf(cg.x, x[j] * inv_s, cq.x * (u[j] * inv_u));
+          s.o[i + j + 1][row] = fmaf(cg.y, x[j + 1] * inv_s, cq.y * (u[j + 1] * inv_u));
+          s.o[i + j + 2][row] = fmaf(cg.z, x[j + 2] * inv_s, cq.z * (u[j + 2] * inv_u));
+          s.o[i + j + 3][row] = fmaf(cg.w, x[j + 3] * inv_s, cq.w * (u[j + 3] * inv_u));
         }
       }
       for (int i = first_bad; i < kChunk; ++i) s.o[i][row] = __int_as_float(0x7fffffff);
@@ -946,7 +999,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&s.o_free);
-        mbar_arrive(&s.empty[st]);
+        mbar_arrive(&s.oempty[st]);
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");  // the output warps: every row is staged
 #pragma unroll
@@ -965,11 +1018,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
           const float r = rsqrtf(sum * (1.0f / D) + p.gnorm_eps);
 #pragma unroll
           for (int k = 0; k < E; ++k) {
-            const float zf[4] = {bf16_lo(z[i][k].x), bf16_hi(z[i][k].x), bf16_lo(z[i][k].y), bf16_hi(z[i][k].y)};
-            o[k].x *= r * gw[k][0] * gate(zf[0]);
-            o[k].y *= r * gw[k][1] * gate(zf[1]);
-            o[k].z *= r * gw[k][2] * gate(zf[2]);
-            o[k].w *= r * gw[k][3] * gate(zf[3]);
+            const uint2 gw = __ldg(reinterpret_cast<const uint2*>(p.gnorm_w + 32 * k + l8));
+            o[k].x *= r * bf16_lo(gw.x) * gate(bf16_lo(z[i][k].x));
+            o[k].y *= r * bf16_hi(gw.x) * gate(bf16_hi(z[i][k].x));
+            o[k].z *= r * bf16_lo(gw.y) * gate(bf16_lo(z[i][k].y));
+            o[k].w *= r * bf16_hi(gw.y) * gate(bf16_hi(z[i][k].y));
           }
         }
         if (t < toks) {

@@ -97,8 +97,8 @@ gdn_status gdn_prefill_conv(gdn_prefill_t* h, int32_t seqs, int32_t tokens, cons
  * bf16 or NULL; ba [tokens][ldba >= 2*Hv] bf16, rows b | a; A_log [Hv] f32;
  * dt_bias [Hv] bf16; gated_norm_w [dv] bf16; ssm_state [num_slots][Hv][dv][dk]
  * f32 or bf16; core_out [tokens][ldcore >= Hv*dv] bf16. ldqkv, ldz and ldcore
- * are multiples of 8, the pointers of qkv, z, core_out and ssm_state 16-byte
- * aligned. core_out must overlap no input. One call at a time per handle
+ * are multiples of 8, the pointers of qkv, z, core_out, gated_norm_w and
+ * ssm_state 16-byte aligned. core_out must overlap no input. One call at a time per handle
  * (its calls share the workspace). */
 gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t tokens, int32_t max_len,
                              const void* qkv, int64_t ldqkv, const void* z, int64_t ldz, const void* ba,
