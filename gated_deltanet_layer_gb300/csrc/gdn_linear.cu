@@ -157,7 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       ok = mbar_wait(&s.empty[st], ph ^ 1);
       if (++st == kStages) st = 0, ph ^= 1;
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     constexpr uint32_t idesc = idesc_bf16_f32(256, BN);
     int st = 0, buf = 0;
     uint32_t ph = 0, aph = 0;
@@ -168,13 +168,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int k = 0; k < ksteps; ++k) {
         if (!(ok = mbar_wait(&s.full[st], ph))) break;
         tc_fence_after();
-        const uint64_t a = sdesc_k_sw128(smem_u32(s.a[st])), b = sdesc_k_sw128(smem_u32(s.b[st]));
+        if (elect_one()) {
+          const uint64_t a = sdesc_k_sw128(smem_u32(s.a[st])), b = sdesc_k_sw128(smem_u32(s.b[st]));
 #pragma unroll
-        for (int j = 0; j < kBK / 16; ++j) mma_bf16_pair(d, a + 2 * j, b + 2 * j, idesc, (k | j) != 0);
-        mma_commit_pair(&s.empty[st]);
+          for (int j = 0; j < kBK / 16; ++j) mma_bf16_pair(d, a + 2 * j, b + 2 * j, idesc, (k | j) != 0);
+          mma_commit_pair(&s.empty[st]);
+        }
+        __syncwarp();
         if (++st == kStages) st = 0, ph ^= 1;
       }
-      mma_commit_pair(&s.acc_full[buf]);
+      if (elect_one()) mma_commit_pair(&s.acc_full[buf]);
+      __syncwarp();
       if (++buf == 2) buf = 0, aph ^= 1;
     }
   } else if (warp >= 4) {
@@ -317,20 +321,23 @@ __global__ void __launch_bounds__(kFewThreads) linear_few(const __grid_constant_
       tma_load_2d_plain(w + 128 * 128, &xmap, k * kBK, 0, &full[st]);
       if (++st == f.stages) st = 0, ph ^= 1;
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, TOK);
     int st = 0;
     uint32_t ph = 0;
     for (int k = k0; k < k1; ++k) {
       if (!(ok = mbar_wait(&full[st], ph))) break;
       tc_fence_after();
-      const uint64_t a = sdesc_k_sw128(smem_u32(ring + st * kBytes)), b = sdesc_k_sw128(smem_u32(ring + st * kBytes + 128 * 128));
+      if (elect_one()) {
+        const uint64_t a = sdesc_k_sw128(smem_u32(ring + st * kBytes)), b = sdesc_k_sw128(smem_u32(ring + st * kBytes + 128 * 128));
 #pragma unroll
-      for (int j = 0; j < kBK / 16; ++j) mma_bf16(tmem, a + 2 * j, b + 2 * j, idesc, (k > k0) | (j > 0));
-      mma_commit(&empty[st]);
+        for (int j = 0; j < kBK / 16; ++j) mma_bf16(tmem, a + 2 * j, b + 2 * j, idesc, (k > k0) | (j > 0));
+        mma_commit(&empty[st]);
+      }
+      __syncwarp();
       if (++st == f.stages) st = 0, ph ^= 1;
     }
-    mma_commit(&done);
+    if (elect_one()) mma_commit(&done);
   } else if (warp >= 2) {
     ok = mbar_wait(&done, 0);
     ok = __all_sync(0xffffffffu, ok);

@@ -47,7 +47,9 @@ using namespace tc;
 constexpr float kScaleT = 4096.f;   // of T's f16 images
 // A chunk's images and scalars of a value head, arrays of 64 floats: what the state's
 // chain needs (T hi, T lo) and what the outputs need (causal products hi, lo).
-enum { S_BETA, S_C1, S_CU, S_W, S_END, S_COUNT };
+// S_R: of every two tokens beta, beta, beta c, beta c with c = e^G / |k|; S_B: beta,
+// beta, w, w with w = e^(G_C-G) beta; S_CU: e^(G_C-G) / |k|.
+enum { S_R = 0, S_B = 2, S_CU = 4, S_END, S_COUNT };
 enum { O_CQG, O_CQ, O_COUNT };
 constexpr int kImg = 2 * 8192;  // two images of 64 x 64 f16
 constexpr int kChainBytes = kImg + S_COUNT * 256, kOutBytes = kImg + O_COUNT * 256;
@@ -69,11 +71,13 @@ __device__ __forceinline__ int swz(int row, int col) { return row * 128 + ((((co
 
 __device__ __forceinline__ uint32_t pack_h2(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// y = hi + lo, two f16 each
+// y = hi + lo, two f16 each: hi is y cut to f16's 11 bits, so their difference is exact
+// and needs no conversion back.
 __device__ __forceinline__ void split2(float2 y, uint32_t* hi, uint32_t* lo) {
-  const __half2 h = __float22half2_rn(y);
-  *hi = pack_h2(h);
-  *lo = pack_h2(__float22half2_rn(__ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), y)));
+  const float2 h = make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffffe000u),
+                               __uint_as_float(__float_as_uint(y.y) & 0xffffe000u));
+  *hi = pack_h2(__float22half2_rn(h));
+  *lo = pack_h2(__float22half2_rn(__ffma2_rn(h, make_float2(-1.f, -1.f), y)));
 }
 
 // D[tmem] (+)= A[smem or tmem] B[smem], f16 operands, f32 accumulation.
@@ -161,6 +165,7 @@ struct alignas(1024) PrepSmem {
   unsigned char a[2][2][8192];  // causal products of two heads, hi and lo
   float m[2][64 * kLStride];    // L, then T in its place
   float scal[2][S_COUNT][64], oscal[2][O_COUNT][64];
+  float beta[2][64];
   float ghi[2][64], glo[2][64];  // running sums of the log2 gates
   float bj[2][64];               // 2^(G of the 16-block's end - G_j) / norm of k_j
   float top[2][64];              // of a row of the causal products, by column halves
@@ -308,10 +313,14 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
         s.ghi[warp][tok] = G[k].hi;
         s.glo[warp][tok] = G[k].lo;
         s.bj[warp][tok] = s.rn[tok] * exp2f((bhi - G[k].hi) + (blo - G[k].lo));
-        s.scal[warp][S_BETA][tok] = beta[k];
-        s.scal[warp][S_C1][tok] = gam * s.rn[tok];
+        s.beta[warp][tok] = beta[k];
+        float* r = s.scal[warp][S_R] + 4 * lane + k;
+        r[0] = beta[k];
+        r[2] = beta[k] * (gam * s.rn[tok]);
         s.scal[warp][S_CU][tok] = left * s.rn[tok];
-        s.scal[warp][S_W][tok] = left * beta[k];
+        float* w = s.scal[warp][S_B] + 4 * lane + k;
+        w[0] = beta[k];
+        w[2] = left * beta[k];
         s.oscal[warp][O_CQG][tok] = p.q_scale * s.rn[64 + tok] * gam;
       }
       if (lane == 0) {
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       float dot[32];
       tmem_ld32(tmem + 32 * half + ((uint32_t)((warp & 3) * 32) << 16), dot);
       const float gi = s.ghi[h][i], li = s.glo[h][i];
-      const float f = lower ? s.scal[h][S_BETA][i] * s.rn[i] : 1.f;
+      const float f = lower ? s.beta[h][i] * s.rn[i] : 1.f;
       float mx = 0.f;
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb) {
@@ -513,6 +522,7 @@ struct ChainSmem {
   ChainIn<D> in[2];
   OutIn<D> oin[2];
   float o[64][132];
+  uint32_t vt[32][128];  // v of two tokens, by rows of the state
   float4 sums[2][128];  // of a row's v: sum beta |v|, sum e^(G_C-G) beta |v|, max |v|, first token not finite
   float part[2][128];   // of a row's squares, by halves of its columns
   float inv_s[2][128], inv_u[2][128];
@@ -618,75 +628,95 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       if (ok) ok = mbar_wait(&s.full[n & 1], (n >> 1) & 1);
       if (ok) ok = mbar_wait(&s.ofull[n & 1], (n >> 1) & 1);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
+    // the whole warp waits, one lane issues
     constexpr uint32_t idesc = idesc_f16(128, 64, false), idesc_s = idesc_f16(128, 64, true);
     for (int n = 0; n < chunks && ok; ++n) {
       const int st = n & 1;
       const uint32_t ph = n & 1;
       ChainIn<D>& g = s.in[st];
       OutIn<D>& y = s.oin[st];
-      ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      const uint32_t k = smem_u32(g.k), q = smem_u32(y.q);
+      const uint64_t kd = sdesc_k_sw128(smem_u32(g.k)), qd = sdesc_k_sw128(smem_u32(y.q));
+      if (!(ok = mbar_wait(&s.full[st], (n >> 1) & 1))) break;
       // P = S k, in halves of dk as they are ready
+      if (!(ok = mbar_wait(&s.s_ready[0], ph))) break;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        ok = ok && mbar_wait(&s.s_ready[hh], ph);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int j = hh * D / 32; j < (hh + 1) * D / 32; ++j) {
-          const uint64_t bd = sdesc_k_sw128(k + (j >> 2) * 8192) + 2 * (j & 3);
+        for (int j = 0; j < D / 32; ++j) {
+          const uint64_t bd = kd + (j >> 2) * 512 + 2 * (j & 3);
           mma_f16_ts(tmem + kPU, tmem + kShi + 8 * j, bd, idesc, j > 0);
           mma_f16_ts(tmem + kPU, tmem + kSlo + 8 * j, bd, idesc, true);
         }
       }
-      if (!ok) break;
-      mma_commit(&s.p_done);
+      __syncwarp();
+      if (!(ok = mbar_wait(&s.s_ready[1], ph))) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int j = D / 32; j < D / 16; ++j) {
+          const uint64_t bd = kd + (j >> 2) * 512 + 2 * (j & 3);
+          mma_f16_ts(tmem + kPU, tmem + kShi + 8 * j, bd, idesc, true);
+          mma_f16_ts(tmem + kPU, tmem + kSlo + 8 * j, bd, idesc, true);
+        }
+        mma_commit(&s.p_done);
+      }
+      __syncwarp();
       // the state's part of the outputs, under the chain
       if (!(ok = mbar_wait(&s.ofull[st], (n >> 1) & 1))) break;
       if (!(ok = mbar_wait(&s.o_free, ph ^ 1))) break;
       tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        const uint64_t bd = sdesc_k_sw128(q + (j >> 2) * 8192) + 2 * (j & 3);
-        mma_f16_ts(tmem + kQS, tmem + kShi + 8 * j, bd, idesc, j > 0);
-        mma_f16_ts(tmem + kQS, tmem + kSlo + 8 * j, bd, idesc, true);
+        for (int j = 0; j < D / 16; ++j) {
+          const uint64_t bd = qd + (j >> 2) * 512 + 2 * (j & 3);
+          mma_f16_ts(tmem + kQS, tmem + kShi + 8 * j, bd, idesc, j > 0);
+          mma_f16_ts(tmem + kQS, tmem + kSlo + 8 * j, bd, idesc, true);
+        }
       }
+      __syncwarp();
       // U = R T^T
       if (!(ok = mbar_wait(&s.r_ready, ph))) break;
       tc_fence_after();
-      const uint64_t th = sdesc_k_sw128(smem_u32(g.thi)), tl = sdesc_k_sw128(smem_u32(g.tlo));
+      if (elect_one()) {
+        const uint64_t th = sdesc_k_sw128(smem_u32(g.thi)), tl = sdesc_k_sw128(smem_u32(g.tlo));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_f16_ts(tmem + kPU, tmem + kRhi + 8 * j, th + 2 * j, idesc, j > 0);
-        mma_f16_ts(tmem + kPU, tmem + kRhi + 8 * j, tl + 2 * j, idesc, true);
-        mma_f16_ts(tmem + kPU, tmem + kRlo + 8 * j, th + 2 * j, idesc, true);
+        for (int j = 0; j < 4; ++j) {
+          mma_f16_ts(tmem + kPU, tmem + kRhi + 8 * j, th + 2 * j, idesc, j > 0);
+          mma_f16_ts(tmem + kPU, tmem + kRhi + 8 * j, tl + 2 * j, idesc, true);
+          mma_f16_ts(tmem + kPU, tmem + kRlo + 8 * j, th + 2 * j, idesc, true);
+        }
+        mma_commit(&s.u_done);
       }
-      mma_commit(&s.u_done);
+      __syncwarp();
       // S += U' k, 64 columns of dk at a time (U' hi, lo stand where R's were)
       if (!(ok = mbar_wait(&s.u_ready, ph))) break;
       tc_fence_after();
+      if (elect_one()) {
+        const uint64_t km = sdesc_mn_sw128(smem_u32(g.k), 8192);
 #pragma unroll
-      for (int a = 0; a < D / 64; ++a) {
+        for (int a = 0; a < D / 64; ++a) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t bd = km + a * 512 + j * 128;
+            mma_f16_ts(tmem + kS + a * 64, tmem + kRhi + 8 * j, bd, idesc_s, true);
+            mma_f16_ts(tmem + kS + a * 64, tmem + kRlo + 8 * j, bd, idesc_s, true);
+          }
+          mma_commit(&s.s_done[a]);
+        }
+        if (D == 64) mma_commit(&s.s_done[1]);
+        mma_commit(&s.empty[st]);
+        const uint64_t ah = sdesc_k_sw128(smem_u32(y.ahi)), al = sdesc_k_sw128(smem_u32(y.alo));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint64_t bd = sdesc_mn_sw128(k + a * 8192 + j * 2048, 8192);
-          mma_f16_ts(tmem + kS + a * 64, tmem + kRhi + 8 * j, bd, idesc_s, true);
-          mma_f16_ts(tmem + kS + a * 64, tmem + kRlo + 8 * j, bd, idesc_s, true);
+          mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, ah + 2 * j, idesc, j > 0);
+          mma_f16_ts(tmem + kAU, tmem + kUlo + 8 * j, ah + 2 * j, idesc, true);
+          mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, al + 2 * j, idesc, true);
         }
-        mma_commit(&s.s_done[a]);
+        mma_commit(&s.o_done);
+        mma_commit(&s.oempty[st]);
       }
-      if (D == 64) mma_commit(&s.s_done[1]);
-      mma_commit(&s.empty[st]);
-      const uint64_t ah = sdesc_k_sw128(smem_u32(y.ahi)), al = sdesc_k_sw128(smem_u32(y.alo));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, ah + 2 * j, idesc, j > 0);
-        mma_f16_ts(tmem + kAU, tmem + kUlo + 8 * j, ah + 2 * j, idesc, true);
-        mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, al + 2 * j, idesc, true);
-      }
-      mma_commit(&s.o_done);
-      mma_commit(&s.oempty[st]);
+      __syncwarp();
     }
     // no MMA is in flight when the TMEM is freed
     if (ok) ok = mbar_wait(&s.o_done, (chunks - 1) & 1);
@@ -800,17 +830,16 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 #pragma unroll 1
       for (int i = tok0; i < tok0 + 32; i += 16) {
         float x[16];
-        uint32_t v[16], hi[8], lo[8];
+        uint32_t v[8], hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __bfloat16_as_ushort(g.v[i + j][vrow]);
+        for (int j = 0; j < 8; ++j) v[j] = s.vt[i / 2 + j][row];
         tmem_ld16(tmem + kPU + i + lanes, x);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const float2 be = *reinterpret_cast<const float2*>(&g.scal[S_BETA][i + j]);
-          const float2 c1 = *reinterpret_cast<const float2*>(&g.scal[S_C1][i + j]);
-          const float2 vv = make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j + 1] << 16));
-          const float2 q = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), c1);
-          const float2 r = __fmul2_rn(be, __ffma2_rn(f2, vv, q));
+          const float4 rc = *reinterpret_cast<const float4*>(&g.scal[S_R][2 * (i + j)]);
+          const float2 vv = __fmul2_rn(make_float2(bf16_lo(v[j / 2]), bf16_hi(v[j / 2])), f2);
+          const float2 q = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), make_float2(rc.z, rc.w));
+          const float2 r = __ffma2_rn(vv, make_float2(rc.x, rc.y), q);
           x[j] = r.x, x[j + 1] = r.y;
         }
         if (until < kChunk) {
@@ -843,7 +872,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         }
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const float2 cu = *reinterpret_cast<const float2*>(&g.scal[S_CU][i + j]);
+          const float4 c4 = *reinterpret_cast<const float4*>(&g.scal[S_CU][i + (j & ~3)]);
+          const float2 cu = j & 2 ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
           const float2 y = __fmul2_rn(make_float2(u[j], u[j + 1]), t2);
           split2(y, &ohi[j / 2], &olo[j / 2]);
           float2 w = __fmul2_rn(__fmul2_rn(y, us2), cu);
@@ -897,7 +927,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     // ---- the outputs
     const int row = tid & 127, w = warp - 12;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    // Sums of this row's v over chunk n: see ChainSmem::sums.
+    // Sums of this row's v over chunk n (ChainSmem::sums), and v by rows.
     const auto sum_up = [&](int n) {
       const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
       ChainIn<D>& g = s.in[st];
@@ -907,19 +937,21 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       float m = 0.f;
 #pragma unroll 1
       for (int i = 0; i < toks; i += 16) {
-        float a[16];
+        uint32_t a[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) a[j] = fabsf(bf16_to_f(v[(i + j) * D]));
+        for (int j = 0; j < 8; ++j)
+          a[j] = __bfloat16_as_ushort(v[(i + 2 * j) * D]) | ((uint32_t)__bfloat16_as_ushort(v[(i + 2 * j + 1) * D]) << 16);
         if (i + 16 > toks) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (i + j >= toks) a[j] = 0.f;
+          for (int j = 0; j < 8; ++j) a[j] &= i + 2 * j + 1 < toks ? 0xffffffffu : i + 2 * j < toks ? 0xffffu : 0u;
         }
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float2 y = make_float2(a[j], a[j + 1]);
-          b2 = __ffma2_rn(*reinterpret_cast<const float2*>(&g.scal[S_BETA][i + j]), y, b2);
-          w2 = __ffma2_rn(*reinterpret_cast<const float2*>(&g.scal[S_W][i + j]), y, w2);
+        for (int j = 0; j < 8; ++j) {
+          s.vt[i / 2 + j][row] = a[j];
+          const float4 bw = *reinterpret_cast<const float4*>(&g.scal[S_B][2 * (i + 2 * j)]);
+          const float2 y = make_float2(fabsf(bf16_lo(a[j])), fabsf(bf16_hi(a[j])));
+          b2 = __ffma2_rn(make_float2(bw.x, bw.y), y, b2);
+          w2 = __ffma2_rn(make_float2(bw.z, bw.w), y, w2);
           m = fmaxf(m, fmaxf(y.x, y.y));
         }
       }
@@ -968,9 +1000,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         }
       }
       if (n + 1 < chunks) {
-        // P of this chunk says that its sums are read, so sums_ready never runs two
-        // phases ahead of the state's rows
-        if (ok) ok = mbar_wait(&s.p_done, ph);
+        // U of this chunk says that its sums and vt are read, so they may be written
+        // and sums_ready never runs two phases ahead of the state's rows
+        if (ok) ok = mbar_wait(&s.u_done, ph);
         sum_up(n + 1);
       }
       if (ok) ok = mbar_wait(&s.row_ready, ph);
