@@ -490,12 +490,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
 // ------------------------------------------------------------------ the chunks of a sequence
 
 // Warps: 0 loads, 1 issues MMAs, 2 holds the TMEM; 4 to 11 keep the state's rows (a
-// thread is a row of S^T and half of its columns, or of the chunk's tokens); 12 to 15
-// write the outputs, and sum up the next chunk's v on the side.
+// thread is a row of S^T and half of its columns, or of the chunk's tokens); 12 to 19
+// write the outputs, half of the tokens each four, and sum up the next chunk's v on the
+// side.
 // The loops over columns and tokens are rolled, 16 at a time: one warp a scheduler in
 // code that runs straight through waits for its instructions (unrolled, a chunk took 4
 // times as long).
-constexpr int kChainThreads = 512;
+constexpr int kChainThreads = 640;
 
 // TMEM columns
 constexpr uint32_t kS = 0, kShi = 128, kSlo = 192, kPU = 256, kRhi = 320, kRlo = 352, kQS = 384, kAU = 448;
@@ -510,6 +511,8 @@ struct alignas(1024) ChainIn {
   float scal[S_COUNT][64];
   __nv_bfloat16 v[64][D];
 };
+// When the chunk's products are done, the outputs are staged over the images
+// ([token][D] f32).
 template <int D>
 struct alignas(1024) OutIn {
   unsigned char q[64 * D * 2];
@@ -521,9 +524,10 @@ template <int D>
 struct ChainSmem {
   ChainIn<D> in[2];
   OutIn<D> oin[2];
-  float o[64][132];
   uint32_t vt[32][128];  // v of two tokens, by rows of the state
-  float4 sums[2][128];  // of a row's v: sum beta |v|, sum e^(G_C-G) beta |v|, max |v|, first token not finite
+  // of a row's v, by halves of the tokens: sum beta |v|, sum e^(G_C-G) beta |v|, max |v|,
+  // first token not finite
+  float4 sums[2][2][128];
   float part[2][128];   // of a row's squares, by halves of its columns
   float inv_s[2][128], inv_u[2][128];
   int first_bad[2][128];
@@ -570,9 +574,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 5);  // the MMAs' commit, and the output warps' sums
+      mbar_init(&s.empty[i], 9);  // the MMAs' commit, and the output warps' sums
       mbar_init(&s.ofull[i], 1);
-      mbar_init(&s.oempty[i], 5);  // the MMAs' commit, and the output warps
+      mbar_init(&s.oempty[i], 9);  // the MMAs' commit, and the output warps
       mbar_init(&s.s_ready[i], 4);
       mbar_init(&s.s_done[i], 1);
     }
@@ -581,9 +585,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     mbar_init(&s.u_done, 1);
     mbar_init(&s.u_ready, 8);
     mbar_init(&s.o_done, 1);
-    mbar_init(&s.o_free, 4);
+    mbar_init(&s.o_free, 8);
     mbar_init(&s.row_ready, 4);
-    mbar_init(&s.sums_ready, 4);
+    mbar_init(&s.sums_ready, 8);
     fence_mbar_init();
   }
   if (warp == 2) tmem_alloc(&s.tmem, 512);
@@ -769,7 +773,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       if (ok) ok = mbar_wait(&s.sums_ready, ph);
       // both halves of the last chunk's squares are written
       asm volatile("bar.sync 2, 256;" ::: "memory");
-      const float4 sum = s.sums[st][row];
+      float4 sum = s.sums[st][0][row];
+      {
+        const float4 late = s.sums[st][1][row];
+        sum.x += late.x, sum.y += late.y, sum.z = fmaxf(sum.z, late.z);
+        sum.w = __int_as_float(min(__float_as_int(sum.w), __float_as_int(late.w)));
+      }
       if (n > 0) bound = fminf(bound, fmaf(near_mul, sqrtf(s.part[0][row] + s.part[1][row]), near) * 1.01f);
       const int first_bad = dead ? 0 : __float_as_int(sum.w);
       const float gam_end = first_bad < kChunk ? 0.f : g.scal[S_END][0], sw = first_bad < kChunk ? 0.f : sum.y;
@@ -925,7 +934,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     }
   } else if (warp >= 12) {
     // ---- the outputs
-    const int row = tid & 127, w = warp - 12;
+    const int row = tid & 127, w = warp - 12, half = w >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     // Sums of this row's v over chunk n (ChainSmem::sums), and v by rows.
     const auto sum_up = [&](int n) {
@@ -936,7 +945,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       float2 b2 = make_float2(0.f, 0.f), w2 = b2;
       float m = 0.f;
 #pragma unroll 1
-      for (int i = 0; i < toks; i += 16) {
+      for (int i = 32 * half; i < min(toks, 32 * half + 32); i += 16) {
         uint32_t a[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -960,7 +969,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       if (bad < kChunk || !finite(sum.x)) {
         // up to the first token whose v, k or gates are not finite (beta <= 1)
         sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < min(toks, bad); ++i) {
+        for (int i = 32 * half; i < min(min(toks, bad), 32 * half + 32); ++i) {
           const float a = fabsf(bf16_to_f(v[i * D]));
           if (!finite(a)) {
             bad = i;
@@ -971,7 +980,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         }
       }
       sum.w = __int_as_float(bad);
-      s.sums[st][row] = sum;
+      s.sums[st][half][row] = sum;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&s.sums_ready);
@@ -980,18 +989,19 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     };
     sum_up(0);
     // On the way out eight lanes take a row, four columns in every 32 each; a warp
-    // the rows 16 w .. 16 w + 15, four at a time.
+    // the rows 8 w .. 8 w + 7, four at a time.
     constexpr int E = D / 32;
     const int sub = lane >> 3, l8 = (lane & 7) * 4;
     for (int n = 0; n < chunks; ++n) {
       const int st = n & 1, t0 = b + n * kChunk, toks = min(kChunk, e - t0);
       const uint32_t ph = n & 1;
       OutIn<D>& y = s.oin[st];
+      float* o32 = reinterpret_cast<float*>(y.q);
       // this warp's rows of z, in flight while the chunk is finished
-      uint2 z[4][E];
+      uint2 z[2][E];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * w + 4 * i + sub;
+      for (int i = 0; i < 2; ++i) {
+        const int t = 8 * w + 4 * i + sub;
 #pragma unroll
         for (int k = 0; k < E; ++k) {
           z[i][k] = make_uint2(0, 0);
@@ -1012,7 +1022,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       if (ok) ok = mbar_wait(&s.o_done, ph);
       tc_fence_after();
 #pragma unroll 1
-      for (int i = 0; i < kChunk; i += 16) {
+      for (int i = 32 * half; i < 32 * half + 32; i += 16) {
         float x[16], u[16];
         tmem_ld16(tmem + kQS + i + lanes, x);
         tmem_ld16(tmem + kAU + i + lanes, u);
@@ -1020,26 +1030,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         for (int j = 0; j < 16; j += 4) {
           const float4 cg = *reinterpret_cast<const float4*>(&y.scal[O_CQG][i + j]);
           const float4 cq = *reinterpret_cast<const float4*>(&y.scal[O_CQ][i + j]);
-          s.o[i + j][row] = fmaf(cg.x, x[j] * inv_s, cq.x * (u[j] * inv_u));
-          s.o[i + j + 1][row] = fmaf(cg.y, x[j + 1] * inv_s, cq.y * (u[j + 1] * inv_u));
-          s.o[i + j + 2][row] = fmaf(cg.z, x[j + 2] * inv_s, cq.z * (u[j + 2] * inv_u));
-          s.o[i + j + 3][row] = fmaf(cg.w, x[j + 3] * inv_s, cq.w * (u[j + 3] * inv_u));
+          u[j] = fmaf(cg.x, x[j] * inv_s, cq.x * (u[j] * inv_u));
+          u[j + 1] = fmaf(cg.y, x[j + 1] * inv_s, cq.y * (u[j + 1] * inv_u));
+          u[j + 2] = fmaf(cg.z, x[j + 2] * inv_s, cq.z * (u[j + 2] * inv_u));
+          u[j + 3] = fmaf(cg.w, x[j + 3] * inv_s, cq.w * (u[j + 3] * inv_u));
+        }
+        if (row < D) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o32[(i + j) * D + row] = i + j < first_bad ? u[j] : __int_as_float(0x7fffffff);
         }
       }
-      for (int i = first_bad; i < kChunk; ++i) s.o[i][row] = __int_as_float(0x7fffffff);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s.o_free);
-        mbar_arrive(&s.oempty[st]);
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the output warps: every row is staged
+      if (lane == 0) mbar_arrive(&s.o_free);
+      asm volatile("bar.sync %0, 128;" ::"r"(3 + half) : "memory");  // this half's rows are staged
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * w + 4 * i + sub;
+      for (int i = 0; i < 2; ++i) {
+        const int t = 8 * w + 4 * i + sub;
         float4 o[E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) o[k] = *reinterpret_cast<const float4*>(&s.o[t][32 * k + l8]);
+        for (int k = 0; k < E; ++k) o[k] = *reinterpret_cast<const float4*>(o32 + t * D + 32 * k + l8);
         if (p.z) {
           float sum = 0.f;
 #pragma unroll
@@ -1064,7 +1074,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
             *reinterpret_cast<uint2*>(dst + 32 * k) = make_uint2(pack_bf16x2(o[k].x, o[k].y), pack_bf16x2(o[k].z, o[k].w));
         }
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // before the next chunk is staged
+      fence_proxy_async_smem();  // the next images come by bulk copies
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.oempty[st]);
     }
   }
   if (!ok) record(p.r.error, kStatusDeadline, kWhatWait, sq);
