@@ -25,10 +25,15 @@ __device__ unsigned int g_linear_error;
 
 constexpr int kBK = 64;  // K columns of a stage: 128 bytes, one swizzle row
 
+// SiLU(y) = y sigmoid(y); GELU's tanh form is y sigmoid(2 u), u = sqrt(2/pi) (y +
+// 0.044715 y^3). The fast exponential and division (a few 2^-22) are far below the
+// rounding to bf16, and short: with expf and tanhf inlined for every value the epilogue
+// outgrew the instruction cache.
+template <bool ACT>
 __device__ __forceinline__ float act_f(float y, int act) {
-  if (act == 1) return silu_f(y);
-  if (act == 2) return 0.5f * y * (1.0f + tanhf(0.7978845608028654f * (y + 0.044715f * y * y * y)));
-  return y;
+  if (!ACT) return y;
+  const float s = act == 1 ? y : y * fmaf(0.07135481627f, y * y, 1.595769122f);
+  return __fdividef(y, 1.0f + __expf(-s));
 }
 
 // ------------------------------------------------------------- many rows
@@ -64,23 +69,25 @@ __device__ __forceinline__ void tile_at(const PairTiles& t, int i, int* m, int* 
 }
 
 // Eight columns of one output row, 16 bytes of residual in and of output out.
+template <bool ACT>
 __device__ __forceinline__ void put8(const LinearParams& p, long long m, int n, const float* v, const float (&bias)[8],
                                      const uint4& res) {
   const uint32_t r[4] = {res.x, res.y, res.z, res.w};
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    o[j] = pack_bf16x2(act_f(v[2 * j] + bias[2 * j], p.act) + bf16_lo(r[j]),
-                       act_f(v[2 * j + 1] + bias[2 * j + 1], p.act) + bf16_hi(r[j]));
+    o[j] = pack_bf16x2(act_f<ACT>(v[2 * j] + bias[2 * j], p.act) + bf16_lo(r[j]),
+                       act_f<ACT>(v[2 * j + 1] + bias[2 * j + 1], p.act) + bf16_hi(r[j]));
   *reinterpret_cast<uint4*>(p.out + m * p.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Two columns of one output row (any alignment).
+template <bool ACT>
 __device__ __forceinline__ void put2(const LinearParams& p, long long m, int n, float a, float b, float bias_a, float bias_b,
                                      bool wide) {
   const bool two = n + 1 < p.N;
-  a = act_f(a + bias_a, p.act);
-  b = act_f(b + bias_b, p.act);
+  a = act_f<ACT>(a + bias_a, p.act);
+  b = act_f<ACT>(b + bias_b, p.act);
   if (p.residual) {
     const __nv_bfloat16* r = p.residual + m * p.ldr + n;
     if (wide && two) {
@@ -100,7 +107,7 @@ __device__ __forceinline__ void put2(const LinearParams& p, long long m, int n, 
   }
 }
 
-template <int BN>
+template <int BN, bool ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const LinearParams p,
                 const PairTiles tiles) {
@@ -240,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
               const int row = 4 * r + (lane >> 3);
-              if (row < rows) put8(p, m0 + row, n8, sm + row * kStageStride + (lane & 7) * 8, bias, res[r]);
+              if (row < rows) put8<ACT>(p, m0 + row, n8, sm + row * kStageStride + (lane & 7) * 8, bias, res[r]);
             }
           }
         } else {
@@ -250,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll 4
             for (int r = 0; r < rows; ++r) {
               const float2 v = *reinterpret_cast<const float2*>(sm + r * kStageStride + 2 * lane);
-              put2(p, m0 + r, n, v.x, v.y, ba, bb, wide);
+              put2<ACT>(p, m0 + r, n, v.x, v.y, ba, bb, wide);
             }
           }
         }
@@ -376,7 +383,8 @@ __global__ void __launch_bounds__(kFewThreads) linear_few(const __grid_constant_
     else
       y = part[i];
     if (n >= p.N) continue;
-    y = act_f(y + (p.bias ? bf16_to_f(p.bias[n]) : 0.f), p.act);
+    y += p.bias ? bf16_to_f(p.bias[n]) : 0.f;
+    if (p.act) y = act_f<true>(y, p.act);
     if (p.residual) y += bf16_to_f(p.residual[m * p.ldr + n]);
     p.out[m * p.ldo + n] = __float2bfloat16_rn(y);
   }
@@ -442,14 +450,17 @@ cudaError_t launch_pair(const LinearParams& p, cudaStream_t s) {
   CUtensorMap xm, wm;
   if (!encode_map(&xm, p.x, p.M, p.K, p.ldx, 128) || !encode_map(&wm, p.w, p.N, p.K, p.ldw, BN / 2)) return cudaErrorInvalidValue;
   const size_t smem = sizeof(PairSmem<BN>) + 1024;
-  const cudaError_t e = opt_in<linear_pair<BN>>(smem);
+  const cudaError_t e = p.act ? opt_in<linear_pair<BN, true>>(smem) : opt_in<linear_pair<BN, false>>(smem);
   if (e != cudaSuccess) return e;
   PairTiles t;
   t.tiles_m = (p.M + 255) / 256;
   t.tiles_n = (p.N + BN - 1) / BN;
   t.total = t.tiles_m * t.tiles_n;
   const int pairs = std::min(t.total, sm_count() / 2);
-  linear_pair<BN><<<2 * pairs, kPairThreads, smem, s>>>(xm, wm, p, t);
+  if (p.act)
+    linear_pair<BN, true><<<2 * pairs, kPairThreads, smem, s>>>(xm, wm, p, t);
+  else
+    linear_pair<BN, false><<<2 * pairs, kPairThreads, smem, s>>>(xm, wm, p, t);
   return cudaGetLastError();
 }
 

@@ -151,26 +151,26 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 
 // ------------------------------------------------------------------ prepare
 
-constexpr int kPrepThreads = 256;
+// A CTA takes a chunk of one key head and four of its value heads at once, 128 threads
+// each, which meet at barriers of their own: every step is short and waits on the one
+// before, so heads side by side (and two CTAs an SM) are what fills the time.
+constexpr int kPrepHeads = 4;
+constexpr int kPrepThreads = 128 * kPrepHeads;
 constexpr int kLStride = 68;  // floats of a row of L: 16-byte rows, apart in banks
 constexpr int kXStride = 36;
 
 template <int D>
 struct alignas(1024) PrepSmem {
   union {
-    unsigned char kq[D / 64][128 * 128];  // rows k 0..63, q 0..63, in atoms of 64 columns
-    unsigned char t[2][2][8192];          // then T of two heads, hi and lo
-    float x[2][32 * kXStride];            // and between, a product on T's way
+    unsigned char kq[D / 64][128 * 128];     // rows k 0..63, q 0..63, in atoms of 64 columns
+    float x[kPrepHeads][32 * kXStride];      // later a product on T's way
   };
-  unsigned char a[2][2][8192];  // causal products of two heads, hi and lo
-  float m[2][64 * kLStride];    // L, then T in its place
-  float scal[2][S_COUNT][64], oscal[2][O_COUNT][64];
-  float beta[2][64];
-  float ghi[2][64], glo[2][64];  // running sums of the log2 gates
-  float bj[2][64];               // 2^(G of the 16-block's end - G_j) / norm of k_j
-  float top[2][64];              // of a row of the causal products, by column halves
-  float rn[128];                 // 1 / norm of the f16 rows (k, q)
-  int bad[64];                   // k not finite
+  float m[kPrepHeads][64 * kLStride];        // L, then T in its place
+  float ghi[kPrepHeads][64], glo[kPrepHeads][64];  // running sums of the log2 gates
+  float bj[kPrepHeads][64];                  // 2^(G of the 16-block's end - G_j) / |k_j|
+  float beta[kPrepHeads][64];
+  float rn[128];                             // 1 / norm of the f16 rows (k, q)
+  int bad[64];                               // k not finite
   uint64_t done;
   uint32_t tmem;
 };
@@ -178,7 +178,7 @@ struct alignas(1024) PrepSmem {
 // x[i] += sum_l A[i][l] B[l][c..c+3] for R rows i of A, l0 <= l < l1 (multiples of 4).
 template <int R>
 __device__ __forceinline__ void mac4(float4 (&x)[R], const float* A, int lda, const float* B, int ldb, int l0, int l1) {
-#pragma unroll 1
+#pragma unroll 2
   for (int l = l0; l < l1; l += 4) {
     float4 a[R];
 #pragma unroll
@@ -208,20 +208,25 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
   seq_rows(p.r, sq, &b, &e);
   const int t0 = b + (place - chunk_first_place(p.r, sq)) * kChunk, n = min(kChunk, e - t0);
   if (n <= 0 || e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) return;
+  // k and q rows: norms, and f16 images scaled by a power of two each
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = 128 / (kPrepThreads / 32) / kRows;
+  uint4 row_in[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int row = (warp * kIter + i) * kRows + lane / kLanes, tok = row & 63, col = (lane % kLanes) * 8;
+    row_in[i] = make_uint4(0, 0, 0, 0);
+    if (tok < n)
+      row_in[i] = __ldg(reinterpret_cast<const uint4*>(p.qkv + (long long)(t0 + tok) * p.ldqkv + (row < 64 ? p.Hk + kh : kh) * D + col));
+  }
   if (warp == 0) tmem_alloc(&s.tmem, 64);
   if (tid == 0) {
     mbar_init(&s.done, 1);
     fence_mbar_init();
   }
-  // k and q rows: norms, and f16 images scaled by a power of two each
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-#pragma unroll 4
-  for (int i = 0; i < 16; i += kRows) {
-    const int row = warp * 16 + i + lane / kLanes, tok = row & 63, col = (lane % kLanes) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (tok < n)
-      v = __ldg(reinterpret_cast<const uint4*>(p.qkv + (long long)(t0 + tok) * p.ldqkv + (row < 64 ? p.Hk + kh : kh) * D + col));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int row = (warp * kIter + i) * kRows + lane / kLanes, col = (lane % kLanes) * 8;
+    const uint32_t w[4] = {row_in[i].x, row_in[i].y, row_in[i].z, row_in[i].w};
     float f[8], ss = 0.f, mx = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
@@ -264,32 +269,36 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       bulk_store(kq + (D / 64 + a) * 8192, s.kq[a] + 8192, 8192);
     }
     bulk_commit();
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the room is x's below
   }
-  const int i = tid & 63;            // row of L (lanes 0..63) or of the causal products (64..127)
-  const bool lower = (tid & 64) == 0;
-  const int half = tid >> 7;         // columns 32 half ..
+  const int hd = tid >> 7, q = tid & 127;  // this thread's head of the four, and its place in it
+  const int i = q & 63;                    // row of L (TMEM lanes 0..63) or of the causal products (64..127)
+  const bool lower = q < 64;
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + hd) : "memory"); };
   bool ok = true;
-  for (int g0 = 0; g0 < p.group; g0 += 2) {
-    const int heads = min(2, p.group - g0);
-    // gates: a warp for each head, two tokens a lane
-    if (warp < heads) {
-      const int h = kh * p.group + g0 + warp;
+  for (int g0 = 0; g0 < p.group; g0 += kPrepHeads) {
+    const int g = g0 + hd, h = kh * p.group + g;
+    const bool mine = g < p.group;
+    unsigned char* img = c.head + ((size_t)place * p.Hv + h) * kHeadBytes;
+    // gates: one warp a head, two tokens a lane
+    if (q < 32 && mine) {
       const float rate = 1.4426950408889634f * expf(p.A_log[h]), shift = bf16_to_f(p.dt_bias[h]);
-      float g[2], beta[2];
+      float gt[2], beta[2];
       int first_bad = 64;
 #pragma unroll
       for (int k = 1; k >= 0; --k) {
         const int tok = 2 * lane + k;
-        g[k] = beta[k] = 0.f;
+        gt[k] = beta[k] = 0.f;
         if (tok < n) {
           const __nv_bfloat16* ba = p.ba + (long long)(t0 + tok) * p.ldba;
           beta[k] = sigmoid_f(bf16_to_f(ba[h]));
           const float x = -rate * softplus_f(bf16_to_f(ba[p.Hv + h]) + shift);
-          g[k] = x < -1e4f ? -1e4f : x;  // 2^-1e4 is 0, and sums of it stay ordinary
-          if (!(finite(g[k]) && finite(beta[k])) || s.bad[tok]) first_bad = tok;
+          gt[k] = x < -1e4f ? -1e4f : x;  // 2^-1e4 is 0, and sums of it stay ordinary
+          if (!(finite(gt[k]) && finite(beta[k])) || s.bad[tok]) first_bad = tok;
         }
       }
-      Two a = add(Two{g[0], 0.f}, Two{g[1], 0.f});
+      Two a = add(Two{gt[0], 0.f}, Two{gt[1], 0.f});
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const Two u{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       }
       Two before{__shfl_up_sync(0xffffffffu, a.hi, 1), __shfl_up_sync(0xffffffffu, a.lo, 1)};
       if (lane == 0) before = Two{0.f, 0.f};
-      const Two G[2] = {add(before, Two{g[0], 0.f}), a};
+      const Two G[2] = {add(before, Two{gt[0], 0.f}), a};
       const float ehi = __shfl_sync(0xffffffffu, a.hi, 31), elo = __shfl_sync(0xffffffffu, a.lo, 31);
       // of the last token of this lane's block of 16
       const float bhi = __shfl_sync(0xffffffffu, a.hi, lane | 7), blo = __shfl_sync(0xffffffffu, a.lo, lane | 7);
@@ -306,96 +315,97 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
         first_bad = min(first_bad, __shfl_xor_sync(0xffffffffu, first_bad, o));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
+      float gam[2], left[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int tok = 2 * lane + k;
-        const float gam = exp2f(G[k].hi + G[k].lo), left = exp2f((ehi - G[k].hi) + (elo - G[k].lo));
-        s.ghi[warp][tok] = G[k].hi;
-        s.glo[warp][tok] = G[k].lo;
-        s.bj[warp][tok] = s.rn[tok] * exp2f((bhi - G[k].hi) + (blo - G[k].lo));
-        s.beta[warp][tok] = beta[k];
-        float* r = s.scal[warp][S_R] + 4 * lane + k;
-        r[0] = beta[k];
-        r[2] = beta[k] * (gam * s.rn[tok]);
-        s.scal[warp][S_CU][tok] = left * s.rn[tok];
-        float* w = s.scal[warp][S_B] + 4 * lane + k;
-        w[0] = beta[k];
-        w[2] = left * beta[k];
-        s.oscal[warp][O_CQG][tok] = p.q_scale * s.rn[64 + tok] * gam;
+        gam[k] = exp2f(G[k].hi + G[k].lo), left[k] = exp2f((ehi - G[k].hi) + (elo - G[k].lo));
+        s.ghi[hd][tok] = G[k].hi;
+        s.glo[hd][tok] = G[k].lo;
+        s.bj[hd][tok] = s.rn[tok] * exp2f((bhi - G[k].hi) + (blo - G[k].lo));
+        s.beta[hd][tok] = beta[k];
       }
-      if (lane == 0) {
-        s.scal[warp][S_END][0] = exp2f(ehi + elo);
-        s.scal[warp][S_END][1] = __int_as_float(first_bad);
-        s.scal[warp][S_END][2] = top;
-      }
+      const float2 rn = *reinterpret_cast<const float2*>(&s.rn[2 * lane]), rq = *reinterpret_cast<const float2*>(&s.rn[64 + 2 * lane]);
+      float* sc = reinterpret_cast<float*>(img + kImg);
+      *reinterpret_cast<float4*>(sc + 64 * S_R + 4 * lane) =
+          make_float4(beta[0], beta[1], beta[0] * (gam[0] * rn.x), beta[1] * (gam[1] * rn.y));
+      *reinterpret_cast<float4*>(sc + 64 * S_B + 4 * lane) = make_float4(beta[0], beta[1], left[0] * beta[0], left[1] * beta[1]);
+      *reinterpret_cast<float2*>(sc + 64 * S_CU + 2 * lane) = make_float2(left[0] * rn.x, left[1] * rn.y);
+      if (lane == 0) *reinterpret_cast<float4*>(sc + 64 * S_END) = make_float4(exp2f(ehi + elo), __int_as_float(first_bad), top, 0.f);
+      *reinterpret_cast<float2*>(img + kChainBytes + kImg + 256 * O_CQG + 8 * lane) =
+          make_float2(p.q_scale * rq.x * gam[0], p.q_scale * rq.y * gam[1]);
     }
     if (g0 == 0) {
       ok = mbar_wait(&s.done, 0);
       if (!ok) record(p.r.error, kStatusDeadline, kWhatWait, sq);
+      __syncthreads();  // and kq is read out
+      tc_fence_after();
+    } else {
+      meet();
     }
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // kq's room is free
-    __syncthreads();
-    tc_fence_after();
-#pragma unroll 1
-    for (int h = 0; h < heads; ++h) {
-      // L_ij = beta_i e^(G_i-G_j) k_i.k_j and e^(G_i-G_j) q_i.k_j. Off the diagonal
-      // blocks of 16, e^(G_i-G_j) is (from j to its block's end) x (from there to i),
-      // both at most 1: one exponential a block and row.
-      float dot[32];
-      tmem_ld32(tmem + 32 * half + ((uint32_t)((warp & 3) * 32) << 16), dot);
-      const float gi = s.ghi[h][i], li = s.glo[h][i];
-      const float f = lower ? s.beta[h][i] * s.rn[i] : 1.f;
-      float mx = 0.f;
+    if (!mine) continue;  // a whole head's threads
+    // L_ij = beta_i e^(G_i-G_j) k_i.k_j and e^(G_i-G_j) q_i.k_j, 16 columns at a time.
+    // Off the diagonal blocks of 16, e^(G_i-G_j) is (from j to its block's end) x (from
+    // there to i), both at most 1: one exponential a block and row.
+    const float gi = s.ghi[hd][i], li = s.glo[hd][i];
+    const float f = lower ? s.beta[hd][i] * s.rn[i] : 1.f;
+    const auto block = [&](int j0, float (&x)[16]) {
+      tmem_ld16(tmem + j0 + lanes, x);
+      if (j0 > i) {
 #pragma unroll
-      for (int jb = 0; jb < 2; ++jb) {
-        const int j0 = 32 * half + 16 * jb;
-        if (j0 > i) {
+        for (int j = 0; j < 16; ++j) x[j] = 0.f;
+      } else if (j0 + 16 <= i) {
+        const float a = f * exp2f((gi - s.ghi[hd][j0 + 15]) + (li - s.glo[hd][j0 + 15]));
 #pragma unroll
-          for (int j = 0; j < 16; ++j) dot[16 * jb + j] = 0.f;
-        } else if (j0 + 16 <= i) {
-          const float a = f * exp2f((gi - s.ghi[h][j0 + 15]) + (li - s.glo[h][j0 + 15]));
-#pragma unroll
-          for (int j = 0; j < 16; ++j) dot[16 * jb + j] *= a * s.bj[h][j0 + j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int jj = j0 + j;
-            const float x = f * s.rn[jj] * exp2f((gi - s.ghi[h][jj]) + (li - s.glo[h][jj])) * dot[16 * jb + j];
-            dot[16 * jb + j] = jj < i || (jj == i && !lower) ? x : 0.f;
-          }
-        }
-      }
-      if (lower) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          *reinterpret_cast<float4*>(s.m[h] + i * kLStride + 32 * half + j) = make_float4(dot[j], dot[j + 1], dot[j + 2], dot[j + 3]);
+        for (int j = 0; j < 16; ++j) x[j] *= a * s.bj[hd][j0 + j];
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fabsf(dot[j]));
-        s.top[half][i] = mx;
-      }
-      __syncthreads();
-      if (!lower) {
-        // a row of the causal products takes a power of two of its own (O_CQ undoes it)
-        const float f = row_scale(fmaxf(s.top[0][i], s.top[1][i]));
-        if (half == 0) s.oscal[h][O_CQ][i] = p.q_scale * s.rn[64 + i] * inverse_pow2(f);
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t w[4], wl[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) split2(make_float2(dot[j + 2 * k] * f, dot[j + 2 * k + 1] * f), &w[k], &wl[k]);
-          *reinterpret_cast<uint4*>(s.a[h][0] + swz(i, 32 * half + j)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(s.a[h][1] + swz(i, 32 * half + j)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        for (int j = 0; j < 16; ++j) {
+          const int jj = j0 + j;
+          const float y = f * s.rn[jj] * exp2f((gi - s.ghi[hd][jj]) + (li - s.glo[hd][jj])) * x[j];
+          x[j] = jj < i || (jj == i && !lower) ? y : 0.f;
         }
       }
-      __syncthreads();
+    };
+    float mx = 0.f;
+#pragma unroll 1
+    for (int j0 = 0; j0 < 64; j0 += 16) {
+      float x[16];
+      block(j0, x);
+      if (lower) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4*>(s.m[hd] + i * kLStride + j0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(x[j]));
+      }
     }
-    // T = (I + L)^-1, in place of L. First its diagonal blocks of 16, a column a
-    // thread: t_i = [i = col] - sum_{l < i} L_il t_l.
-    const int hd = tid >> 7;  // the head this half of the threads works on
-    if (tid < 64 * heads) {
-      const int col = tid & 63, c16 = col & 15;
-      float* L = s.m[tid >> 6] + (col & 48) * (kLStride + 1);
+    meet();
+    if (!lower) {
+      // the causal products, a row at a power of two of its own (O_CQ undoes it),
+      // while the other two warps begin on T
+      const float fa = row_scale(mx);
+      unsigned char* a = img + kChainBytes;
+      reinterpret_cast<float*>(a + kImg)[64 * O_CQ + i] = p.q_scale * s.rn[64 + i] * inverse_pow2(fa);
+#pragma unroll 1
+      for (int j0 = 0; j0 < 64; j0 += 16) {
+        float x[16];
+        block(j0, x);
+#pragma unroll
+        for (int j = 0; j < 16; j += 8) {
+          uint32_t w[4], wl[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) split2(make_float2(x[j + 2 * k] * fa, x[j + 2 * k + 1] * fa), &w[k], &wl[k]);
+          *reinterpret_cast<uint4*>(a + swz(i, j0 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(a + 8192 + swz(i, j0 + j)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        }
+      }
+    } else {
+      // T = (I + L)^-1, in place of L. First its diagonal blocks of 16, a column a
+      // thread: t_i = [i = col] - sum_{l < i} L_il t_l.
+      const int c16 = i & 15;
+      float* L = s.m[hd] + (i & 48) * (kLStride + 1);
       float t[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -414,72 +424,49 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
 #pragma unroll
       for (int r = 0; r < 16; ++r) L[r * kLStride + c16] = t[r];
     }
-    __syncthreads();
+    meet();
     // Then twice the size at a time: [T11 0; L21 .] -> T21 = -T22 (L21 T11).
     {
-      const int q = tid & 127, o = (q >> 6) * 32, r = (q & 63) >> 2, cc = (q & 3) * 4;
+      const int o = (q >> 6) * 32, r = (q & 63) >> 2, cc = (q & 3) * 4;
       float* m = s.m[hd] + o * (kLStride + 1);
       float* x = s.x[hd] + (q >> 6) * 16 * kXStride;
-      if (hd < heads) {
-        float4 v[1] = {};
-        mac4(v, m + (16 + r) * kLStride, kLStride, m + cc, kLStride, 0, 16);
-        *reinterpret_cast<float4*>(x + r * kXStride + cc) = v[0];
-      }
-      __syncthreads();
-      if (hd < heads) {
-        float4 v[1] = {};
-        mac4(v, m + (16 + r) * kLStride + 16, kLStride, x + cc, kXStride, 0, 16);
-        *reinterpret_cast<float4*>(m + (16 + r) * kLStride + cc) = minus(v[0]);
-      }
-      __syncthreads();
+      float4 v[1] = {};
+      mac4(v, m + (16 + r) * kLStride, kLStride, m + cc, kLStride, 0, 16);
+      *reinterpret_cast<float4*>(x + r * kXStride + cc) = v[0];
+      meet();
+      v[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+      mac4(v, m + (16 + r) * kLStride + 16, kLStride, x + cc, kXStride, 0, 16);
+      *reinterpret_cast<float4*>(m + (16 + r) * kLStride + cc) = minus(v[0]);
+      meet();
     }
     {
-      const int q = tid & 127, r = (q >> 3) * 2, cc = (q & 7) * 4;
+      const int r = (q >> 3) * 2, cc = (q & 7) * 4;
       float *m = s.m[hd], *x = s.x[hd];
-      if (hd < heads) {
-        float4 v[2] = {};
-        mac4(v, m + (32 + r) * kLStride, kLStride, m + cc, kLStride, cc & 16, 32);  // T11 is 0 above its diagonal
-        *reinterpret_cast<float4*>(x + r * kXStride + cc) = v[0];
-        *reinterpret_cast<float4*>(x + (r + 1) * kXStride + cc) = v[1];
-      }
-      __syncthreads();
-      if (hd < heads) {
-        float4 v[2] = {};
-        mac4(v, m + (32 + r) * kLStride + 32, kLStride, x + cc, kXStride, 0, (r & 16) + 16);  // and so is T22
-        *reinterpret_cast<float4*>(m + (32 + r) * kLStride + cc) = minus(v[0]);
-        *reinterpret_cast<float4*>(m + (33 + r) * kLStride + cc) = minus(v[1]);
-      }
-      __syncthreads();
+      float4 v[2] = {};
+      mac4(v, m + (32 + r) * kLStride, kLStride, m + cc, kLStride, cc & 16, 32);  // T11 is 0 above its diagonal
+      *reinterpret_cast<float4*>(x + r * kXStride + cc) = v[0];
+      *reinterpret_cast<float4*>(x + (r + 1) * kXStride + cc) = v[1];
+      meet();
+      v[0] = v[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      mac4(v, m + (32 + r) * kLStride + 32, kLStride, x + cc, kXStride, 0, (r & 16) + 16);  // and so is T22
+      *reinterpret_cast<float4*>(m + (32 + r) * kLStride + cc) = minus(v[0]);
+      *reinterpret_cast<float4*>(m + (33 + r) * kLStride + cc) = minus(v[1]);
+      meet();
     }
-    if (hd < heads) {
 #pragma unroll 2
-      for (int q = tid & 127; q < 512; q += 128) {
-        const int r = q >> 3, j = (q & 7) * 8;
-        const float4 u = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j);
-        const float4 v = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j + 4);
-        uint32_t w[4], wl[4];
-        split2(make_float2(u.x * kScaleT, u.y * kScaleT), &w[0], &wl[0]);
-        split2(make_float2(u.z * kScaleT, u.w * kScaleT), &w[1], &wl[1]);
-        split2(make_float2(v.x * kScaleT, v.y * kScaleT), &w[2], &wl[2]);
-        split2(make_float2(v.z * kScaleT, v.w * kScaleT), &w[3], &wl[3]);
-        *reinterpret_cast<uint4*>(s.t[hd][0] + swz(r, j)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(s.t[hd][1] + swz(r, j)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-      }
+    for (int u = q; u < 512; u += 128) {
+      const int r = u >> 3, j = (u & 7) * 8;
+      const float4 y = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j);
+      const float4 v = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j + 4);
+      uint32_t w[4], wl[4];
+      split2(make_float2(y.x * kScaleT, y.y * kScaleT), &w[0], &wl[0]);
+      split2(make_float2(y.z * kScaleT, y.w * kScaleT), &w[1], &wl[1]);
+      split2(make_float2(v.x * kScaleT, v.y * kScaleT), &w[2], &wl[2]);
+      split2(make_float2(v.z * kScaleT, v.w * kScaleT), &w[3], &wl[3]);
+      *reinterpret_cast<uint4*>(img + swz(r, j)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(img + 8192 + swz(r, j)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
     }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      for (int h = 0; h < heads; ++h) {
-        unsigned char* img = c.head + ((size_t)place * p.Hv + kh * p.group + g0 + h) * kHeadBytes;
-        bulk_store(img, s.t[h][0], 16384);
-        bulk_store(img + kImg, s.scal[h], S_COUNT * 256);
-        bulk_store(img + kChainBytes, s.a[h][0], 16384);
-        bulk_store(img + kChainBytes + kImg, s.oscal[h], O_COUNT * 256);
-      }
-      bulk_commit();
-      if (g0 + 2 < p.group) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    }
-    __syncthreads();
+    meet();  // before the next head's gates and L
   }
   if (tid == 0) bulk_wait_all();
   tc_fence_before();
@@ -524,7 +511,7 @@ template <int D>
 struct ChainSmem {
   ChainIn<D> in[2];
   OutIn<D> oin[2];
-  uint32_t vt[32][128];  // v of two tokens, by rows of the state
+  uint32_t vt[2][32][128];  // v of two tokens, by rows of the state
   // of a row's v, by halves of the tokens: sum beta |v|, sum e^(G_C-G) beta |v|, max |v|,
   // first token not finite
   float4 sums[2][2][128];
@@ -764,33 +751,37 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       }
       tmem_wait_st();
     }
+    // A chunk's scales, worked out while the chunk before waits for its U: first_bad,
+    // the first token not finite; fu, of U; fs_next, of the state after the chunk;
+    // shrink, what takes S from one to the other.
+    int first_bad = 0;
+    float fu = 1.f, fs_next = 1.f, shrink = 0.f;
     float near = 0.f, near_mul = 0.f;  // of the last chunk: sum of v's part, factor of the norm before it
+    const auto scales = [&](int n) {
+      const int st = n & 1;
+      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
+      if (ok) ok = mbar_wait(&s.sums_ready, n & 1);
+      const float4 end = *reinterpret_cast<const float4*>(s.in[st].scal[S_END]);
+      const float4 a = s.sums[st][0][row], o = s.sums[st][1][row];
+      first_bad = dead ? 0 : min(__float_as_int(a.w), __float_as_int(o.w));
+      const bool bad = first_bad < kChunk;
+      const float gam_end = bad ? 0.f : end.x, sw = bad ? 0.f : a.y + o.y;
+      fu = row_scale((bad ? 1.f : end.z) * (fmaxf(a.z, o.z) + bound + (a.x + o.x)));
+      bound = fmaf(gam_end, bound, sw) * 1.01f;
+      fs_next = row_scale(bound);
+      shrink = gam_end * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
+      near = sw;
+      near_mul = gam_end * inverse_pow2(fs);
+    };
+    scales(0);
     for (int n = 0; n < chunks; ++n) {
       const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
       const uint32_t ph = n & 1;
       ChainIn<D>& g = s.in[st];
-      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      if (ok) ok = mbar_wait(&s.sums_ready, ph);
-      // both halves of the last chunk's squares are written
-      asm volatile("bar.sync 2, 256;" ::: "memory");
-      float4 sum = s.sums[st][0][row];
-      {
-        const float4 late = s.sums[st][1][row];
-        sum.x += late.x, sum.y += late.y, sum.z = fmaxf(sum.z, late.z);
-        sum.w = __int_as_float(min(__float_as_int(sum.w), __float_as_int(late.w)));
-      }
-      if (n > 0) bound = fminf(bound, fmaf(near_mul, sqrtf(s.part[0][row] + s.part[1][row]), near) * 1.01f);
-      const int first_bad = dead ? 0 : __float_as_int(sum.w);
-      const float gam_end = first_bad < kChunk ? 0.f : g.scal[S_END][0], sw = first_bad < kChunk ? 0.f : sum.y;
-      // scales: of U, and of the state after this chunk
-      const float fu = row_scale((first_bad < kChunk ? 1.f : g.scal[S_END][2]) * (sum.z + bound + sum.x));
-      bound = fmaf(gam_end, bound, sw) * 1.01f;
-      const float fs_next = row_scale(bound);
-      const float shrink = gam_end * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
       const float inv_s = inverse_pow2(fs), p_scale = fminf(fu * inv_s, 0x1p126f);
       const float u_scale = fminf(fs_next * inverse_pow2(fu), 0x1p126f);
-      near = sw;
-      near_mul = gam_end * inv_s;
+      const int until = min(first_bad, toks);  // R is zero from there on
+      const bool bad = first_bad < kChunk;
       if (half == 0) {
         s.inv_s[st][row] = inv_s;
         s.inv_u[st][row] = inverse_pow2(fu);
@@ -829,24 +820,24 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.s_ready[half]);
-      // R: zeros from the first token on that is past the end or not finite
-      const int until = min(first_bad, toks);
+      // R, with this row's v read ahead
+      uint32_t v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = s.vt[st][tok0 / 2 + j][row];
       const float2 f2 = make_float2(fu, fu), p2 = make_float2(-p_scale, -p_scale);
       if (ok) ok = mbar_wait(&s.p_done, ph);
       tc_fence_after();
-      // the two halves' squares: both have read the last chunk's (P waited for both)
       s.part[half][row] = ss2.x + ss2.y;
-#pragma unroll 1
-      for (int i = tok0; i < tok0 + 32; i += 16) {
-        float x[16];
-        uint32_t v[8], hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = s.vt[i / 2 + j][row];
+      for (int k = 0; k < 2; ++k) {
+        const int i = tok0 + 16 * k;
+        float x[16];
+        uint32_t hi[8], lo[8];
         tmem_ld16(tmem + kPU + i + lanes, x);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float4 rc = *reinterpret_cast<const float4*>(&g.scal[S_R][2 * (i + j)]);
-          const float2 vv = __fmul2_rn(make_float2(bf16_lo(v[j / 2]), bf16_hi(v[j / 2])), f2);
+          const float2 vv = __fmul2_rn(make_float2(bf16_lo(v[8 * k + j / 2]), bf16_hi(v[8 * k + j / 2])), f2);
           const float2 q = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), make_float2(rc.z, rc.w));
           const float2 r = __ffma2_rn(vv, make_float2(rc.x, rc.y), q);
           x[j] = r.x, x[j + 1] = r.y;
@@ -865,19 +856,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.r_ready);
+      // the next chunk's scales; both halves' squares are there to tighten its bound
+      const int bad_from = first_bad;
+      fs = fs_next;
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      bound = fminf(bound, fmaf(near_mul, sqrtf(s.part[0][row] + s.part[1][row]), near) * 1.01f);
+      if (bad) dead = true;  // from the next chunk on
+      if (n + 1 < chunks) scales(n + 1);
       // U for the outputs, and e^(G_C-G) U at the state's scale
       const float2 us2 = make_float2(u_scale, u_scale), t2 = make_float2(1.0f / kScaleT, 1.0f / kScaleT);
       if (ok) ok = mbar_wait(&s.u_done, ph);
       tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
       for (int i = tok0; i < tok0 + 32; i += 16) {
         float u[16];
         uint32_t hi[8], lo[8], ohi[8], olo[8];
         tmem_ld16(tmem + kPU + i + lanes, u);
-        if (first_bad < kChunk) {
+        if (bad) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (i + j >= first_bad) u[j] = 0.f;
+            if (i + j >= bad_from) u[j] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -886,7 +884,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
           const float2 y = __fmul2_rn(make_float2(u[j], u[j + 1]), t2);
           split2(y, &ohi[j / 2], &olo[j / 2]);
           float2 w = __fmul2_rn(__fmul2_rn(y, us2), cu);
-          if (first_bad < kChunk) w = make_float2(0.f, 0.f);
+          if (bad) w = make_float2(0.f, 0.f);
           split2(w, &hi[j / 2], &lo[j / 2]);
         }
         tmem_st8(tmem + kRhi + i / 2 + lanes, hi);
@@ -894,8 +892,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         tmem_st8(tmem + kUhi + i / 2 + lanes, ohi);
         tmem_st8(tmem + kUlo + i / 2 + lanes, olo);
       }
-      if (first_bad < kChunk) dead = true;  // from now on
-      fs = fs_next;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -956,7 +952,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          s.vt[i / 2 + j][row] = a[j];
+          s.vt[st][i / 2 + j][row] = a[j];
           const float4 bw = *reinterpret_cast<const float4*>(&g.scal[S_B][2 * (i + 2 * j)]);
           const float2 y = make_float2(fabsf(bf16_lo(a[j])), fabsf(bf16_hi(a[j])));
           b2 = __ffma2_rn(make_float2(bw.x, bw.y), y, b2);
@@ -1010,9 +1006,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         }
       }
       if (n + 1 < chunks) {
-        // U of this chunk says that its sums and vt are read, so they may be written
-        // and sums_ready never runs two phases ahead of the state's rows
-        if (ok) ok = mbar_wait(&s.u_done, ph);
+        // P of this chunk says that its sums are read and the last chunk's v is, so
+        // sums_ready never runs two phases ahead of the state's rows
+        if (ok) ok = mbar_wait(&s.p_done, ph);
         sum_up(n + 1);
       }
       if (ok) ok = mbar_wait(&s.row_ready, ph);

@@ -95,7 +95,9 @@ __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
   if (live && e - b > kRecurrentMax) return;  // the chunked form's
   const int row = threadIdx.x;  // the dv row this lane finishes
   if (!live) {
-    for (int t = b; t < e; ++t) p.out[(long long)t * p.ldo + h * D + row] = __float2bfloat16_rn(0.f);
+    // padding: zero rows, 16 bytes a thread
+    for (int t = b + threadIdx.x / (D / 8); t < e; t += 8)
+      *reinterpret_cast<uint4*>(p.out + (long long)t * p.ldo + h * D + threadIdx.x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
   const int kh = h / p.group;

@@ -15,11 +15,12 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (globaltimer_ns() - t0 > kWaitNs) return false;
-  }
+  bool ok;
+#pragma unroll 1
+  do {
+    ok = mbar_try_wait(bar, parity);
+  } while (!ok && globaltimer_ns() - t0 < kWaitNs);
+  return ok;
 }
 
 // One lane of a converged warp. What it issues under such a branch has its operands in
