@@ -25,8 +25,9 @@
 // beta <= 1 a token's step S <- e^g S (I - beta k k^T) + beta v k^T does not lengthen a
 // row by more than beta |v|, so over a chunk
 //   |S'| <= e^(G_C) |S0| + sum_j e^(G_C-G_j) beta_j |v_j|  (every e^(G_C-G_j) u_j too),
-//   |u_j|, |R_j| <= max(beta) (max |v| + |S0| + sum beta |v|);
-// |T| <= 1 takes the constant 2^12. Two terms reach 2^-39 of such a bound.
+//   |u_j|, |R_j| <= max(beta) (max |v| + |S0| + sum beta |v|),
+// with the largest |v| of the head's chunk for every |v|, and a row's norm measured every
+// eighth chunk; |T| <= 1 takes the constant 2^12. Two terms reach 2^-39 of such a bound.
 //
 // Values that are not finite stay where the definition has them: a row of S^T knows
 // the first token whose v, k or gates are not, multiplies zeros from there on, and
@@ -47,15 +48,15 @@ using namespace tc;
 constexpr float kScaleT = 4096.f;   // of T's f16 images
 // A chunk's images and scalars of a value head, arrays of 64 floats: what the state's
 // chain needs (T hi, T lo) and what the outputs need (causal products hi, lo).
-// S_R: of every two tokens beta, beta, beta c, beta c with c = e^G / |k|; S_B: beta,
-// beta, w, w with w = e^(G_C-G) beta; S_CU: e^(G_C-G) / |k|.
-enum { S_R = 0, S_B = 2, S_CU = 4, S_END, S_COUNT };
+// S_R: of every two tokens beta, beta, beta c, beta c with c = e^G / |k|; S_CU:
+// e^(G_C-G) / |k|; S_END: see below.
+enum { S_R = 0, S_CU = 2, S_END, S_COUNT };
 enum { O_CQG, O_CQ, O_COUNT };
 constexpr int kImg = 2 * 8192;  // two images of 64 x 64 f16
 constexpr int kChainBytes = kImg + S_COUNT * 256, kOutBytes = kImg + O_COUNT * 256;
 constexpr int kHeadBytes = kChainBytes + kOutBytes;
 // S_END: [0] e^(G_C), [1] (an int) the first token whose k or gates are not finite,
-// else 64, [2] the largest beta
+// else 64, [2] the largest beta, [3] sum beta, [4] sum e^(G_C-G) beta.
 
 template <int D>
 constexpr int kq_bytes() { return 2 * kChunk * D * 2; }  // the k image, then q's
@@ -329,9 +330,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       float* sc = reinterpret_cast<float*>(img + kImg);
       *reinterpret_cast<float4*>(sc + 64 * S_R + 4 * lane) =
           make_float4(beta[0], beta[1], beta[0] * (gam[0] * rn.x), beta[1] * (gam[1] * rn.y));
-      *reinterpret_cast<float4*>(sc + 64 * S_B + 4 * lane) = make_float4(beta[0], beta[1], left[0] * beta[0], left[1] * beta[1]);
       *reinterpret_cast<float2*>(sc + 64 * S_CU + 2 * lane) = make_float2(left[0] * rn.x, left[1] * rn.y);
-      if (lane == 0) *reinterpret_cast<float4*>(sc + 64 * S_END) = make_float4(exp2f(ehi + elo), __int_as_float(first_bad), top, 0.f);
+      const float sum_b = warp_sum(beta[0] + beta[1]), sum_w = warp_sum(left[0] * beta[0] + left[1] * beta[1]);
+      if (lane == 0) {
+        *reinterpret_cast<float4*>(sc + 64 * S_END) = make_float4(exp2f(ehi + elo), __int_as_float(first_bad), top, sum_b);
+        sc[64 * S_END + 4] = sum_w;
+      }
       *reinterpret_cast<float2*>(img + kChainBytes + kImg + 256 * O_CQG + 8 * lane) =
           make_float2(p.q_scale * rq.x * gam[0], p.q_scale * rq.y * gam[1]);
     }
@@ -476,10 +480,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
 
 // ------------------------------------------------------------------ the chunks of a sequence
 
-// Warps: 0 loads, 1 issues MMAs, 2 holds the TMEM; 4 to 11 keep the state's rows (a
+// Warps: 0 loads, 1 issues MMAs, 2 holds the TMEM, 3 looks each chunk's v over; 4 to 11 keep the state's rows (a
 // thread is a row of S^T and half of its columns, or of the chunk's tokens); 12 to 19
-// write the outputs, half of the tokens each four, and sum up the next chunk's v on the
-// side.
+// write the outputs, half of the tokens each four.
 // The loops over columns and tokens are rolled, 16 at a time: one warp a scheduler in
 // code that runs straight through waits for its instructions (unrolled, a chunk took 4
 // times as long).
@@ -511,21 +514,23 @@ template <int D>
 struct ChainSmem {
   ChainIn<D> in[2];
   OutIn<D> oin[2];
-  uint32_t vt[2][32][128];  // v of two tokens, by rows of the state
-  // of a row's v, by halves of the tokens: sum beta |v|, sum e^(G_C-G) beta |v|, max |v|,
-  // first token not finite
-  float4 sums[2][2][128];
   float part[2][128];   // of a row's squares, by halves of its columns
   float inv_s[2][128], inv_u[2][128];
   int first_bad[2][128];
-  uint64_t full[2], empty[2], ofull[2], oempty[2], s_ready[2], s_done[2];
-  uint64_t p_done, r_ready, u_done, u_ready, o_done, o_free, row_ready, sums_ready;
+  uint32_t vmax[2];  // of the chunk's v: the largest |v|, bf16 bits
+  uint64_t full[2], empty[2], ofull[2], oempty[2], s_ready[2], s_done[2], v_ready[2];
+  uint64_t p_done, r_ready, u_done, u_ready, o_done, o_free, row_ready;
   uint32_t tmem;
 };
 
 // silu(z) before a rounding to bf16: the fast exponential and division (a few 2^-22)
 // are far below it.
-__device__ __forceinline__ float gate(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float gate(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return z * r;
+}
 
 // 16 columns of a row of a state.
 template <bool BF16>
@@ -561,7 +566,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 9);  // the MMAs' commit, and the output warps' sums
+      mbar_init(&s.empty[i], 2);  // the MMAs' commit, and the warp that looks v over
+      mbar_init(&s.v_ready[i], 1);
       mbar_init(&s.ofull[i], 1);
       mbar_init(&s.oempty[i], 9);  // the MMAs' commit, and the output warps
       mbar_init(&s.s_ready[i], 4);
@@ -574,7 +580,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     mbar_init(&s.o_done, 1);
     mbar_init(&s.o_free, 8);
     mbar_init(&s.row_ready, 4);
-    mbar_init(&s.sums_ready, 8);
     fence_mbar_init();
   }
   if (warp == 2) tmem_alloc(&s.tmem, 512);
@@ -711,6 +716,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     }
     // no MMA is in flight when the TMEM is freed
     if (ok) ok = mbar_wait(&s.o_done, (chunks - 1) & 1);
+  } else if (warp == 3) {
+    // the chunk's largest |v|, from the bits (a NaN or an infinity is larger than any)
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    for (int n = 0; n < chunks; ++n) {
+      const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
+      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
+      uint32_t m = 0;
+#pragma unroll 4
+      for (int t = lane / kLanes; t < toks; t += kRows) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&s.in[st].v[t][lane % kLanes * 8]);
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      }
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      if (lane == 0) {
+        s.vmax[st] = m;
+        mbar_arrive(&s.v_ready[st]);
+        mbar_arrive(&s.empty[st]);
+      }
+      __syncwarp();
+    }
   } else if (warp >= 4 && warp < 12) {
     // ---- the state's rows
     const int row = tid & 127, half = (warp - 4) >> 2;
@@ -754,24 +779,35 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     // A chunk's scales, worked out while the chunk before waits for its U: first_bad,
     // the first token not finite; fu, of U; fs_next, of the state after the chunk;
     // shrink, what takes S from one to the other.
+    // added, the bound's part from v.
     int first_bad = 0;
-    float fu = 1.f, fs_next = 1.f, shrink = 0.f;
-    float near = 0.f, near_mul = 0.f;  // of the last chunk: sum of v's part, factor of the norm before it
+    float fu = 1.f, fs_next = 1.f, shrink = 0.f, added = 0.f;
     const auto scales = [&](int n) {
-      const int st = n & 1;
+      const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
+      ChainIn<D>& g = s.in[st];
       if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      if (ok) ok = mbar_wait(&s.sums_ready, n & 1);
-      const float4 end = *reinterpret_cast<const float4*>(s.in[st].scal[S_END]);
-      const float4 a = s.sums[st][0][row], o = s.sums[st][1][row];
-      first_bad = dead ? 0 : min(__float_as_int(a.w), __float_as_int(o.w));
-      const bool bad = first_bad < kChunk;
-      const float gam_end = bad ? 0.f : end.x, sw = bad ? 0.f : a.y + o.y;
-      fu = row_scale((bad ? 1.f : end.z) * (fmaxf(a.z, o.z) + bound + (a.x + o.x)));
-      bound = fmaf(gam_end, bound, sw) * 1.01f;
+      if (ok) ok = mbar_wait(&s.v_ready[st], (n >> 1) & 1);
+      const float4 end = *reinterpret_cast<const float4*>(g.scal[S_END]);
+      float mv = __uint_as_float(s.vmax[st] << 16), gam_end = end.x, top = end.z, sum_b = end.w, sum_w = g.scal[S_END][4];
+      first_bad = __float_as_int(end.y);
+      if (first_bad < kChunk || !finite(mv)) {
+        // up to the first token of this row whose v, k or gates are not finite
+        mv = 0.f;
+        for (int i = 0; i < min(toks, first_bad); ++i) {
+          const float a = fabsf(bf16_to_f(g.v[i][vrow]));
+          if (!finite(a))
+            first_bad = i;
+          else
+            mv = fmaxf(mv, a);
+        }
+        if (first_bad < kChunk) gam_end = sum_w = 0.f, top = 1.f, sum_b = kChunk;
+      }
+      if (dead) first_bad = 0, gam_end = sum_w = 0.f;
+      fu = row_scale(top * (mv + bound + mv * sum_b));
+      added = sum_w * mv;
+      bound = fmaf(gam_end, bound, added) * 1.01f;
       fs_next = row_scale(bound);
       shrink = gam_end * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
-      near = sw;
-      near_mul = gam_end * inverse_pow2(fs);
     };
     scales(0);
     for (int n = 0; n < chunks; ++n) {
@@ -794,6 +830,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       }
       // S hi, lo for this chunk's products, and S shrunk for what is added to it
       float2 ss2 = make_float2(0.f, 0.f);
+      const bool measure = (n & 7) == 7;
       const float2 shrink2 = make_float2(shrink, shrink);
 #pragma unroll 1
       for (int col = col0; col < col0 + D / 2; col += 16) {
@@ -804,10 +841,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[j] = 0.f;
         }
+        if (measure) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) ss2 = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(x[j], x[j + 1]), ss2);
+        }
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float2 y = make_float2(x[j], x[j + 1]);
-          ss2 = __ffma2_rn(y, y, ss2);
           split2(y, &hi[j / 2], &lo[j / 2]);
           const float2 z = __fmul2_rn(y, shrink2);
           x[j] = z.x, x[j + 1] = z.y;
@@ -823,11 +863,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       // R, with this row's v read ahead
       uint32_t v[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = s.vt[st][tok0 / 2 + j][row];
+      for (int j = 0; j < 16; ++j)
+        v[j] = __bfloat16_as_ushort(g.v[tok0 + 2 * j][vrow]) | ((uint32_t)__bfloat16_as_ushort(g.v[tok0 + 2 * j + 1][vrow]) << 16);
       const float2 f2 = make_float2(fu, fu), p2 = make_float2(-p_scale, -p_scale);
       if (ok) ok = mbar_wait(&s.p_done, ph);
       tc_fence_after();
-      s.part[half][row] = ss2.x + ss2.y;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int i = tok0 + 16 * k;
@@ -856,11 +896,16 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.r_ready);
-      // the next chunk's scales; both halves' squares are there to tighten its bound
+      // the next chunk's scales, while U is worked out
       const int bad_from = first_bad;
+      if (measure) {
+        // the norm of S before this chunk, its halves put together, tightens the bound after it
+        s.part[half][row] = ss2.x + ss2.y;
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        const float norm = sqrtf(s.part[0][row] + s.part[1][row]) * inv_s;
+        bound = fminf(bound, fmaf(shrink * fs, norm * inverse_pow2(fs_next), added) * 1.01f);
+      }
       fs = fs_next;
-      asm volatile("bar.sync 2, 256;" ::: "memory");
-      bound = fminf(bound, fmaf(near_mul, sqrtf(s.part[0][row] + s.part[1][row]), near) * 1.01f);
       if (bad) dead = true;  // from the next chunk on
       if (n + 1 < chunks) scales(n + 1);
       // U for the outputs, and e^(G_C-G) U at the state's scale
@@ -932,58 +977,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     // ---- the outputs
     const int row = tid & 127, w = warp - 12, half = w >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    // Sums of this row's v over chunk n (ChainSmem::sums), and v by rows.
-    const auto sum_up = [&](int n) {
-      const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
-      ChainIn<D>& g = s.in[st];
-      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      const __nv_bfloat16* v = &g.v[0][row & (D - 1)];
-      float2 b2 = make_float2(0.f, 0.f), w2 = b2;
-      float m = 0.f;
-#pragma unroll 1
-      for (int i = 32 * half; i < min(toks, 32 * half + 32); i += 16) {
-        uint32_t a[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          a[j] = __bfloat16_as_ushort(v[(i + 2 * j) * D]) | ((uint32_t)__bfloat16_as_ushort(v[(i + 2 * j + 1) * D]) << 16);
-        if (i + 16 > toks) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) a[j] &= i + 2 * j + 1 < toks ? 0xffffffffu : i + 2 * j < toks ? 0xffffu : 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s.vt[st][i / 2 + j][row] = a[j];
-          const float4 bw = *reinterpret_cast<const float4*>(&g.scal[S_B][2 * (i + 2 * j)]);
-          const float2 y = make_float2(fabsf(bf16_lo(a[j])), fabsf(bf16_hi(a[j])));
-          b2 = __ffma2_rn(make_float2(bw.x, bw.y), y, b2);
-          w2 = __ffma2_rn(make_float2(bw.z, bw.w), y, w2);
-          m = fmaxf(m, fmaxf(y.x, y.y));
-        }
-      }
-      int bad = __float_as_int(g.scal[S_END][1]);
-      float4 sum = make_float4(b2.x + b2.y, w2.x + w2.y, m, 0.f);
-      if (bad < kChunk || !finite(sum.x)) {
-        // up to the first token whose v, k or gates are not finite (beta <= 1)
-        sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 32 * half; i < min(min(toks, bad), 32 * half + 32); ++i) {
-          const float a = fabsf(bf16_to_f(v[i * D]));
-          if (!finite(a)) {
-            bad = i;
-            break;
-          }
-          sum.x += a;
-          sum.z = fmaxf(sum.z, a);
-        }
-      }
-      sum.w = __int_as_float(bad);
-      s.sums[st][half][row] = sum;
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s.sums_ready);
-        mbar_arrive(&s.empty[st]);
-      }
-    };
-    sum_up(0);
     // On the way out eight lanes take a row, four columns in every 32 each; a warp
     // the rows 8 w .. 8 w + 7, four at a time.
     constexpr int E = D / 32;
@@ -1005,15 +998,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
             z[i][k] = __ldg(reinterpret_cast<const uint2*>(p.z + (long long)(t0 + t) * p.ldz + h * D + 32 * k + l8));
         }
       }
-      if (n + 1 < chunks) {
-        // P of this chunk says that its sums are read and the last chunk's v is, so
-        // sums_ready never runs two phases ahead of the state's rows
-        if (ok) ok = mbar_wait(&s.p_done, ph);
-        sum_up(n + 1);
-      }
       if (ok) ok = mbar_wait(&s.row_ready, ph);
       if (ok) ok = mbar_wait(&s.ofull[st], (n >> 1) & 1);
-      const float inv_s = s.inv_s[st][row], inv_u = s.inv_u[st][row];
+      const float2 is2 = make_float2(s.inv_s[st][row], s.inv_s[st][row]), iu2 = make_float2(s.inv_u[st][row], s.inv_u[st][row]);
       const int first_bad = s.first_bad[st][row];
       if (ok) ok = mbar_wait(&s.o_done, ph);
       tc_fence_after();
@@ -1026,14 +1013,23 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         for (int j = 0; j < 16; j += 4) {
           const float4 cg = *reinterpret_cast<const float4*>(&y.scal[O_CQG][i + j]);
           const float4 cq = *reinterpret_cast<const float4*>(&y.scal[O_CQ][i + j]);
-          u[j] = fmaf(cg.x, x[j] * inv_s, cq.x * (u[j] * inv_u));
-          u[j + 1] = fmaf(cg.y, x[j + 1] * inv_s, cq.y * (u[j + 1] * inv_u));
-          u[j + 2] = fmaf(cg.z, x[j + 2] * inv_s, cq.z * (u[j + 2] * inv_u));
-          u[j + 3] = fmaf(cg.w, x[j + 3] * inv_s, cq.w * (u[j + 3] * inv_u));
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const float2 a = __fmul2_rn(make_float2(x[j + k], x[j + k + 1]), is2);
+            const float2 w = __fmul2_rn(make_float2(u[j + k], u[j + k + 1]), iu2);
+            const float2 o = __ffma2_rn(a, k ? make_float2(cg.z, cg.w) : make_float2(cg.x, cg.y),
+                                        __fmul2_rn(w, k ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y)));
+            u[j + k] = o.x, u[j + k + 1] = o.y;
+          }
+        }
+        if (first_bad < i + 16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (i + j >= first_bad) u[j] = __int_as_float(0x7fffffff);
         }
         if (row < D) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o32[(i + j) * D + row] = i + j < first_bad ? u[j] : __int_as_float(0x7fffffff);
+          for (int j = 0; j < 16; ++j) o32[(i + j) * D + row] = u[j];
         }
       }
       tc_fence_before();
