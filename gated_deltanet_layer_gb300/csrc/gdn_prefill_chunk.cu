@@ -510,15 +510,22 @@ struct alignas(1024) OutIn {
   float scal[O_COUNT][64];
 };
 
+// Chunks of inputs in shared memory: what the chain needs three deep (a chunk's scales
+// are worked out a chunk ahead, and a load takes most of a chunk's time), what the
+// outputs need two deep.
+constexpr int kIn = 3;
+__device__ __forceinline__ int in_stage(int n) { return n % kIn; }
+__device__ __forceinline__ uint32_t in_phase(int n) { return (n / kIn) & 1; }
+
 template <int D>
 struct ChainSmem {
-  ChainIn<D> in[2];
+  ChainIn<D> in[kIn];
   OutIn<D> oin[2];
   float part[2][128];   // of a row's squares, by halves of its columns
   float inv_s[2][128], inv_u[2][128];
   int first_bad[2][128];
-  uint32_t vmax[2];  // of the chunk's v: the largest |v|, bf16 bits
-  uint64_t full[2], empty[2], ofull[2], oempty[2], s_ready[2], s_done[2], v_ready[2];
+  uint32_t vmax[kIn];  // of the chunk's v: the largest |v|, bf16 bits
+  uint64_t full[kIn], empty[kIn], v_ready[kIn], ofull[2], oempty[2], s_ready[2], s_done[2];
   uint64_t p_done, r_ready, u_done, u_ready, o_done, o_free, row_ready;
   uint32_t tmem;
 };
@@ -564,10 +571,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   if (e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) return;
   const int chunks = (e - b + kChunk - 1) / kChunk, place0 = chunk_first_place(p.r, sq);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kIn; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 2);  // the MMAs' commit, and the warp that looks v over
       mbar_init(&s.v_ready[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s.ofull[i], 1);
       mbar_init(&s.oempty[i], 9);  // the MMAs' commit, and the output warps
       mbar_init(&s.s_ready[i], 4);
@@ -591,13 +600,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 
   if (warp == 0) {
     for (int n = 0; n < chunks; ++n) {
-      const int t0 = b + n * kChunk, toks = min(kChunk, e - t0), st = n & 1;
-      const uint32_t ph = ((n >> 1) & 1) ^ 1;
+      const int t0 = b + n * kChunk, toks = min(kChunk, e - t0), st = in_stage(n), so = n & 1;
       const size_t place = place0 + n;
       const unsigned char* kq = c.kq + (place * p.Hk + kh) * kq_bytes<D>();
       const unsigned char* img = c.head + (place * p.Hv + h) * kHeadBytes;
       ChainIn<D>& g = s.in[st];
-      ok = ok && mbar_wait(&s.empty[st], ph);
+      ok = ok && mbar_wait(&s.empty[st], in_phase(n) ^ 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (lane == 0) {
@@ -608,32 +616,32 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       for (int t = lane; t < toks; t += 32)
         bulk_load(g.v[t], p.qkv + (long long)(t0 + t) * p.ldqkv + 2 * p.Hk * D + h * D, D * 2, &s.full[st]);
       if (lane == 0) bulk_load(g.k, kq, kq_bytes<D>() / 2, &s.full[st]);
-      ok = mbar_wait(&s.oempty[st], ph);
+      ok = mbar_wait(&s.oempty[so], ((n >> 1) & 1) ^ 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (lane == 0) {
-        OutIn<D>& y = s.oin[st];
-        mbar_arrive_expect_tx(&s.ofull[st], kq_bytes<D>() / 2 + kOutBytes);
-        bulk_load(y.q, kq + kq_bytes<D>() / 2, kq_bytes<D>() / 2, &s.ofull[st]);
-        bulk_load(y.ahi, img + kChainBytes, kOutBytes, &s.ofull[st]);
+        OutIn<D>& y = s.oin[so];
+        mbar_arrive_expect_tx(&s.ofull[so], kq_bytes<D>() / 2 + kOutBytes);
+        bulk_load(y.q, kq + kq_bytes<D>() / 2, kq_bytes<D>() / 2, &s.ofull[so]);
+        bulk_load(y.ahi, img + kChainBytes, kOutBytes, &s.ofull[so]);
       }
       __syncwarp();
     }
     // no copy is in flight when the CTA leaves
-    for (int n = max(0, chunks - 2); n < chunks; ++n) {
-      if (ok) ok = mbar_wait(&s.full[n & 1], (n >> 1) & 1);
+    for (int n = max(0, chunks - kIn); n < chunks; ++n)
+      if (ok) ok = mbar_wait(&s.full[in_stage(n)], in_phase(n));
+    for (int n = max(0, chunks - 2); n < chunks; ++n)
       if (ok) ok = mbar_wait(&s.ofull[n & 1], (n >> 1) & 1);
-    }
   } else if (warp == 1) {
     // the whole warp waits, one lane issues
     constexpr uint32_t idesc = idesc_f16(128, 64, false), idesc_s = idesc_f16(128, 64, true);
     for (int n = 0; n < chunks && ok; ++n) {
       const int st = n & 1;
       const uint32_t ph = n & 1;
-      ChainIn<D>& g = s.in[st];
+      ChainIn<D>& g = s.in[in_stage(n)];
       OutIn<D>& y = s.oin[st];
       const uint64_t kd = sdesc_k_sw128(smem_u32(g.k)), qd = sdesc_k_sw128(smem_u32(y.q));
-      if (!(ok = mbar_wait(&s.full[st], (n >> 1) & 1))) break;
+      if (!(ok = mbar_wait(&s.full[in_stage(n)], in_phase(n)))) break;
       // P = S k, in halves of dk as they are ready
       if (!(ok = mbar_wait(&s.s_ready[0], ph))) break;
       tc_fence_after();
@@ -701,7 +709,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
           mma_commit(&s.s_done[a]);
         }
         if (D == 64) mma_commit(&s.s_done[1]);
-        mma_commit(&s.empty[st]);
+        mma_commit(&s.empty[in_stage(n)]);
         const uint64_t ah = sdesc_k_sw128(smem_u32(y.ahi)), al = sdesc_k_sw128(smem_u32(y.alo));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -720,8 +728,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     // the chunk's largest |v|, from the bits (a NaN or an infinity is larger than any)
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     for (int n = 0; n < chunks; ++n) {
-      const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
-      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
+      const int st = in_stage(n), toks = min(kChunk, e - (b + n * kChunk));
+      if (ok) ok = mbar_wait(&s.full[st], in_phase(n));
       uint32_t m = 0;
 #pragma unroll 4
       for (int t = lane / kLanes; t < toks; t += kRows) {
@@ -783,10 +791,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     int first_bad = 0;
     float fu = 1.f, fs_next = 1.f, shrink = 0.f, added = 0.f;
     const auto scales = [&](int n) {
-      const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
+      const int st = in_stage(n), toks = min(kChunk, e - (b + n * kChunk));
       ChainIn<D>& g = s.in[st];
-      if (ok) ok = mbar_wait(&s.full[st], (n >> 1) & 1);
-      if (ok) ok = mbar_wait(&s.v_ready[st], (n >> 1) & 1);
+      if (ok) ok = mbar_wait(&s.full[st], in_phase(n));
+      if (ok) ok = mbar_wait(&s.v_ready[st], in_phase(n));
       const float4 end = *reinterpret_cast<const float4*>(g.scal[S_END]);
       float mv = __uint_as_float(s.vmax[st] << 16), gam_end = end.x, top = end.z, sum_b = end.w, sum_w = g.scal[S_END][4];
       first_bad = __float_as_int(end.y);
@@ -813,7 +821,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     for (int n = 0; n < chunks; ++n) {
       const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
       const uint32_t ph = n & 1;
-      ChainIn<D>& g = s.in[st];
+      ChainIn<D>& g = s.in[in_stage(n)];
       const float inv_s = inverse_pow2(fs), p_scale = fminf(fu * inv_s, 0x1p126f);
       const float u_scale = fminf(fs_next * inverse_pow2(fu), 0x1p126f);
       const int until = min(first_bad, toks);  // R is zero from there on
