@@ -59,15 +59,18 @@ __host__ __device__ __forceinline__ int chunk_places(int tokens, int seqs) { ret
 __device__ __forceinline__ int chunk_first_place(const Ragged& r, int s) {
   return min(max(__ldg(r.cu + s), 0), r.tokens) / kChunk + s;
 }
-// Place -> sequence (the last whose first place is at or before it).
+// Place -> sequence (the last whose first place is at or before it). Every lane of a
+// converged warp calls it: the lanes look at 32 sequences at a time, so the search is
+// one step of dependent loads for up to 31 sequences and two for up to 1023.
 __device__ __forceinline__ int chunk_seq(const Ragged& r, int place) {
-  int lo = 0, hi = r.seqs;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (chunk_first_place(r, mid) <= place)
-      lo = mid;
-    else
-      hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = r.seqs + 1;
+  while (n > 1) {
+    const int stride = (n + 31) / 32, at = lane * stride;
+    const unsigned below = __ballot_sync(0xffffffffu, at < n && chunk_first_place(r, lo + min(at, n - 1)) <= place);
+    const int last = below ? (31 - __clz(below)) * stride : 0;
+    lo += last;
+    n = min(stride, n - last);
   }
   return lo;
 }

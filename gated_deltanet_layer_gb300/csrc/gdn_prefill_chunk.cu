@@ -169,6 +169,7 @@ struct alignas(1024) PrepSmem {
   float m[kPrepHeads][64 * kLStride];        // L, then T in its place
   float ghi[kPrepHeads][64], glo[kPrepHeads][64];  // running sums of the log2 gates
   float bj[kPrepHeads][64];                  // 2^(G of the 16-block's end - G_j) / |k_j|
+  int steep[kPrepHeads][4];                  // a block's gates fall by more than 2^100
   float beta[kPrepHeads][64];
   float rn[128];                             // 1 / norm of the f16 rows (k, q)
   int bad[64];                               // k not finite
@@ -219,6 +220,19 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
     if (tok < n)
       row_in[i] = __ldg(reinterpret_cast<const uint4*>(p.qkv + (long long)(t0 + tok) * p.ldqkv + (row < 64 ? p.Hk + kh : kh) * D + col));
   }
+  // and what the first heads' gates are made of
+  const int hd = tid >> 7, q = tid & 127;  // this thread's head of the four, and its place in it
+  float gate_in[2][2] = {}, gate_w[2] = {};
+  const auto load_gates = [&](int h) {
+    gate_w[0] = p.A_log[h], gate_w[1] = bf16_to_f(p.dt_bias[h]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (2 * lane + k < n) {
+        const __nv_bfloat16* ba = p.ba + (long long)(t0 + 2 * lane + k) * p.ldba;
+        gate_in[k][0] = bf16_to_f(ba[h]), gate_in[k][1] = bf16_to_f(ba[p.Hv + h]);
+      }
+  };
+  if (q < 32 && hd < p.group) load_gates(kh * p.group + hd);
   if (warp == 0) tmem_alloc(&s.tmem, 64);
   if (tid == 0) {
     mbar_init(&s.done, 1);
@@ -255,7 +269,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  if (tid == 0) {
+  constexpr int kStoreWarp = kPrepThreads / 32 - 1;
+  if (warp == 1 && elect_one()) {
     constexpr uint32_t idesc = idesc_f16(128, 64, false);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
@@ -263,6 +278,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       mma_bf16(tmem, d, d, idesc, j > 0);
     }
     mma_commit(&s.done);
+  }
+  if (warp == kStoreWarp && lane == 0) {
     unsigned char* kq = c.kq + ((size_t)place * p.Hk + kh) * kq_bytes<D>();
 #pragma unroll
     for (int a = 0; a < D / 64; ++a) {
@@ -272,7 +289,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
     bulk_commit();
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the room is x's below
   }
-  const int hd = tid >> 7, q = tid & 127;  // this thread's head of the four, and its place in it
+  __syncwarp();
   const int i = q & 63;                    // row of L (TMEM lanes 0..63) or of the causal products (64..127)
   const bool lower = q < 64;
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -284,7 +301,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
     unsigned char* img = c.head + ((size_t)place * p.Hv + h) * kHeadBytes;
     // gates: one warp a head, two tokens a lane
     if (q < 32 && mine) {
-      const float rate = 1.4426950408889634f * expf(p.A_log[h]), shift = bf16_to_f(p.dt_bias[h]);
+      if (g0 > 0) load_gates(h);
+      const float rate = 1.4426950408889634f * expf(gate_w[0]), shift = gate_w[1];
       float gt[2], beta[2];
       int first_bad = 64;
 #pragma unroll
@@ -292,9 +310,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
         const int tok = 2 * lane + k;
         gt[k] = beta[k] = 0.f;
         if (tok < n) {
-          const __nv_bfloat16* ba = p.ba + (long long)(t0 + tok) * p.ldba;
-          beta[k] = sigmoid_f(bf16_to_f(ba[h]));
-          const float x = -rate * softplus_f(bf16_to_f(ba[p.Hv + h]) + shift);
+          beta[k] = sigmoid_f(gate_in[k][0]);
+          const float x = -rate * softplus_f(gate_in[k][1] + shift);
           gt[k] = x < -1e4f ? -1e4f : x;  // 2^-1e4 is 0, and sums of it stay ordinary
           if (!(finite(gt[k]) && finite(beta[k])) || s.bad[tok]) first_bad = tok;
         }
@@ -316,6 +333,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
         first_bad = min(first_bad, __shfl_xor_sync(0xffffffffu, first_bad, o));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
+      if ((lane & 7) == 0) s.steep[hd][lane >> 3] = !(G[0].hi - bhi < 100.f);
       float gam[2], left[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -348,28 +366,36 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       meet();
     }
     if (!mine) continue;  // a whole head's threads
-    // L_ij = beta_i e^(G_i-G_j) k_i.k_j and e^(G_i-G_j) q_i.k_j, 16 columns at a time.
-    // Off the diagonal blocks of 16, e^(G_i-G_j) is (from j to its block's end) x (from
-    // there to i), both at most 1: one exponential a block and row.
+    // L_ij = beta_i e^(G_i-G_j) k_i.k_j and e^(G_i-G_j) q_i.k_j, 16 columns at a time:
+    // e^(G_i-G_j) is (from j to its block's end) x (from there to i), one exponential a
+    // block and row. Both are at most 1 but on the diagonal, where the second undoes up
+    // to the block's whole fall; a block that falls by more than 2^100 takes an
+    // exponential a value there.
     const float gi = s.ghi[hd][i], li = s.glo[hd][i];
     const float f = lower ? s.beta[hd][i] * s.rn[i] : 1.f;
+    const int until = lower ? i : i + 1;
     const auto block = [&](int j0, float (&x)[16]) {
       tmem_ld16(tmem + j0 + lanes, x);
-      if (j0 > i) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = 0.f;
-      } else if (j0 + 16 <= i) {
-        const float a = f * exp2f((gi - s.ghi[hd][j0 + 15]) + (li - s.glo[hd][j0 + 15]));
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] *= a * s.bj[hd][j0 + j];
-      } else {
+      if (s.steep[hd][j0 >> 4] && j0 <= i && i < j0 + 16) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int jj = j0 + j;
-          const float y = f * s.rn[jj] * exp2f((gi - s.ghi[hd][jj]) + (li - s.glo[hd][jj])) * x[j];
-          x[j] = jj < i || (jj == i && !lower) ? y : 0.f;
+          x[j] *= f * s.rn[jj] * exp2f(jj <= i ? (gi - s.ghi[hd][jj]) + (li - s.glo[hd][jj]) : 0.f);
+        }
+      } else {
+        const float a = j0 > i ? 0.f : f * exp2f((gi - s.ghi[hd][j0 + 15]) + (li - s.glo[hd][j0 + 15]));
+        const float2 a2 = make_float2(a, a);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 bj = *reinterpret_cast<const float4*>(&s.bj[hd][j0 + j]);
+          const float2 y0 = __fmul2_rn(make_float2(x[j], x[j + 1]), __fmul2_rn(a2, make_float2(bj.x, bj.y)));
+          const float2 y1 = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), __fmul2_rn(a2, make_float2(bj.z, bj.w)));
+          x[j] = y0.x, x[j + 1] = y0.y, x[j + 2] = y1.x, x[j + 3] = y1.y;
         }
       }
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j0 + j >= until) x[j] = 0.f;
     };
     float mx = 0.f;
 #pragma unroll 1
@@ -472,7 +498,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
     }
     meet();  // before the next head's gates and L
   }
-  if (tid == 0) bulk_wait_all();
+  if (warp == kStoreWarp && lane == 0) bulk_wait_all();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 64);
