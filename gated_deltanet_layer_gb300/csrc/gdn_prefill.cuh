@@ -9,6 +9,9 @@ namespace gdn {
 constexpr int kChunk = 64;  // tokens of one chunk of a sequence
 // Longest sequence that the delta rule takes token by token.
 constexpr int kRecurrentMax = 8;
+// Up to this many sequences the chunked form starts the longest ones first, where they
+// take more than one wave; with more of them the waves level out by themselves.
+constexpr int kSorted = 128;
 
 // What of an index error (bits 23..16 of the error word).
 constexpr uint32_t kWhatSlot = 1, kWhatOffsets = 2, kWhatLength = 3, kWhatWait = 4;
@@ -102,6 +105,7 @@ struct DeltaParams {
   __nv_bfloat16* out;
   long long ldo;
   float gnorm_eps, l2_eps, q_scale;
+  int* order;  // [kSorted] of the workspace: the sequences by length, or nullptr: as they come
 };
 
 struct LinearParams {

@@ -15,7 +15,8 @@ struct gdn_prefill {
 
 namespace {
 
-constexpr size_t kErrorBytes = 256;  // the error word, on lines of its own
+constexpr size_t kErrorBytes = 256;                     // the error word, on lines of its own
+constexpr size_t kHeadBytes = kErrorBytes + kSorted * 4;  // and the sequences' order
 
 gdn_status validate(const gdn_prefill_config* c) {
   if (!c) return GDN_ERR_ARG;
@@ -75,7 +76,7 @@ Ragged ragged(const gdn_prefill* h, int32_t seqs, int32_t tokens, int32_t max_le
 
 extern "C" size_t gdn_prefill_workspace_bytes(const gdn_prefill_config* cfg) {
   if (validate(cfg) != GDN_OK) return 0;
-  return kErrorBytes + delta_chunk_bytes(cfg->max_tokens, cfg->max_seqs, cfg->num_k_heads, cfg->num_v_heads, cfg->head_k_dim);
+  return kHeadBytes + delta_chunk_bytes(cfg->max_tokens, cfg->max_seqs, cfg->num_k_heads, cfg->num_v_heads, cfg->head_k_dim);
 }
 
 extern "C" gdn_status gdn_prefill_create(const gdn_prefill_config* cfg, void* workspace, size_t workspace_bytes,
@@ -166,7 +167,8 @@ extern "C" gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t 
   p.gnorm_eps = c.gated_norm_eps;
   p.l2_eps = c.l2_eps;
   p.q_scale = c.q_scale;
-  return cuda_status(launch_delta(p, c.head_k_dim, c.ssm_dtype == GDN_STATE_BF16, h->ws + kErrorBytes,
+  p.order = seqs <= kSorted && (long long)seqs * Hv > 152 ? reinterpret_cast<int*>(h->ws + kErrorBytes) : nullptr;
+  return cuda_status(launch_delta(p, c.head_k_dim, c.ssm_dtype == GDN_STATE_BF16, h->ws + kHeadBytes,
                                   (cudaStream_t)stream));
 }
 

@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   extern __shared__ unsigned char raw[];
   ChainSmem<D>& s = *reinterpret_cast<ChainSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x, sq = blockIdx.y, kh = h / p.group;
+  const int h = blockIdx.x, kh = h / p.group;
+  const int sq = p.order ? __ldg(p.order + blockIdx.y) : blockIdx.y;
   int b, e, in, out;
   seq_rows(p.r, sq, &b, &e);
   if (e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) return;

@@ -94,6 +94,21 @@ __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
   const bool live = seq_slots(p.r, s, h == 0 && threadIdx.x == 0, &in, &out);
   if (live && e - b > kRecurrentMax) return;  // the chunked form's
   const int row = threadIdx.x;  // the dv row this lane finishes
+  if (p.order && s == p.r.seqs && h == 0) {
+    // the sequences' order for the chunked form, longest first
+    __shared__ int len[kSorted];
+    for (int i = row; i < s; i += D) {
+      int lo, hi;
+      seq_rows(p.r, i, &lo, &hi);
+      len[i] = hi - lo;
+    }
+    __syncthreads();
+    for (int i = row; i < s; i += D) {
+      int rank = 0;
+      for (int j = 0; j < s; ++j) rank += len[j] > len[i] || (len[j] == len[i] && j < i);
+      p.order[rank] = i;
+    }
+  }
   if (!live) {
     // padding: zero rows, 16 bytes a thread
     for (int t = b + threadIdx.x / (D / 8); t < e; t += 8)
