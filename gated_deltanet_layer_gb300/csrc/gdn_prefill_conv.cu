@@ -14,14 +14,26 @@ namespace gdn {
 namespace {
 
 constexpr int kConvThreads = 128;
+constexpr int kAhead = 8;  // rows in flight
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+
+// Two values of silu before their rounding to bf16: the fast exponential and reciprocal
+// (2^-22) are far below it, and expf with a division took twice the memory's time.
+__device__ __forceinline__ uint32_t silu2(float2 y) {
+  const float2 t = __fmul2_rn(y, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  const float2 o = __fmul2_rn(y, r);
+  return pack_bf16x2(o.x, o.y);
 }
 
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) {
@@ -41,18 +53,16 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) 
       *reinterpret_cast<uint4*>(p.out + (long long)t * p.ldo + c) = make_uint4(0, 0, 0, 0);
     return;
   }
-  float w[4][8];
+  float2 w[4][4];  // [tap][pair of channels]
   {
     const uint4* wp = reinterpret_cast<const uint4*>(p.w + (size_t)c * 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float f[8];
+      float2 f[4];
       unpack8(__ldg(wp + i), f);  // two channels' four taps
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w[k][2 * i] = f[k];
-        w[k][2 * i + 1] = f[4 + k];
-      }
+      for (int k = 0; k < 4; ++k)
+        w[k][i] = k & 1 ? make_float2(f[k / 2].y, f[2 + k / 2].y) : make_float2(f[k / 2].x, f[2 + k / 2].x);
     }
   }
   // the three taps before the chunk: rows of the sequence, or the old state
@@ -100,38 +110,30 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) 
 #pragma unroll
     for (int i = 0; i < 3; ++i) sp[i] = reinterpret_cast<const uint4*>(raw)[i];
   }
-  float x0[8], x1[8], x2[8];
+  float2 x0[4], x1[4], x2[4];
   unpack8(h[0], x0);
   unpack8(h[1], x1);
   unpack8(h[2], x2);
-  constexpr int kAhead = 8;  // rows in flight
-  uint4 q[kAhead];
-  for (int t = t0; t < t1; t += kAhead) {
+  const auto row = [&](int t, const uint4& v) {
+    float2 f[4];
+    unpack8(v, f);
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (t + i < t1) q[i] = __ldg(reinterpret_cast<const uint4*>(x + (long long)(t + i) * p.ldx));
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (t + i >= t1) break;
-      float f[8];
-      unpack8(q[i], f);
-      uint32_t o[4];
-#pragma unroll
-      for (int k = 0; k < 8; k += 2) {
-        const float a = fmaf(w[3][k], f[k], fmaf(w[2][k], x2[k], fmaf(w[1][k], x1[k], w[0][k] * x0[k])));
-        const float d = fmaf(w[3][k + 1], f[k + 1],
-                             fmaf(w[2][k + 1], x2[k + 1], fmaf(w[1][k + 1], x1[k + 1], w[0][k + 1] * x0[k + 1])));
-        o[k / 2] = pack_bf16x2(silu_f(a), silu_f(d));
-      }
-      *reinterpret_cast<uint4*>(p.out + (long long)(t + i) * p.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x0[k] = x1[k];
-        x1[k] = x2[k];
-        x2[k] = f[k];
-      }
+    for (int k = 0; k < 4; ++k) {
+      o[k] = silu2(__ffma2_rn(w[3][k], f[k], __ffma2_rn(w[2][k], x2[k], __ffma2_rn(w[1][k], x1[k], __fmul2_rn(w[0][k], x0[k])))));
+      x0[k] = x1[k], x1[k] = x2[k], x2[k] = f[k];
     }
+    *reinterpret_cast<uint4*>(p.out + (long long)t * p.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  };
+  uint4 q[kAhead];
+  int t = t0;
+  for (; t + kAhead <= t1; t += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(x + (long long)(t + i) * p.ldx));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) row(t + i, q[i]);
   }
+  for (; t < t1; ++t) row(t, __ldg(reinterpret_cast<const uint4*>(x + (long long)t * p.ldx)));
 }
 
 }  // namespace

@@ -14,7 +14,8 @@ from collections import namedtuple
 import torch
 
 from . import _native
-from ._native import (GDN_ACT_GELU_TANH, GDN_ACT_NONE, GDN_ACT_SILU, GDN_OK, GDN_STATE_BF16, GDN_STATE_F32, GdnError)
+from ._native import (GDN_ACT_GELU_TANH, GDN_ACT_NONE, GDN_ACT_SILU, GDN_OK, GDN_STATE_BF16, GDN_STATE_F32,
+                      GdnError)
 
 __all__ = ["GdnPrefill", "SlotMap", "linear", "linear_check", "slot_map"]
 
@@ -25,27 +26,32 @@ SlotMap = namedtuple("SlotMap", "cu_seqlens token_seq token_pos slots free_count
 _bf16, _i32 = torch.bfloat16, torch.int32
 
 
-def _stream(stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+# The calling thread's current stream as a number, without building a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t, name, dtype=_bf16):
-    """A [rows, columns] CUDA tensor with packed columns; its row stride."""
-    if t.dim() != 2 or t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a two-dimensional {dtype} CUDA tensor")
-    rows, ld = t.shape[0], t.stride(0)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _stream(stream, t):
+    return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
+
+
+def _rows(t, name):
+    """A [rows, columns] bf16 CUDA tensor with packed columns; its row stride."""
+    if t.dtype is not _bf16 or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a two-dimensional bf16 CUDA tensor")
+    (rows, cols), (ld, unit) = t.shape, t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"the columns of {name} must be packed")
-    if rows <= 1 or ld < t.shape[1]:
-        if rows > 1:
-            raise ValueError(f"the rows of {name} must not overlap")
-        return -(-t.shape[1] // 8) * 8  # a single row's stride does not matter
-    return ld
+    if rows > 1 and ld >= cols:
+        return ld
+    if rows > 1:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return -(-cols // 8) * 8  # a single row's stride does not matter
 
 
-def _dense(t, name, dtype, shape=None):
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor" + (f" of shape {shape}" if shape else ""))
+def _dense(t, name, dtype, n):
+    """The address of a contiguous CUDA tensor of n values."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} values")
     return t.data_ptr()
 
 
@@ -55,24 +61,25 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, stream=Non
     (x, w). activation: None, "silu" or "gelu" (tanh form). out may be
     residual. Returns out."""
     ldx, ldw = _rows(x, "x"), _rows(w, "w")
-    (M, K), N = x.shape, w.shape[0]
-    if w.shape[1] != K:
+    (M, K), (N, inner) = x.shape, w.shape
+    if inner != K:
         raise ValueError("x and w have different inner sizes")
-    if out is None:
-        out = torch.empty((M, N), dtype=_bf16, device=x.device)
-    elif out.shape != (M, N):
-        raise ValueError("out must be [M, N]")
-    ldr = 0
-    if residual is not None:
-        if residual.shape != (M, N):
-            raise ValueError("residual must be [M, N]")
-        ldr = _rows(residual, "residual")
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
+    if out is None:
+        out, ldo = torch.empty((M, N), dtype=_bf16, device=x.device), N
+    else:
+        ldo = _rows(out, "out")
+        if out.shape != (M, N):
+            raise ValueError("out must be [M, N]")
+    r, ldr = None, 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows(residual, "residual")
+        if residual.shape != (M, N):
+            raise ValueError("residual must be [M, N]")
     st = _native.lib().gdn_linear(
-        M, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else _dense(bias, "bias", _bf16, (N,)),
-        ACTIVATIONS[activation], None if residual is None else residual.data_ptr(), ldr, out.data_ptr(),
-        _rows(out, "out"), _stream(stream, x.device))
+        M, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else _dense(bias, "bias", _bf16, N),
+        ACTIVATIONS[activation], r, ldr, out.data_ptr(), ldo, _stream(stream, x))
     if st != GDN_OK:
         raise GdnError("gdn_linear", st)
     return out
@@ -82,7 +89,8 @@ def linear_check(stream=None):
     """(status, detail word) of the device's gdn_linear calls; synchronises
     and clears the word."""
     d = ctypes.c_uint32()
-    st = _native.lib().gdn_linear_check(_stream(stream, None), ctypes.byref(d))
+    s = stream if stream is not None else torch.cuda.current_stream()
+    st = _native.lib().gdn_linear_check(s.cuda_stream, ctypes.byref(d))
     return st, d.value
 
 
@@ -95,20 +103,25 @@ def slot_map(new_lens, context_lens, block_size, block_table, free_list, free_co
     this call's); error: int32 [1], optional. Returns a SlotMap of int32
     cu_seqlens [R + 1], token_seq [tokens], token_pos [tokens], int64 slots
     [tokens] and int32 free_count [1]."""
-    R, dev = new_lens.shape[0], new_lens.device
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("block_table must be [requests, max_blocks]")
+    R, wide = block_table.shape
+    n = R + 1
     if out is None:
-        i = torch.empty(R + 2 + 2 * tokens, dtype=_i32, device=dev)
-        cu, seq, pos, left = i.split((R + 1, tokens, tokens, 1))
-        out = SlotMap(cu, seq, pos, torch.empty(tokens, dtype=torch.int64, device=dev), left)
+        dev = new_lens.device
+        i = torch.empty(n + 1 + 2 * tokens, dtype=_i32, device=dev)
+        a, b, c, d = i.split_with_sizes((n, tokens, tokens, 1))
+        out = SlotMap(a, b, c, torch.empty(tokens, dtype=torch.int64, device=dev), d)
+        cu = i.data_ptr()
+        seq = cu + 4 * n
+        pos = seq + 4 * tokens
+        left, slots = pos + 4 * tokens, out.slots.data_ptr()
+    else:
+        cu, seq, pos = (_dense(t, "out", _i32, m) for t, m in zip(out, (n, tokens, tokens)))
+        slots, left = _dense(out.slots, "slots", torch.int64, tokens), _dense(out.free_count, "free_count", _i32, 1)
     st = _native.lib().gdn_slot_map(
-        R, tokens, _dense(new_lens, "new_lens", _i32), _dense(context_lens, "context_lens", _i32, (R,)), block_size,
-        block_table.shape[1], _dense(block_table, "block_table", _i32), _dense(free_list, "free_list", _i32),
-        free_list.numel(), _dense(free_count, "free_count", _i32, (1,)), _dense(out.free_count, "free_count", _i32, (1,)),
-        _dense(out.cu_seqlens, "cu_seqlens", _i32, (R + 1,)), _dense(out.token_seq, "token_seq", _i32, (tokens,)),
-        _dense(out.token_pos, "token_pos", _i32, (tokens,)), _dense(out.slots, "slots", torch.int64, (tokens,)),
-        None if error is None else _dense(error, "error", _i32, (1,)), _stream(stream, dev))
+        R, tokens, _dense(new_lens, "new_lens", _i32, R), _dense(context_lens, "context_lens", _i32, R), block_size, wide,
+        _dense(block_table, "block_table", _i32, R * wide), _dense(free_list, "free_list", _i32, free_list.numel()),
+        free_list.numel(), _dense(free_count, "free_count", _i32, 1), left, cu, seq, pos, slots,
+        None if error is None else _dense(error, "error", _i32, 1), _stream(stream, new_lens))
     if st != GDN_OK:
         raise GdnError("gdn_slot_map", st)
     return out
@@ -135,11 +148,12 @@ class GdnPrefill:
         self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
         self._channels = 2 * shape.num_k_heads * shape.head_k_dim + shape.num_v_heads * shape.head_v_dim
         self._columns = shape.num_v_heads * shape.head_v_dim
-        self._state = (torch.bfloat16 if shape.ssm_dtype == "bf16" else torch.float32,
-                       (shape.num_slots, shape.num_v_heads, shape.head_v_dim, shape.head_k_dim))
+        self._state = torch.bfloat16 if shape.ssm_dtype == "bf16" else torch.float32
+        self._state_values = shape.num_slots * self._columns * shape.head_k_dim
+        self._conv_values = shape.num_slots * self._channels * 3
         h = ctypes.c_void_p()
-        st = L.gdn_prefill_create(ctypes.byref(self.cfg), self.workspace.data_ptr(), n,
-                                  _stream(stream, self.workspace.device), ctypes.byref(h))
+        st = L.gdn_prefill_create(ctypes.byref(self.cfg), self.workspace.data_ptr(), n, _stream(stream, self.workspace),
+                                  ctypes.byref(h))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_create", st)
         self._h = h
@@ -151,11 +165,12 @@ class GdnPrefill:
             self._h = None
 
     def _out(self, out, like, cols):
+        """The output and its row stride."""
         if out is None:
-            return torch.empty((like.shape[0], cols), dtype=_bf16, device=like.device)
+            return torch.empty((like.shape[0], cols), dtype=_bf16, device=like.device), cols
         if out.shape != (like.shape[0], cols):
             raise ValueError(f"out must be [tokens, {cols}]")
-        return out
+        return out, _rows(out, "out")
 
     def conv(self, x, conv_w, cu_seqlens, state_in, state_out, conv_state, out=None, stream=None):
         """Causal conv1d + SiLU over the rows x [tokens, C] (a view of the
@@ -163,15 +178,16 @@ class GdnPrefill:
         slots state_in and state_out [S]. conv_state [slots, C, 3] is updated.
         Returns out [tokens, C]."""
         C, S = self._channels, state_in.shape[0]
-        if x.shape[1] != C:
+        ldx = _rows(x, "x")
+        T, cols = x.shape
+        if cols != C:
             raise ValueError(f"x must be [tokens, {C}]")
-        out = self._out(out, x, C)
+        out, ldo = self._out(out, x, C)
         st = _native.lib().gdn_prefill_conv(
-            self._h, S, x.shape[0], x.data_ptr(), _rows(x, "x"), _dense(conv_w, "conv_w", _bf16, (C, 4)),
-            _dense(cu_seqlens, "cu_seqlens", _i32, (S + 1,)), _dense(state_in, "state_in", _i32),
-            _dense(state_out, "state_out", _i32, (S,)),
-            _dense(conv_state, "conv_state", _bf16, (self.shape.num_slots, C, 3)), out.data_ptr(), _rows(out, "out"),
-            _stream(stream, x.device))
+            self._h, S, T, x.data_ptr(), ldx, _dense(conv_w, "conv_w", _bf16, 4 * C),
+            _dense(cu_seqlens, "cu_seqlens", _i32, S + 1), _dense(state_in, "state_in", _i32, S),
+            _dense(state_out, "state_out", _i32, S), _dense(conv_state, "conv_state", _bf16, self._conv_values),
+            out.data_ptr(), ldo, _stream(stream, x))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_conv", st)
         return out
@@ -183,19 +199,22 @@ class GdnPrefill:
         the gate z [tokens, Hv*dv], gated_norm_w. ssm_state is updated. max_len:
         no sequence is longer (None: no better bound than the rows). Returns
         core [tokens, Hv*dv]."""
-        C, S, Hv = self._channels, state_in.shape[0], self.shape.num_v_heads
-        T = qkv.shape[0]
-        if qkv.shape[1] != C or ba.shape != (T, 2 * Hv) or (z is not None and z.shape != (T, self._columns)):
-            raise ValueError("qkv, ba and z must be [tokens, C], [tokens, 2 Hv] and [tokens, Hv*dv]")
-        out = self._out(out, qkv, self._columns)
+        S, Hv, T = state_in.shape[0], self.shape.num_v_heads, qkv.shape[0]
+        ldqkv, ldba, zp, ldz, norm = _rows(qkv, "qkv"), _rows(ba, "ba"), None, 0, None
+        if qkv.shape[1] != self._channels or ba.shape != (T, 2 * Hv):
+            raise ValueError("qkv and ba must be [tokens, C] and [tokens, 2 Hv]")
+        if z is not None:
+            zp, ldz = z.data_ptr(), _rows(z, "z")
+            if z.shape != (T, self._columns):
+                raise ValueError("z must be [tokens, Hv*dv]")
+            norm = _dense(weights["gated_norm_w"], "gated_norm_w", _bf16, self.shape.head_v_dim)
+        out, ldo = self._out(out, qkv, self._columns)
         st = _native.lib().gdn_prefill_delta(
-            self._h, S, T, T if max_len is None else max_len, qkv.data_ptr(), _rows(qkv, "qkv"),
-            None if z is None else z.data_ptr(), 0 if z is None else _rows(z, "z"), ba.data_ptr(), _rows(ba, "ba"),
-            _dense(weights["A_log"], "A_log", torch.float32, (Hv,)), _dense(weights["dt_bias"], "dt_bias", _bf16, (Hv,)),
-            None if z is None else _dense(weights["gated_norm_w"], "gated_norm_w", _bf16, (self.shape.head_v_dim,)),
-            _dense(cu_seqlens, "cu_seqlens", _i32, (S + 1,)), _dense(state_in, "state_in", _i32),
-            _dense(state_out, "state_out", _i32, (S,)), _dense(ssm_state, "ssm_state", *self._state), out.data_ptr(),
-            _rows(out, "out"), _stream(stream, qkv.device))
+            self._h, S, T, T if max_len is None else max_len, qkv.data_ptr(), ldqkv, zp, ldz, ba.data_ptr(), ldba,
+            _dense(weights["A_log"], "A_log", torch.float32, Hv), _dense(weights["dt_bias"], "dt_bias", _bf16, Hv), norm,
+            _dense(cu_seqlens, "cu_seqlens", _i32, S + 1), _dense(state_in, "state_in", _i32, S),
+            _dense(state_out, "state_out", _i32, S), _dense(ssm_state, "ssm_state", self._state, self._state_values),
+            out.data_ptr(), ldo, _stream(stream, qkv))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_delta", st)
         return out
@@ -203,10 +222,10 @@ class GdnPrefill:
     def check(self, stream=None):
         """(status, detail word) of the sticky device error word; synchronises."""
         d = ctypes.c_uint32()
-        st = _native.lib().gdn_prefill_check(self._h, _stream(stream, self.workspace.device), ctypes.byref(d))
+        st = _native.lib().gdn_prefill_check(self._h, _stream(stream, self.workspace), ctypes.byref(d))
         return st, d.value
 
     def reset(self, stream=None):
-        st = _native.lib().gdn_prefill_reset(self._h, _stream(stream, self.workspace.device))
+        st = _native.lib().gdn_prefill_reset(self._h, _stream(stream, self.workspace))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_reset", st)
