@@ -397,31 +397,35 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       for (int j = 0; j < 16; ++j)
         if (j0 + j >= until) x[j] = 0.f;
     };
-    float mx = 0.f;
+    const int last = i & 32 ? 64 : 32;  // this warp's rows end before this column
+    if (lower) {
 #pragma unroll 1
-    for (int j0 = 0; j0 < 64; j0 += 16) {
-      float x[16];
-      block(j0, x);
-      if (lower) {
+      for (int j0 = 0; j0 < last; j0 += 16) {
+        float x[16];
+        block(j0, x);
 #pragma unroll
         for (int j = 0; j < 16; j += 4)
           *reinterpret_cast<float4*>(s.m[hd] + i * kLStride + j0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-      } else {
+      }
+      asm volatile("bar.sync %0, 64;" ::"r"(5 + hd) : "memory");  // the two warps of L
+    } else {
+      // The causal products, a row at a power of two of its own (O_CQ undoes it), while
+      // the other two warps begin on T.
+      float mx = 0.f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < last; j0 += 16) {
+        float x[16];
+        block(j0, x);
 #pragma unroll
         for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(x[j]));
       }
-    }
-    meet();
-    if (!lower) {
-      // the causal products, a row at a power of two of its own (O_CQ undoes it),
-      // while the other two warps begin on T
       const float fa = row_scale(mx);
       unsigned char* a = img + kChainBytes;
       reinterpret_cast<float*>(a + kImg)[64 * O_CQ + i] = p.q_scale * s.rn[64 + i] * inverse_pow2(fa);
 #pragma unroll 1
       for (int j0 = 0; j0 < 64; j0 += 16) {
-        float x[16];
-        block(j0, x);
+        float x[16] = {};
+        if (j0 < last) block(j0, x);
 #pragma unroll
         for (int j = 0; j < 16; j += 8) {
           uint32_t w[4], wl[4];
@@ -431,7 +435,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
           *reinterpret_cast<uint4*>(a + 8192 + swz(i, j0 + j)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
         }
       }
-    } else {
+    }
+    if (lower) {
       // T = (I + L)^-1, in place of L. First its diagonal blocks of 16, a column a
       // thread: t_i = [i = col] - sum_{l < i} L_il t_l.
       const int c16 = i & 15;
@@ -486,8 +491,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
 #pragma unroll 2
     for (int u = q; u < 512; u += 128) {
       const int r = u >> 3, j = (u & 7) * 8;
-      const float4 y = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j);
-      const float4 v = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j + 4);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f), v = y;
+      if (j <= r) {  // T is 0 above its diagonal (in m only the diagonal blocks are)
+        y = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j);
+        v = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j + 4);
+      }
       uint32_t w[4], wl[4];
       split2(make_float2(y.x * kScaleT, y.y * kScaleT), &w[0], &wl[0]);
       split2(make_float2(y.z * kScaleT, y.w * kScaleT), &w[1], &wl[1]);
