@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
 
 // ------------------------------------------------------------------ the chunks of a sequence
 
-// Warps: 0 loads, 1 issues MMAs, 2 holds the TMEM, 3 looks each chunk's v over; 4 to 11 keep the state's rows (a
+// Warps: 0 and 2 load, 1 issues MMAs, 3 looks each chunk's v over; 4 to 11 keep the state's rows (a
 // thread is a row of S^T and half of its columns, or of the chunk's tokens); 12 to 19
 // write the outputs, half of the tokens each four.
 // The loops over columns and tokens are rolled, 16 at a time: one warp a scheduler in
@@ -559,7 +559,10 @@ struct ChainSmem {
   float part[2][128];   // of a row's squares, by halves of its columns
   float inv_s[2][128], inv_u[2][128];
   int first_bad[2][128];
-  uint32_t vmax[kIn];  // of the chunk's v: the largest |v|, bf16 bits
+  // Of a chunk, for its scales: bounds of R and U as [0] + [1] |S0|, of the state after it
+  // as [2] |S0| + [3]; and whether all its v, k and gates are finite.
+  float4 scale[kIn];
+  int finite_in[kIn];
   uint64_t full[kIn], empty[kIn], v_ready[kIn], ofull[2], oempty[2], s_ready[2], s_done[2];
   uint64_t p_done, r_ready, u_done, u_ready, o_done, o_free, row_ready;
   uint32_t tmem;
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 
   if (warp == 0) {
     for (int n = 0; n < chunks; ++n) {
-      const int t0 = b + n * kChunk, toks = min(kChunk, e - t0), st = in_stage(n), so = n & 1;
+      const int t0 = b + n * kChunk, toks = min(kChunk, e - t0), st = in_stage(n);
       const size_t place = place0 + n;
       const unsigned char* kq = c.kq + (place * p.Hk + kh) * kq_bytes<D>();
       const unsigned char* img = c.head + (place * p.Hv + h) * kHeadBytes;
@@ -652,20 +655,25 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       for (int t = lane; t < toks; t += 32)
         bulk_load(g.v[t], p.qkv + (long long)(t0 + t) * p.ldqkv + 2 * p.Hk * D + h * D, D * 2, &s.full[st]);
       if (lane == 0) bulk_load(g.k, kq, kq_bytes<D>() / 2, &s.full[st]);
-      ok = mbar_wait(&s.oempty[so], ((n >> 1) & 1) ^ 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        OutIn<D>& y = s.oin[so];
-        mbar_arrive_expect_tx(&s.ofull[so], kq_bytes<D>() / 2 + kOutBytes);
-        bulk_load(y.q, kq + kq_bytes<D>() / 2, kq_bytes<D>() / 2, &s.ofull[so]);
-        bulk_load(y.ahi, img + kChainBytes, kOutBytes, &s.ofull[so]);
-      }
-      __syncwarp();
     }
     // no copy is in flight when the CTA leaves
     for (int n = max(0, chunks - kIn); n < chunks; ++n)
       if (ok) ok = mbar_wait(&s.full[in_stage(n)], in_phase(n));
+  } else if (warp == 2) {
+    // what the outputs need, with a wait of its own: the outputs may lag behind the chain
+    for (int n = 0; n < chunks; ++n) {
+      const int st = n & 1;
+      ok = ok && mbar_wait(&s.oempty[st], ((n >> 1) & 1) ^ 1);
+      if (!ok) break;
+      const size_t place = place0 + n;
+      if (elect_one()) {
+        OutIn<D>& y = s.oin[st];
+        mbar_arrive_expect_tx(&s.ofull[st], kq_bytes<D>() / 2 + kOutBytes);
+        bulk_load(y.q, c.kq + (place * p.Hk + kh) * kq_bytes<D>() + kq_bytes<D>() / 2, kq_bytes<D>() / 2, &s.ofull[st]);
+        bulk_load(y.ahi, c.head + (place * p.Hv + h) * kHeadBytes + kChainBytes, kOutBytes, &s.ofull[st]);
+      }
+      __syncwarp();
+    }
     for (int n = max(0, chunks - 2); n < chunks; ++n)
       if (ok) ok = mbar_wait(&s.ofull[n & 1], (n >> 1) & 1);
   } else if (warp == 1) {
@@ -767,14 +775,22 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       const int st = in_stage(n), toks = min(kChunk, e - (b + n * kChunk));
       if (ok) ok = mbar_wait(&s.full[st], in_phase(n));
       uint32_t m = 0;
-#pragma unroll 4
-      for (int t = lane / kLanes; t < toks; t += kRows) {
+      const auto look = [&](int t) {
         const uint4 v = *reinterpret_cast<const uint4*>(&s.in[st].v[t][lane % kLanes * 8]);
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+      };
+      if (toks == kChunk) {
+#pragma unroll 8
+        for (int t = 0; t < kChunk; t += kRows) m = __vmaxu2(m, look(t + lane / kLanes));
+      } else {
+        for (int t = lane / kLanes; t < toks; t += kRows) m = __vmaxu2(m, look(t));
       }
       m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
       if (lane == 0) {
-        s.vmax[st] = m;
+        const float4 end = *reinterpret_cast<const float4*>(s.in[st].scal[S_END]);
+        const float mv = __uint_as_float(m << 16);
+        s.scale[st] = make_float4(end.z * (mv + mv * end.w), end.z, end.x, s.in[st].scal[S_END][4] * mv);
+        s.finite_in[st] = __float_as_int(end.y) == kChunk && m < 0x7f80;
         mbar_arrive(&s.v_ready[st]);
         mbar_arrive(&s.empty[st]);
       }
@@ -831,12 +847,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       ChainIn<D>& g = s.in[st];
       if (ok) ok = mbar_wait(&s.full[st], in_phase(n));
       if (ok) ok = mbar_wait(&s.v_ready[st], in_phase(n));
-      const float4 end = *reinterpret_cast<const float4*>(g.scal[S_END]);
-      float mv = __uint_as_float(s.vmax[st] << 16), gam_end = end.x, top = end.z, sum_b = end.w, sum_w = g.scal[S_END][4];
-      first_bad = __float_as_int(end.y);
-      if (first_bad < kChunk || !finite(mv)) {
+      float4 k = s.scale[st];
+      first_bad = kChunk;
+      if (!s.finite_in[st]) {
         // up to the first token of this row whose v, k or gates are not finite
-        mv = 0.f;
+        const float4 end = *reinterpret_cast<const float4*>(g.scal[S_END]);
+        float mv = 0.f;
+        first_bad = __float_as_int(end.y);
         for (int i = 0; i < min(toks, first_bad); ++i) {
           const float a = fabsf(bf16_to_f(g.v[i][vrow]));
           if (!finite(a))
@@ -844,14 +861,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
           else
             mv = fmaxf(mv, a);
         }
-        if (first_bad < kChunk) gam_end = sum_w = 0.f, top = 1.f, sum_b = kChunk;
+        k = first_bad < kChunk ? make_float4((1.f + kChunk) * mv, 1.f, 0.f, 0.f)
+                               : make_float4(end.z * (mv + mv * end.w), end.z, end.x, g.scal[S_END][4] * mv);
       }
-      if (dead) first_bad = 0, gam_end = sum_w = 0.f;
-      fu = row_scale(top * (mv + bound + mv * sum_b));
-      added = sum_w * mv;
-      bound = fmaf(gam_end, bound, added) * 1.01f;
+      if (dead) first_bad = 0, k.z = k.w = 0.f;
+      fu = row_scale(fmaf(k.y, bound, k.x));
+      added = k.w;
+      bound = fmaf(k.z, bound, added) * 1.01f;
       fs_next = row_scale(bound);
-      shrink = gam_end * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
+      shrink = k.z * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
     };
     scales(0);
     for (int n = 0; n < chunks; ++n) {
