@@ -41,9 +41,9 @@ __device__ __forceinline__ float act_f(float y, int act) {
 // Stages of the ring: what the 227 KB hold beside the epilogue's staging.
 template <int BN>
 constexpr int pair_stages() {
-  return BN == 256 ? 5 : BN == 128 ? 7 : 8;
+  return BN == 256 ? 4 : BN == 128 ? 6 : 7;
 }
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 384;  // producer, MMA, TMEM, -; eight epilogue warps
 constexpr int kStageStride = 68;  // floats a staged row takes: 64 and four, against bank conflicts
 
 template <int BN>
@@ -51,7 +51,7 @@ struct alignas(1024) PairSmem {
   static constexpr int kStages = pair_stages<BN>();
   unsigned char a[kStages][128 * 128];
   unsigned char b[kStages][BN / 2 * 128];
-  float stage[4][32 * kStageStride];
+  float stage[8][32 * kStageStride];
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   uint32_t tmem;
 };
@@ -81,29 +81,24 @@ __device__ __forceinline__ void put8(const LinearParams& p, long long m, int n, 
   *reinterpret_cast<uint4*>(p.out + m * p.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Two columns of one output row (any alignment).
-template <bool ACT>
-__device__ __forceinline__ void put2(const LinearParams& p, long long m, int n, float a, float b, float bias_a, float bias_b,
-                                     bool wide) {
-  const bool two = n + 1 < p.N;
-  a = act_f<ACT>(a + bias_a, p.act);
-  b = act_f<ACT>(b + bias_b, p.act);
-  if (p.residual) {
-    const __nv_bfloat16* r = p.residual + m * p.ldr + n;
-    if (wide && two) {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(r);
-      a += bf16_lo(v), b += bf16_hi(v);
-    } else {
-      a += bf16_to_f(r[0]);
-      if (two) b += bf16_to_f(r[1]);
-    }
+// Two columns of one output row (any alignment): the residual, and the output.
+__device__ __forceinline__ float2 get2(const LinearParams& p, long long m, int n, bool wide) {
+  const __nv_bfloat16* r = p.residual + m * p.ldr + n;
+  if (wide && n + 1 < p.N) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(r);
+    return make_float2(bf16_lo(v), bf16_hi(v));
   }
+  return make_float2(bf16_to_f(r[0]), n + 1 < p.N ? bf16_to_f(r[1]) : 0.f);
+}
+template <bool ACT>
+__device__ __forceinline__ void put2(const LinearParams& p, long long m, int n, float2 v, float2 bias, float2 res, bool wide) {
+  const float a = act_f<ACT>(v.x + bias.x, p.act) + res.x, b = act_f<ACT>(v.y + bias.y, p.act) + res.y;
   __nv_bfloat16* o = p.out + m * p.ldo + n;
-  if (wide && two) {
+  if (wide && n + 1 < p.N) {
     *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(a, b);
   } else {
     o[0] = __float2bfloat16_rn(a);
-    if (two) o[1] = __float2bfloat16_rn(b);
+    if (n + 1 < p.N) o[1] = __float2bfloat16_rn(b);
   }
 }
 
@@ -125,7 +120,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.acc_full[i], 1);
-      mbar_init(&s.acc_empty[i], 8);  // four epilogue warps of both CTAs
+      mbar_init(&s.acc_empty[i], 16);  // eight epilogue warps of both CTAs
     }
     fence_mbar_init();
     prefetch_tensormap(&xmap);
@@ -189,11 +184,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (++buf == 2) buf = 0, aph ^= 1;
     }
   } else if (warp >= 4) {
-    const int q = warp - 4;  // TMEM lanes 32 q .. 32 q + 31: rows of this CTA's half
-    float* sm = s.stage[q];
+    // Two warps share each 32 rows (TMEM lanes 32 q ..), in turns of kCols columns.
+    constexpr int kCols = BN == 64 ? 32 : 64;
+    constexpr int kLanes8 = kCols / 8, kRows8 = 32 / kLanes8;  // 16-byte rows: lanes a row, rows a turn
+    constexpr int kLanes2 = kCols / 2, kRows2 = 32 / kLanes2;  // two columns a lane
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    float* sm = s.stage[warp - 4];
     const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0 &&
                       p.ldo % 2 == 0 && (!p.residual || p.ldr % 2 == 0);
-    // rows of 16 bytes throughout: a lane takes 8 columns of every fourth row
+    // rows of 16 bytes throughout
     const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 15) == 0 &&
                      p.N % 8 == 0 && p.ldo % 8 == 0 && (!p.residual || p.ldr % 8 == 0);
     int buf = 0;
@@ -203,19 +202,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tile_at(tiles, i, &tm, &tn);
       const int m0 = tm * 256 + (int)rank * 128 + q * 32;
       const int rows = min(32, p.M - m0);
-      for (int c = 0; c < BN; c += 64) {
+      for (int c = half * kCols; c < BN; c += 2 * kCols) {
         // the residual's loads are in flight while the tile is multiplied
-        const int n8 = tn * BN + c + (lane & 7) * 8;
+        const int n8 = tn * BN + c + (lane % kLanes8) * 8;
         const bool mine = vec && n8 < p.N;
-        uint4 res[8];
+        uint4 res[kLanes8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        for (int r = 0; r < kLanes8; ++r) {
           res[r] = make_uint4(0, 0, 0, 0);
-          const int row = 4 * r + (lane >> 3);
+          const int row = kRows8 * r + lane / kLanes8;
           if (mine && p.residual && row < rows)
             res[r] = *reinterpret_cast<const uint4*>(p.residual + (long long)(m0 + row) * p.ldr + n8);
         }
-        if (c == 0) {
+        if (c < 2 * kCols) {
           ok = mbar_wait(&s.acc_full[buf], aph);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -223,15 +222,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         const uint32_t t = tmem + buf * 256 + c + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-        for (int h = 0; h < 64; h += 32) {
+        for (int h = 0; h < kCols; h += 32) {
           float v[32];
           tmem_ld32(t + h, v);
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<float4*>(sm + lane * kStageStride + h + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
-        if (c + 64 == BN) {
-          // the accumulator is out: the next tile but one may take it
+        if (c + 2 * kCols >= BN) {
+          // this warp's part of the accumulator is out: the next tile but one may take it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_rank(&s.acc_empty[buf], 0));
@@ -245,19 +244,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               for (int j = 0; j < 8; ++j) bias[j] = bf16_to_f(p.bias[n8 + j]);
             }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const int row = 4 * r + (lane >> 3);
-              if (row < rows) put8<ACT>(p, m0 + row, n8, sm + row * kStageStride + (lane & 7) * 8, bias, res[r]);
+            for (int r = 0; r < kLanes8; ++r) {
+              const int row = kRows8 * r + lane / kLanes8;
+              if (row < rows) put8<ACT>(p, m0 + row, n8, sm + row * kStageStride + (lane % kLanes8) * 8, bias, res[r]);
             }
           }
         } else {
-          const int n = tn * BN + c + 2 * lane;
+          const int n = tn * BN + c + 2 * (lane % kLanes2);
           if (n < p.N) {
-            const float ba = p.bias ? bf16_to_f(p.bias[n]) : 0.f, bb = p.bias && n + 1 < p.N ? bf16_to_f(p.bias[n + 1]) : 0.f;
-#pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
-              const float2 v = *reinterpret_cast<const float2*>(sm + r * kStageStride + 2 * lane);
-              put2<ACT>(p, m0 + r, n, v.x, v.y, ba, bb, wide);
+            float2 bias = make_float2(0.f, 0.f);
+            if (p.bias) bias = make_float2(bf16_to_f(p.bias[n]), n + 1 < p.N ? bf16_to_f(p.bias[n + 1]) : 0.f);
+#pragma unroll 1
+            for (int r0 = lane / kLanes2; r0 < rows; r0 += 8 * kRows2) {
+              float2 rs[8];
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                rs[r] = make_float2(0.f, 0.f);
+                if (p.residual && r0 + r * kRows2 < rows) rs[r] = get2(p, m0 + r0 + r * kRows2, n, wide);
+              }
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                const int row = r0 + r * kRows2;
+                if (row < rows)
+                  put2<ACT>(p, m0 + row, n, *reinterpret_cast<const float2*>(sm + row * kStageStride + 2 * (lane % kLanes2)),
+                            bias, rs[r], wide);
+              }
             }
           }
         }

@@ -170,6 +170,7 @@ struct alignas(1024) PrepSmem {
   float ghi[kPrepHeads][64], glo[kPrepHeads][64];  // running sums of the log2 gates
   float bj[kPrepHeads][64];                  // 2^(G of the 16-block's end - G_j) / |k_j|
   int steep[kPrepHeads][4];                  // a block's gates fall by more than 2^100
+  int first_bad[kPrepHeads];                 // first token whose k or gates are not finite, else 64
   float beta[kPrepHeads][64];
   float rn[128];                             // 1 / norm of the f16 rows (k, q)
   int bad[64];                               // k not finite
@@ -201,6 +202,8 @@ __device__ __forceinline__ float4 minus(float4 v) { return make_float4(-v.x, -v.
 
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkParams c) {
+  // The delta kernel may take an SM as soon as no CTA of this one is left to start.
+  griddep_launch_dependents();
   const DeltaParams& p = c.p;
   extern __shared__ unsigned char raw[];
   PrepSmem<D>& s = *reinterpret_cast<PrepSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -209,7 +212,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
   int b, e, in, out;
   seq_rows(p.r, sq, &b, &e);
   const int t0 = b + (place - chunk_first_place(p.r, sq)) * kChunk, n = min(kChunk, e - t0);
-  if (n <= 0 || e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) return;
+  if (n <= 0 || e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) {
+    griddep_wait();
+    return;
+  }
   // k and q rows: norms, and f16 images scaled by a power of two each
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = 128 / (kPrepThreads / 32) / kRows;
   uint4 row_in[kIter];
@@ -353,6 +359,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       if (lane == 0) {
         *reinterpret_cast<float4*>(sc + 64 * S_END) = make_float4(exp2f(ehi + elo), __int_as_float(first_bad), top, sum_b);
         sc[64 * S_END + 4] = sum_w;
+        s.first_bad[hd] = first_bad;
       }
       *reinterpret_cast<float2*>(img + kChainBytes + kImg + 256 * O_CQG + 8 * lane) =
           make_float2(p.q_scale * rq.x * gam[0], p.q_scale * rq.y * gam[1]);
@@ -403,6 +410,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       for (int j0 = 0; j0 < last; j0 += 16) {
         float x[16];
         block(j0, x);
+        // U is zero from the first token on that is not finite; so is L, or its NaN
+        // would reach earlier rows of T through products with T's zeros
+        if (i >= s.first_bad[hd]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < 16; j += 4)
           *reinterpret_cast<float4*>(s.m[hd] + i * kLStride + j0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
@@ -511,6 +524,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 64);
+  // This kernel needs nothing of the recurrent one, which it overlaps, but ends after it:
+  // what comes next in the stream waits for both.
+  griddep_wait();
 }
 
 // ------------------------------------------------------------------ the chunks of a sequence
@@ -603,8 +619,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   extern __shared__ unsigned char raw[];
   ChainSmem<D>& s = *reinterpret_cast<ChainSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
   const int h = blockIdx.x, kh = h / p.group;
-  const int sq = p.order ? __ldg(p.order + blockIdx.y) : blockIdx.y;
+  const int sq = p.order ? __ldcg(p.order + blockIdx.y) : blockIdx.y;
   int b, e, in, out;
   seq_rows(p.r, sq, &b, &e);
   if (e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) return;
@@ -1162,11 +1179,23 @@ cudaError_t launch(const ChunkParams& c, cudaStream_t s) {
   if (e == cudaSuccess) e = opt_in<delta_kernel<D, BF16>>(chain);
   if (e != cudaSuccess) return e;
   const dim3 places(chunk_places(c.p.r.tokens, c.p.r.seqs) - 1, c.p.Hk);  // the last is the pad rows'
-  prepare_kernel<D><<<places, kPrepThreads, prep, s>>>(c);
-  e = cudaGetLastError();
+  // Each may start while the kernel before it ends (programmatic stream serialisation).
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.gridDim = places;
+  cfg.blockDim = dim3(kPrepThreads);
+  cfg.dynamicSmemBytes = prep;
+  e = cudaLaunchKernelEx(&cfg, prepare_kernel<D>, c);
   if (e != cudaSuccess) return e;
-  delta_kernel<D, BF16><<<dim3(c.p.Hv, c.p.r.seqs), kChainThreads, chain, s>>>(c);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(c.p.Hv, c.p.r.seqs);
+  cfg.blockDim = dim3(kChainThreads);
+  cfg.dynamicSmemBytes = chain;
+  return cudaLaunchKernelEx(&cfg, delta_kernel<D, BF16>, c);
 }
 
 }  // namespace

@@ -87,6 +87,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
   constexpr int E = D / 32, W = D / 32;
   __shared__ float red[2][W];
+  griddep_launch_dependents();  // the chunked form's first kernel touches nothing of this one's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s = blockIdx.x, h = blockIdx.y;
   int b, e, in = 0, out = 0;

@@ -39,13 +39,13 @@ def _rows(t, name):
     if t.dtype is not _bf16 or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a two-dimensional bf16 CUDA tensor")
     (rows, cols), (ld, unit) = t.shape, t.stride()
-    if unit != 1 and cols > 1:
+    if unit != 1 and cols > 1 and rows:
         raise ValueError(f"the columns of {name} must be packed")
     if rows > 1 and ld >= cols:
         return ld
     if rows > 1:
         raise ValueError(f"the rows of {name} must not overlap")
-    return -(-cols // 8) * 8  # a single row's stride does not matter
+    return -(-cols // 8) * 8  # the stride of one row, or none, does not matter
 
 
 def _dense(t, name, dtype, n):

@@ -158,7 +158,7 @@ def delta_reference(b, gated):
             most = np.maximum(most, np.maximum(np.sqrt((S * S).sum((1, 2))), np.sqrt((v * v).sum(1))))
         pool[b.last[s]] = S
         norm[s] = most
-    return core.reshape(b.T, -1), scale.reshape(b.T, -1), pool, norm
+    return core.reshape(b.T, Hv * d), scale.reshape(b.T, Hv * d), pool, norm
 
 
 def check_delta(b, core, gated, *, core_tol=2.0 ** -8, state_tol=2e-5):

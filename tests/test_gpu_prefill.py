@@ -371,3 +371,132 @@ def test_slots_for_a_verify_step():
     i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
     m = slot_map(i(3, 3), i(0, 2), 1, table, i(4, 5, 6, 7, 8, 9), i(6), 6)
     assert m.slots.tolist() == [9, 8, 7, 6, 5, 4] and int(m.free_count) == 0
+
+
+# ------------------------------------------------------------------ ends and accidents
+
+@pytest.mark.parametrize("lens,extra", [([0], 0), ([0, 0, 0], 0), ([], 5), ([0, 9], 70)], ids=str)
+def test_prefill_of_nothing(lens, extra):
+    b = P.Batch(P.SMALL, lens, 16, extra=extra)
+    h = handle(b)
+    y = h.conv(b.dx, b.dw, b.dcu, b.dfirst, b.dlast, b.dconv)
+    np.testing.assert_array_equal(P.f64(b.dconv), P.conv_reference(b)[2])
+    core = h.delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, b.dssm, z=b.dz)
+    P.check_delta(b, core, True)
+    used = int(b.cu[-1])
+    assert not y[used:].any() and not core[used:].any()
+
+
+def test_prefill_of_many_sequences():
+    rng = np.random.default_rng(17)
+    lens = [int(n) for n in rng.choice([0, 1, 2, 8, 9, 20, 70], 150)]
+    b = P.Batch(P.SMALL.with_(num_slots=310), lens, 17, pad=[3, 40], fresh=range(0, 150, 7))
+    h = handle(b)
+    want, scale, pool = P.conv_reference(b)
+    got = P.f64(h.conv(b.dx, b.dw, b.dcu, b.dfirst, b.dlast, b.dconv))
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * scale).all()
+    np.testing.assert_array_equal(P.f64(b.dconv), pool)
+    P.check_delta(b, h.delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, b.dssm, z=b.dz), True)
+    assert h.check()[0] == 0
+
+
+@pytest.mark.parametrize("what", ["v", "k", "q", "b", "a"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [0, 13, 70, 149])
+def test_delta_of_values_that_are_not_finite(what, value, at):
+    """Nothing before such a token changes, nor any row of the state that the
+    token's value is not part of."""
+    b = P.Batch(P.WIDE, [150, 30], 18)
+    sh = b.shape
+    Hk, Hv, d = sh.num_k_heads, sh.num_v_heads, sh.head_k_dim
+    good = handle(b).delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, b.dssm.clone(), z=None).view(-1, Hv, d).clone()
+    dx, dba, ssm = b.dx.clone(), b.dba.clone(), b.dssm.clone()
+    ref = b.dssm.clone()
+    handle(b).delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, ref)
+    head, row = 4, 77
+    hit = torch.zeros(Hv, d, dtype=torch.bool, device="cuda")  # state rows the value is part of
+    if what == "v":
+        dx[at, 2 * Hk * d + head * d + row] = value
+        hit[head, row] = True
+    elif what in "qk":
+        dx[at, (Hk * d if what == "k" else 0) + (head // sh.group) * d + 5] = value
+        hit[head // sh.group * sh.group:(head // sh.group + 1) * sh.group] = True
+    else:
+        dba[at, (Hv if what == "a" else 0) + head] = value
+        hit[head] = True
+    core = handle(b).delta(dx, dba, b.weights, b.dcu, b.dfirst, b.dlast, ssm).view(-1, Hv, d)
+    same = lambda a, c: torch.equal(a.contiguous().view(torch.int16), c.contiguous().view(torch.int16))
+    before = at // 64 * 64  # whole chunks before the token's; the rest of its chunk within the usual bounds
+    assert same(core[:before], good[:before]) and same(core[150:], good[150:])
+    want, scale, _, _ = P.delta_reference(b, False)
+    off = np.abs(P.f64(core).reshape(180, -1) - want)[:at] - 2.0 ** -8 * (np.abs(want) + scale)[:at]
+    assert off.max(initial=-1) <= 0
+    if what in "ab" and value == float("inf"):  # gates at their ends: beta 1, e^g 0
+        assert core.isfinite().all() and ssm[b.last[0]].isfinite().all()
+        return
+    assert torch.allclose(core[:150, ~hit].float(), good[:150, ~hit].float(), rtol=2.0 ** -7, atol=1e-6)
+    assert not core[at, hit].isfinite().any()
+    if what == "q":
+        assert same(core[at + 1:150], good[at + 1:150]) and torch.equal(ssm[b.last[0]], ref[b.last[0]])
+    else:
+        assert not core[at:150, hit].isfinite().any() and not ssm[b.last[0]][hit].isfinite().any()
+        err = (ssm[b.last[0]] - ref[b.last[0]])[~hit].double().norm() / ref[b.last[0]][~hit].double().norm()
+        assert err <= 2e-5
+
+
+def test_delta_of_a_state_that_is_not_finite():
+    for n in (3, 100):
+        b = P.Batch(P.WIDE, [n], 19)
+        ref, ssm = b.dssm.clone(), b.dssm.clone()
+        good = handle(b).delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, ref)
+        ssm[b.first[0], 2, 50, 3] = float("nan")
+        core = handle(b).delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, ssm)
+        bad = 2 * 128 + 50
+        assert not core[:, bad].isfinite().any() and not ssm[b.last[0], 2, 50].isfinite().all()
+        keep = torch.arange(core.shape[1], device="cuda") != bad
+        assert torch.equal(core[:, keep], good[:, keep])
+        ssm[b.last[0], 2, 50] = ref[b.last[0], 2, 50]
+        assert torch.equal(ssm[b.last[0]], ref[b.last[0]])
+
+
+def test_python_refusals():
+    b = P.Batch(P.SMALL, [5, 66], 20)
+    h = handle(b)
+    conv = lambda **k: h.conv(**{**dict(x=b.dx, conv_w=b.dw, cu_seqlens=b.dcu, state_in=b.dfirst, state_out=b.dlast,
+                                        conv_state=b.dconv), **k})
+    delta = lambda **k: h.delta(**{**dict(qkv=b.dx, ba=b.dba, weights=b.weights, cu_seqlens=b.dcu, state_in=b.dfirst,
+                                          state_out=b.dlast, ssm_state=b.dssm, z=b.dz), **k})
+    for call in (lambda: conv(x=b.dx.float()), lambda: conv(x=b.dx[:, 1:]), lambda: conv(x=b.dx.cpu()),
+                 lambda: conv(x=b.dx.T), lambda: conv(cu_seqlens=b.dcu[:2]), lambda: conv(state_out=b.dlast.long()),
+                 lambda: conv(conv_state=b.dconv[1:]), lambda: delta(z=b.dz[:, 1:]), lambda: delta(ba=b.dba[1:]),
+                 lambda: delta(ssm_state=b.dssm.half()), lambda: delta(out=torch.empty_like(b.dx)),
+                 lambda: linear(b.dx, b.dx[:, 8:]), lambda: linear(b.dx, b.dx, activation="relu"),
+                 lambda: linear(b.dx, b.dx, bias=b.dx[0])):
+        with pytest.raises(ValueError):
+            call()
+    wide = torch.zeros(71, b.dx.shape[1] + 8, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: conv(x=wide[:, 1:1 + b.dx.shape[1]]), lambda: conv(out=b.dx),
+                 lambda: delta(qkv=wide[:, 4:4 + b.dx.shape[1]]), lambda: linear(wide[:, 1:65], wide[:, 8:72])):
+        with pytest.raises(GdnError) as e:
+            call()
+        assert e.value.code == _native.GDN_ERR_ARG
+    big = P.Batch(P.SMALL, [99], 21)
+    with pytest.raises(GdnError):  # more rows than the handle was made for
+        h.conv(big.dx, big.dw, big.dcu, big.dfirst, big.dlast, big.dconv)
+
+
+def test_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "prefill_then_decode.py")
+    spec = importlib.util.spec_from_file_location("prefill_then_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    y, cores, conv, ssm, slots, m = ex.main("tiny", 3)
+    assert y.shape == (232, WL.TINY.hidden) and y.isfinite().all()
+    assert m.cu_seqlens.tolist() == [0, 37, 38, 168, 232] and len(set(slots.tolist())) == 4 and min(slots.tolist()) >= 1
+    assert int(m.free_count) == WL.TINY.num_slots - 1 - 4
+    for core in cores:
+        assert core.isfinite().all() and core.abs().sum(1).min() > 0
+    idle = [i for i in range(WL.TINY.num_slots) if i not in slots.tolist()]
+    assert not ssm[idle].any() and not conv[idle].any()
