@@ -41,10 +41,10 @@ __device__ __forceinline__ float act_f(float y, int act) {
 // Stages of the ring: what the 227 KB hold beside the epilogue's staging.
 template <int BN>
 constexpr int pair_stages() {
-  return BN == 256 ? 4 : BN == 128 ? 6 : 7;
+  return BN == 256 ? 5 : BN == 128 ? 7 : 8;
 }
 constexpr int kPairThreads = 384;  // producer, MMA, TMEM, -; eight epilogue warps
-constexpr int kStageStride = 68;  // floats a staged row takes: 64 and four, against bank conflicts
+constexpr int kStageStride = 36;  // floats a staged row takes: 32 and four, against bank conflicts
 
 template <int BN>
 struct alignas(1024) PairSmem {
@@ -185,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp >= 4) {
     // Two warps share each 32 rows (TMEM lanes 32 q ..), in turns of kCols columns.
-    constexpr int kCols = BN == 64 ? 32 : 64;
+    constexpr int kCols = 32;
     constexpr int kLanes8 = kCols / 8, kRows8 = 32 / kLanes8;  // 16-byte rows: lanes a row, rows a turn
     constexpr int kLanes2 = kCols / 2, kRows2 = 32 / kLanes2;  // two columns a lane
     const int q = warp & 3, half = (warp - 4) >> 2;

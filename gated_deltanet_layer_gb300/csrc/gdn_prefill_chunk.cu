@@ -81,6 +81,17 @@ __device__ __forceinline__ void split2(float2 y, uint32_t* hi, uint32_t* lo) {
   *lo = pack_h2(__float22half2_rn(__ffma2_rn(h, make_float2(-1.f, -1.f), y)));
 }
 
+// 16 columns (a multiple of 16 on) of a row of such an image: the swizzle keeps the two
+// 16-byte pieces in one aligned 32 bytes, the second first in odd rows.
+__device__ __forceinline__ void store_pair(unsigned char* image, int row, int col, const uint32_t (&w)[8]) {
+  const bool odd = row & 1;
+  unsigned char* p = image + (swz(row, col) & ~31);
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(odd ? w[4] : w[0]), "r"(odd ? w[5] : w[1]),
+               "r"(odd ? w[6] : w[2]), "r"(odd ? w[7] : w[3]), "r"(odd ? w[0] : w[4]), "r"(odd ? w[1] : w[5]),
+               "r"(odd ? w[2] : w[6]), "r"(odd ? w[3] : w[7])
+               : "memory");
+}
+
 // D[tmem] (+)= A[smem or tmem] B[smem], f16 operands, f32 accumulation.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -439,14 +450,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       for (int j0 = 0; j0 < 64; j0 += 16) {
         float x[16] = {};
         if (j0 < last) block(j0, x);
+        uint32_t w[8], wl[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 8) {
-          uint32_t w[4], wl[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) split2(make_float2(x[j + 2 * k] * fa, x[j + 2 * k + 1] * fa), &w[k], &wl[k]);
-          *reinterpret_cast<uint4*>(a + swz(i, j0 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(a + 8192 + swz(i, j0 + j)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-        }
+        for (int k = 0; k < 8; ++k) split2(make_float2(x[2 * k] * fa, x[2 * k + 1] * fa), &w[k], &wl[k]);
+        store_pair(a, i, j0, w);
+        store_pair(a + 8192, i, j0, wl);
       }
     }
     if (lower) {
