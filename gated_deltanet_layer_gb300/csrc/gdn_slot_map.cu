@@ -6,14 +6,15 @@
 // by the 16 bytes a token of its outputs for many. One launch: every CTA scans
 // all requests (a few KB, from L2), 1024 at a time with carried sums, and fills
 // its own tokens and blocks of each batch of 1024 by bisection in shared memory;
-// no CTA waits for another.
+// no CTA waits for another. With tokens enough a thread fills four in a row, in 16-byte
+// stores, and looks for the request of the first only; positions of a good request are
+// below 2^31, so the divisions by the block size are 32-bit ones.
 #include "gdn_prefill.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kSlotThreads = 1024;
-constexpr int kBlockRun = 256;  // consecutive blocks one CTA writes
 
 struct Tile {
   long long tok[kSlotThreads + 1];   // first token of each request, and the end
@@ -53,7 +54,9 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
   const long long B = p.B;
   const int avail = min(max(*p.free_count, 0), p.free_cap);
   // this CTA's tokens
-  const long long per = ((long long)p.N + gridDim.x - 1) / gridDim.x;
+  const long long per = (((long long)p.N + gridDim.x - 1) / gridDim.x + 3) & ~3LL;
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.token_seq) | reinterpret_cast<uintptr_t>(p.token_pos) |
+                      reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
   const long long my0 = min((long long)p.N, per * blockIdx.x), my1 = min((long long)p.N, my0 + per);
   long long tok_carry = 0, need_carry = 0;
   long long taken = 0;
@@ -65,8 +68,10 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
       const int a = __ldg(p.new_lens + r), c = __ldg(p.ctx_lens + r);
       nl = max(a, 0);
       cl = max(c, 0);
-      have = (cl + B - 1) / B;
-      const long long want = (cl + nl + B - 1) / B;
+      // rounded up: the sums are below 2^32
+      const unsigned end = (unsigned)min(cl + nl, 0x7fffffffLL);
+      have = ((unsigned)cl + (unsigned)p.B - 1) / (unsigned)p.B;
+      const long long want = (end + (unsigned)p.B - 1) / (unsigned)p.B;
       bad = a < 0 || c < 0 || want > p.max_blocks || cl + nl > 0x7fffffffLL;
       need = bad ? 0 : want - have;
     }
@@ -112,27 +117,53 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
       taken = t.need[last_at_most(t.need, kSlotThreads + 1, avail)];
     // tokens of this batch that are this CTA's
     const long long a0 = max(my0, t.tok[0]), a1 = min(my1, tok_carry);
-    for (long long k = a0 + tid; k < a1; k += kSlotThreads) {
-      const int i = last_at_most(t.tok, n, k);
+    const auto entry = [&](int i, long long k, int* at, long long* slot) {
       const long long pos = t.ctx[i] + (k - t.tok[i]);
-      const long long col = pos / B;
-      long long slot = -1;
-      if (t.have[i] >= 0) {
-        // a block of this step comes off the free list; an older one is in the table
-        const long long block = col >= t.have[i] ? __ldg(p.free_list + (avail - 1 - (t.need[i] + col - t.have[i])))
-                                                 : p.table[(long long)(base + i) * p.max_blocks + col];
-        slot = block * B + pos % B;
-      }
+      *at = (int)min(pos, 0x7fffffffLL);
+      *slot = -1;
+      if (t.have[i] < 0) return;
+      // a block of this step comes off the free list; an older one is in the table
+      const int col = (unsigned)*at / (unsigned)p.B;
+      const long long block = col >= t.have[i] ? __ldg(p.free_list + (avail - 1 - (t.need[i] + col - t.have[i])))
+                                               : p.table[(long long)(base + i) * p.max_blocks + col];
+      *slot = block * B + (*at - (long long)col * B);
+    };
+    const auto single = [&](long long k) {
+      const int i = last_at_most(t.tok, n, k);
+      int at;
+      long long slot;
+      entry(i, k, &at, &slot);
       p.token_seq[k] = base + i;
-      p.token_pos[k] = (int)min(pos, 0x7fffffffLL);
+      p.token_pos[k] = at;
       p.slots[k] = slot;
+    };
+    if (!wide || a1 - a0 <= kSlotThreads) {
+      for (long long k = a0 + tid; k < a1; k += kSlotThreads) single(k);
+    } else {
+      const long long v0 = (a0 + 3) & ~3LL, v1 = a1 & ~3LL;
+      if (tid < 3 && a0 + tid < v0) single(a0 + tid);
+      if (tid < 3 && v1 + tid < a1) single(v1 + tid);
+      for (long long k = v0 + 4 * tid; k < v1; k += 4 * kSlotThreads) {
+        int seq[4], at[4];
+        long long slot[4];
+        int i = last_at_most(t.tok, n, k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          while (t.tok[i + 1] <= k + j) ++i;  // the token is before the batch's end, so this ends
+          seq[j] = base + i;
+          entry(i, k + j, &at[j], &slot[j]);
+        }
+        *reinterpret_cast<int4*>(p.token_seq + k) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+        *reinterpret_cast<int4*>(p.token_pos + k) = make_int4(at[0], at[1], at[2], at[3]);
+        *reinterpret_cast<longlong2*>(p.slots + k) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2*>(p.slots + k + 2) = make_longlong2(slot[2], slot[3]);
+      }
     }
-    // needed blocks of this batch that are this CTA's: every gridDim.x-th run
-    const long long b1 = min(need_carry, taken);
-    for (long long run = t.need[0] / kBlockRun + tid / kBlockRun; run * kBlockRun < b1; run += kSlotThreads / kBlockRun) {
-      if (run % gridDim.x != blockIdx.x) continue;
-      const long long k = run * kBlockRun + tid % kBlockRun;
-      if (k < t.need[0] || k >= b1) continue;
+    // an even share of the batch's needed blocks
+    const int blocks = (int)max(0LL, min(need_carry, taken) - t.need[0]);
+    const int share = (blocks + gridDim.x - 1) / gridDim.x, b0 = share * blockIdx.x;
+    for (int u = b0 + tid; u < min(blocks, b0 + share); u += kSlotThreads) {
+      const long long k = t.need[0] + u;
       const int i = last_at_most(t.need, n, k);
       p.table[(long long)(base + i) * p.max_blocks + t.have[i] + (k - t.need[i])] = __ldg(p.free_list + (avail - 1 - k));
     }

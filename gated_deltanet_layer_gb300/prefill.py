@@ -106,14 +106,17 @@ def slot_map(new_lens, context_lens, block_size, block_table, free_list, free_co
     R, wide = block_table.shape
     n = R + 1
     if out is None:
-        dev = new_lens.device
-        i = torch.empty(n + 1 + 2 * tokens, dtype=_i32, device=dev)
-        a, b, c, d = i.split_with_sizes((n, tokens, tokens, 1))
-        out = SlotMap(a, b, c, torch.empty(tokens, dtype=torch.int64, device=dev), d)
-        cu = i.data_ptr()
-        seq = cu + 4 * n
-        pos = seq + 4 * tokens
-        left, slots = pos + 4 * tokens, out.slots.data_ptr()
+        # one allocation; the rows' arrays on 16 bytes
+        dev, up = new_lens.device, -(-tokens // 4) * 4
+        i = torch.empty(2 * up + n + 1, dtype=_i32, device=dev)
+        a, b, c, d = i.split_with_sizes((up, up, n, 1))
+        if up != tokens:
+            a, b = a[:tokens], b[:tokens]
+        out = SlotMap(c, a, b, torch.empty(tokens, dtype=torch.int64, device=dev), d)
+        seq = i.data_ptr()
+        pos = seq + 4 * up
+        cu = pos + 4 * up
+        left, slots = cu + 4 * n, out.slots.data_ptr()
     else:
         cu, seq, pos = (_dense(t, "out", _i32, m) for t, m in zip(out, (n, tokens, tokens)))
         slots, left = _dense(out.slots, "slots", torch.int64, tokens), _dense(out.free_count, "free_count", _i32, 1)
