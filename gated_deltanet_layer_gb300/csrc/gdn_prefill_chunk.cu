@@ -834,16 +834,17 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     float bound, fs;
     bool dead;  // the row holds a value that is not finite
     {
+      // this thread's half of the row, all its loads under way at once
       const size_t at = (((size_t)max(in, 0) * p.Hv + h) * D + vrow) * D + col0;
+      float x[D / 32][16] = {};
       float zero = 0.f, mx = 0.f;
       if (real && in > 0) {
-#pragma unroll 2
-        for (int col = 0; col < D / 2; col += 16) {
-          float x[16];
-          state16<BF16>(p.state, at + col, x);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(x[j])), zero += x[j] * 0.f;
-        }
+        for (int k = 0; k < D / 32; ++k) state16<BF16>(p.state, at + 16 * k, x[k]);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(x[k][j])), zero += x[k][j] * 0.f;
       }
       s.part[half][row] = zero == 0.f ? mx : __int_as_float(0x7fffffff);
       asm volatile("bar.sync 2, 256;" ::: "memory");
@@ -851,13 +852,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       dead = !(finite(a) && finite(o));
       bound = dead ? 0.f : 12.f * fmaxf(a, o);  // at least the 2-norm of 128 values
       fs = row_scale(bound);
-#pragma unroll 1
-      for (int col = 0; col < D / 2; col += 16) {
-        float x[16] = {};
-        if (real && in > 0 && !dead) state16<BF16>(p.state, at + col, x);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] *= fs;
-        tmem_st16f(tmem + kS + col0 + col + lanes, x);
+      for (int k = 0; k < D / 32; ++k) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[k][j] = dead ? 0.f : x[k][j] * fs;
+        tmem_st16f(tmem + kS + col0 + 16 * k + lanes, x[k]);
       }
       tmem_wait_st();
     }
