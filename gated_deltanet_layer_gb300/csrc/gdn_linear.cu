@@ -9,6 +9,13 @@
 //
 // Both read x and W through tile maps with zero fill, so odd M, N and K need no
 // care in the main loop: what is outside either matrix is zero in both operands.
+//
+// Measured (us): 8192 x 20480 x 8192 1376 by itself (2.0 PFLOP/s, 104% of the measured
+// library product) and 1674 back to back, where the power limit holds the clock down;
+// 4100 x 8192 x 1024 with a residual 61, of which 36 are the products and 24 the bytes:
+// 17 x 32 tiles on 76 pairs leave 8 rounds for 7.2, and each pair reads 1 MB of tiles
+// from L2 in the 7 us it has for a round; 5 x 2560 x 8192 8.0 in a graph, the weights'
+// bytes being 6.2.
 #include <algorithm>
 #include <atomic>
 
@@ -43,7 +50,9 @@ template <int BN>
 constexpr int pair_stages() {
   return BN == 256 ? 5 : BN == 128 ? 7 : 8;
 }
-constexpr int kPairThreads = 384;  // producer, MMA, TMEM, -; eight epilogue warps
+// Producer, MMA, TMEM, -; eight epilogue warps (with four, each with all the columns of 32
+// rows, 4100 x 8192 x 1024 took 74 us).
+constexpr int kPairThreads = 384;
 constexpr int kStageStride = 36;  // floats a staged row takes: 32 and four, against bank conflicts
 
 template <int BN>
