@@ -28,7 +28,7 @@ gdn_status validate(const gdn_prefill_config* c) {
   if (c->conv_kernel != 4 || c->head_k_dim != c->head_v_dim) return GDN_ERR_UNSUPPORTED;
   if (c->head_k_dim != 64 && c->head_k_dim != 128) return GDN_ERR_UNSUPPORTED;
   if (c->num_v_heads % c->num_k_heads != 0 || c->num_v_heads > 1024) return GDN_ERR_UNSUPPORTED;
-  if (c->max_tokens > (1 << 24) || c->max_seqs > (1 << 16)) return GDN_ERR_UNSUPPORTED;
+  if (c->max_tokens > (1 << 24) || c->max_seqs > 65535) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 

@@ -30,6 +30,7 @@ def config(**kw):
     ("l2_eps", -1.0, ARG), ("gated_norm_eps", float("nan"), ARG), ("q_scale", float("nan"), ARG),
     ("conv_kernel", 3, UNSUPPORTED), ("head_k_dim", 96, UNSUPPORTED), ("head_v_dim", 64, UNSUPPORTED),
     ("num_k_heads", 3, UNSUPPORTED), ("max_tokens", 1 << 25, UNSUPPORTED), ("max_seqs", 1 << 17, UNSUPPORTED),
+    ("max_seqs", 1 << 16, UNSUPPORTED),
 ])
 def test_config_refused(lib, field, value, status):
     c, h = config(**{field: value}), ctypes.c_void_p()
