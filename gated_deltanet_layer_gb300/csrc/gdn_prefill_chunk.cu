@@ -73,6 +73,7 @@ struct ChunkParams {
   DeltaParams p;
   unsigned char* kq;    // [place][Hk] f16 images of k and q
   unsigned char* head;  // [place][Hv] images and scalars
+  int ahead;            // prepare CTAs that run at once
 };
 
 // Byte of (row, column) in a K-major operand image of 64 f16 columns, 128-byte swizzle.
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
   const DeltaParams& p = c.p;
   extern __shared__ unsigned char raw[];
   PrepSmem<D>& s = *reinterpret_cast<PrepSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  const int place = blockIdx.x, kh = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int place = blockIdx.x / p.Hk, kh = blockIdx.x % p.Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int sq = chunk_seq(p.r, place);
   int b, e, in, out;
   seq_rows(p.r, sq, &b, &e);
@@ -244,6 +245,14 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
     row_in[i] = make_uint4(0, 0, 0, 0);
     if (tok < n)
       row_in[i] = __ldg(reinterpret_cast<const uint4*>(p.qkv + (long long)(t0 + tok) * p.ldqkv + (row < 64 ? p.Hk + kh : kh) * D + col));
+  }
+  // The rows of the CTA that will follow this one on its SM, two CTAs an SM, into L2:
+  // k and q come from memory, and nothing else is there to do meanwhile.
+  {
+    const long long ahead = (long long)t0 + (c.ahead + p.Hk - 1) / p.Hk * kChunk + (tid >> 3 & 63);
+    const int part = (tid & 7) * 64;  // 128 bytes of k's D columns (the first lanes), then of q's
+    if (tid < 512 && part < 2 * D && ahead < p.r.tokens)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.qkv + ahead * p.ldqkv + (part < D ? (p.Hk + kh) * D + part : kh * D + part - D)));
   }
   // and what the first heads' gates are made of
   const int hd = tid >> 7, q = tid & 127;  // this thread's head of the four, and its place in it
@@ -1193,7 +1202,7 @@ cudaError_t launch(const ChunkParams& c, cudaStream_t s) {
   cudaError_t e = opt_in<prepare_kernel<D>>(prep);
   if (e == cudaSuccess) e = opt_in<delta_kernel<D, BF16>>(chain);
   if (e != cudaSuccess) return e;
-  const dim3 places(chunk_places(c.p.r.tokens, c.p.r.seqs) - 1, c.p.Hk);  // the last is the pad rows'
+  const dim3 places((unsigned)(chunk_places(c.p.r.tokens, c.p.r.seqs) - 1) * c.p.Hk);  // the last is the pad rows'
   // Each may start while the kernel before it ends (programmatic stream serialisation).
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1224,6 +1233,7 @@ cudaError_t launch_delta_chunks(const DeltaParams& p, int d, bool state_bf16, un
   ChunkParams c;
   c.p = p;
   c.kq = ws;
+  c.ahead = 2 * 152;
   c.head = ws + (size_t)chunk_places(p.r.tokens, p.r.seqs) * p.Hk * 2 * kChunk * d * 2;
   if (d == 128) return state_bf16 ? launch<128, true>(c, s) : launch<128, false>(c, s);
   return state_bf16 ? launch<64, true>(c, s) : launch<64, false>(c, s);
