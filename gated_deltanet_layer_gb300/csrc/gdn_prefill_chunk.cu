@@ -526,21 +526,20 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       *reinterpret_cast<float4*>(m + (33 + r) * kLStride + cc) = minus(v[1]);
       meet();
     }
-#pragma unroll 2
-    for (int u = q; u < 512; u += 128) {
-      const int r = u >> 3, j = (u & 7) * 8;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f), v = y;
+#pragma unroll
+    for (int u = q; u < 256; u += 128) {
+      const int r = u >> 2, j = (u & 3) * 16;
+      uint32_t w[8] = {}, wl[8] = {};
       if (j <= r) {  // T is 0 above its diagonal (in m only the diagonal blocks are)
-        y = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j);
-        v = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 y = *reinterpret_cast<const float4*>(s.m[hd] + r * kLStride + j + 4 * k);
+          split2(make_float2(y.x * kScaleT, y.y * kScaleT), &w[2 * k], &wl[2 * k]);
+          split2(make_float2(y.z * kScaleT, y.w * kScaleT), &w[2 * k + 1], &wl[2 * k + 1]);
+        }
       }
-      uint32_t w[4], wl[4];
-      split2(make_float2(y.x * kScaleT, y.y * kScaleT), &w[0], &wl[0]);
-      split2(make_float2(y.z * kScaleT, y.w * kScaleT), &w[1], &wl[1]);
-      split2(make_float2(v.x * kScaleT, v.y * kScaleT), &w[2], &wl[2]);
-      split2(make_float2(v.z * kScaleT, v.w * kScaleT), &w[3], &wl[3]);
-      *reinterpret_cast<uint4*>(img + swz(r, j)) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(img + 8192 + swz(r, j)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+      store_pair(img, r, j, w);
+      store_pair(img + 8192, r, j, wl);
     }
     meet();  // before the next head's gates and L
   }
