@@ -47,7 +47,7 @@ __device__ __forceinline__ bool seq_slots(const Ragged& r, int s, bool report, i
   *in = __ldg(r.state_in + s);
   *out = __ldg(r.state_out + s);
   const int lo = __ldg(r.cu + s), hi = __ldg(r.cu + s + 1);
-  const bool bad_rows = lo < 0 || hi < lo || hi > r.tokens;
+  const bool bad_rows = lo < 0 || hi < lo || hi > r.tokens || (s == 0 && lo != 0);
   if (report && bad_rows) record(r.error, kStatusIndex, kWhatOffsets, s);
   if (*out <= 0 || bad_rows) return false;
   const bool bad_slot = *in >= r.num_slots || *out >= r.num_slots, too_long = hi - lo > r.max_len;

@@ -201,6 +201,8 @@ extern "C" gdn_status gdn_linear(int32_t rows, int32_t cols, int32_t inner, cons
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 2) || !aligned(residual, 2) || !aligned(out, 2)) return GDN_ERR_ARG;
   if (ldx < inner || ldw < inner || ldo < cols || (residual && ldr < cols) || ldx % 8 || ldw % 8) return GDN_ERR_ARG;
   if (ldx >= (1LL << 38) || ldw >= (1LL << 38)) return GDN_ERR_UNSUPPORTED;  // a tile map's largest stride
+  constexpr int32_t kEdge = INT32_MAX - 255;  // a tile may reach past the matrix, its coordinates are 32 bits
+  if (rows > kEdge || cols > kEdge || inner > kEdge) return GDN_ERR_UNSUPPORTED;
   const Span o{out, extent(rows, ldo, cols)}, r{residual, residual ? extent(rows, ldr, cols) : 0};
   const Span in[] = {{x, extent(rows, ldx, inner)}, {w, extent(cols, ldw, inner)}, {bias, bias ? (size_t)cols * 2 : 0}};
   if (overlaps_any(o, in)) return GDN_ERR_ARG;

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
 
 cudaError_t launch_slot_map(const SlotParams& p, cudaStream_t s) {
   // a CTA for every 2048 tokens, one for each SM at most
-  const int grid = min(152, max(1, (p.N + 2047) / 2048));
+  const int grid = min(152, max(1, (p.N - 1) / 2048 + 1));
   slot_map_kernel<<<grid, kSlotThreads, 0, s>>>(p);
   return cudaGetLastError();
 }

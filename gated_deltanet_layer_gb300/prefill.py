@@ -4,7 +4,9 @@ CUDA tensors: argument marshalling only, as for the decode step.
 `slot_map` turns request lengths into offsets, block tables and slots,
 `linear` runs a projection with its epilogue, and `GdnPrefill` the conv and the
 gated delta rule over ragged prompts; the states they leave are those
-`GdnDecode.step` continues from.
+`GdnDecode.step` continues from. Every call runs on the current stream, or on
+`stream`; what it allocates is allocated there, and tensors of another stream
+are the caller's to order and to keep (Tensor.record_stream).
 """
 from __future__ import annotations
 
@@ -32,6 +34,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _stream(stream, t):
     return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
+
+
+def _empty(size, dtype, like, stream):
+    """A new tensor on like's device, in the memory of the stream that writes it first."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=like.device)
 
 
 def _rows(t, name):
@@ -67,7 +77,7 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, stream=Non
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
     if out is None:
-        out, ldo = torch.empty((M, N), dtype=_bf16, device=x.device), N
+        out, ldo = _empty((M, N), _bf16, x, stream), N
     else:
         ldo = _rows(out, "out")
         if out.shape != (M, N):
@@ -107,12 +117,12 @@ def slot_map(new_lens, context_lens, block_size, block_table, free_list, free_co
     n = R + 1
     if out is None:
         # one allocation; the rows' arrays on 16 bytes
-        dev, up = new_lens.device, -(-tokens // 4) * 4
-        i = torch.empty(2 * up + n + 1, dtype=_i32, device=dev)
+        up = -(-tokens // 4) * 4
+        i = _empty(2 * up + n + 1, _i32, new_lens, stream)
         a, b, c, d = i.split_with_sizes((up, up, n, 1))
         if up != tokens:
             a, b = a[:tokens], b[:tokens]
-        out = SlotMap(c, a, b, torch.empty(tokens, dtype=torch.int64, device=dev), d)
+        out = SlotMap(c, a, b, _empty(tokens, torch.int64, new_lens, stream), d)
         seq = i.data_ptr()
         pos = seq + 4 * up
         cu = pos + 4 * up
@@ -148,7 +158,8 @@ class GdnPrefill:
         n = L.gdn_prefill_workspace_bytes(ctypes.byref(self.cfg))
         if n == 0:
             raise GdnError("gdn_prefill_workspace_bytes", _native.GDN_ERR_UNSUPPORTED)
-        self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+        with torch.cuda.stream(stream):  # None: the current one
+            self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
         self._channels = 2 * shape.num_k_heads * shape.head_k_dim + shape.num_v_heads * shape.head_v_dim
         self._columns = shape.num_v_heads * shape.head_v_dim
         self._state = torch.bfloat16 if shape.ssm_dtype == "bf16" else torch.float32
@@ -167,10 +178,10 @@ class GdnPrefill:
             _native.lib().gdn_prefill_destroy(h)
             self._h = None
 
-    def _out(self, out, like, cols):
+    def _out(self, out, like, cols, stream):
         """The output and its row stride."""
         if out is None:
-            return torch.empty((like.shape[0], cols), dtype=_bf16, device=like.device), cols
+            return _empty((like.shape[0], cols), _bf16, like, stream), cols
         if out.shape != (like.shape[0], cols):
             raise ValueError(f"out must be [tokens, {cols}]")
         return out, _rows(out, "out")
@@ -185,7 +196,7 @@ class GdnPrefill:
         T, cols = x.shape
         if cols != C:
             raise ValueError(f"x must be [tokens, {C}]")
-        out, ldo = self._out(out, x, C)
+        out, ldo = self._out(out, x, C, stream)
         st = _native.lib().gdn_prefill_conv(
             self._h, S, T, x.data_ptr(), ldx, _dense(conv_w, "conv_w", _bf16, 4 * C),
             _dense(cu_seqlens, "cu_seqlens", _i32, S + 1), _dense(state_in, "state_in", _i32, S),
@@ -211,7 +222,7 @@ class GdnPrefill:
             if z.shape != (T, self._columns):
                 raise ValueError("z must be [tokens, Hv*dv]")
             norm = _dense(weights["gated_norm_w"], "gated_norm_w", _bf16, self.shape.head_v_dim)
-        out, ldo = self._out(out, qkv, self._columns)
+        out, ldo = self._out(out, qkv, self._columns, stream)
         st = _native.lib().gdn_prefill_delta(
             self._h, S, T, T if max_len is None else max_len, qkv.data_ptr(), ldqkv, zp, ldz, ba.data_ptr(), ldba,
             _dense(weights["A_log"], "A_log", torch.float32, Hv), _dense(weights["dt_bias"], "dt_bias", _bf16, Hv), norm,

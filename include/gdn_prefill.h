@@ -111,8 +111,8 @@ gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t tokens, int
 
 /* Synchronise `stream` and read the sticky error word: GDN_OK or the first
  * recorded device status. *detail (optional) receives the raw word: bits
- * 31..24 status, 23..16 what (1 a state slot >= num_slots, 2 cu_seqlens out of
- * order or past `tokens`, 3 a sequence longer than max_len, 4 a wait inside
+ * 31..24 status, 23..16 what (1 a state slot >= num_slots, 2 cu_seqlens not from
+ * 0 on, out of order or past `tokens`, 3 a sequence longer than max_len, 4 a wait inside
  * the kernel that passed its limit), 15..0 the sequence. A sequence with an
  * index error is treated as padding; the others are not affected. */
 gdn_status gdn_prefill_check(gdn_prefill_t* h, void* stream, uint32_t* detail);

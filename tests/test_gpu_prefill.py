@@ -177,6 +177,44 @@ def test_prefill_index_errors_pad_their_sequence_only():
     assert h.check() == (_native.GDN_ERR_INDEX, (5 << 24) | (2 << 16) | 2)
 
 
+@pytest.mark.parametrize("start", [1, 64, 130])
+def test_prefill_offsets_that_do_not_start_at_0(start):
+    """The first sequence is an error and padding; the others are not affected, and rows
+    before the first offset are not taken for a sequence's."""
+    b = P.Batch(P.SMALL, [200, 66, 9], 14)
+    cu = b.dcu.clone()
+    cu[0] = start
+    h = handle(b)
+    b.last[0] = 0
+    core = torch.zeros_like(b.dz)
+    h.delta(b.dx, b.dba, b.weights, cu, b.dfirst, b.dlast, b.dssm, out=core)
+    assert h.check() == (_native.GDN_ERR_INDEX, (5 << 24) | (2 << 16))
+    P.check_delta(b, core, False)
+    h.reset()
+    y = torch.zeros_like(b.dx)
+    h.conv(b.dx, b.dw, cu, b.dfirst, b.dlast, b.dconv, out=y)
+    assert h.check() == (_native.GDN_ERR_INDEX, (5 << 24) | (2 << 16))
+    want, scale, pool = P.conv_reference(b)
+    got = P.f64(y)
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * scale).all()
+    np.testing.assert_array_equal(P.f64(b.dconv), pool)
+
+
+def test_outputs_belong_to_the_stream_that_writes_them():
+    """An output that a call on a stream of its own makes is that stream's memory: what
+    is free on the current stream alone is not taken for it."""
+    x, w = torch.ones(300, 64, device="cuda").bfloat16(), torch.ones(520, 64, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    free = torch.empty(300, 520, dtype=torch.bfloat16, device="cuda")
+    was = free.data_ptr()
+    del free
+    y = linear(x, w, stream=side)
+    assert y.data_ptr() != was
+    torch.cuda.synchronize()
+    assert (y == 64).all()
+
+
 def test_prefill_graph_replay_and_another_stream():
     b = P.Batch(P.WIDE, [70, 1, 129], 15)
     h = handle(b)

@@ -74,6 +74,12 @@ def test_linear_refuses(lib, defect):
     assert lib.gdn_linear(*linear_args(**defect)) == ARG
 
 
+@pytest.mark.parametrize("edge", [dict(rows=2**31 - 1), dict(cols=2**31 - 1, ldo=2**31, ldr=2**31, residual=None),
+                                  dict(inner=2**31 - 1, ldx=2**31, ldw=2**31), dict(ldx=2**38)], ids=str)
+def test_linear_beyond_a_tile_map(lib, edge):
+    assert lib.gdn_linear(*linear_args(**edge)) == UNSUPPORTED
+
+
 def test_linear_of_nothing(lib):
     assert lib.gdn_linear(*linear_args(rows=0)) == 0
     assert lib.gdn_linear(*linear_args(cols=0)) == 0
