@@ -720,6 +720,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   } else if (warp == 1) {
     // the whole warp waits, one lane issues
     constexpr uint32_t idesc = idesc_f16(128, 64, false), idesc_s = idesc_f16(128, 64, true);
+    // T and the causal products are zero above their diagonals: 16 of their columns meet
+    // the rows from there down. In a descriptor, 16 rows and 16 columns on.
+    constexpr int kDown = 128 + 2;
     for (int n = 0; n < chunks && ok; ++n) {
       const int st = n & 1;
       const uint32_t ph = n & 1;
@@ -771,9 +774,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         const uint64_t th = sdesc_k_sw128(smem_u32(g.thi)), tl = sdesc_k_sw128(smem_u32(g.tlo));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          mma_f16_ts(tmem + kPU, tmem + kRhi + 8 * j, th + 2 * j, idesc, j > 0);
-          mma_f16_ts(tmem + kPU, tmem + kRhi + 8 * j, tl + 2 * j, idesc, true);
-          mma_f16_ts(tmem + kPU, tmem + kRlo + 8 * j, th + 2 * j, idesc, true);
+          const uint32_t id = idesc_f16(128, 64 - 16 * j, false), d = tmem + kPU + 16 * j;
+          mma_f16_ts(d, tmem + kRhi + 8 * j, th + kDown * j, id, j > 0);
+          mma_f16_ts(d, tmem + kRhi + 8 * j, tl + kDown * j, id, true);
+          mma_f16_ts(d, tmem + kRlo + 8 * j, th + kDown * j, id, true);
         }
         mma_commit(&s.u_done);
       }
@@ -798,9 +802,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         const uint64_t ah = sdesc_k_sw128(smem_u32(y.ahi)), al = sdesc_k_sw128(smem_u32(y.alo));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, ah + 2 * j, idesc, j > 0);
-          mma_f16_ts(tmem + kAU, tmem + kUlo + 8 * j, ah + 2 * j, idesc, true);
-          mma_f16_ts(tmem + kAU, tmem + kUhi + 8 * j, al + 2 * j, idesc, true);
+          const uint32_t id = idesc_f16(128, 64 - 16 * j, false), d = tmem + kAU + 16 * j;
+          mma_f16_ts(d, tmem + kUhi + 8 * j, ah + kDown * j, id, j > 0);
+          mma_f16_ts(d, tmem + kUlo + 8 * j, ah + kDown * j, id, true);
+          mma_f16_ts(d, tmem + kUhi + 8 * j, al + kDown * j, id, true);
         }
         mma_commit(&s.o_done);
         mma_commit(&s.oempty[st]);
