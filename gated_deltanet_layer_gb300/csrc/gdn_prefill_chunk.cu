@@ -81,13 +81,21 @@ __device__ __forceinline__ int swz(int row, int col) { return row * 128 + ((((co
 
 __device__ __forceinline__ uint32_t pack_h2(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// y = hi + lo, two f16 each: hi is y cut to f16's 11 bits, so their difference is exact
-// and needs no conversion back.
+// y = hi + lo, two f16 each: hi is y rounded to f16's 11 bits, and what is left is exact, by
+// a multiply-add that takes the f16 itself. (An instruction in ten fewer than with y cut
+// and subtracted in f32: 13 sequences, 16384 tokens 411 -> 395 us.)
 __device__ __forceinline__ void split2(float2 y, uint32_t* hi, uint32_t* lo) {
-  const float2 h = make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffffe000u),
-                               __uint_as_float(__float_as_uint(y.y) & 0xffffe000u));
-  *hi = pack_h2(__float22half2_rn(h));
-  *lo = pack_h2(__float22half2_rn(__ffma2_rn(h, make_float2(-1.f, -1.f), y)));
+  const uint32_t h = pack_h2(__float22half2_rn(y));
+  float2 d;
+  asm("{\n\t.reg .b16 a, b, m;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "mov.b16 m, 0xBC00;\n\t"
+      "fma.rn.f32.f16 %0, a, m, %3;\n\t"
+      "fma.rn.f32.f16 %1, b, m, %4;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(h), "f"(y.x), "f"(y.y));
+  *hi = h;
+  *lo = pack_h2(__float22half2_rn(d));
 }
 
 // 16 columns (a multiple of 16 on) of a row of such an image: the swizzle keeps the two
