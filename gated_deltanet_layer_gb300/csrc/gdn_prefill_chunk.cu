@@ -618,11 +618,15 @@ struct ChainSmem {
 
 // silu(z) before a rounding to bf16: the fast exponential and division (a few 2^-22)
 // are far below it.
-__device__ __forceinline__ float gate(float z) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return z * r;
+__device__ __forceinline__ float2 gate(float2 z) {
+  const float2 t = __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return __fmul2_rn(z, r);
 }
 
 // 16 columns of a row of a state.
@@ -1158,20 +1162,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 #pragma unroll
         for (int k = 0; k < E; ++k) o[k] = *reinterpret_cast<const float4*>(o32 + t * D + 32 * k + l8);
         if (p.z) {
-          float sum = 0.f;
+          float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < E; ++k)
-            sum = fmaf(o[k].x, o[k].x, fmaf(o[k].y, o[k].y, fmaf(o[k].z, o[k].z, fmaf(o[k].w, o[k].w, sum))));
+          for (int k = 0; k < E; ++k) {
+            const float2 a = make_float2(o[k].x, o[k].y), b = make_float2(o[k].z, o[k].w);
+            ss = __ffma2_rn(a, a, __ffma2_rn(b, b, ss));
+          }
+          float sum = ss.x + ss.y;
 #pragma unroll
           for (int m = 4; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
           const float r = rsqrtf(sum * (1.0f / D) + p.gnorm_eps);
+          const float2 r2 = make_float2(r, r);
 #pragma unroll
           for (int k = 0; k < E; ++k) {
             const uint2 gw = __ldg(reinterpret_cast<const uint2*>(p.gnorm_w + 32 * k + l8));
-            o[k].x *= r * bf16_lo(gw.x) * gate(bf16_lo(z[i][k].x));
-            o[k].y *= r * bf16_hi(gw.x) * gate(bf16_hi(z[i][k].x));
-            o[k].z *= r * bf16_lo(gw.y) * gate(bf16_lo(z[i][k].y));
-            o[k].w *= r * bf16_hi(gw.y) * gate(bf16_hi(z[i][k].y));
+            const auto out = [&](float2 v, uint32_t g, uint32_t zz) {
+              const float2 w = __fmul2_rn(__fmul2_rn(v, r2), make_float2(bf16_lo(g), bf16_hi(g)));
+              return __fmul2_rn(w, gate(make_float2(bf16_lo(zz), bf16_hi(zz))));
+            };
+            const float2 a = out(make_float2(o[k].x, o[k].y), gw.x, z[i][k].x), b = out(make_float2(o[k].z, o[k].w), gw.y, z[i][k].y);
+            o[k] = make_float4(a.x, a.y, b.x, b.y);
           }
         }
         if (t < toks) {
