@@ -56,7 +56,7 @@ using namespace tc;
 constexpr float kScaleT = 4096.f;   // of T's f16 images
 // A chunk's images and scalars of a value head, arrays of 64 floats: what the state's
 // chain needs (T hi, T lo) and what the outputs need (causal products hi, lo).
-// S_R: of every two tokens beta, beta, beta c, beta c with c = e^G / |k|; S_CU:
+// S_R: of every two tokens beta, beta, c, c with c = e^G / |k|; S_CU:
 // e^(G_C-G) / |k|; S_END: see below.
 enum { S_R = 0, S_CU = 2, S_END, S_COUNT };
 enum { O_CQG, O_CQ, O_COUNT };
@@ -96,6 +96,18 @@ __device__ __forceinline__ void split2(float2 y, uint32_t* hi, uint32_t* lo) {
       : "r"(h), "f"(y.x), "f"(y.y));
   *hi = h;
   *lo = pack_h2(__float22half2_rn(d));
+}
+
+// v f + q for two bf16 v and a bf16 f.
+__device__ __forceinline__ float2 add_scaled(uint32_t v, uint16_t f, float2 q) {
+  float2 r;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, a, %3, %4;\n\t"
+      "fma.rn.f32.bf16 %1, b, %3, %5;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(v), "h"(f), "f"(q.x), "f"(q.y));
+  return r;
 }
 
 // 16 columns (a multiple of 16 on) of a row of such an image: the swizzle keeps the two
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       const float2 rn = *reinterpret_cast<const float2*>(&s.rn[2 * lane]), rq = *reinterpret_cast<const float2*>(&s.rn[64 + 2 * lane]);
       float* sc = reinterpret_cast<float*>(img + kImg);
       *reinterpret_cast<float4*>(sc + 64 * S_R + 4 * lane) =
-          make_float4(beta[0], beta[1], beta[0] * (gam[0] * rn.x), beta[1] * (gam[1] * rn.y));
+          make_float4(beta[0], beta[1], gam[0] * rn.x, gam[1] * rn.y);
       *reinterpret_cast<float2*>(sc + 64 * S_CU + 2 * lane) = make_float2(left[0] * rn.x, left[1] * rn.y);
       const float sum_b = warp_sum(beta[0] + beta[1]), sum_w = warp_sum(left[0] * beta[0] + left[1] * beta[1]);
       if (lane == 0) {
@@ -984,7 +996,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         v[j] = __bfloat16_as_ushort(g.v[tok0 + 2 * j][vrow]) | ((uint32_t)__bfloat16_as_ushort(g.v[tok0 + 2 * j + 1][vrow]) << 16);
-      const float2 f2 = make_float2(fu, fu), p2 = make_float2(-p_scale, -p_scale);
+      const float2 p2 = make_float2(-p_scale, -p_scale);
+      const uint16_t fu_bf16 = (uint16_t)(__float_as_uint(fu) >> 16);  // a power of two
       if (ok) ok = mbar_wait(&s.p_done, ph);
       tc_fence_after();
 #pragma unroll
@@ -996,9 +1009,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float4 rc = *reinterpret_cast<const float4*>(&g.scal[S_R][2 * (i + j)]);
-          const float2 vv = __fmul2_rn(make_float2(bf16_lo(v[8 * k + j / 2]), bf16_hi(v[8 * k + j / 2])), f2);
           const float2 q = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), make_float2(rc.z, rc.w));
-          const float2 r = __ffma2_rn(vv, make_float2(rc.x, rc.y), q);
+          const float2 r = __fmul2_rn(add_scaled(v[8 * k + j / 2], fu_bf16, q), make_float2(rc.x, rc.y));
           x[j] = r.x, x[j + 1] = r.y;
         }
         if (until < kChunk) {
