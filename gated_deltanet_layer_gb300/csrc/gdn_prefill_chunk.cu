@@ -914,8 +914,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     const auto scales = [&](int n) {
       const int st = in_stage(n), toks = min(kChunk, e - (b + n * kChunk));
       ChainIn<D>& g = s.in[st];
-      if (ok) ok = mbar_wait(&s.full[st], in_phase(n));
-      if (ok) ok = mbar_wait(&s.v_ready[st], in_phase(n));
+      if (ok) ok = mbar_wait(&s.v_ready[st], in_phase(n));  // after full[st]
       float4 k = s.scale[st];
       first_bad = kChunk;
       if (!s.finite_in[st]) {
