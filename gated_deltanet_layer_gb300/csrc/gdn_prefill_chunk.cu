@@ -448,9 +448,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
           x[j] = y0.x, x[j + 1] = y0.y, x[j + 2] = y1.x, x[j + 3] = y1.y;
         }
       }
+      if (j0 + 16 > (i & 32)) {  // the warp's rows cross the diagonal here
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j0 + j >= until) x[j] = 0.f;
+        for (int j = 0; j < 16; ++j)
+          if (j0 + j >= until) x[j] = 0.f;
+      }
     };
     const int last = i & 32 ? 64 : 32;  // this warp's rows end before this column
     if (lower) {
