@@ -11,7 +11,7 @@
 // care in the main loop: what is outside either matrix is zero in both operands.
 //
 // Measured (us): 8192 x 20480 x 8192 1376 by itself (2.0 PFLOP/s, 104% of the measured
-// library product) and 1674 back to back, where the power limit holds the clock down;
+// library product) and 1584 to 1674 back to back, where the power limit holds the clock down;
 // 4100 x 8192 x 1024 with a residual 61, of which 36 are the products and 24 the bytes:
 // 17 x 32 tiles on 76 pairs leave 8 rounds for 7.2, and each pair reads 1 MB of tiles
 // from L2 in the 7 us it has for a round; 5 x 2560 x 8192 8.0 in a graph, the weights'

@@ -8,9 +8,9 @@ namespace gdn {
 
 constexpr int kChunk = 64;  // tokens of one chunk of a sequence
 // Longest sequence that the delta rule takes token by token. The two forms take the same
-// time at 14 to 18 tokens (us, token by token / in chunks, for 64 requests of the full
-// layer 178.7 / 474.5 at 4, 426.2 / 482.8 at 12, 549.7 / 484.4 at 16; for 8 requests of a
-// shard 9.5 / 32.7, 21.4 / 32.6, 27.4 / 32.6 and 39.2 / 32.7 at 24).
+// time at 12 to 18 tokens (us, token by token / in chunks, for 64 requests of the full
+// layer 178.7 / 429.7 at 4, 426.2 / 439.3 at 12, 549.7 / 441.4 at 16; for 8 requests of a
+// shard 9.5 / 30.0, 21.3 / 30.0, 27.3 / 29.9 and 39.4 / 30.0 at 24).
 constexpr int kRecurrentMax = 14;
 // Up to this many sequences the chunked form starts the longest ones first, where they
 // take more than one wave; with more of them the waves level out by themselves.
