@@ -627,7 +627,7 @@ struct ChainSmem {
   float4 scale[kIn];
   int finite_in[kIn];
   uint64_t full[kIn], empty[kIn], v_ready[kIn], ofull[2], oempty[2], s_ready[2], s_done[2];
-  uint64_t p_done, r_ready, u_done, u_ready, o_done, o_free, row_ready;
+  uint64_t p_done, r_ready, u_done, u_ready, o_done, o_free, row_ready, state_in, state_read;
   uint32_t tmem;
 };
 
@@ -644,13 +644,19 @@ __device__ __forceinline__ float2 gate(float2 z) {
   return __fmul2_rn(z, r);
 }
 
-// 16 columns of a row of a state.
+// A state passes through shared memory on its way in (where the outputs' inputs come
+// later) and out (where the chain's were): a thread's row at a time from global memory, the
+// two took 7 us a CTA. Rows 16 bytes further apart than they are long: no bank conflicts.
+template <int D, bool BF16>
+constexpr int state_row() { return D * (BF16 ? 2 : 4) + 16; }
+
+// 16 columns of a row of a state in shared memory.
 template <bool BF16>
-__device__ __forceinline__ void state16(const void* base, size_t at, float (&x)[16]) {
+__device__ __forceinline__ void state16(const unsigned char* row, int col, float (&x)[16]) {
   if constexpr (BF16) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at + 8 * j);
+      const uint4 v = *reinterpret_cast<const uint4*>(row + 2 * col + 16 * j);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[8 * j + 2 * k] = bf16_lo(w[k]), x[8 * j + 2 * k + 1] = bf16_hi(w[k]);
@@ -658,7 +664,7 @@ __device__ __forceinline__ void state16(const void* base, size_t at, float (&x)[
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + 4 * j);
+      const float4 v = *reinterpret_cast<const float4*>(row + 4 * col + 16 * j);
       x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
     }
   }
@@ -696,6 +702,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     mbar_init(&s.o_done, 1);
     mbar_init(&s.o_free, 8);
     mbar_init(&s.row_ready, 4);
+    mbar_init(&s.state_in, 1);
+    mbar_init(&s.state_read, 8);
     fence_mbar_init();
   }
   if (warp == 2) tmem_alloc(&s.tmem, 512);
@@ -704,6 +712,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   tc_fence_after();
   const uint32_t tmem = s.tmem;
   bool ok = true;
+  constexpr int kRow = state_row<D, BF16>(), kRowData = kRow - 16;
+  static_assert(D * kRow <= sizeof(s.oin) && D * kRow <= sizeof(s.in), "a state passes through these");
 
   if (warp == 0) {
     for (int n = 0; n < chunks; ++n) {
@@ -728,6 +738,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     for (int n = max(0, chunks - kIn); n < chunks; ++n)
       if (ok) ok = mbar_wait(&s.full[in_stage(n)], in_phase(n));
   } else if (warp == 2) {
+    if (in > 0) {
+      if (lane == 0) mbar_arrive_expect_tx(&s.state_in, D * kRowData);
+      __syncwarp();
+      const unsigned char* src = static_cast<const unsigned char*>(p.state) + ((size_t)in * p.Hv + h) * D * kRowData;
+      for (int r = lane; r < D; r += 32)
+        bulk_load(reinterpret_cast<unsigned char*>(s.oin) + r * kRow, src + r * kRowData, kRowData, &s.state_in);
+      ok = mbar_wait(&s.state_read, 0);
+      ok = __all_sync(0xffffffffu, ok);
+    }
     // what the outputs need, with a wait of its own: the outputs may lag behind the chain
     for (int n = 0; n < chunks; ++n) {
       const int st = n & 1;
@@ -882,18 +901,21 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     float bound, fs;
     bool dead;  // the row holds a value that is not finite
     {
-      // this thread's half of the row, all its loads under way at once
-      const size_t at = (((size_t)max(in, 0) * p.Hv + h) * D + vrow) * D + col0;
+      // this thread's half of the row
       float x[D / 32][16] = {};
       float zero = 0.f, mx = 0.f;
+      if (in > 0) ok = mbar_wait(&s.state_in, 0);
       if (real && in > 0) {
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) state16<BF16>(p.state, at + 16 * k, x[k]);
+        for (int k = 0; k < D / 32; ++k)
+          state16<BF16>(reinterpret_cast<const unsigned char*>(s.oin) + row * kRow, col0 + 16 * k, x[k]);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
 #pragma unroll
           for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(x[k][j])), zero += x[k][j] * 0.f;
       }
+      __syncwarp();
+      if (in > 0 && lane == 0) mbar_arrive(&s.state_read);
       s.part[half][row] = zero == 0.f ? mx : __int_as_float(0x7fffffff);
       asm volatile("bar.sync 2, 256;" ::: "memory");
       const float a = s.part[0][row], o = s.part[1][row];
@@ -1081,30 +1103,37 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
         if (half == 0) mbar_arrive(&s.row_ready);
       }
     }
-    // the state after the last chunk
-    if (ok) ok = mbar_wait(&s.s_done[half], (chunks - 1) & 1);
+    // the state after the last chunk, through the room of the chain's inputs: every MMA that
+    // reads them is done
+    if (ok) ok = mbar_wait(&s.s_done[1], (chunks - 1) & 1);
     tc_fence_after();
     const float nan = __int_as_float(0x7fffffff), inv = inverse_pow2(fs);
+    constexpr int kHalf = kRowData / 2;  // bytes of this thread's half of the row
+    unsigned char* mine = reinterpret_cast<unsigned char*>(s.in) + row * kRow + half * kHalf;
 #pragma unroll 1
-    for (int col = col0; col < col0 + D / 2; col += 16) {
+    for (int c = 0; c < D / 2; c += 16) {
       float x[16];
-      tmem_ld16(tmem + kS + col + lanes, x);
+      tmem_ld16(tmem + kS + col0 + c + lanes, x);
       if (!real || !ok) continue;
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] = dead ? nan : x[j] * inv;
-      const size_t at = (((size_t)out * p.Hv + h) * D + row) * D + col;
       if constexpr (BF16) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.state) + at + 8 * j) =
+          *reinterpret_cast<uint4*>(mine + 2 * c + 16 * j) =
               make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
                          pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7]));
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(static_cast<float*>(p.state) + at + 4 * j) =
-              make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+          *reinterpret_cast<float4*>(mine + 4 * c + 16 * j) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
       }
+    }
+    if (real && ok) {
+      fence_proxy_async_smem();
+      bulk_store(static_cast<unsigned char*>(p.state) + (((size_t)out * p.Hv + h) * D + row) * kRowData + half * kHalf, mine, kHalf);
+      bulk_commit();
+      bulk_wait_all();
     }
   } else if (warp >= 12) {
     // ---- the outputs
