@@ -8,9 +8,10 @@ namespace gdn {
 
 constexpr int kChunk = 64;  // tokens of one chunk of a sequence
 // Longest sequence that the delta rule takes token by token. The two forms take the same
-// time at 12 to 18 tokens (us, token by token / in chunks, for 64 requests of the full
-// layer 178.7 / 429.7 at 4, 426.2 / 439.3 at 12, 549.7 / 441.4 at 16; for 8 requests of a
-// shard 9.5 / 30.0, 21.3 / 30.0, 27.3 / 29.9 and 39.4 / 30.0 at 24).
+// time at 11 tokens (many requests of many heads) to 18 (few) (us, token by token / in
+// chunks, for 64 requests of the full layer 302.5 / 388.2 at 8, 426.4 / 390.6 at 12, 550.0 /
+// 391.3 at 16; for 8 requests of a shard 15.4 / 29.1, 21.4 / 29.0, 27.3 / 28.9 and 33.2 /
+// 29.2 at 20).
 constexpr int kRecurrentMax = 14;
 // Up to this many sequences the chunked form starts the longest ones first, where they
 // take more than one wave; with more of them the waves level out by themselves.

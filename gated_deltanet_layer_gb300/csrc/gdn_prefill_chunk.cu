@@ -29,11 +29,11 @@
 // with the largest |v| of the head's chunk for every |v|, and a row's norm measured every
 // eighth chunk; |T| <= 1 takes the constant 2^12. Two terms reach 2^-39 of such a bound.
 //
-// What bounds it. One chunk follows the other: a sequence's chunk takes 3.3 us (2916
-// tokens on one rank's shard: 160 us for 46), of which the three dependent products are
+// What bounds it. One chunk follows the other: a sequence's chunk takes 3.2 us (2916
+// tokens on one rank's shard: 153 us for 46), of which the three dependent products are
 // about 0.9 and the conversions of S, R and U to f16 between them the rest; the tensor
-// pipe is 28% busy, an SM issues every second cycle. A CTA's start and end take 11 us
-// beside its chunks. 13 sequences of 16384 tokens on 64 heads take 373 us, 16700 chunks on
+// pipe is 30% busy, an SM issues every second cycle. A CTA's start and end take 9 us
+// beside its chunks. 13 sequences of 16384 tokens on 64 heads take 353 us, 16700 chunks on
 // 152 SMs. prepare_kernel takes 29 us for one round of CTAs and 291 for those 16384
 // tokens; it is bound by its instructions (an SM issues 46% of its slots) between short
 // steps that wait for one another.
