@@ -315,8 +315,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
     for (int j = 0; j < 4; ++j) h[j] = pack_h2(__floats2half2_rn(f[2 * j] * down, f[2 * j + 1] * down));
     *reinterpret_cast<uint4*>(s.kq[col >> 6] + swz(row, col & 63)) = make_uint4(h[0], h[1], h[2], h[3]);
     if (lane % kLanes == 0) {
-      s.rn[row] = up / sqrtf(ss + p.l2_eps);
-      if (row < 64) s.bad[row] = !finite(mx) || ss != ss;
+      // Without an l2_eps a zero row has no norm: a key's token is then one that is not
+      // finite. Rows past the last token are zeros of nobody's.
+      const float rn = (row & 63) < n ? up / sqrtf(ss + p.l2_eps) : 0.f;
+      s.rn[row] = rn;
+      if (row < 64) s.bad[row] = !finite(mx) || ss != ss || !finite(rn);
     }
   }
   fence_proxy_async_smem();
