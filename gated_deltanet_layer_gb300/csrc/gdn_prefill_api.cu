@@ -15,8 +15,16 @@ struct gdn_prefill {
 
 namespace {
 
-constexpr size_t kErrorBytes = 256;                     // the error word, on lines of its own
-constexpr size_t kHeadBytes = kErrorBytes + kSorted * 4;  // and the sequences' order
+// The workspace: the error word, on lines of its own; the sequences' order; what the chunked
+// form has to do; the tables of the conv's and the delta rule's offsets, where there can be
+// more sequences than are scanned; then the chunks.
+constexpr size_t kErrorBytes = 256;
+constexpr size_t kOrderBytes = kSorted * 4;
+size_t table_bytes(const gdn_prefill_config& c) {
+  return c.max_seqs > kScanned ? ((size_t)(c.max_seqs + 1) * 4 + 255) / 256 * 256 : 0;
+}
+size_t plan_bytes(const gdn_prefill_config& c) { return ((size_t)c.max_seqs * 16 + 255) / 256 * 256; }
+size_t head_bytes(const gdn_prefill_config& c) { return kErrorBytes + kOrderBytes + plan_bytes(c) + 2 * table_bytes(c); }
 
 gdn_status validate(const gdn_prefill_config* c) {
   if (!c) return GDN_ERR_ARG;
@@ -67,16 +75,44 @@ gdn_status check_ragged(const gdn_prefill* h, int32_t seqs, int32_t tokens, cons
   return GDN_OK;
 }
 
+// which: the table, 0 the conv's, 1 the delta rule's
 Ragged ragged(const gdn_prefill* h, int32_t seqs, int32_t tokens, int32_t max_len, const int32_t* cu, const int32_t* in,
-              const int32_t* out) {
-  return Ragged{cu, in, out, seqs, tokens, h->cfg.num_slots, max_len, reinterpret_cast<unsigned int*>(h->ws)};
+              const int32_t* out, int which) {
+  int* table = reinterpret_cast<int*>(h->ws + kErrorBytes + kOrderBytes + plan_bytes(h->cfg) + which * table_bytes(h->cfg));
+  return Ragged{cu,   in, out, seqs, tokens, h->cfg.num_slots, max_len, reinterpret_cast<unsigned int*>(h->ws),
+                seqs > kScanned ? table : nullptr};
+}
+
+// The table of the offsets (see seq_rows): a running maximum, 1024 sequences at a time.
+__global__ void __launch_bounds__(1024) offsets_kernel(const Ragged r) {
+  griddep_launch_dependents();
+  __shared__ int tops[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int before = 0;
+  for (int i0 = 0, k = 0; i0 <= r.seqs; i0 += 1024, k ^= 1) {
+    const int i = i0 + threadIdx.x;
+    int m = max(i > 0 && i <= r.seqs ? offset_inside(r, __ldg(r.cu + i)) : 0, before);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = max(m, __shfl_up_sync(0xffffffffu, m, o));
+    if (lane == 31) tops[k][warp] = m;
+    __syncthreads();  // two buffers: one barrier a turn is enough
+    const int top = tops[k][lane];
+    m = max(m, __reduce_max_sync(0xffffffffu, lane < warp ? top : 0));
+    before = __reduce_max_sync(0xffffffffu, top);
+    if (i <= r.seqs) r.table[i] = m;
+  }
 }
 
 }  // namespace
 
+cudaError_t gdn::launch_offsets(const Ragged& r, cudaStream_t s) {
+  offsets_kernel<<<1, 1024, 0, s>>>(r);
+  return cudaGetLastError();
+}
+
 extern "C" size_t gdn_prefill_workspace_bytes(const gdn_prefill_config* cfg) {
   if (validate(cfg) != GDN_OK) return 0;
-  return kHeadBytes + delta_chunk_bytes(cfg->max_tokens, cfg->max_seqs, cfg->num_k_heads, cfg->num_v_heads, cfg->head_k_dim);
+  return head_bytes(*cfg) + delta_chunk_bytes(cfg->max_tokens, cfg->max_seqs, cfg->num_k_heads, cfg->num_v_heads, cfg->head_k_dim);
 }
 
 extern "C" gdn_status gdn_prefill_create(const gdn_prefill_config* cfg, void* workspace, size_t workspace_bytes,
@@ -111,7 +147,7 @@ extern "C" gdn_status gdn_prefill_conv(gdn_prefill_t* h, int32_t seqs, int32_t t
   if (overlaps_any(o, in) || overlap(o, state) || overlaps_any(state, in)) return GDN_ERR_ARG;
   if (seqs == 0 && tokens == 0) return GDN_OK;
   ConvParams p{};
-  p.r = ragged(h, seqs, tokens, tokens, cu_seqlens, state_in, state_out);
+  p.r = ragged(h, seqs, tokens, tokens, cu_seqlens, state_in, state_out, 0);
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.ldx = ldx;
   p.w = static_cast<const __nv_bfloat16*>(conv_w);
@@ -148,7 +184,7 @@ extern "C" gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t 
   if (overlaps_any(o, in) || overlap(o, state) || overlaps_any(state, in)) return GDN_ERR_ARG;
   if (seqs == 0 && tokens == 0) return GDN_OK;
   DeltaParams p{};
-  p.r = ragged(h, seqs, tokens, max_len, cu_seqlens, state_in, state_out);
+  p.r = ragged(h, seqs, tokens, max_len, cu_seqlens, state_in, state_out, 1);
   p.Hk = c.num_k_heads;
   p.Hv = Hv;
   p.group = Hv / c.num_k_heads;
@@ -168,7 +204,8 @@ extern "C" gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t 
   p.l2_eps = c.l2_eps;
   p.q_scale = c.q_scale;
   p.order = seqs <= kSorted && (long long)seqs * Hv > 152 ? reinterpret_cast<int*>(h->ws + kErrorBytes) : nullptr;
-  return cuda_status(launch_delta(p, c.head_k_dim, c.ssm_dtype == GDN_STATE_BF16, h->ws + kHeadBytes,
+  p.plan = reinterpret_cast<int4*>(h->ws + kErrorBytes + kOrderBytes);
+  return cuda_status(launch_delta(p, c.head_k_dim, c.ssm_dtype == GDN_STATE_BF16, h->ws + head_bytes(c),
                                   (cudaStream_t)stream));
 }
 

@@ -249,11 +249,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
   extern __shared__ unsigned char raw[];
   PrepSmem<D>& s = *reinterpret_cast<PrepSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int place = blockIdx.x / p.Hk, kh = blockIdx.x % p.Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int sq = chunk_seq(p.r, place);
-  int b, e, in, out;
-  seq_rows(p.r, sq, &b, &e);
-  const int t0 = b + (place - chunk_first_place(p.r, sq)) * kChunk, n = min(kChunk, e - t0);
-  if (n <= 0 || e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) {
+  int b, e;
+  const int sq = chunk_seq(p.r, place, &b, &e);
+  const int t0 = b + (place - chunk_first_place(sq, b)) * kChunk, n = min(kChunk, e - t0);
+  if (n <= 0 || e - b <= kRecurrentMax || !seq_live(p.r, sq, seq_in(p.r, sq), b, e, false)) {
     griddep_wait();
     return;
   }
@@ -682,10 +681,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   griddep_wait();
   const int h = blockIdx.x, kh = h / p.group;
   const int sq = p.order ? __ldcg(p.order + blockIdx.y) : blockIdx.y;
-  int b, e, in, out;
-  seq_rows(p.r, sq, &b, &e);
-  if (e - b <= kRecurrentMax || !seq_slots(p.r, sq, false, &in, &out)) return;
-  const int chunks = (e - b + kChunk - 1) / kChunk, place0 = chunk_first_place(p.r, sq);
+  // four loads: of one of 16 bytes the parts had no uniform registers, and the spills took 3%
+  const int* plan = reinterpret_cast<const int*>(p.plan + sq);
+  const int b = __ldcg(plan), e = __ldcg(plan + 1), in = __ldcg(plan + 2), out = __ldcg(plan + 3);
+  if (e <= b) return;
+  const int chunks = (e - b + kChunk - 1) / kChunk, place0 = chunk_first_place(sq, b);
   if (tid == 0) {
     for (int i = 0; i < kIn; ++i) {
       mbar_init(&s.full[i], 1);
@@ -1271,23 +1271,11 @@ cudaError_t launch(const ChunkParams& c, cudaStream_t s) {
   if (e == cudaSuccess) e = opt_in<delta_kernel<D, BF16>>(chain);
   if (e != cudaSuccess) return e;
   const dim3 places((unsigned)(chunk_places(c.p.r.tokens, c.p.r.seqs) - 1) * c.p.Hk);  // the last is the pad rows'
-  // Each may start while the kernel before it ends (programmatic stream serialisation).
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cfg.gridDim = places;
-  cfg.blockDim = dim3(kPrepThreads);
-  cfg.dynamicSmemBytes = prep;
-  e = cudaLaunchKernelEx(&cfg, prepare_kernel<D>, c);
+  // Each may start while the kernel before it ends.
+  const Launch first(places, kPrepThreads, prep, true, s), second(dim3(c.p.Hv, c.p.r.seqs), kChainThreads, chain, true, s);
+  e = cudaLaunchKernelEx(&first.cfg, prepare_kernel<D>, c);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(c.p.Hv, c.p.r.seqs);
-  cfg.blockDim = dim3(kChainThreads);
-  cfg.dynamicSmemBytes = chain;
-  return cudaLaunchKernelEx(&cfg, delta_kernel<D, BF16>, c);
+  return cudaLaunchKernelEx(&second.cfg, delta_kernel<D, BF16>, c);
 }
 
 }  // namespace

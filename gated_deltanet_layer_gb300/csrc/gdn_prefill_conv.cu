@@ -47,12 +47,13 @@ __device__ __forceinline__ uint32_t silu2(float2 y) {
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) {
   extern __shared__ __align__(128) unsigned char rows[];  // [24][2048]
   __shared__ uint64_t full[kRuns];
+  griddep_wait();  // for the table of the offsets
   const int place = blockIdx.x;
-  const int s = chunk_seq(p.r, place);
-  int b, e, in = 0, out = 0;
-  seq_rows(p.r, s, &b, &e);
-  const int j = place - chunk_first_place(p.r, s);
-  const bool live = seq_slots(p.r, s, j == 0 && blockIdx.y == 0 && threadIdx.x == 0, &in, &out);
+  int b, e;
+  const int s = chunk_seq(p.r, place, &b, &e);
+  const int j = place - chunk_first_place(s, b);
+  const SeqIn seq = seq_in(p.r, s);
+  const bool live = seq_live(p.r, s, seq, b, e, j == 0 && blockIdx.y == 0 && threadIdx.x == 0);
   const int t0 = b + j * kChunk, t1 = min(t0 + kChunk, e);
   const int c0 = blockIdx.y * kConvThreads * 8, c = c0 + threadIdx.x * 8;
   // A place past the sequence's last chunk has no rows, and none before it to
@@ -104,8 +105,8 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) 
   } else if (j > 0) {
 #pragma unroll
     for (int k = 0; k < 3; ++k) h[k] = __ldg(reinterpret_cast<const uint4*>(x + (long long)(t0 - 3 + k) * p.ldx));
-  } else if (in > 0) {
-    const uint4* sp = reinterpret_cast<const uint4*>(p.state + ((size_t)in * p.C + c) * 3);
+  } else if (seq.in > 0) {
+    const uint4* sp = reinterpret_cast<const uint4*>(p.state + ((size_t)seq.in * p.C + c) * 3);
     __align__(16) uint16_t raw[24];
 #pragma unroll
     for (int i = 0; i < 3; ++i) reinterpret_cast<uint4*>(raw)[i] = sp[i];
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) 
         raw[6 * i + 3 + k] = (uint16_t)(v[i] >> 16);
       }
     }
-    uint4* sp = reinterpret_cast<uint4*>(p.state + ((size_t)out * p.C + c) * 3);
+    uint4* sp = reinterpret_cast<uint4*>(p.state + ((size_t)seq.out * p.C + c) * 3);
 #pragma unroll
     for (int i = 0; i < 3; ++i) sp[i] = reinterpret_cast<const uint4*>(raw)[i];
   }
@@ -189,8 +190,9 @@ cudaError_t launch_conv(const ConvParams& p, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   const dim3 grid(chunk_places(p.r.tokens, p.r.seqs), (p.C / 8 + kConvThreads - 1) / kConvThreads);
-  conv_kernel<<<grid, kConvThreads, kConvSmem, s>>>(p);
-  return cudaGetLastError();
+  if (p.r.table && (e = launch_offsets(p.r, s)) != cudaSuccess) return e;
+  const Launch l(grid, kConvThreads, kConvSmem, p.r.table != nullptr, s);
+  return cudaLaunchKernelEx(&l.cfg, conv_kernel, p);
 }
 
 }  // namespace gdn

@@ -89,22 +89,22 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
   constexpr int E = D / 32, W = D / 32;
   __shared__ float red[2][W];
-  griddep_launch_dependents();  // the chunked form's first kernel touches nothing of this one's
+  griddep_wait();               // for the table of the offsets, which the chunked form's first kernel reads as well
+  griddep_launch_dependents();  // that kernel touches nothing of this one's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s = blockIdx.x, h = blockIdx.y;
-  int b, e, in = 0, out = 0;
-  seq_rows(p.r, s, &b, &e);
-  const bool live = seq_slots(p.r, s, h == 0 && threadIdx.x == 0, &in, &out);
+  const SeqIn seq = seq_in(p.r, s);
+  int b, e;
+  seq_rows(p.r, s, seq, &b, &e);
+  const bool live = seq_live(p.r, s, seq, b, e, h == 0 && threadIdx.x == 0);
+  if (h == 0 && threadIdx.x == 0 && s < p.r.seqs && p.plan)
+    p.plan[s] = make_int4(b, live && e - b > kRecurrentMax ? e : b, seq.in, seq.out);
   if (live && e - b > kRecurrentMax) return;  // the chunked form's
   const int row = threadIdx.x;  // the dv row this lane finishes
   if (p.order && s == p.r.seqs && h == 0) {
-    // the sequences' order for the chunked form, longest first
-    __shared__ int len[kSorted];
-    for (int i = row; i < s; i += D) {
-      int lo, hi;
-      seq_rows(p.r, i, &lo, &hi);
-      len[i] = hi - lo;
-    }
+    // the sequences' order for the chunked form, longest first (bad offsets: any order)
+    __shared__ unsigned len[kSorted];
+    for (int i = row; i < s; i += D) len[i] = (unsigned)__ldg(p.r.cu + i + 1) - (unsigned)__ldg(p.r.cu + i);
     __syncthreads();
     for (int i = row; i < s; i += D) {
       int rank = 0;
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
   }
   const int kh = h / p.group;
   float S[32][E] = {};
-  if (in > 0) {
-    const size_t at = (((size_t)in * p.Hv + h) * D + warp * 32) * D + lane * E;
+  if (seq.in > 0) {
+    const size_t at = (((size_t)seq.in * p.Hv + h) * D + warp * 32) * D + lane * E;
 #pragma unroll
     for (int i = 0; i < 32; ++i) load_state<E, BF16>(p.state, at + (size_t)i * D, S[i]);
   }
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
     }
     p.out[(long long)t * p.ldo + h * D + row] = __float2bfloat16_rn(o);
   }
-  const size_t at = (((size_t)out * p.Hv + h) * D + warp * 32) * D + lane * E;
+  const size_t at = (((size_t)seq.out * p.Hv + h) * D + warp * 32) * D + lane * E;
 #pragma unroll
   for (int i = 0; i < 32; ++i) store_state<E, BF16>(p.state, at + (size_t)i * D, S[i]);
 }
@@ -184,18 +184,22 @@ __global__ void __launch_bounds__(D) recurrent_kernel(const DeltaParams p) {
 template <int D>
 cudaError_t launch_d(const DeltaParams& p, bool state_bf16, cudaStream_t s) {
   const dim3 grid(p.r.seqs + 1, p.Hv);  // the last sequence is the pad rows
-  if (state_bf16)
-    recurrent_kernel<D, true><<<grid, D, 0, s>>>(p);
-  else
-    recurrent_kernel<D, false><<<grid, D, 0, s>>>(p);
-  return cudaGetLastError();
+  if (p.r.table) {
+    const cudaError_t e = launch_offsets(p.r, s);
+    if (e != cudaSuccess) return e;
+  }
+  const Launch l(grid, D, 0, p.r.table != nullptr, s);
+  return cudaLaunchKernelEx(&l.cfg, state_bf16 ? recurrent_kernel<D, true> : recurrent_kernel<D, false>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_delta(const DeltaParams& p, int d, bool state_bf16, unsigned char* ws, cudaStream_t s) {
+cudaError_t launch_delta(const DeltaParams& whole, int d, bool state_bf16, unsigned char* ws, cudaStream_t s) {
+  DeltaParams p = whole;
+  const bool chunks = p.r.seqs > 0 && std::min(p.r.max_len, p.r.tokens) > kRecurrentMax;
+  if (!chunks) p.order = nullptr, p.plan = nullptr;
   const cudaError_t e = d == 128 ? launch_d<128>(p, state_bf16, s) : launch_d<64>(p, state_bf16, s);
-  if (e != cudaSuccess || p.r.seqs == 0 || std::min(p.r.max_len, p.r.tokens) <= kRecurrentMax) return e;
+  if (e != cudaSuccess || !chunks) return e;
   return launch_delta_chunks(p, d, state_bf16, ws, s);
 }
 

@@ -61,7 +61,7 @@ typedef struct gdn_prefill gdn_prefill_t;
 /* Device bytes of the workspace for this config; 0 if the config is invalid
  * or unsupported. It holds what a call prepares for every chunk of 64 tokens
  * (34 KB a value head and 256 x dk bytes a key head): 41 KB a token with 64
- * value and 16 key heads of 128. */
+ * value and 16 key heads of 128; and up to 24 bytes a sequence. */
 size_t gdn_prefill_workspace_bytes(const gdn_prefill_config* cfg);
 
 /* Validate the config, bind the caller's workspace (256-byte aligned device
@@ -101,7 +101,8 @@ gdn_status gdn_prefill_conv(gdn_prefill_t* h, int32_t seqs, int32_t tokens, cons
  * f32 or bf16; core_out [tokens][ldcore >= Hv*dv] bf16. ldqkv, ldz and ldcore
  * are multiples of 8, the pointers of qkv, z, core_out, gated_norm_w and
  * ssm_state 16-byte aligned. core_out must overlap no input. One call at a time per handle
- * (its calls share the workspace). */
+ * (its calls share the workspace; so do calls of gdn_prefill_conv with more than
+ * 128 sequences among themselves). */
 gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t tokens, int32_t max_len,
                              const void* qkv, int64_t ldqkv, const void* z, int64_t ldz, const void* ba,
                              int64_t ldba, const float* A_log, const void* dt_bias,
@@ -114,7 +115,11 @@ gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t tokens, int
  * 31..24 status, 23..16 what (1 a state slot >= num_slots, 2 cu_seqlens not from
  * 0 on, out of order or past `tokens`, 3 a sequence longer than max_len, 4 a wait inside
  * the kernel that passed its limit), 15..0 the sequence. A sequence with an
- * index error is treated as padding; the others are not affected. */
+ * index error is treated as padding; the others are not affected. Offsets that
+ * lie outside the rows concern the two sequences that they bound alone. After
+ * an offset that goes back, every sequence that starts before the largest
+ * offset so far would have rows of an earlier one: it is padding as well, and
+ * the sequence whose end went back is the one recorded. */
 gdn_status gdn_prefill_check(gdn_prefill_t* h, void* stream, uint32_t* detail);
 
 /* Clear the error word on `stream`. */

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_deltanet_layer_gb300 import GdnPrefill
+from gated_deltanet_layer_gb300 import GdnPrefill, _native, workloads as WL
 import prefill_harness as P
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +69,92 @@ def test_delta_of_a_zero_row_without_l2_eps(what, n, at):
         for head in range(sh.num_v_heads):
             if np.isfinite(ref[head]).all():
                 assert np.linalg.norm(state[head] - ref[head]) <= 2e-5 * norm[s][head]
+
+
+# ------------------------------------------------------------------ offsets that are not in order
+
+LINE = WL.LayerShape("line", hidden=64, num_k_heads=1, num_v_heads=1, head_k_dim=64, head_v_dim=64, num_slots=10010)
+EVEN = [100 * s for s in range(41)]
+
+
+def _with(offsets, at, value):
+    return offsets[:at] + [value] + offsets[at + 1:]
+
+
+def _long():
+    n = np.random.default_rng(33).choice([0, 1, 1, 2, 20, 70], 5000)
+    return np.concatenate([[0], np.cumsum(n)]).tolist()
+
+
+# offsets, rows, sequences that stay as they are, sequences that are to blame
+OFFSETS = {
+    "goes back over a chunk": ([0, 130, 5, 200], 200, [0], [1]),
+    "goes back by one token": ([0, 130, 129, 200], 200, [0], [1]),
+    "owns no chunk place": ([0, 70, 4, 80], 80, [0], [1]),
+    "past the rows": ([0, 10, 5000, 60, 70], 100, [0, 3], [1, 2]),
+    "past the rows, chunks": ([0, 100, 5000, 300, 430], 450, [0, 3], [1, 2]),
+    "the last": ([0, 70, 140, 0], 150, [0, 1], [2]),
+    "the first": ([3, 70, 140], 150, [1], [0]),
+    "the first below 0": ([-3, 70, 140], 150, [1], [0]),
+    "all": ([-5, 300, 7, 2 ** 31 - 1, -2 ** 31], 120, [], [0, 1, 2, 3]),
+    "one of 40, past": (_with(EVEN, 4, 4001), 4000, [s for s in range(40) if s not in (3, 4)], [3, 4]),
+    "one of 40, far past": (_with(EVEN, 31, 2 ** 31 - 1), 4000, [s for s in range(40) if s not in (30, 31)], [30, 31]),
+    "one of 40, below 0": (_with(EVEN, 33, -1), 4000, [s for s in range(40) if s not in (32, 33)], [32, 33]),
+    # the nineteenth's rows reach over those of the fifteen that follow
+    "one of 40, too far": (_with(EVEN, 20, 3500), 4000, [*range(20), *range(35, 40)], [20]),
+    "one of 128": (_with([20 * s for s in range(129)], 64, 5), 2600, [s for s in range(128) if s not in (63, 64)], [63]),
+    "the last but one of 128": (_with([20 * s for s in range(129)], 127, 2580), 2600, list(range(127)), [127]),
+    "one of 129": (_with([20 * s for s in range(130)], 65, 2601), 2600, [s for s in range(129) if s not in (64, 65)], [64, 65]),
+    "one of 5000": (_with(_long(), 777, 5), None, [s for s in range(5000) if s not in (776, 777)], [776]),
+    "none of 5000": (_long(), None, list(range(5000)), []),
+}
+
+
+def _bad_batch(name):
+    """A batch with these offsets. The sequences that they make padding have slots all the
+    same, which are not to be touched; rows that no other sequence owns hold NaN."""
+    cu, T, good, blamed = OFFSETS[name]
+    S = len(cu) - 1
+    T = T if T is not None else max(cu) + 9
+    b = P.Batch(LINE if S > 100 else P.SMALL.with_(num_slots=2 * S + 4), [T] + [0] * (S - 1), 34)
+    b.cu = np.array(cu, np.int64)
+    b.lens = [cu[s + 1] - cu[s] if s in set(good) else 0 for s in range(S)]
+    b.dcu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    owned = np.zeros(T, bool)
+    for s in good:
+        owned[cu[s]:cu[s + 1]] = True
+    for t in (b.dx, b.dz, b.dba):
+        t[torch.from_numpy(~owned).cuda()] = float("nan")
+    b.last = np.where(np.isin(np.arange(S), good), b.last, 0)  # of the references; b.dlast keeps the slots
+    h = handle(b)
+    h.workspace[4096:] = 255  # nothing that an earlier call may have left
+    return b, h, blamed
+
+
+def _check_blame(h, blamed):
+    status, word = h.check()
+    if not blamed:
+        assert status == 0
+    else:
+        assert status == _native.GDN_ERR_INDEX and word >> 16 == (5 << 8 | 2) and word & 0xffff in blamed
+
+
+@pytest.mark.parametrize("name", OFFSETS)
+def test_conv_of_bad_offsets(name):
+    b, h, blamed = _bad_batch(name)
+    out = torch.full_like(b.dx, float("nan"))
+    h.conv(b.dx, b.dw, b.dcu, b.dfirst, b.dlast, b.dconv, out=out)
+    _check_blame(h, blamed)
+    want, scale, pool = P.conv_reference(b)
+    got = P.f64(out)
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * scale).all()
+    np.testing.assert_array_equal(P.f64(b.dconv), pool)
+
+
+@pytest.mark.parametrize("name", OFFSETS)
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+def test_delta_of_bad_offsets(name, gated):
+    b, h, blamed = _bad_batch(name)
+    core = delta(h, b, gated, out=torch.full_like(b.dz, float("nan")))
+    _check_blame(h, blamed)
+    P.check_delta(b, core, gated)
