@@ -26,8 +26,9 @@
 // row by more than beta |v|, so over a chunk
 //   |S'| <= e^(G_C) |S0| + sum_j e^(G_C-G_j) beta_j |v_j|  (every e^(G_C-G_j) u_j too),
 //   |u_j|, |R_j| <= max(beta) (max |v| + |S0| + sum beta |v|),
-// with the largest |v| of the head's chunk for every |v|, and a row's norm measured every
-// eighth chunk; |T| <= 1 takes the constant 2^12. Two terms reach 2^-39 of such a bound.
+// with the row's largest |v| of the chunk for every |v|, and its norm measured every eighth
+// chunk; |T| <= 1 takes the constant 2^12. Two terms reach 2^-39 of such a bound, which no
+// other row's values are part of.
 //
 // What bounds it. One chunk follows the other: a sequence's chunk takes 3.2 us (2916
 // tokens on one rank's shard: 153 us for 46), of which the three dependent products are
@@ -624,8 +625,10 @@ struct ChainSmem {
   float part[2][128];   // of a row's squares, by halves of its columns
   float inv_s[2][128], inv_u[2][128];
   int first_bad[2][128];
-  // Of a chunk, for its scales: bounds of R and U as [0] + [1] |S0|, of the state after it
-  // as [2] |S0| + [3]; and whether all its v, k and gates are finite.
+  // Of a chunk, for its scales: with v a row's largest |v| (v_max, as bf16), bounds of R and
+  // U as [0] v + [1] |S0|, of the state after it as [2] |S0| + [3] v; and whether all its v,
+  // k and gates are finite.
+  uint16_t v_max[kIn][D];
   float4 scale[kIn];
   int finite_in[kIn];
   uint64_t full[kIn], empty[kIn], v_ready[kIn], ofull[2], oempty[2], s_ready[2], s_done[2];
@@ -864,28 +867,37 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
     // no MMA is in flight when the TMEM is freed
     if (ok) ok = mbar_wait(&s.o_done, (chunks - 1) & 1);
   } else if (warp == 3) {
-    // the chunk's largest |v|, from the bits (a NaN or an infinity is larger than any)
+    // each row's largest |v| of the chunk, from the bits (a NaN or an infinity is larger than any)
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     for (int n = 0; n < chunks; ++n) {
       const int st = in_stage(n), toks = min(kChunk, e - (b + n * kChunk));
       if (ok) ok = mbar_wait(&s.full[st], in_phase(n));
-      uint32_t m = 0;
+      // eight rows of S^T a lane (columns of v), their largest of every kRows-th token
+      uint4 m = make_uint4(0, 0, 0, 0);
       const auto look = [&](int t) {
         const uint4 v = *reinterpret_cast<const uint4*>(&s.in[st].v[t][lane % kLanes * 8]);
-        return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        m.x = __vmaxu2(m.x, v.x & 0x7fff7fffu), m.y = __vmaxu2(m.y, v.y & 0x7fff7fffu);
+        m.z = __vmaxu2(m.z, v.z & 0x7fff7fffu), m.w = __vmaxu2(m.w, v.w & 0x7fff7fffu);
       };
       if (toks == kChunk) {
 #pragma unroll 8
-        for (int t = 0; t < kChunk; t += kRows) m = __vmaxu2(m, look(t + lane / kLanes));
+        for (int t = 0; t < kChunk; t += kRows) look(t + lane / kLanes);
       } else {
-        for (int t = lane / kLanes; t < toks; t += kRows) m = __vmaxu2(m, look(t));
+        for (int t = lane / kLanes; t < toks; t += kRows) look(t);
       }
-      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+#pragma unroll
+      for (int o = 16; o >= kLanes; o >>= 1) {
+        m.x = __vmaxu2(m.x, __shfl_xor_sync(0xffffffffu, m.x, o)), m.y = __vmaxu2(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+        m.z = __vmaxu2(m.z, __shfl_xor_sync(0xffffffffu, m.z, o)), m.w = __vmaxu2(m.w, __shfl_xor_sync(0xffffffffu, m.w, o));
+      }
+      if (lane < kLanes) *reinterpret_cast<uint4*>(&s.v_max[st][lane * 8]) = m;
+      const uint32_t two = __vmaxu2(__vmaxu2(m.x, m.y), __vmaxu2(m.z, m.w));
+      const uint32_t all = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16));
+      __syncwarp();  // v_max, before the arrival
       if (lane == 0) {
         const float4 end = *reinterpret_cast<const float4*>(s.in[st].scal[S_END]);
-        const float mv = __uint_as_float(m << 16);
-        s.scale[st] = make_float4(end.z * (mv + mv * end.w), end.z, end.x, s.in[st].scal[S_END][4] * mv);
-        s.finite_in[st] = __float_as_int(end.y) == kChunk && m < 0x7f80;
+        s.scale[st] = make_float4(end.z * (1.f + end.w), end.z, end.x, s.in[st].scal[S_END][4]);
+        s.finite_in[st] = __float_as_int(end.y) == kChunk && all < 0x7f80;
         mbar_arrive(&s.v_ready[st]);
         mbar_arrive(&s.empty[st]);
       }
@@ -944,6 +956,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       ChainIn<D>& g = s.in[st];
       if (ok) ok = mbar_wait(&s.v_ready[st], in_phase(n));  // after full[st]
       float4 k = s.scale[st];
+      const float most = __uint_as_float((uint32_t)s.v_max[st][vrow] << 16);
+      k.x *= most, k.w *= most;
       first_bad = kChunk;
       if (!s.finite_in[st]) {
         // up to the first token of this row whose v, k or gates are not finite

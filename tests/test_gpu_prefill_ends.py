@@ -158,3 +158,45 @@ def test_delta_of_bad_offsets(name, gated):
     core = delta(h, b, gated, out=torch.full_like(b.dz, float("nan")))
     _check_blame(h, blamed)
     P.check_delta(b, core, gated)
+
+
+# ------------------------------------------------------------------ rows of other magnitudes
+
+@pytest.mark.parametrize("shape", [P.SMALL, P.WIDE], ids=lambda s: s.name)
+@pytest.mark.parametrize("how", ["small", "large"])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_delta_rows_do_not_share_their_precision(shape, how, fresh):
+    """A row of the state needs no other row, so the bounds of a head's state and of its
+    outputs hold for each of its rows by itself, however large the others are: the state's
+    2e-5 of the row's own norms, the outputs' 2^-8 of what |S| |q| allows."""
+    b = P.Batch(shape, [130, 70, 9], 35, fresh=[0, 1, 2] if fresh else [])
+    Hk, Hv, d = shape.num_k_heads, shape.num_v_heads, shape.head_k_dim
+    # rows of 1, 2^-13, 2^-26 and 2^-40 side by side, or one row of 2^40 among them
+    f = 2.0 ** torch.tensor([0, -13, -26, -40] if how == "small" else [0, 0, 0, 0]).repeat(Hv * d // 4)
+    if how == "large":
+        f[5::d] = 2.0 ** 40
+    f = f.cuda()
+    b.dx[:, 2 * Hk * d:] *= f.to(torch.bfloat16)
+    b.dssm *= f.view(1, Hv, d, 1)
+    b.ssm0 = P.f64(b.dssm)
+    core, ssm = P.f64(delta(handle(b), b)).reshape(b.T, Hv, d), P.f64(b.dssm)
+    assert np.isfinite(core).all()
+    x, ba = P.f64(b.dx), P.f64(b.dba)
+    rate, shift = np.exp(P.f64(b.weights["A_log"])), P.f64(b.weights["dt_bias"])
+    for s in range(b.S):
+        S = b.ssm0[b.first[s]].copy() if b.first[s] > 0 else np.zeros((Hv, d, d))
+        most = np.sqrt((S * S).sum(2))
+        for t in range(int(b.cu[s]), int(b.cu[s + 1])):
+            q, k, v = (x[t, i:j].reshape(-1, d) for i, j in ((0, Hk * d), (Hk * d, 2 * Hk * d), (2 * Hk * d, None)))
+            q = np.repeat(q / np.sqrt((q * q).sum(1, keepdims=True) + shape.l2_eps) * shape.scale_q, shape.group, 0)
+            k = np.repeat(k / np.sqrt((k * k).sum(1, keepdims=True) + shape.l2_eps), shape.group, 0)
+            beta = 1 / (1 + np.exp(-ba[t, :Hv]))
+            S *= np.exp(-rate * np.logaddexp(0, ba[t, Hv:] + shift))[:, None, None]
+            S += (beta[:, None] * (v - np.einsum("hvk,hk->hv", S, k)))[:, :, None] * k[:, None, :]
+            most = np.maximum(most, np.maximum(np.sqrt((S * S).sum(2)), np.abs(v)))
+            o = np.einsum("hvk,hk->hv", S, q)
+            off = np.abs(core[t] - o) - 2.0 ** -8 * (np.abs(o) + np.sqrt((S * S).sum(2)) * np.sqrt((q * q).sum(1))[:, None])
+            assert off.max() <= 0
+        d2 = ssm[b.last[s]] - S
+        err = np.sqrt((d2 * d2).sum(2)) / most
+        assert err.max() <= 2e-5, f"state rows of sequence {s}: {err.max():.3g}"
