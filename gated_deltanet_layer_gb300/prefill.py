@@ -143,7 +143,9 @@ def slot_map(new_lens, context_lens, block_size, block_table, free_list, free_co
 class GdnPrefill:
     """The conv and the gated delta rule of one GDN layer shape over ragged
     prompts, bound to one workspace on one device. `shape` has the fields of
-    workloads.LayerShape; max_tokens and max_seqs bound one call."""
+    workloads.LayerShape; max_tokens and max_seqs bound one call. The handle may be
+    dropped while its calls run; a graph that captured them needs it for as long
+    as it is replayed."""
 
     def __init__(self, shape, *, max_tokens: int, max_seqs: int, stream=None):
         L = _native.lib()
@@ -160,14 +162,14 @@ class GdnPrefill:
             raise GdnError("gdn_prefill_workspace_bytes", _native.GDN_ERR_UNSUPPORTED)
         with torch.cuda.stream(stream):  # None: the current one
             self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+        self._home = _stream(stream, self.workspace)  # the stream whose memory it is
         self._channels = 2 * shape.num_k_heads * shape.head_k_dim + shape.num_v_heads * shape.head_v_dim
         self._columns = shape.num_v_heads * shape.head_v_dim
         self._state = torch.bfloat16 if shape.ssm_dtype == "bf16" else torch.float32
         self._state_values = shape.num_slots * self._columns * shape.head_k_dim
         self._conv_values = shape.num_slots * self._channels * 3
         h = ctypes.c_void_p()
-        st = L.gdn_prefill_create(ctypes.byref(self.cfg), self.workspace.data_ptr(), n, _stream(stream, self.workspace),
-                                  ctypes.byref(h))
+        st = L.gdn_prefill_create(ctypes.byref(self.cfg), self.workspace.data_ptr(), n, self._home, ctypes.byref(h))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_create", st)
         self._h = h
@@ -177,6 +179,14 @@ class GdnPrefill:
         if h:
             _native.lib().gdn_prefill_destroy(h)
             self._h = None
+
+    def _on(self, stream):
+        """The stream of a call, as a number. The workspace is kept until what runs there is
+        done, also past the handle's end."""
+        st = _stream(stream, self.workspace)
+        if st != self._home:
+            self.workspace.record_stream(stream if stream is not None else torch.cuda.current_stream(self.workspace.device))
+        return st
 
     def _out(self, out, like, cols, stream):
         """The output and its row stride."""
@@ -201,7 +211,7 @@ class GdnPrefill:
             self._h, S, T, x.data_ptr(), ldx, _dense(conv_w, "conv_w", _bf16, 4 * C),
             _dense(cu_seqlens, "cu_seqlens", _i32, S + 1), _dense(state_in, "state_in", _i32, S),
             _dense(state_out, "state_out", _i32, S), _dense(conv_state, "conv_state", _bf16, self._conv_values),
-            out.data_ptr(), ldo, _stream(stream, x))
+            out.data_ptr(), ldo, self._on(stream))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_conv", st)
         return out
@@ -228,7 +238,7 @@ class GdnPrefill:
             _dense(weights["A_log"], "A_log", torch.float32, Hv), _dense(weights["dt_bias"], "dt_bias", _bf16, Hv), norm,
             _dense(cu_seqlens, "cu_seqlens", _i32, S + 1), _dense(state_in, "state_in", _i32, S),
             _dense(state_out, "state_out", _i32, S), _dense(ssm_state, "ssm_state", self._state, self._state_values),
-            out.data_ptr(), ldo, _stream(stream, qkv))
+            out.data_ptr(), ldo, self._on(stream))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_delta", st)
         return out
@@ -236,10 +246,10 @@ class GdnPrefill:
     def check(self, stream=None):
         """(status, detail word) of the sticky device error word; synchronises."""
         d = ctypes.c_uint32()
-        st = _native.lib().gdn_prefill_check(self._h, _stream(stream, self.workspace), ctypes.byref(d))
+        st = _native.lib().gdn_prefill_check(self._h, self._on(stream), ctypes.byref(d))
         return st, d.value
 
     def reset(self, stream=None):
-        st = _native.lib().gdn_prefill_reset(self._h, _stream(stream, self.workspace))
+        st = _native.lib().gdn_prefill_reset(self._h, self._on(stream))
         if st != GDN_OK:
             raise GdnError("gdn_prefill_reset", st)

@@ -200,3 +200,35 @@ def test_delta_rows_do_not_share_their_precision(shape, how, fresh):
         d2 = ssm[b.last[s]] - S
         err = np.sqrt((d2 * d2).sum(2)) / most
         assert err.max() <= 2e-5, f"state rows of sequence {s}: {err.max():.3g}"
+
+
+# ------------------------------------------------------------------ streams
+
+@pytest.mark.parametrize("given", [True, False], ids=["given", "current"])
+@pytest.mark.parametrize("call", ["conv", "delta"])
+def test_workspace_outlives_a_dropped_handle(call, given):
+    """A handle dropped while its call runs on another stream leaves its workspace to
+    that call: the stream that it was made on does not get the memory before."""
+    b = P.Batch(P.SMALL, [100, 3], 36)
+    side = torch.cuda.Stream()
+    out = torch.empty_like(b.dx if call == "conv" else b.dz)
+
+    def run(h, **kw):
+        if call == "conv":
+            h.conv(b.dx, b.dw, b.dcu, b.dfirst, b.dlast, b.dconv, out=out, **kw)
+        else:
+            h.delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, b.dssm, out=out, **kw)
+
+    run(handle(b))  # a kernel's first launch waits for the device
+    h = GdnPrefill(b.shape, max_tokens=5000, max_seqs=2)
+    torch.cuda.synchronize()
+    where, size = h.workspace.data_ptr(), h.workspace.numel()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # what comes next on this stream is not done for a tenth of a second
+    with torch.cuda.stream(None if given else side):
+        run(h, stream=side if given else None)
+    del h
+    held = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert not side.query() and where not in [t.data_ptr() for t in held]
+    torch.cuda.synchronize()
+    assert out.isfinite().all()
