@@ -63,6 +63,13 @@ bool overlaps_any(const Span& out, const Span (&in)[N]) {
   return false;
 }
 
+// GDN_ERR_ARG where the current device is not the handle's.
+gdn_status check_device(const gdn_prefill* h) {
+  int device;
+  if (cudaGetDevice(&device) != cudaSuccess) return GDN_ERR_CUDA;
+  return device == h->device ? GDN_OK : GDN_ERR_ARG;
+}
+
 gdn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 // Checks common to the two calls over a ragged batch.
@@ -72,7 +79,7 @@ gdn_status check_ragged(const gdn_prefill* h, int32_t seqs, int32_t tokens, cons
   if (seqs > h->cfg.max_seqs || tokens > h->cfg.max_tokens) return GDN_ERR_ARG;
   if (!cu || !aligned(cu, 4)) return GDN_ERR_ARG;
   if (seqs > 0 && (!in || !out || !aligned(in, 4) || !aligned(out, 4))) return GDN_ERR_ARG;
-  return GDN_OK;
+  return check_device(h);
 }
 
 // which: the table, 0 the conv's, 1 the delta rule's
@@ -211,6 +218,8 @@ extern "C" gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t 
 
 extern "C" gdn_status gdn_prefill_check(gdn_prefill_t* h, void* stream, uint32_t* detail) {
   if (!h) return GDN_ERR_ARG;
+  const gdn_status st = check_device(h);
+  if (st != GDN_OK) return st;
   uint32_t word = 0;
   if (cudaMemcpyAsync(&word, h->ws, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream) != cudaSuccess ||
       cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
@@ -223,6 +232,8 @@ extern "C" gdn_status gdn_prefill_check(gdn_prefill_t* h, void* stream, uint32_t
 
 extern "C" gdn_status gdn_prefill_reset(gdn_prefill_t* h, void* stream) {
   if (!h) return GDN_ERR_ARG;
+  const gdn_status st = check_device(h);
+  if (st != GDN_OK) return st;
   return cuda_status(cudaMemsetAsync(h->ws, 0, kErrorBytes, (cudaStream_t)stream));
 }
 

@@ -4,9 +4,10 @@ CUDA tensors: argument marshalling only, as for the decode step.
 `slot_map` turns request lengths into offsets, block tables and slots,
 `linear` runs a projection with its epilogue, and `GdnPrefill` the conv and the
 gated delta rule over ragged prompts; the states they leave are those
-`GdnDecode.step` continues from. Every call runs on the current stream, or on
-`stream`; what it allocates is allocated there, and tensors of another stream
-are the caller's to order and to keep (Tensor.record_stream).
+`GdnDecode.step` continues from. Every call runs on the current device, where
+its tensors must be, and on the current stream, or on `stream`; what it
+allocates is allocated there, and tensors of another stream are the caller's to
+order and to keep (Tensor.record_stream).
 """
 from __future__ import annotations
 
@@ -32,8 +33,23 @@ _bf16, _i32 = torch.bfloat16, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream(stream, t):
-    return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
+# The calling thread's current device, where the library launches.
+_device = torch._C._cuda_getDevice
+# Whether this process sees several devices (2: not known yet); with one there is no other to
+# be on, and asking each tensor for its own takes 2 us a call.
+_several = 2
+
+
+def _stream(stream):
+    """The stream of a call, as a number; one of the current device."""
+    global _several
+    if _several == 2:
+        _several = torch.cuda.device_count() > 1
+    if stream is None:
+        return _raw_stream(_device())
+    if _several and stream.device_index != _device():
+        raise ValueError("the stream must be one of the current device")
+    return stream.cuda_stream
 
 
 def _empty(size, dtype, like, stream):
@@ -46,8 +62,8 @@ def _empty(size, dtype, like, stream):
 
 def _rows(t, name):
     """A [rows, columns] bf16 CUDA tensor with packed columns; its row stride."""
-    if t.dtype is not _bf16 or not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{name} must be a two-dimensional bf16 CUDA tensor")
+    if t.dtype is not _bf16 or not t.is_cuda or t.dim() != 2 or (_several and t.get_device() != _device()):
+        raise ValueError(f"{name} must be a two-dimensional bf16 CUDA tensor on the current device")
     (rows, cols), (ld, unit) = t.shape, t.stride()
     if unit != 1 and cols > 1 and rows:
         raise ValueError(f"the columns of {name} must be packed")
@@ -60,8 +76,9 @@ def _rows(t, name):
 
 def _dense(t, name, dtype, n):
     """The address of a contiguous CUDA tensor of n values."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} values")
+    if (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n
+            or (_several and t.get_device() != _device())):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} values on the current device")
     return t.data_ptr()
 
 
@@ -89,7 +106,7 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, stream=Non
             raise ValueError("residual must be [M, N]")
     st = _native.lib().gdn_linear(
         M, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else _dense(bias, "bias", _bf16, N),
-        ACTIVATIONS[activation], r, ldr, out.data_ptr(), ldo, _stream(stream, x))
+        ACTIVATIONS[activation], r, ldr, out.data_ptr(), ldo, _stream(stream))
     if st != GDN_OK:
         raise GdnError("gdn_linear", st)
     return out
@@ -99,8 +116,8 @@ def linear_check(stream=None):
     """(status, detail word) of the device's gdn_linear calls; synchronises
     and clears the word."""
     d = ctypes.c_uint32()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    st = _native.lib().gdn_linear_check(s.cuda_stream, ctypes.byref(d))
+    s = _stream(stream) if stream is not None else torch.cuda.current_stream().cuda_stream
+    st = _native.lib().gdn_linear_check(s, ctypes.byref(d))
     return st, d.value
 
 
@@ -134,7 +151,7 @@ def slot_map(new_lens, context_lens, block_size, block_table, free_list, free_co
         R, tokens, _dense(new_lens, "new_lens", _i32, R), _dense(context_lens, "context_lens", _i32, R), block_size, wide,
         _dense(block_table, "block_table", _i32, R * wide), _dense(free_list, "free_list", _i32, free_list.numel()),
         free_list.numel(), _dense(free_count, "free_count", _i32, 1), left, cu, seq, pos, slots,
-        None if error is None else _dense(error, "error", _i32, 1), _stream(stream, new_lens))
+        None if error is None else _dense(error, "error", _i32, 1), _stream(stream))
     if st != GDN_OK:
         raise GdnError("gdn_slot_map", st)
     return out
@@ -162,7 +179,7 @@ class GdnPrefill:
             raise GdnError("gdn_prefill_workspace_bytes", _native.GDN_ERR_UNSUPPORTED)
         with torch.cuda.stream(stream):  # None: the current one
             self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
-        self._home = _stream(stream, self.workspace)  # the stream whose memory it is
+        self._home = _stream(stream)  # the stream whose memory it is
         self._channels = 2 * shape.num_k_heads * shape.head_k_dim + shape.num_v_heads * shape.head_v_dim
         self._columns = shape.num_v_heads * shape.head_v_dim
         self._state = torch.bfloat16 if shape.ssm_dtype == "bf16" else torch.float32
@@ -183,9 +200,9 @@ class GdnPrefill:
     def _on(self, stream):
         """The stream of a call, as a number. The workspace is kept until what runs there is
         done, also past the handle's end."""
-        st = _stream(stream, self.workspace)
+        st = _stream(stream)
         if st != self._home:
-            self.workspace.record_stream(stream if stream is not None else torch.cuda.current_stream(self.workspace.device))
+            self.workspace.record_stream(stream if stream is not None else torch.cuda.current_stream())
         return st
 
     def _out(self, out, like, cols, stream):

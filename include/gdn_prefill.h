@@ -66,7 +66,8 @@ size_t gdn_prefill_workspace_bytes(const gdn_prefill_config* cfg);
 
 /* Validate the config, bind the caller's workspace (256-byte aligned device
  * memory that outlives the handle) and clear its error word on `stream`. The
- * handle holds host state only. */
+ * handle holds host state only. It belongs to the device that is current here;
+ * calls with another one current are GDN_ERR_ARG. */
 gdn_status gdn_prefill_create(const gdn_prefill_config* cfg, void* workspace, size_t workspace_bytes,
                               void* stream, gdn_prefill_t** out);
 

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_deltanet_layer_gb300 import GdnPrefill, _native, workloads as WL
+from gated_deltanet_layer_gb300 import GdnPrefill, _native, linear, prefill, slot_map, workloads as WL
 import prefill_harness as P
 
 pytestmark = pytest.mark.gpu
@@ -232,3 +232,28 @@ def test_workspace_outlives_a_dropped_handle(call, given):
     assert not side.query() and where not in [t.data_ptr() for t in held]
     torch.cuda.synchronize()
     assert out.isfinite().all()
+
+
+# ------------------------------------------------------------------ devices
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Kernels run on the current device. What belongs to another one (here: everything,
+    once the binding is told of several devices, 1 the current one) is an error, not a launch."""
+    b = P.Batch(P.SMALL, [20, 3], 37)
+    h = handle(b)
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    lens, ctx, table, free, count = i(3, 3), i(0, 2), torch.zeros(2, 8, dtype=torch.int32, device="cuda"), i(4, 5, 6, 7, 8), i(5)
+    own = torch.cuda.Stream()
+    conv, ssm = b.dconv.clone(), b.dssm.clone()
+    monkeypatch.setattr(prefill, "_device", lambda: 1)
+    monkeypatch.setattr(prefill, "_several", True)
+    for call in (lambda: linear(b.dx, b.dx), lambda: slot_map(lens, ctx, 1, table, free, count, 6),
+                 lambda: h.conv(b.dx, b.dw, b.dcu, b.dfirst, b.dlast, b.dconv), lambda: delta(h, b)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    with pytest.raises(ValueError, match="current device"):
+        prefill._stream(own)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    same = lambda a, c: torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+    assert same(conv, b.dconv) and same(ssm, b.dssm) and not table.any()
