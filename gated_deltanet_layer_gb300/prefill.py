@@ -27,6 +27,7 @@ ACTIVATIONS = {None: GDN_ACT_NONE, "none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "
 SlotMap = namedtuple("SlotMap", "cu_seqlens token_seq token_pos slots free_count")
 
 _bf16, _i32 = torch.bfloat16, torch.int32
+_INT_MAX = 2**31 - 1  # sizes cross the C ABI as int32, and ctypes would cut what is larger
 
 
 # The calling thread's current stream as a number, without building a Stream object.
@@ -93,6 +94,8 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, stream=Non
         raise ValueError("x and w have different inner sizes")
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        raise GdnError("gdn_linear", _native.GDN_ERR_UNSUPPORTED)
     if out is None:
         out, ldo = _empty((M, N), _bf16, x, stream), N
     else:
@@ -132,6 +135,8 @@ def slot_map(new_lens, context_lens, block_size, block_table, free_list, free_co
     [tokens] and int32 free_count [1]."""
     R, wide = block_table.shape
     n = R + 1
+    if not 0 < block_size <= _INT_MAX or not 0 <= tokens <= _INT_MAX or max(R, wide, free_list.numel()) > _INT_MAX:
+        raise GdnError("gdn_slot_map", _native.GDN_ERR_ARG)
     if out is None:
         # one allocation; the rows' arrays on 16 bytes
         up = -(-tokens // 4) * 4
@@ -174,6 +179,10 @@ class GdnPrefill:
             ssm_dtype=GDN_STATE_BF16 if shape.ssm_dtype == "bf16" else GDN_STATE_F32,
             gated_norm_eps=shape.gated_norm_eps, l2_eps=shape.l2_eps,
             q_scale=shape.q_scale if shape.q_scale is not None else float(shape.head_k_dim) ** -0.5)
+        sizes = (shape.num_k_heads, shape.num_v_heads, shape.head_k_dim, shape.head_v_dim, shape.conv_kernel,
+                 shape.num_slots, max_tokens, max_seqs)
+        if max(sizes) > _INT_MAX or min(sizes) < 0:
+            raise GdnError("gdn_prefill_create", _native.GDN_ERR_ARG)
         n = L.gdn_prefill_workspace_bytes(ctypes.byref(self.cfg))
         if n == 0:
             raise GdnError("gdn_prefill_workspace_bytes", _native.GDN_ERR_UNSUPPORTED)
@@ -223,6 +232,8 @@ class GdnPrefill:
         T, cols = x.shape
         if cols != C:
             raise ValueError(f"x must be [tokens, {C}]")
+        if T > _INT_MAX or S >= _INT_MAX:
+            raise GdnError("gdn_prefill_conv", _native.GDN_ERR_ARG)
         out, ldo = self._out(out, x, C, stream)
         st = _native.lib().gdn_prefill_conv(
             self._h, S, T, x.data_ptr(), ldx, _dense(conv_w, "conv_w", _bf16, 4 * C),
@@ -244,6 +255,10 @@ class GdnPrefill:
         ldqkv, ldba, zp, ldz, norm = _rows(qkv, "qkv"), _rows(ba, "ba"), None, 0, None
         if qkv.shape[1] != self._channels or ba.shape != (T, 2 * Hv):
             raise ValueError("qkv and ba must be [tokens, C] and [tokens, 2 Hv]")
+        if max_len is None or max_len > T:
+            max_len = T
+        if T > _INT_MAX or S >= _INT_MAX or max_len < 0:
+            raise GdnError("gdn_prefill_delta", _native.GDN_ERR_ARG)
         if z is not None:
             zp, ldz = z.data_ptr(), _rows(z, "z")
             if z.shape != (T, self._columns):
@@ -251,7 +266,7 @@ class GdnPrefill:
             norm = _dense(weights["gated_norm_w"], "gated_norm_w", _bf16, self.shape.head_v_dim)
         out, ldo = self._out(out, qkv, self._columns, stream)
         st = _native.lib().gdn_prefill_delta(
-            self._h, S, T, T if max_len is None else max_len, qkv.data_ptr(), ldqkv, zp, ldz, ba.data_ptr(), ldba,
+            self._h, S, T, max_len, qkv.data_ptr(), ldqkv, zp, ldz, ba.data_ptr(), ldba,
             _dense(weights["A_log"], "A_log", torch.float32, Hv), _dense(weights["dt_bias"], "dt_bias", _bf16, Hv), norm,
             _dense(cu_seqlens, "cu_seqlens", _i32, S + 1), _dense(state_in, "state_in", _i32, S),
             _dense(state_out, "state_out", _i32, S), _dense(ssm_state, "ssm_state", self._state, self._state_values),

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_deltanet_layer_gb300 import GdnPrefill, _native, linear, prefill, slot_map, workloads as WL
+from gated_deltanet_layer_gb300 import GdnError, GdnPrefill, _native, linear, prefill, slot_map, workloads as WL
 import prefill_harness as P
 
 pytestmark = pytest.mark.gpu
@@ -257,3 +257,36 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     torch.cuda.synchronize()
     same = lambda a, c: torch.equal(a.view(torch.uint8), c.view(torch.uint8))
     assert same(conv, b.dconv) and same(ssm, b.dssm) and not table.any()
+
+
+# ------------------------------------------------------------------ sizes past 32 bits
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes are 32 bits at the C ABI. A larger one is an error, not what is left of it."""
+    long = torch.empty(1, 2 ** 32 + 8, dtype=torch.bfloat16, device="cuda")
+    for x, w in ((long, long), (long[:, :1], long.T), (long.T, long[:, :1])):
+        with pytest.raises(GdnError) as e:
+            linear(x, w)
+        assert e.value.code == _native.GDN_ERR_UNSUPPORTED
+    del long, x, w
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    table = torch.zeros(1, 8, dtype=torch.int32, device="cuda")
+    for block, tokens in ((2 ** 32 + 4, 3), (4, 2 ** 32 + 3), (-2 ** 32 + 4, 3), (0, 3)):
+        with pytest.raises(GdnError) as e:
+            slot_map(i(3), i(0), block, table, i(4, 5), i(2), tokens)
+        assert e.value.code == _native.GDN_ERR_ARG and not table.any()
+    for kw in (dict(max_tokens=2 ** 32 + 64), dict(max_seqs=2 ** 32 + 2)):
+        with pytest.raises(GdnError):
+            GdnPrefill(P.SMALL, **{**dict(max_tokens=64, max_seqs=2), **kw})
+
+
+@pytest.mark.parametrize("most", [2 ** 31, 2 ** 32, 2 ** 40, 2 ** 32 + 5])
+def test_any_bound_of_the_lengths_will_do(most):
+    """max_len is an upper bound, however large."""
+    b = P.Batch(P.SMALL, [20, 3], 38)
+    h = handle(b)
+    P.check_delta(b, delta(h, b, max_len=most), False)
+    assert h.check()[0] == 0
+    for below in (-1, -2 ** 32):
+        with pytest.raises(GdnError):
+            delta(h, b, max_len=below)
