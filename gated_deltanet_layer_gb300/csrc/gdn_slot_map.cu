@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
   const long long my0 = min((long long)p.N, per * blockIdx.x), my1 = min((long long)p.N, my0 + per);
   long long tok_carry = 0, need_carry = 0;
   long long taken = 0;
-  for (int base = 0; base < p.R; base += kSlotThreads) {
-    const int n = min(kSlotThreads, p.R - base), r = base + tid;
+  for (long long at_request = 0; at_request < p.R; at_request += kSlotThreads) {
+    const int base = (int)at_request, n = min(kSlotThreads, p.R - base), r = base + tid;
     long long nl = 0, cl = 0, have = 0, need = 0;
     bool bad = false;
     if (tid < n) {
@@ -161,10 +161,10 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
         *reinterpret_cast<longlong2*>(p.slots + k + 2) = make_longlong2(slot[2], slot[3]);
       }
     }
-    // an even share of the batch's needed blocks
-    const int blocks = (int)max(0LL, min(need_carry, taken) - t.need[0]);
-    const int share = (blocks + gridDim.x - 1) / gridDim.x, b0 = share * blockIdx.x;
-    for (int u = b0 + tid; u < min(blocks, b0 + share); u += kSlotThreads) {
+    // an even share of the batch's needed blocks, of which there can be 2^31 - 1
+    const unsigned blocks = (unsigned)max(0LL, min(need_carry, taken) - t.need[0]);
+    const unsigned share = (blocks + gridDim.x - 1) / gridDim.x, b0 = share * blockIdx.x, b1 = min(blocks, b0 + share);
+    for (unsigned u = b0 + tid; u < b1; u += kSlotThreads) {
       const long long k = t.need[0] + u;
       const int i = last_at_most(t.need, n, k);
       p.table[(long long)(base + i) * p.max_blocks + t.have[i] + (k - t.need[i])] = __ldg(p.free_list + (avail - 1 - k));

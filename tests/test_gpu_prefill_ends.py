@@ -290,3 +290,20 @@ def test_any_bound_of_the_lengths_will_do(most):
     for below in (-1, -2 ** 32):
         with pytest.raises(GdnError):
             delta(h, b, max_len=below)
+
+
+@pytest.mark.parametrize("tokens", [0, 300000])
+def test_slot_map_of_two_billion_blocks(tokens):
+    """A request of 2^31 - 1 new blocks: every one of them is written, by one CTA or many."""
+    n = 2 ** 31 - 1
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    free = torch.arange(n, dtype=torch.int32, device="cuda")
+    table = torch.full((1, n), -1, dtype=torch.int32, device="cuda")
+    error = i(0)
+    m = slot_map(i(n), i(0), 1, table, free, i(n), tokens, error=error)
+    assert int(m.free_count) == 0 and int(error) == (5 << 24 | 3 << 16)  # more tokens than rows
+    step = 1 << 28
+    for at in range(0, n, step):
+        end = min(n, at + step)
+        assert torch.equal(table[0, at:end], torch.arange(n - 1 - at, n - 1 - end, -1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(m.slots, torch.arange(n - 1, n - 1 - tokens, -1, device="cuda"))
