@@ -164,10 +164,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     // every stage consumed: no copy is in flight when the CTAs leave
+    const int next = st;
+    const uint32_t round = ph;
     for (int k = 0; k < kStages && ok; ++k) {
       ok = mbar_wait(&s.empty[st], ph ^ 1);
       if (++st == kStages) st = 0, ph ^= 1;
     }
+    // nor where a wait has failed: stages from the next one on were last filled a round before
+    if (!ok && rank == 0)
+      for (int k = 0; k < kStages; ++k) mbar_wait(&s.full[k], k < next ? round : round ^ 1);
   } else if (warp == 1 && rank == 0) {
     constexpr uint32_t idesc = idesc_bf16_f32(256, BN);
     int st = 0, buf = 0;
@@ -348,11 +353,15 @@ __global__ void __launch_bounds__(kFewThreads) linear_few(const __grid_constant_
       tma_load_2d_plain(w + 128 * 128, &xmap, k * kBK, 0, &full[st]);
       if (++st == f.stages) st = 0, ph ^= 1;
     }
+    // A wait has failed: no copy is in flight when the CTA leaves (stages from st on were last
+    // filled a round before).
+    if (!ok)
+      for (int i = 0; i < f.stages; ++i) mbar_wait(&full[i], i < st ? ph : ph ^ 1);
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, TOK);
-    int st = 0;
+    int st = 0, k = k0;
     uint32_t ph = 0;
-    for (int k = k0; k < k1; ++k) {
+    for (; k < k1; ++k) {
       if (!(ok = mbar_wait(&full[st], ph))) break;
       tc_fence_after();
       if (elect_one()) {
@@ -362,6 +371,11 @@ __global__ void __launch_bounds__(kFewThreads) linear_few(const __grid_constant_
         mma_commit(&empty[st]);
       }
       __syncwarp();
+      if (++st == f.stages) st = 0, ph ^= 1;
+    }
+    // a wait has failed: nor the copies that the producer goes on to make before it waits itself
+    for (int left = ok ? 0 : min(f.stages, k1 - k); left > 0; --left) {
+      mbar_wait(&full[st], ph);
       if (++st == f.stages) st = 0, ph ^= 1;
     }
     if (elect_one()) mma_commit(&done);

@@ -722,7 +722,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
   static_assert(D * kRow <= sizeof(s.oin) && D * kRow <= sizeof(s.in), "a state passes through these");
 
   if (warp == 0) {
-    for (int n = 0; n < chunks; ++n) {
+    int n = 0;
+    for (; n < chunks; ++n) {
       const int t0 = b + n * kChunk, toks = min(kChunk, e - t0), st = in_stage(n);
       const size_t place = place0 + n;
       const unsigned char* kq = c.kq + (place * p.Hk + kh) * kq_bytes<D>();
@@ -741,8 +742,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       if (lane == 0) bulk_load(g.k, kq, kq_bytes<D>() / 2, &s.full[st]);
     }
     // no copy is in flight when the CTA leaves
-    for (int n = max(0, chunks - kIn); n < chunks; ++n)
-      if (ok) ok = mbar_wait(&s.full[in_stage(n)], in_phase(n));
+    for (int m = max(0, n - kIn); m < n; ++m) ok = mbar_wait(&s.full[in_stage(m)], in_phase(m)) && ok;
   } else if (warp == 2) {
     if (in > 0) {
       if (lane == 0) mbar_arrive_expect_tx(&s.state_in, D * kRowData);
@@ -754,7 +754,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       ok = __all_sync(0xffffffffu, ok);
     }
     // what the outputs need, with a wait of its own: the outputs may lag behind the chain
-    for (int n = 0; n < chunks; ++n) {
+    int n = 0;
+    for (; n < chunks; ++n) {
       const int st = n & 1;
       ok = ok && mbar_wait(&s.oempty[st], ((n >> 1) & 1) ^ 1);
       if (!ok) break;
@@ -767,8 +768,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       }
       __syncwarp();
     }
-    for (int n = max(0, chunks - 2); n < chunks; ++n)
-      if (ok) ok = mbar_wait(&s.ofull[n & 1], (n >> 1) & 1);
+    for (int m = max(0, n - 2); m < n; ++m) ok = mbar_wait(&s.ofull[m & 1], (m >> 1) & 1) && ok;
+    if (!ok && in > 0) mbar_wait(&s.state_in, 0);
   } else if (warp == 1) {
     // the whole warp waits, one lane issues
     constexpr uint32_t idesc = idesc_f16(128, 64, false), idesc_s = idesc_f16(128, 64, true);

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) 
   bool ok = true;
   for (int run = 0; run * kRun < n_rows; ++run) {
     const int slot = run % kRuns, i = run * kRun, n = min(kRun, n_rows - i);
-    ok = ok && tc::mbar_wait(&full[slot], (run / kRuns) & 1);
+    ok = tc::mbar_wait(&full[slot], (run / kRuns) & 1) && ok;
     if (mine && ok) {
       if (n == kRun) {
 #pragma unroll
@@ -172,7 +172,13 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) 
         for (int k = 0; k < n; ++k) row(t0 + i + k, *reinterpret_cast<const uint4*>(at + (slot * kRun + k) * kRowBytes));
       }
     }
-    __syncthreads();  // the run is read: its place may be filled again
+    if ((run + kRuns) * kRun >= n_rows) continue;
+    ok = __syncthreads_and(ok);  // the run is read: its place may be filled again
+    if (!ok) {
+      // no copy is in flight when the CTA leaves
+      for (int r = run; r < run + kRuns; ++r) tc::mbar_wait(&full[r % kRuns], (r / kRuns) & 1);
+      break;
+    }
     if (threadIdx.x < 32) fetch(run + kRuns);
   }
   if (!ok) record(p.r.error, kStatusDeadline, kWhatWait, s);
