@@ -25,7 +25,7 @@
 // beta <= 1 a token's step S <- e^g S (I - beta k k^T) + beta v k^T does not lengthen a
 // row by more than beta |v|, so over a chunk
 //   |S'| <= e^(G_C) |S0| + sum_j e^(G_C-G_j) beta_j |v_j|  (every e^(G_C-G_j) u_j too),
-//   |u_j|, |R_j| <= max(beta) (max |v| + |S0| + sum beta |v|),
+//   |u_j|, |R_j| <= max(beta) (max |v| + sum beta |v|) + max(e^G beta) |S0|,
 // with the row's largest |v| of the chunk for every |v|, and its norm measured every eighth
 // chunk; |T| <= 1 takes the constant 2^12. Two terms reach 2^-39 of such a bound, which no
 // other row's values are part of.
@@ -66,7 +66,8 @@ constexpr int kImg = 2 * 8192;  // two images of 64 x 64 f16
 constexpr int kChainBytes = kImg + S_COUNT * 256, kOutBytes = kImg + O_COUNT * 256;
 constexpr int kHeadBytes = kChainBytes + kOutBytes;
 // S_END: [0] e^(G_C), [1] (an int) the first token whose k or gates are not finite,
-// else 64, [2] the largest beta, [3] sum beta, [4] sum e^(G_C-G) beta.
+// else 64, [2] the largest beta, [3] sum beta, [4] sum e^(G_C-G) beta, [5] the largest
+// e^G beta.
 
 template <int D>
 constexpr int kq_bytes() { return 2 * kChunk * D * 2; }  // the k image, then q's
@@ -169,6 +170,11 @@ __device__ __forceinline__ void tmem_st16f(uint32_t t, const float (&v)[16]) {
   tmem_st16(t, r);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A bound past the largest float is the largest: infinity x a gate of 0 would be no bound.
+// For the same reason a scale that takes a power of two back multiplies last, after the
+// gates.
+constexpr float kLargest = 0x1.fffffep127f;
 
 // Power of two f with |x| f < 2^14 for every |x| <= b, kept where f, 1 / f and the
 // ratios of two of them are ordinary floats.
@@ -386,11 +392,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
       const float ehi = __shfl_sync(0xffffffffu, a.hi, 31), elo = __shfl_sync(0xffffffffu, a.lo, 31);
       // of the last token of this lane's block of 16
       const float bhi = __shfl_sync(0xffffffffu, a.hi, lane | 7), blo = __shfl_sync(0xffffffffu, a.lo, lane | 7);
-      float top = fmaxf(beta[0], beta[1]);
-      for (int o = 16; o > 0; o >>= 1) {
-        first_bad = min(first_bad, __shfl_xor_sync(0xffffffffu, first_bad, o));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      }
+      first_bad = __reduce_min_sync(0xffffffffu, first_bad);
+      const auto largest = [](float a, float b) {  // of values that are not negative: as their bits
+        return __uint_as_float(__reduce_max_sync(0xffffffffu, max(__float_as_uint(a), __float_as_uint(b))));
+      };
       if ((lane & 7) == 0) s.steep[hd][lane >> 3] = !(G[0].hi - bhi < 100.f);
       float gam[2], left[2];
 #pragma unroll
@@ -408,9 +413,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
           make_float4(beta[0], beta[1], gam[0] * rn.x, gam[1] * rn.y);
       *reinterpret_cast<float2*>(sc + 64 * S_CU + 2 * lane) = make_float2(left[0] * rn.x, left[1] * rn.y);
       const float sum_b = warp_sum(beta[0] + beta[1]), sum_w = warp_sum(left[0] * beta[0] + left[1] * beta[1]);
+      const float top = largest(beta[0], beta[1]), reach = largest(beta[0] * gam[0], beta[1] * gam[1]);
       if (lane == 0) {
         *reinterpret_cast<float4*>(sc + 64 * S_END) = make_float4(exp2f(ehi + elo), __int_as_float(first_bad), top, sum_b);
-        sc[64 * S_END + 4] = sum_w;
+        *reinterpret_cast<float2*>(sc + 64 * S_END + 4) = make_float2(sum_w, reach);
         s.first_bad[hd] = first_bad;
       }
       *reinterpret_cast<float2*>(img + kChainBytes + kImg + 256 * O_CQG + 8 * lane) =
@@ -897,7 +903,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       __syncwarp();  // v_max, before the arrival
       if (lane == 0) {
         const float4 end = *reinterpret_cast<const float4*>(s.in[st].scal[S_END]);
-        s.scale[st] = make_float4(end.z * (1.f + end.w), end.z, end.x, s.in[st].scal[S_END][4]);
+        const float2 rest = *reinterpret_cast<const float2*>(&s.in[st].scal[S_END][4]);
+        s.scale[st] = make_float4(end.z * (1.f + end.w), rest.y, end.x, rest.x);
         s.finite_in[st] = __float_as_int(end.y) == kChunk && all < 0x7f80;
         mbar_arrive(&s.v_ready[st]);
         mbar_arrive(&s.empty[st]);
@@ -936,7 +943,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       asm volatile("bar.sync 2, 256;" ::: "memory");
       const float a = s.part[0][row], o = s.part[1][row];
       dead = !(finite(a) && finite(o));
-      bound = dead ? 0.f : 12.f * fmaxf(a, o);  // at least the 2-norm of 128 values
+      bound = dead ? 0.f : fminf(12.f * fmaxf(a, o), kLargest);  // at least the 2-norm of 128 values
       fs = row_scale(bound);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
@@ -973,12 +980,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
             mv = fmaxf(mv, a);
         }
         k = first_bad < kChunk ? make_float4((1.f + kChunk) * mv, 1.f, 0.f, 0.f)
-                               : make_float4(end.z * (mv + mv * end.w), end.z, end.x, g.scal[S_END][4] * mv);
+                               : make_float4(end.z * (mv + mv * end.w), g.scal[S_END][5], end.x, g.scal[S_END][4] * mv);
       }
       if (dead) first_bad = 0, k.z = k.w = 0.f;
       fu = row_scale(fmaf(k.y, bound, k.x));
       added = k.w;
-      bound = fmaf(k.z, bound, added) * 1.01f;
+      bound = fminf(fmaf(k.z, bound, added) * 1.01f, kLargest);
       fs_next = row_scale(bound);
       shrink = k.z * fminf(fs_next * inverse_pow2(fs), 0x1p126f);
     };
@@ -987,7 +994,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
       const int st = n & 1, toks = min(kChunk, e - (b + n * kChunk));
       const uint32_t ph = n & 1;
       ChainIn<D>& g = s.in[in_stage(n)];
-      const float inv_s = inverse_pow2(fs), p_scale = fminf(fu * inv_s, 0x1p126f);
+      const float inv_s = inverse_pow2(fs), p_scale = fminf(fu * inv_s, 0x1p127f);
       const float u_scale = fminf(fs_next * inverse_pow2(fu), 0x1p126f);
       const int until = min(first_bad, toks);  // R is zero from there on
       const bool bad = first_bad < kChunk;
@@ -1051,7 +1058,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float4 rc = *reinterpret_cast<const float4*>(&g.scal[S_R][2 * (i + j)]);
-          const float2 q = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), p2), make_float2(rc.z, rc.w));
+          const float2 q = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(rc.z, rc.w)), p2);
           const float2 r = __fmul2_rn(add_scaled(v[8 * k + j / 2], fu_bf16, q), make_float2(rc.x, rc.y));
           x[j] = r.x, x[j + 1] = r.y;
         }
@@ -1101,7 +1108,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
           const float2 cu = j & 2 ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
           const float2 y = __fmul2_rn(make_float2(u[j], u[j + 1]), t2);
           split2(y, &ohi[j / 2], &olo[j / 2]);
-          float2 w = __fmul2_rn(__fmul2_rn(y, us2), cu);
+          float2 w = __fmul2_rn(__fmul2_rn(y, cu), us2);
           if (bad) w = make_float2(0.f, 0.f);
           split2(w, &hi[j / 2], &lo[j / 2]);
         }
@@ -1195,10 +1202,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_kernel(const ChunkPara
           const float4 cq = *reinterpret_cast<const float4*>(&y.scal[O_CQ][i + j]);
 #pragma unroll
           for (int k = 0; k < 4; k += 2) {
-            const float2 a = __fmul2_rn(make_float2(x[j + k], x[j + k + 1]), is2);
-            const float2 w = __fmul2_rn(make_float2(u[j + k], u[j + k + 1]), iu2);
-            const float2 o = __ffma2_rn(a, k ? make_float2(cg.z, cg.w) : make_float2(cg.x, cg.y),
-                                        __fmul2_rn(w, k ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y)));
+            const float2 a = __fmul2_rn(k ? make_float2(cg.z, cg.w) : make_float2(cg.x, cg.y), is2);
+            const float2 w = __fmul2_rn(k ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y), iu2);
+            const float2 o = __ffma2_rn(make_float2(x[j + k], x[j + k + 1]), a, __fmul2_rn(make_float2(u[j + k], u[j + k + 1]), w));
             u[j + k] = o.x, u[j + k + 1] = o.y;
           }
         }

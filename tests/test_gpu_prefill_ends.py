@@ -307,3 +307,26 @@ def test_slot_map_of_two_billion_blocks(tokens):
         end = min(n, at + step)
         assert torch.equal(table[0, at:end], torch.arange(n - 1 - at, n - 1 - end, -1, dtype=torch.int32, device="cuda"))
     assert torch.equal(m.slots, torch.arange(n - 1, n - 1 - tokens, -1, device="cuda"))
+
+
+# ------------------------------------------------------------------ states near the largest float
+
+@pytest.mark.parametrize("n", [9, 100, 700])
+def test_delta_forgets_a_state_near_the_largest_float(n):
+    """A finite state however large, once it is forgotten, leaves nothing behind."""
+    b = P.Batch(P.SMALL, [n, 70], 39, a_log=6.0)
+    b.dssm[b.first[0]] *= 1 / b.dssm[b.first[0]].abs().max()
+    b.dssm[b.first[0]] *= 2e38
+    assert b.dssm[b.first[0]].isfinite().all()
+    b.ssm0 = P.f64(b.dssm)
+    b.dba[:, b.shape.num_v_heads:] = 3.0  # e^g is 0 in f32 from the first token on
+    core = delta(handle(b), b)
+    fresh = P.Batch(P.SMALL, [n, 70], 39, a_log=6.0, fresh=[0])
+    fresh.dba[:, b.shape.num_v_heads:] = 3.0
+    want = delta(handle(fresh), fresh)
+    rows = P.f64(want).reshape(b.T, -1, 64)
+    rms = np.sqrt((rows * rows).mean(2, keepdims=True))
+    off = np.abs(P.f64(core).reshape(rows.shape) - rows)
+    assert (off <= 2.0 ** -8 * np.abs(rows) + 2.0 ** -8 * rms).all()
+    s, f = P.f64(b.dssm)[b.last[0]], P.f64(fresh.dssm)[fresh.last[0]]
+    assert np.linalg.norm(s - f) <= 2e-5 * np.linalg.norm(f)
