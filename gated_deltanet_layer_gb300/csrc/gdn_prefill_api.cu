@@ -44,17 +44,23 @@ int channels(const gdn_prefill_config& c) { return 2 * c.num_k_heads * c.head_k_
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Bytes from the first to the last value of a strided matrix of 2-byte values.
-size_t extent(long long rows, long long ld, long long cols) { return rows > 0 ? (size_t)((rows - 1) * ld + cols) * 2 : 0; }
-
+// Memory that a call reads or writes: n bytes from p, or of a matrix the `width` bytes of rows
+// `ld` bytes apart.
 struct Span {
   const void* p;
-  size_t n;
+  size_t n, ld = 0, width = 0;
 };
+Span matrix(const void* p, long long rows, long long ld, long long cols) {
+  return Span{p, rows > 0 ? (size_t)((rows - 1) * ld + cols) * 2 : 0, (size_t)ld * 2, (size_t)cols * 2};
+}
 bool overlap(const Span& a, const Span& b) {
   if (!a.p || !b.p || !a.n || !b.n) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + b.n && y < x + a.n;
+  if (x >= y + b.n || y >= x + a.n) return false;
+  if (!a.ld || a.ld != b.ld) return true;
+  // columns of the same rows: b's begin `at` bytes after a's in a row, or in the one before
+  const size_t at = y >= x ? (y - x) % a.ld : (a.ld - (x - y) % a.ld) % a.ld;
+  return at < a.width || at + b.width > a.ld;
 }
 template <int N>
 bool overlaps_any(const Span& out, const Span (&in)[N]) {
@@ -147,8 +153,8 @@ extern "C" gdn_status gdn_prefill_conv(gdn_prefill_t* h, int32_t seqs, int32_t t
   if (!conv_w || !conv_state || (tokens > 0 && (!x || !out))) return GDN_ERR_ARG;
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(conv_w, 16) || !aligned(conv_state, 16)) return GDN_ERR_ARG;
   if (ldx < C || ldo < C || ldx % 8 || ldo % 8) return GDN_ERR_ARG;
-  const Span o{out, extent(tokens, ldo, C)}, state{conv_state, (size_t)h->cfg.num_slots * C * 6};
-  const Span in[] = {{x, extent(tokens, ldx, C)}, {conv_w, (size_t)C * 8}, {cu_seqlens, (size_t)(seqs + 1) * 4},
+  const Span o = matrix(out, tokens, ldo, C), state{conv_state, (size_t)h->cfg.num_slots * C * 6};
+  const Span in[] = {matrix(x, tokens, ldx, C), {conv_w, (size_t)C * 8}, {cu_seqlens, (size_t)(seqs + 1) * 4},
                      {state_in, (size_t)seqs * 4}, {state_out, (size_t)seqs * 4},
                      {h->ws, gdn_prefill_workspace_bytes(&h->cfg)}};
   if (overlaps_any(o, in) || overlap(o, state) || overlaps_any(state, in)) return GDN_ERR_ARG;
@@ -181,9 +187,9 @@ extern "C" gdn_status gdn_prefill_delta(gdn_prefill_t* h, int32_t seqs, int32_t 
   if (ldqkv < C || ldba < 2 * Hv || ldcore < cols || (z && ldz < cols)) return GDN_ERR_ARG;
   if (ldqkv % 8 || ldcore % 8 || (z && ldz % 8)) return GDN_ERR_ARG;
   const size_t sdt = c.ssm_dtype == GDN_STATE_BF16 ? 2 : 4;
-  const Span o{core_out, extent(tokens, ldcore, cols)};
+  const Span o = matrix(core_out, tokens, ldcore, cols);
   const Span state{ssm_state, (size_t)c.num_slots * cols * c.head_k_dim * sdt};
-  const Span in[] = {{qkv, extent(tokens, ldqkv, C)}, {z, z ? extent(tokens, ldz, cols) : 0}, {ba, extent(tokens, ldba, 2 * Hv)},
+  const Span in[] = {matrix(qkv, tokens, ldqkv, C), matrix(z, tokens, ldz, cols), matrix(ba, tokens, ldba, 2 * Hv),
                      {A_log, (size_t)Hv * 4}, {dt_bias, (size_t)Hv * 2},
                      {gated_norm_w, z ? (size_t)c.head_v_dim * 2 : 0}, {cu_seqlens, (size_t)(seqs + 1) * 4},
                      {state_in, (size_t)seqs * 4}, {state_out, (size_t)seqs * 4},
@@ -251,8 +257,8 @@ extern "C" gdn_status gdn_linear(int32_t rows, int32_t cols, int32_t inner, cons
   if (ldx >= (1LL << 38) || ldw >= (1LL << 38)) return GDN_ERR_UNSUPPORTED;  // a tile map's largest stride
   constexpr int32_t kEdge = INT32_MAX - 255;  // a tile may reach past the matrix, its coordinates are 32 bits
   if (rows > kEdge || cols > kEdge || inner > kEdge) return GDN_ERR_UNSUPPORTED;
-  const Span o{out, extent(rows, ldo, cols)}, r{residual, residual ? extent(rows, ldr, cols) : 0};
-  const Span in[] = {{x, extent(rows, ldx, inner)}, {w, extent(cols, ldw, inner)}, {bias, bias ? (size_t)cols * 2 : 0}};
+  const Span o = matrix(out, rows, ldo, cols), r = matrix(residual, rows, ldr, cols);
+  const Span in[] = {matrix(x, rows, ldx, inner), matrix(w, cols, ldw, inner), {bias, bias ? (size_t)cols * 2 : 0}};
   if (overlaps_any(o, in)) return GDN_ERR_ARG;
   if (overlap(o, r) && !(residual == out && ldr == ldo)) return GDN_ERR_ARG;
   LinearParams p{};

@@ -30,7 +30,9 @@
  *    passes its state on. The two may be the same slot; several sequences may
  *    start from one slot (a shared prefix), but state_out slots must be
  *    distinct and none may be another sequence's state_in.
- *  - Row strides (ld*) count elements; rows need not be packed.
+ *  - Row strides (ld*) count elements; rows need not be packed. Outputs may be
+ *    columns beside an input's in the same rows (an equal stride); that is not
+ *    an overlap.
  */
 #ifndef GDN_PREFILL_H_
 #define GDN_PREFILL_H_

@@ -330,3 +330,49 @@ def test_delta_forgets_a_state_near_the_largest_float(n):
     assert (off <= 2.0 ** -8 * np.abs(rows) + 2.0 ** -8 * rms).all()
     s, f = P.f64(b.dssm)[b.last[0]], P.f64(fresh.dssm)[fresh.last[0]]
     assert np.linalg.norm(s - f) <= 2e-5 * np.linalg.norm(f)
+
+
+# ------------------------------------------------------------------ outputs beside inputs
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_linear_writes_beside_its_inputs(M):
+    """x, the residual and the output as columns of the same rows."""
+    g = torch.Generator(device="cuda").manual_seed(46)
+    K, N = 64, 77
+    rows = torch.randn(M, 64 + 2 * N + 6, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(N, K, generator=g, device="cuda").to(torch.bfloat16)
+    before = rows.clone()
+    want = linear(rows[:, :K].clone(), w, residual=rows[:, K:K + N].clone())
+    out = rows[:, K + N:K + 2 * N]
+    assert linear(rows[:, :K], w, residual=rows[:, K:K + N], out=out) is out
+    assert torch.equal(out, want) and torch.equal(rows[:, :K + N], before[:, :K + N])
+    assert torch.equal(rows[:, K + 2 * N:], before[:, K + 2 * N:])
+
+
+def test_prefill_writes_beside_its_inputs():
+    """The conv's outputs beside its inputs, and the delta rule's in the q | k | v columns of
+    the projection's rows, beside z: the conv is the last to read those."""
+    b = P.Batch(P.SMALL, [70, 5], 47)
+    C, cols = b.shape.conv_channels, b.shape.num_v_heads * 64
+    h = handle(b)
+    conv, ssm = b.dconv.clone(), b.dssm.clone()
+    y = h.conv(b.dx, b.dw, b.dcu, b.dfirst, b.dlast, conv)
+    want = h.delta(y, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, ssm, z=b.dz)
+    rows = torch.cat([b.dx, torch.zeros_like(b.dx), b.dz], 1)
+    beside = h.conv(rows[:, :C], b.dw, b.dcu, b.dfirst, b.dlast, b.dconv, out=rows[:, C:2 * C])
+    assert torch.equal(beside, y) and torch.equal(rows[:, :C], b.dx)
+    core = h.delta(beside, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, b.dssm, z=rows[:, 2 * C:], out=rows[:, :cols])
+    live = b.dlast.long()
+    assert torch.equal(core, want) and torch.equal(rows[:, 2 * C:], b.dz) and torch.equal(b.dssm[live], ssm[live])
+
+
+@pytest.mark.parametrize("shift", [-1, 1, 63, -63])
+def test_outputs_over_inputs_are_refused(shift):
+    rows = torch.zeros(9, 320, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(64, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(GdnError) as e:
+        linear(rows[:, 128:192], w, out=rows[:, 128 + shift:192 + shift])
+    assert e.value.code == _native.GDN_ERR_ARG
+    flat = rows.view(-1)
+    with pytest.raises(GdnError):  # the output's rows run on into x's of the next row
+        linear(rows[1:5, :64], w, out=torch.as_strided(flat, (4, 64), (320, 1), 300))
