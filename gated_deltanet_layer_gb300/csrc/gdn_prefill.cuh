@@ -41,7 +41,9 @@ __device__ __forceinline__ void record(unsigned int* error, uint32_t status, uin
 // own, and a bad offset takes nothing from a sequence that is right. Offsets that are in
 // order are their own m; a sequence whose offsets are not is padding.
 // Up to kScanned sequences every warp works out the m it needs from all the offsets, four a
-// lane; with more of them a kernel before leaves the m in a table.
+// lane; with more of them a kernel before leaves the m in a table. (The conv of single tokens
+// of a small layer: 128 take 3.1 us scanned and 129 4.4 by the table; 400 take 5.2 by the
+// table and, 32 offsets a lane, 7.1 scanned.)
 constexpr int kScanned = 128;
 
 // v, or 0 where it lies outside the rows.

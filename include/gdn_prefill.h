@@ -94,7 +94,15 @@ gdn_status gdn_prefill_conv(gdn_prefill_t* h, int32_t seqs, int32_t tokens, cons
  * and with z: core = o / sqrt(mean o^2 + gated_norm_eps) * gated_norm_w *
  * silu(z) per value head; without (z NULL, gated_norm_w ignored): core = o.
  * States, sums and gates are f32 throughout a sequence; a bf16 state is
- * rounded once, when it is stored.
+ * rounded once, when it is stored. Sequences of up to 14 tokens run token by
+ * token, all in f32. Longer ones run in chunks of 64 on the tensor cores, where
+ * what is multiplied is two f16 terms, 22 bits (q and k as they are): on
+ * ordinary inputs an f32 state ends within 2.2e-7 of the 64-bit result, token by
+ * token within 0.6e-7. Within a chunk a row of the state keeps what is above
+ * 2^-39 of the largest of its own values and of its state there, and q and k
+ * what is above 2^-25 of the token's largest element (exact above 2^-17). A
+ * caller that needs f32 products throughout passes a prompt in pieces of up to 14
+ * tokens. The gate's SiLU is within a few 2^-22, and 0 where it is below 2^-126.
  * max_len is an upper bound of the sequences' lengths known to the host
  * (tokens if nothing better is known); sequences longer than it record
  * GDN_ERR_INDEX and are padding.
@@ -134,7 +142,10 @@ void gdn_prefill_destroy(gdn_prefill_t* h);
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU_TANH = 2 } gdn_activation;
 
 /* out[m][n] = bf16(act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]) with
- * f32 sums and one rounding. x [rows][ldx >= inner], w [cols][ldw >= inner],
+ * f32 sums and one rounding. The sums are the tensor cores', which cut where an
+ * f32 addition rounds: 1e-5 of the result at an inner size of 8192, a hundredth of
+ * the last rounding. The activations are within a few 2^-22, and 0 where they
+ * are below 2^-126. x [rows][ldx >= inner], w [cols][ldw >= inner],
  * bias [cols] or NULL, residual [rows][ldr >= cols] or NULL, out [rows][ldo >=
  * cols], all bf16. GELU is the tanh form. x and w are 16-byte aligned with ldx
  * and ldw multiples of 8; bias, residual and out have no alignment rule beyond
