@@ -11,11 +11,12 @@
 // care in the main loop: what is outside either matrix is zero in both operands.
 //
 // Measured (us): 8192 x 20480 x 8192 1376 by itself (2.0 PFLOP/s, 104% of the measured
-// library product) and 1584 to 1674 back to back, where the power limit holds the clock down;
+// library product) and 1485 to 1674 back to back, where the power limit holds the clock down;
 // 4100 x 8192 x 1024 with a residual 61, of which 36 are the products and 24 the bytes:
-// 17 x 32 tiles on 76 pairs leave 8 rounds for 7.2, and each pair reads 1 MB of tiles
-// from L2 in the 7 us it has for a round; 5 x 2560 x 8192 8.0 in a graph, the weights'
-// bytes being 6.2.
+// 17 x 32 tiles, the last row of them with 4 rows of 256, on 76 pairs leave 8 rounds for
+// 7.2, and each pair reads 1 MB of tiles from L2 in the 7 us it has for a round; 5 x 2560 x
+// 8192 8.0 in a graph, the weights' bytes being 6.2, and 128 rows of it 15.4. 129 to 512
+// rows of it take 30 to 32: 40 tiles on 76 pairs, 128 steps in a row.
 #include <algorithm>
 #include <atomic>
 

@@ -9,9 +9,9 @@ namespace gdn {
 constexpr int kChunk = 64;  // tokens of one chunk of a sequence
 // Longest sequence that the delta rule takes token by token. The two forms take the same
 // time at 11 tokens (many requests of many heads) to 18 (few) (us, token by token / in
-// chunks, for 64 requests of the full layer 302.5 / 388.2 at 8, 426.4 / 390.6 at 12, 550.0 /
-// 391.3 at 16; for 8 requests of a shard 15.4 / 29.1, 21.4 / 29.0, 27.3 / 28.9 and 33.2 /
-// 29.2 at 20).
+// chunks, for 64 requests of the full layer 304.1 / 383.2 at 8, 429.1 / 385.9 at 12, 553.1 /
+// 387.8 at 16; for 8 requests of a shard 15.4 / 28.6, 21.3 / 28.7, 27.4 / 28.7 and 33.3 /
+// 28.7 at 20).
 constexpr int kRecurrentMax = 14;
 // Up to this many sequences the chunked form starts the longest ones first, where they
 // take more than one wave; with more of them the waves level out by themselves.

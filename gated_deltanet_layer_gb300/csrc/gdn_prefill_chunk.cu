@@ -31,13 +31,14 @@
 // other row's values are part of.
 //
 // What bounds it. One chunk follows the other: a sequence's chunk takes 3.2 us (2916
-// tokens on one rank's shard: 153 us for 46), of which the three dependent products are
+// tokens on one rank's shard: 152 us for 46), of which the three dependent products are
 // about 0.9 and the conversions of S, R and U to f16 between them the rest; the tensor
 // pipe is 30% busy, an SM issues every second cycle. A CTA's start and end take 9 us
-// beside its chunks. 13 sequences of 16384 tokens on 64 heads take 353 us, 16700 chunks on
-// 152 SMs. prepare_kernel takes 29 us for one round of CTAs and 291 for those 16384
-// tokens; it is bound by its instructions (an SM issues 46% of its slots) between short
-// steps that wait for one another.
+// beside its chunks. 13 sequences of 16384 tokens on 64 heads take 359 us, 16700 chunks on
+// 152 SMs, and 1.35 GB from and to memory (3.7 TB/s), of which the images are half.
+// prepare_kernel takes 28 us for one round of CTAs and 291 for those 16384 tokens; it is
+// bound by its instructions (an SM issues half of its slots) between short steps that wait
+// for one another, and moves 0.70 GB (2.4 TB/s), the images it writes being 0.55.
 //
 // Values that are not finite stay where the definition has them: a row of S^T knows
 // the first token whose v, k or gates are not, multiplies zeros from there on, and

@@ -7,7 +7,7 @@
 // bytes a value). A CTA takes one chunk of 64 tokens of one sequence and 1024 channels, 8
 // a thread. Its rows come as bulk copies of 2 KB into a ring of 24 in shared memory, four
 // CTAs and 192 KB under way on an SM, and a thread walks them with the three older taps in
-// registers. 16384 rows of 12288 channels take 127 us, 94% of the measured copy rate (212
+// registers. 16384 rows of 12288 channels take 132 us, 91% of the measured copy rate (212
 // with rows read into registers, 8 in flight: the warps waited for memory 13 cycles of 18).
 #include <algorithm>
 #include <atomic>

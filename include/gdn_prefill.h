@@ -97,7 +97,7 @@ gdn_status gdn_prefill_conv(gdn_prefill_t* h, int32_t seqs, int32_t tokens, cons
  * rounded once, when it is stored. Sequences of up to 14 tokens run token by
  * token, all in f32. Longer ones run in chunks of 64 on the tensor cores, where
  * what is multiplied is two f16 terms, 22 bits (q and k as they are): on
- * ordinary inputs an f32 state ends within 2.2e-7 of the 64-bit result, token by
+ * ordinary inputs an f32 state ends within 2.3e-7 of the 64-bit result, token by
  * token within 0.6e-7. Within a chunk a row of the state keeps what is above
  * 2^-39 of the largest of its own values and of its state there, and q and k
  * what is above 2^-25 of the token's largest element (exact above 2^-17). A
