@@ -118,3 +118,57 @@ def test_linear_wide_tiles(M, N, K, act, bias, residual):
     off = (got.double() - y).abs() - (2.0 ** -8 * y.abs() + 1.2 * (K / 16 + 16) * 2.0 ** -23 * scale)
     assert off.max() <= 0
     assert linear_check() == (0, 0)
+
+
+# ------------------------------------------------------------------ one handle, call after call
+
+@pytest.mark.parametrize("S", [40, 200])
+@pytest.mark.parametrize("graph", [False, True], ids=["calls", "graph"])
+def test_calls_of_one_handle_do_not_see_each_other(S, graph):
+    """Calls of different offsets and slots, one right after the other on one handle, give
+    what each gives by itself: nothing of a call before is left in the workspace."""
+    sh = shape(1, 4, 64, 2 * S + 4)
+    batches = []
+    for seed in (50, 51, 52):
+        rng = np.random.default_rng(seed)
+        lens = [int(n) for n in rng.choice([0, 1, 14, 15, 20, 64, 65, 130], S)]
+        batches.append(P.Batch(sh, lens, seed, pad=[seed - 45], fresh=range(0, S, 7), extra=3))
+    most = max(b.T for b in batches)
+    make = lambda: GdnPrefill(sh, max_tokens=most, max_seqs=S)
+
+    def call(h, b, y, core):
+        h.conv(b.dx, b.dw, b.dcu, b.dfirst, b.dlast, b.dconv, out=y)
+        h.delta(b.dx, b.dba, b.weights, b.dcu, b.dfirst, b.dlast, b.dssm, z=b.dz, out=core)
+
+    outs = lambda b: (torch.zeros_like(b.dx), torch.zeros_like(b.dz))
+    want = []
+    for b in batches:
+        o = outs(b)
+        call(make(), b, *o)  # first and last slots are apart, so a call again gives the same
+        want.append((*o, b.dconv.clone(), b.dssm.clone()))
+    torch.cuda.synchronize()
+    h, got = make(), [outs(b) for b in batches]
+
+    def several():
+        for _ in range(4):
+            for b, o in zip(batches, got):
+                call(h, b, *o)
+
+    if graph:
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            several()
+        torch.cuda.synchronize()
+        for o in got:
+            o[0].zero_(), o[1].zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            several()
+        g.replay()
+    else:
+        several()
+    torch.cuda.synchronize()
+    assert h.check()[0] == 0
+    same = lambda a, c: torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+    for b, o, w in zip(batches, got, want):
+        assert same(o[0], w[0]) and same(o[1], w[1]) and same(b.dconv, w[2]) and same(b.dssm, w[3])
