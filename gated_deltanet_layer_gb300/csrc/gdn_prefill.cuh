@@ -97,9 +97,13 @@ __device__ __forceinline__ bool seq_live(const Ragged& r, int s, const SeqIn& q,
 __host__ __device__ __forceinline__ int chunk_places(int tokens, int seqs) { return tokens / kChunk + seqs + 1; }
 __device__ __forceinline__ int chunk_first_place(int s, int b) { return b / kChunk + s; }
 // Place -> sequence (the last whose first place is at or before it; the first one's is 0)
-// and its rows. Every lane of a converged warp calls it.
+// and its rows. Every lane of a converged warp calls it. WAITED: this grid has waited for the
+// kernel that filled the table, so what L1 holds of it is new; else only L2 is sure to be (the
+// grid before has waited, and then let this one start).
+template <bool WAITED>
 __device__ __forceinline__ int chunk_seq(const Ragged& r, int place, int* b, int* e) {
   const int lane = threadIdx.x & 31;
+  const auto table = [&](int s) { return WAITED ? r.table[s] : __ldcg(r.table + s); };
   int lo = 0, n = r.seqs + 1;
   if (!r.table) {
     constexpr int kOf = kScanned / 32;  // a lane has m_s of s = kOf lane + 1 .. kOf lane + kOf
@@ -135,13 +139,13 @@ __device__ __forceinline__ int chunk_seq(const Ragged& r, int place, int* b, int
   // 32 sequences at a time: two steps of dependent loads for up to 1023
   while (n > 1) {
     const int stride = (n + 31) / 32, i = lane * stride, s = lo + min(i, n - 1);
-    const unsigned below = __ballot_sync(0xffffffffu, i < n && chunk_first_place(s, r.table[s]) <= place);
+    const unsigned below = __ballot_sync(0xffffffffu, i < n && chunk_first_place(s, table(s)) <= place);
     const int last = below ? (31 - __clz(below)) * stride : 0;
     lo += last;
     n = min(stride, n - last);
   }
-  *b = r.table[lo];
-  *e = lo < r.seqs ? r.table[lo + 1] : r.tokens;
+  *b = table(lo);
+  *e = lo < r.seqs ? table(lo + 1) : r.tokens;
   return lo;
 }
 

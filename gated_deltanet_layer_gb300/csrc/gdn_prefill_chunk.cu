@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_kernel(const ChunkPar
   PrepSmem<D>& s = *reinterpret_cast<PrepSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int place = blockIdx.x / p.Hk, kh = blockIdx.x % p.Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int b, e;
-  const int sq = chunk_seq(p.r, place, &b, &e);
+  const int sq = chunk_seq<false>(p.r, place, &b, &e);
   const int t0 = b + (place - chunk_first_place(sq, b)) * kChunk, n = min(kChunk, e - t0);
   if (n <= 0 || e - b <= kRecurrentMax || !seq_live(p.r, sq, seq_in(p.r, sq), b, e, false)) {
     griddep_wait();

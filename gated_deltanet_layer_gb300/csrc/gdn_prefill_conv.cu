@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvParams p) 
   griddep_wait();  // for the table of the offsets
   const int place = blockIdx.x;
   int b, e;
-  const int s = chunk_seq(p.r, place, &b, &e);
+  const int s = chunk_seq<true>(p.r, place, &b, &e);
   const int j = place - chunk_first_place(s, b);
   const SeqIn seq = seq_in(p.r, s);
   const bool live = seq_live(p.r, s, seq, b, e, j == 0 && blockIdx.y == 0 && threadIdx.x == 0);
