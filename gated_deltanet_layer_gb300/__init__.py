@@ -4,8 +4,9 @@
 torch CUDA tensors: it allocates the workspace with torch, marshals pointers
 and streams, and launches one persistent CUDA kernel per step. It computes
 nothing itself and has no fallback: without the built library it raises.
-`GdnPrefill`, `linear` and `slot_map` (prefill.py) wrap the prompt side
-(include/gdn_prefill.h) in the same way.
+`GdnPrefill`, `linear`, `linear_w4` and `slot_map` (prefill.py) wrap the prompt side
+(include/gdn_prefill.h) in the same way, `kv_append` and `PagedAttention`
+(attention.py) an attention layer over a paged cache (include/gdn_attention.h).
 """
 from __future__ import annotations
 
@@ -17,8 +18,8 @@ from ._native import (GDN_ENGINE_AUTO, GDN_ENGINE_CUDA_CORE, GDN_ENGINE_TCGEN05,
 
 _FORMATS = {"bf16": GDN_W_BF16, "mxfp4": GDN_W_MXFP4, "mxfp6": GDN_W_MXFP6}
 
-__all__ = ["GdnDecode", "GdnError", "GdnPrefill", "SlotMap", "ENGINES", "linear", "linear_check", "slot_map",
-           "step_static"]
+__all__ = ["GdnDecode", "GdnError", "GdnPrefill", "PagedAttention", "SlotMap", "ENGINES", "kv_append", "linear",
+           "linear_check", "linear_w4", "slot_map", "step_static"]
 
 ENGINES = {"auto": GDN_ENGINE_AUTO, "cuda_core": GDN_ENGINE_CUDA_CORE, "tcgen05": GDN_ENGINE_TCGEN05}
 _WEIGHT_KEYS = ("input_norm_w", "qkvz", "qkvz_scales", "ba", "conv_w", "A_log", "dt_bias", "gated_norm_w",
@@ -213,4 +214,5 @@ def step_static(shape, x, residual, weights, state_indices, conv_state, ssm_stat
     return None
 
 
-from .prefill import GdnPrefill, SlotMap, linear, linear_check, slot_map  # noqa: E402
+from .attention import PagedAttention, kv_append  # noqa: E402
+from .prefill import GdnPrefill, SlotMap, linear, linear_check, linear_w4, slot_map  # noqa: E402

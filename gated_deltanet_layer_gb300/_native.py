@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/gdn_decode.h and include/gdn_prefill.h
+"""ctypes binding of the C ABI in include/gdn_decode.h, include/gdn_prefill.h and include/gdn_attention.h
 (argument marshalling only).
 
 Every step of the decode path runs in the CUDA library libgdn_decode.so. If the
@@ -24,7 +24,8 @@ GDN_LAUNCH_NO_EARLY_WEIGHTS = 0x2
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU_TANH = 0, 1, 2
 
 # Every symbol the headers declare (include/gdn_decode.h, the diagnostics in
-# include/gdn_decode_diag.h and the prompt side in include/gdn_prefill.h).
+# include/gdn_decode_diag.h, the prompt side in include/gdn_prefill.h and the
+# attention in include/gdn_attention.h).
 EXPORTS = (
     "gdn_decode_workspace_bytes", "gdn_decode_create", "gdn_decode_step", "gdn_decode_check",
     "gdn_decode_reset", "gdn_decode_destroy", "gdn_status_string", "gdn_decode_launch_info",
@@ -33,6 +34,8 @@ EXPORTS = (
     "gdn_prefill_workspace_bytes", "gdn_prefill_create", "gdn_prefill_conv", "gdn_prefill_delta",
     "gdn_prefill_check", "gdn_prefill_reset", "gdn_prefill_destroy", "gdn_linear",
     "gdn_linear_check", "gdn_slot_map",
+    "gdn_kv_append", "gdn_attn_workspace_bytes", "gdn_attn_create", "gdn_attn_paged", "gdn_attn_check",
+    "gdn_attn_reset", "gdn_attn_destroy", "gdn_linear_w4",
 )
 
 # Size of the library's fixed device scratch (gdn_decode_step_static).
@@ -57,6 +60,14 @@ class PrefillConfig(ctypes.Structure):
         ("head_v_dim", ctypes.c_int32), ("conv_kernel", ctypes.c_int32), ("num_slots", ctypes.c_int32),
         ("max_tokens", ctypes.c_int32), ("max_seqs", ctypes.c_int32), ("ssm_dtype", ctypes.c_int32),
         ("gated_norm_eps", ctypes.c_float), ("l2_eps", ctypes.c_float), ("q_scale", ctypes.c_float),
+    ]
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = [
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -135,6 +146,24 @@ def lib() -> ctypes.CDLL:
     L.gdn_linear_check.restype = ctypes.c_int
     L.gdn_slot_map.argtypes = [i32, i32, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     L.gdn_slot_map.restype = ctypes.c_int
+    L.gdn_linear_w4.argtypes = [i32, i32, i32, vp, i64, i32, i32, vp, vp, vp, vp, i32, vp, i64, vp, i64, vp]
+    L.gdn_linear_w4.restype = ctypes.c_int
+    acfgp, f32 = ctypes.POINTER(AttnConfig), ctypes.c_float
+    L.gdn_kv_append.argtypes = [i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i32, i32, vp, vp, f32, vp,
+                                i64, vp, i64, vp, i64, vp, vp]
+    L.gdn_kv_append.restype = ctypes.c_int
+    L.gdn_attn_workspace_bytes.argtypes = [acfgp]
+    L.gdn_attn_workspace_bytes.restype = ctypes.c_size_t
+    L.gdn_attn_create.argtypes = [acfgp, vp, ctypes.c_size_t, vp, ctypes.POINTER(vp)]
+    L.gdn_attn_create.restype = ctypes.c_int
+    L.gdn_attn_paged.argtypes = [vp, i32, i32, i32, vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, vp, vp, i64, vp, i64, vp]
+    L.gdn_attn_paged.restype = ctypes.c_int
+    L.gdn_attn_check.argtypes = [vp, vp, u32p]
+    L.gdn_attn_check.restype = ctypes.c_int
+    L.gdn_attn_reset.argtypes = [vp, vp]
+    L.gdn_attn_reset.restype = ctypes.c_int
+    L.gdn_attn_destroy.argtypes = [vp]
+    L.gdn_attn_destroy.restype = None
     _lib = L
     return L
 

@@ -1,0 +1,335 @@
+// Shared definitions of the paged attention (gdn_attn_paged): launch parameters,
+// the plan of its work, and the parts of rows that several CTAs work on.
+//
+// A task is (request, key/value head, tile of M query rows); query row r of a request
+// and key/value head is token r / G, query head r % G of the head's G = Hq / Hkv. A task's
+// units are the tiles of KT keys that its last row sees. All tasks' units form one line, in
+// the order request, head, row tile, key tile, and every CTA takes an equal, contiguous
+// share of it, whatever the lengths: a CTA has whole tasks, and at its two ends
+// parts of tasks that it shares with the CTAs beside it. The parts go to the workspace, and
+// the CTA that finishes last joins them, in order.
+#pragma once
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+// What of an index error (bits 23..16 of the error word).
+constexpr uint32_t kAttnBlock = 1, kAttnOffsets = 2, kAttnLength = 3, kAttnWait = 4, kAttnContext = 5;
+
+// Up to this many requests every CTA plans by itself, in shared memory; with more of
+// them a kernel before leaves the plan in the workspace.
+constexpr int kAttnPlanned = 256;
+
+// n / d for 0 <= n < 2^31.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __host__ static FastDiv of(uint32_t d) {
+    uint32_t l = 0;
+    while (l < 31 && (1u << l) < d) ++l;
+    return FastDiv{d, (uint32_t)((((1ull << 32) * ((1ull << l) - d)) / d) + 1), l};
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+struct AttnParams {
+  const int* cu;     // [seqs + 1]
+  const int* ctx;    // [seqs]
+  const int* table;  // [seqs][max_blocks]
+  int seqs, tokens, max_len, max_blocks, num_blocks;
+  int limit;         // most keys of a request
+  FastDiv block;     // slots of a block
+  FastDiv group;     // query heads of a key/value head
+  int Hkv;
+  const __nv_bfloat16* q;
+  long long ldq;
+  const __nv_bfloat16* k;
+  long long ldk;
+  const __nv_bfloat16* v;
+  long long ldv;
+  const __nv_bfloat16* gate;  // nullptr: none
+  long long ldg;
+  __nv_bfloat16* out;
+  long long ldo;
+  float scale_log2;           // scale times log2(e)
+  unsigned int* error;        // sticky word
+  unsigned int* done;         // [grid] parts finished of the task whose first part is the CTA's; zero between calls
+  float* part;                // [2 grid][M][D] sums of weights times values, relative to the part's maximum
+  float2* part_ml;            // [2 grid][M] maximum (of scores times log2 e) and sum of weights
+  int4* seq;                  // [seqs + 1] of the workspace: the plan, where a kernel before makes it
+  long long* start;           // [seqs + 1]
+};
+
+__device__ __forceinline__ void attn_record(unsigned int* error, uint32_t what, uint32_t who) {
+  atomicCAS(error, 0u, (kStatusIndex << 24) | (what << 16) | (who & 0xffff));
+}
+
+// sum over i < n of floor((a i + b) / m), by the steps of Euclid's algorithm (a, b >= 0).
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+#pragma unroll 1
+  while (n > 0) {
+    if (a >= m) sum += (n - 1) * n / 2 * (a / m), a %= m;
+    if (b >= m) sum += n * (b / m), b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// Row tiles of a request and their key tiles. Tile i's last row is min((i + 1) M, n G) - 1, so
+// all but the last tile see ctx + ceil((i + 1) M / G) keys, which are
+// ceil((G ctx + (i + 1) M) / (G KT)) tiles.
+template <int M, int KT>
+struct Tiles {
+  __device__ __forceinline__ static int rows(int n, int G) { return (n * G + M - 1) / M; }
+  __device__ __forceinline__ static int keys(const AttnParams& p, int n, int ctx, int i) {
+    const uint32_t G = p.group.d, last = min((uint32_t)(i + 1) * M, n * G) - 1;
+    return ((uint32_t)ctx + p.group.div(last) + KT) / KT;
+  }
+  // key tiles before row tile i (at most the last one)
+  __device__ __forceinline__ static long long before(int G, int ctx, int i) {
+    if (i == 0) return 0;
+    const long long m = (long long)G * KT;
+    return floor_sum(i, m, M, (long long)G * ctx + M + m - 1);
+  }
+  __device__ __forceinline__ static long long total(const AttnParams& p, int n, int ctx) {
+    const int t = rows(n, p.group.d);
+    return before(p.group.d, ctx, t - 1) + keys(p, n, ctx, t - 1);
+  }
+};
+
+template <int NT>
+struct PlanScratch {
+  int top[NT / 32];
+  long long sum[NT / 32];
+};
+
+// The plan: seq[s] = {first row, new tokens (0: padding), context, -}, start[s] the units
+// before request s, seq[seqs].x the first pad row and start[seqs] all units. The offsets are the
+// caller's: row ends are the running maximum of the offsets that lie within the rows, and
+// a request whose offsets are not its row ends is padding. A block of NT threads.
+template <int M, int KT, int NT>
+__device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long long* start, PlanScratch<NT>& x, bool report) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int top = 0;
+  long long units = 0;
+#pragma unroll 1
+  for (int base = 0; base < p.seqs; base += NT) {
+    const int s = base + tid;
+    const bool on = s < p.seqs;
+    const int lo = on ? __ldg(p.cu + s) : 0, hi = on ? __ldg(p.cu + s + 1) : 0, c = on ? __ldg(p.ctx + s) : 0;
+    int e = on && (unsigned)hi <= (unsigned)p.tokens ? hi : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) e = max(e, __shfl_up_sync(0xffffffffu, e, o));
+    if (lane == 31) x.top[warp] = e;
+    __syncthreads();
+    int before = top;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      const int t = x.top[w];
+      if (w < warp) before = max(before, t);
+      top = max(top, t);
+    }
+    int b = __shfl_up_sync(0xffffffffu, e, 1);
+    b = lane == 0 ? before : max(b, before);
+    e = max(e, before);
+    int n = on && lo == b && hi == e ? e - b : 0;
+    const bool bad = on && (lo < 0 || hi < lo || hi > p.tokens || (s == 0 && lo != 0));
+    const bool long_ = n > p.max_len, far = n > 0 && (c < 0 || (long long)c + n > p.limit);
+    if (report) {
+      if (bad) attn_record(p.error, kAttnOffsets, s);
+      if (long_) attn_record(p.error, kAttnLength, s);
+      if (far) attn_record(p.error, kAttnContext, s);
+    }
+    if (long_ || far) n = 0;
+    const long long mine = n > 0 ? p.Hkv * Tiles<M, KT>::total(p, n, c) : 0;
+    long long u = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, u, o);
+      if (lane >= o) u += t;
+    }
+    if (lane == 31) x.sum[warp] = u;
+    __syncthreads();
+    long long first = units + u - mine;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      const long long t = x.sum[w];
+      if (w < warp) first += t;
+      units += t;
+    }
+    if (on) {
+      seq[s] = make_int4(b, n, c, 0);
+      start[s] = first;
+    }
+  }
+  if (tid == 0) {
+    seq[p.seqs] = make_int4(top, 0, 0, 0);
+    start[p.seqs] = units;
+  }
+  __syncthreads();
+}
+
+// The CTAs' shares of the units.
+struct Shares {
+  long long each, more, units;  // the first `more` CTAs have one unit more
+  int ctas;
+  __device__ __forceinline__ Shares(long long units, int ctas) : units(units), ctas(ctas) {
+    each = units / ctas;
+    more = units - each * ctas;
+  }
+  __device__ __forceinline__ long long first(int c) const { return c * each + min((long long)c, more); }
+  __device__ __forceinline__ int owner(long long u) const {
+    const long long wide = more * (each + 1);
+    return u < wide ? (int)(u / (each + 1)) : (int)(more + (u - wide) / each);
+  }
+};
+
+// A walk over the units, task by task.
+template <int M, int KT>
+struct Walk {
+  const AttnParams& p;
+  const int4* seq;
+  const long long* start;
+  long long task;  // the task's first unit
+  int s, h, i, j;  // request, key/value head, row tile, key tile
+  int nt, rows;    // key tiles of the task, row tiles of the request
+  int row0, n, ctx;
+
+  __device__ __forceinline__ Walk(const AttnParams& p, const int4* seq, const long long* start) : p(p), seq(seq), start(start) {}
+  __device__ __forceinline__ void load() {
+    const int4 q = seq[s];
+    row0 = q.x;
+    n = q.y;
+    ctx = q.z;
+    rows = Tiles<M, KT>::rows(n, p.group.d);
+  }
+  // To unit u, which is one of start[seqs].
+  __device__ __forceinline__ void to(long long u) {
+    int lo = 0, hi = p.seqs - 1;
+    while (lo < hi) {  // the last request that starts at or before u: it has units
+      const int mid = (lo + hi + 1) >> 1;
+      if (start[mid] <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    s = lo;
+    load();
+    const long long first = start[s], per = (start[s + 1] - first) / p.Hkv;
+    h = (int)((u - first) / per);
+    const long long in = u - first - h * per;
+    lo = 0, hi = rows - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (Tiles<M, KT>::before(p.group.d, ctx, mid) <= in)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    i = lo;
+    j = (int)(in - Tiles<M, KT>::before(p.group.d, ctx, i));
+    nt = Tiles<M, KT>::keys(p, n, ctx, i);
+    task = u - j;
+  }
+  __device__ __forceinline__ void next_task() {
+    task += nt;
+    j = 0;
+    if (++i == rows) {
+      i = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do ++s;
+        while (s < p.seqs && seq[s].y == 0);
+        if (s >= p.seqs) return;
+        load();
+      }
+    }
+    nt = Tiles<M, KT>::keys(p, n, ctx, i);
+  }
+};
+
+// Rows that no request works on: zero. Every warp of the grid calls it, of W a CTA: a warp
+// looks at 32 requests at a time and writes every grid-th row of those that are padding.
+template <int W>
+__device__ __forceinline__ void attn_zero_rows(const AttnParams& p, const int4* seq, int cols) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int s0 = (threadIdx.x >> 5) * 32; s0 <= p.seqs; s0 += W * 32) {
+    const int s = s0 + lane;
+    int b = 0, e = 0;
+    if (s <= p.seqs && (s == p.seqs || seq[s].y == 0)) {
+      b = seq[s].x;
+      e = s < p.seqs ? seq[s + 1].x : p.tokens;
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, b < e);
+    while (todo) {
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int end = __shfl_sync(0xffffffffu, e, l);
+      for (int r = __shfl_sync(0xffffffffu, b, l) + (int)((blockIdx.x + l) % gridDim.x); r < end; r += gridDim.x)
+        for (int c = lane * 8; c < cols; c += 256) *reinterpret_cast<uint4*>(p.out + r * p.ldo + c) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// Key row of position pos (below the request's keys): its slot, or -1 where its block is
+// outside the cache.
+struct KeyBlock {
+  int block, at;  // the table's entry, the slot in it; at < 0: no such key
+};
+__device__ __forceinline__ KeyBlock key_block(const AttnParams& p, int s, int pos, int keys) {
+  if (pos >= keys) return KeyBlock{0, -1};
+  const uint32_t b = p.block.div(pos);
+  return KeyBlock{__ldg(p.table + (long long)s * p.max_blocks + b), (int)(pos - b * p.block.d)};
+}
+__device__ __forceinline__ int key_slot(const AttnParams& p, const KeyBlock& b, int s) {
+  if (b.at < 0) return -1;
+  if ((unsigned)b.block >= (unsigned)p.num_blocks) {
+    attn_record(p.error, kAttnBlock, s);
+    return -1;
+  }
+  return b.block * (int)p.block.d + b.at;
+}
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+struct AppendParams {
+  int tokens, Hq, Hkv, rotary, per;  // per: tokens of a CTA
+  const __nv_bfloat16* q;
+  long long ldq;
+  const __nv_bfloat16* k;
+  long long ldk;
+  const __nv_bfloat16* v;
+  long long ldv;
+  const int* pos;
+  const long long* slots;
+  long long num_slots;
+  const float* freq;
+  const __nv_bfloat16* qw;
+  const __nv_bfloat16* kw;
+  float eps;
+  __nv_bfloat16* q_out;
+  long long ldqo;
+  __nv_bfloat16* k_cache;
+  long long ldkc;
+  __nv_bfloat16* v_cache;
+  long long ldvc;
+  unsigned int* error;
+};
+cudaError_t launch_kv_append(AppendParams p, int d, bool pairs, cudaStream_t s);
+
+// Launchers. grid: CTAs of the launch (the workspace has two parts a CTA).
+cudaError_t launch_attn_rows(const AttnParams& p, int d, int grid, cudaStream_t s);
+constexpr int kAttnRowsM = 16;
+
+}  // namespace gdn

@@ -18,8 +18,8 @@
 // 8192 8.0 in a graph, the weights' bytes being 6.2, and 128 rows of it 15.4. 129 to 512
 // rows of it take 30 to 32: 40 tiles on 76 pairs, 128 steps in a row.
 #include <algorithm>
-#include <atomic>
 
+#include "gdn_host.h"
 #include "gdn_prefill.cuh"
 #include "gdn_tc_pair.cuh"
 
@@ -456,28 +456,6 @@ bool encode_map(CUtensorMap* m, const void* base, long long rows, long long cols
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A kernel's shared memory opt-in (the most any launch of it takes), once a
-// device.
-template <auto* KERNEL>
-cudaError_t opt_in(size_t bytes) {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-  const cudaError_t f = cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (f == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
-  return f;
-}
-
-int sm_count() {
-  static int count[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  if (!count[dev]) cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev);
-  return count[dev] > 0 ? count[dev] : 152;
 }
 
 template <int BN>

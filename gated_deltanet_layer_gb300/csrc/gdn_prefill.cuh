@@ -194,6 +194,23 @@ struct LinearParams {
   int act;
 };
 
+// linear_w4: as LinearParams, with the weights in 4 bits.
+struct W4Params {
+  int M, N, K, group;
+  bool mx;  // E2M1 codes and e8m0 scales; else whole numbers, bf16 scales, zeros (nullptr: 8)
+  const __nv_bfloat16* x;
+  long long ldx;
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* residual;
+  long long ldr;
+  __nv_bfloat16* out;
+  long long ldo;
+  int act, split;  // split: CTAs that share the columns
+};
+
 struct SlotParams {
   int R, N, B, max_blocks, free_cap;
   const int* new_lens;
@@ -234,6 +251,7 @@ cudaError_t launch_delta(const DeltaParams& p, int d, bool state_bf16, unsigned 
 cudaError_t launch_delta_chunks(const DeltaParams& p, int d, bool state_bf16, unsigned char* ws, cudaStream_t s);
 size_t delta_chunk_bytes(long long tokens, long long seqs, int Hk, int Hv, int d);
 cudaError_t launch_linear(const LinearParams& p, cudaStream_t s);
+cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s);
 // Waits for the stream, reads the linear kernels' error word and clears it.
 cudaError_t linear_error(unsigned int* word, cudaStream_t s);
 cudaError_t launch_slot_map(const SlotParams& p, cudaStream_t s);

@@ -2,6 +2,7 @@
 // checks and launches.
 #include <new>
 
+#include "gdn_host.h"
 #include "gdn_prefill.cuh"
 #include "gdn_prefill.h"
 
@@ -42,41 +43,12 @@ gdn_status validate(const gdn_prefill_config* c) {
 
 int channels(const gdn_prefill_config& c) { return 2 * c.num_k_heads * c.head_k_dim + c.num_v_heads * c.head_v_dim; }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Memory that a call reads or writes: n bytes from p, or of a matrix the `width` bytes of rows
-// `ld` bytes apart.
-struct Span {
-  const void* p;
-  size_t n, ld = 0, width = 0;
-};
-Span matrix(const void* p, long long rows, long long ld, long long cols) {
-  return Span{p, rows > 0 ? (size_t)((rows - 1) * ld + cols) * 2 : 0, (size_t)ld * 2, (size_t)cols * 2};
-}
-bool overlap(const Span& a, const Span& b) {
-  if (!a.p || !b.p || !a.n || !b.n) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  if (x >= y + b.n || y >= x + a.n) return false;
-  if (!a.ld || a.ld != b.ld) return true;
-  // columns of the same rows: b's begin `at` bytes after a's in a row, or in the one before
-  const size_t at = y >= x ? (y - x) % a.ld : (a.ld - (x - y) % a.ld) % a.ld;
-  return at < a.width || at + b.width > a.ld;
-}
-template <int N>
-bool overlaps_any(const Span& out, const Span (&in)[N]) {
-  for (const Span& s : in)
-    if (overlap(out, s)) return true;
-  return false;
-}
-
 // GDN_ERR_ARG where the current device is not the handle's.
 gdn_status check_device(const gdn_prefill* h) {
   int device;
   if (cudaGetDevice(&device) != cudaSuccess) return GDN_ERR_CUDA;
   return device == h->device ? GDN_OK : GDN_ERR_ARG;
 }
-
-gdn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 // Checks common to the two calls over a ragged batch.
 gdn_status check_ragged(const gdn_prefill* h, int32_t seqs, int32_t tokens, const int32_t* cu, const int32_t* in,
@@ -276,6 +248,51 @@ extern "C" gdn_status gdn_linear(int32_t rows, int32_t cols, int32_t inner, cons
   p.ldo = ldo;
   p.act = activation;
   return cuda_status(launch_linear(p, (cudaStream_t)stream));
+}
+
+extern "C" gdn_status gdn_linear_w4(int32_t rows, int32_t cols, int32_t inner, const void* x, int64_t ldx, int32_t format,
+                                    int32_t group, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                                    const void* bias, int32_t activation, const void* residual, int64_t ldr, void* out,
+                                    int64_t ldo, void* stream) {
+  if (rows < 0 || cols < 0 || inner < 1) return GDN_ERR_ARG;
+  if (activation < GDN_ACT_NONE || activation > GDN_ACT_GELU_TANH) return GDN_ERR_ARG;
+  if (format != GDN_W4_INT && format != GDN_W4_MXFP4) return GDN_ERR_ARG;
+  if (format == GDN_W4_MXFP4 && zeros) return GDN_ERR_ARG;
+  if (group != 32 && (format == GDN_W4_MXFP4 || (group != 64 && group != 128))) return GDN_ERR_UNSUPPORTED;
+  if (inner % group) return GDN_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return GDN_OK;
+  if (!x || !codes || !scales || !out) return GDN_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, format == GDN_W4_INT ? 2 : 1) || !aligned(bias, 2) ||
+      !aligned(residual, 2) || !aligned(out, 2))
+    return GDN_ERR_ARG;
+  if (ldx < inner || ldo < cols || (residual && ldr < cols) || ldx % 8) return GDN_ERR_ARG;
+  constexpr int32_t kEdge = INT32_MAX - 255;
+  if (rows > (1 << 20) || cols > kEdge / 8 || inner > kEdge) return GDN_ERR_UNSUPPORTED;  // the grid, and a tile past the edge
+  const size_t n = (size_t)cols * (size_t)(inner / group);
+  const Span o = matrix(out, rows, ldo, cols), r = matrix(residual, rows, ldr, cols);
+  const Span in[] = {matrix(x, rows, ldx, inner), {codes, (size_t)cols * (size_t)(inner / 2)},
+                     {scales, n * (format == GDN_W4_INT ? 2 : 1)}, {zeros, zeros ? n : 0},
+                     {bias, bias ? (size_t)cols * 2 : 0}};
+  if (overlaps_any(o, in)) return GDN_ERR_ARG;
+  if (overlap(o, r) && !(residual == out && ldr == ldo)) return GDN_ERR_ARG;
+  W4Params p{};
+  p.M = rows;
+  p.N = cols;
+  p.K = inner;
+  p.group = group;
+  p.mx = format == GDN_W4_MXFP4;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.ldx = ldx;
+  p.codes = codes;
+  p.scales = scales;
+  p.zeros = zeros;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.ldr = ldr;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ldo = ldo;
+  p.act = activation;
+  return cuda_status(launch_linear_w4(p, (cudaStream_t)stream));
 }
 
 extern "C" gdn_status gdn_linear_check(void* stream, uint32_t* detail) {

@@ -156,6 +156,29 @@ gdn_status gdn_linear(int32_t rows, int32_t cols, int32_t inner, const void* x, 
                       int64_t ldw, const void* bias, int32_t activation, const void* residual, int64_t ldr,
                       void* out, int64_t ldo, void* stream);
 
+/* 4-bit weights of gdn_linear_w4: element 2i in the low nibble of byte i.
+ * GDN_W4_INT: code 0 .. 15 stands for (code - zero) * scale, scales bf16 and
+ *   zeros uint8 (NULL: 8), one for each group of 32, 64 or 128 columns.
+ * GDN_W4_MXFP4: E2M1 codes and e8m0 scales for each 32 columns, the layout of
+ *   gdn_decode.h's MXFP4 in_proj_qkvz. */
+typedef enum { GDN_W4_INT = 0, GDN_W4_MXFP4 = 1 } gdn_w4_format;
+
+/* gdn_linear with the weights in 4 bits, for few rows (decode and verify
+ * steps): out[m][n] = bf16(act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]).
+ * The activations stay bf16 (where gdn_decode_step quantises them to MXFP4). Weights
+ * are taken as the codes and scales stand for them, without a rounding; sums
+ * are f32. Within the columns that a CTA adds up, x keeps what is above 2^-31 of its row's
+ * largest value there (exact above 2^-27). Up to 64 rows read the weights once; more
+ * are taken 64 at a time. inner is a multiple of `group`.
+ * x [rows][ldx >= inner] (16-byte aligned, ldx a multiple of 8), codes
+ * [cols][inner / 2] (16-byte aligned), scales and zeros [cols][inner / group];
+ * the rest as for gdn_linear. A value of x that is not finite makes its row of out NaN
+ * or infinite, a scale that is not its column's; no other is touched. No workspace, no handle. */
+gdn_status gdn_linear_w4(int32_t rows, int32_t cols, int32_t inner, const void* x, int64_t ldx, int32_t format,
+                         int32_t group, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                         const void* bias, int32_t activation, const void* residual, int64_t ldr, void* out,
+                         int64_t ldo, void* stream);
+
 /* Synchronise `stream`, read the error word of this device's gdn_linear calls
  * and clear it: GDN_OK, or GDN_ERR_DEADLINE when a wait inside a kernel passed
  * its limit (the call's outputs are then not all written). *detail (optional)
