@@ -17,9 +17,9 @@ namespace gdn {
 // What of an index error (bits 23..16 of the error word).
 constexpr uint32_t kAttnBlock = 1, kAttnOffsets = 2, kAttnLength = 3, kAttnWait = 4, kAttnContext = 5;
 
-// Up to this many requests every CTA plans by itself, in shared memory; with more of
-// them a kernel before leaves the plan in the workspace.
-constexpr int kAttnPlanned = 256;
+// Up to this many requests every CTA plans by itself, in shared memory (as far as it has
+// some left); with more of them a kernel before leaves the plan in the workspace.
+constexpr int kAttnPlanned = 256, kAttnPlannedTiles = 32;
 
 // n / d for 0 <= n < 2^31.
 struct FastDiv {
@@ -53,7 +53,7 @@ struct AttnParams {
   long long ldo;
   float scale_log2;           // scale times log2(e)
   unsigned int* error;        // sticky word
-  unsigned int* done;         // [grid] parts finished of the task whose first part is the CTA's; zero between calls
+  unsigned int* done;         // [2 grid] parts finished of the task whose first part is the CTA's; zero between calls
   float* part;                // [2 grid][M][D] sums of weights times values, relative to the part's maximum
   float2* part_ml;            // [2 grid][M] maximum (of scores times log2 e) and sum of weights
   int4* seq;                  // [seqs + 1] of the workspace: the plan, where a kernel before makes it
@@ -210,31 +210,37 @@ struct Walk {
     ctx = q.z;
     rows = Tiles<M, KT>::rows(n, p.group.d);
   }
-  // To unit u, which is one of start[seqs].
-  __device__ __forceinline__ void to(long long u) {
-    int lo = 0, hi = p.seqs - 1;
-    while (lo < hi) {  // the last request that starts at or before u: it has units
-      const int mid = (lo + hi + 1) >> 1;
-      if (start[mid] <= u)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    s = lo;
-    load();
+  // Where unit u, one of start[seqs], is: at = {s, h, i, j}. A converged warp.
+  __device__ __forceinline__ static void find(const AttnParams& p, const int4* seq, const long long* start, long long u, int (&at)[4]) {
+    const int lane = threadIdx.x & 31;
+    // the last of n candidates for which f holds (it does for the first, and for none after one for
+    // which it does not), 32 at a time
+    const auto last_of = [&](int n, auto f) {
+      int lo = 0;
+      while (n > 1) {
+        const int stride = (n + 31) / 32, k = lane * stride;
+        const unsigned held = __ballot_sync(0xffffffffu, k < n && (lane == 0 || f(lo + k)));
+        const int last = (31 - __clz(held)) * stride;
+        lo += last;
+        n = min(stride, n - last);
+      }
+      return lo;
+    };
+    // the last request that starts at or before u: it has units
+    const int s = last_of(p.seqs, [&](int k) { return start[k] <= u; });
+    const int4 q = seq[s];
     const long long first = start[s], per = (start[s + 1] - first) / p.Hkv;
-    h = (int)((u - first) / per);
+    const int h = (int)((u - first) / per), G = p.group.d;
     const long long in = u - first - h * per;
-    lo = 0, hi = rows - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (Tiles<M, KT>::before(p.group.d, ctx, mid) <= in)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    i = lo;
-    j = (int)(in - Tiles<M, KT>::before(p.group.d, ctx, i));
+    const int i = last_of(Tiles<M, KT>::rows(q.y, G), [&](int k) { return Tiles<M, KT>::before(G, q.z, k) <= in; });
+    if (lane == 0) at[0] = s, at[1] = h, at[2] = i, at[3] = (int)(in - Tiles<M, KT>::before(G, q.z, i));
+  }
+  __device__ __forceinline__ void from(const int (&at)[4], long long u) {
+    s = at[0];
+    load();
+    h = at[1];
+    i = at[2];
+    j = at[3];
     nt = Tiles<M, KT>::keys(p, n, ctx, i);
     task = u - j;
   }
@@ -331,5 +337,6 @@ cudaError_t launch_kv_append(AppendParams p, int d, bool pairs, cudaStream_t s);
 // Launchers. grid: CTAs of the launch (the workspace has two parts a CTA).
 cudaError_t launch_attn_rows(const AttnParams& p, int d, int grid, cudaStream_t s);
 constexpr int kAttnRowsM = 16;
+cudaError_t launch_attn_tiles(const AttnParams& p, int d, int grid, cudaStream_t s);
 
 }  // namespace gdn

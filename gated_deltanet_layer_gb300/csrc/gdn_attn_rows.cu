@@ -44,6 +44,7 @@ struct RowsSmem {
   long long start[kAttnPlanned + 1];
   PlanScratch<C::kW * 32> scan;
   float2 row_ml[kM];
+  int at[4];  // the first unit's request, head, row tile and key tile
   unsigned last;
 };
 
@@ -115,9 +116,12 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const AttnParam
   const long long u0 = shares.first(blockIdx.x), u1 = shares.first(blockIdx.x + 1);
   const int steps = (int)(u1 - u0);
 
+  if (warp == 0) Walk<kM, KT>::find(p, seq, start, u0, s.at);
+  __syncthreads();
+
   // The ring's loads: lanes 0 - 15 know the slots of the warp's 16 keys, a step ahead.
   Walk<kM, KT> ahead(p, seq, start);
-  ahead.to(u0);
+  ahead.from(s.at, u0);
   const uint32_t ring = smem_u32(s.ring[warp]);
   KeyBlock kb = key_block(p, ahead.s, ahead.j * KT + warp * 16 + (lane & 15), ahead.ctx + ahead.n);
   int issued = 0;
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const AttnParam
   for (int i = 0; i < ST - 1; ++i) issue();
 
   Walk<kM, KT> w(p, seq, start);
-  w.to(u0);
+  w.from(s.at, u0);
   float o[D / 8][4], m[2], l[2];
   int last_key[2], first_last = 0;  // last key that the thread's two rows see; the task's first row's
   bool fresh = true;
@@ -382,8 +386,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
 }
 
 template <int D>
-cudaError_t launch(const AttnParams& p, int grid, cudaStream_t s) {
+cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   const size_t smem = sizeof(RowsSmem<D>) + 128;
+  if (p.seqs <= kAttnPlanned) p.seq = nullptr;
   cudaError_t e = opt_in<attn_rows<D>>(smem);
   if (e != cudaSuccess) return e;
   if (p.seq) {
