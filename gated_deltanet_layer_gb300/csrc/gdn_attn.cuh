@@ -3,7 +3,8 @@
 //
 // A task is (request, key/value head, tile of M query rows); query row r of a request
 // and key/value head is token r / G, query head r % G of the head's G = Hq / Hkv. A task's
-// units are the tiles of KT keys that its last row sees. All tasks' units form one line, in
+// units are the tiles of KT keys that its last row sees, and E more for what a task
+// takes beside its tiles (they come last, and nobody does anything in them). All tasks' units form one line, in
 // the order request, head, row tile, key tile, and every CTA takes an equal, contiguous
 // share of it, whatever the lengths: a CTA has whole tasks, and at its two ends
 // parts of tasks that it shares with the CTAs beside it. The parts go to the workspace, and
@@ -85,22 +86,22 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 // Row tiles of a request and their key tiles. Tile i's last row is min((i + 1) M, n G) - 1, so
 // all but the last tile see ctx + ceil((i + 1) M / G) keys, which are
 // ceil((G ctx + (i + 1) M) / (G KT)) tiles.
-template <int M, int KT>
+template <int M, int KT, int E>
 struct Tiles {
   __device__ __forceinline__ static int rows(int n, int G) { return (n * G + M - 1) / M; }
   __device__ __forceinline__ static int keys(const AttnParams& p, int n, int ctx, int i) {
     const uint32_t G = p.group.d, last = min((uint32_t)(i + 1) * M, n * G) - 1;
     return ((uint32_t)ctx + p.group.div(last) + KT) / KT;
   }
-  // key tiles before row tile i (at most the last one)
+  // units before row tile i (at most the last one)
   __device__ __forceinline__ static long long before(int G, int ctx, int i) {
     if (i == 0) return 0;
     const long long m = (long long)G * KT;
-    return floor_sum(i, m, M, (long long)G * ctx + M + m - 1);
+    return floor_sum(i, m, M, (long long)G * ctx + M + m - 1) + (long long)i * E;
   }
   __device__ __forceinline__ static long long total(const AttnParams& p, int n, int ctx) {
     const int t = rows(n, p.group.d);
-    return before(p.group.d, ctx, t - 1) + keys(p, n, ctx, t - 1);
+    return before(p.group.d, ctx, t - 1) + keys(p, n, ctx, t - 1) + E;
   }
 };
 
@@ -114,7 +115,7 @@ struct PlanScratch {
 // before request s, seq[seqs].x the first pad row and start[seqs] all units. The offsets are the
 // caller's: row ends are the running maximum of the offsets that lie within the rows, and
 // a request whose offsets are not its row ends is padding. A block of NT threads.
-template <int M, int KT, int NT>
+template <int M, int KT, int E, int NT>
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long long* start, PlanScratch<NT>& x, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int top = 0;
@@ -148,7 +149,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long l
       if (far) attn_record(p.error, kAttnContext, s);
     }
     if (long_ || far) n = 0;
-    const long long mine = n > 0 ? p.Hkv * Tiles<M, KT>::total(p, n, c) : 0;
+    const long long mine = n > 0 ? p.Hkv * Tiles<M, KT, E>::total(p, n, c) : 0;
     long long u = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -192,7 +193,7 @@ struct Shares {
 };
 
 // A walk over the units, task by task.
-template <int M, int KT>
+template <int M, int KT, int E>
 struct Walk {
   const AttnParams& p;
   const int4* seq;
@@ -208,7 +209,7 @@ struct Walk {
     row0 = q.x;
     n = q.y;
     ctx = q.z;
-    rows = Tiles<M, KT>::rows(n, p.group.d);
+    rows = Tiles<M, KT, E>::rows(n, p.group.d);
   }
   // Where unit u, one of start[seqs], is: at = {s, h, i, j}. A converged warp.
   __device__ __forceinline__ static void find(const AttnParams& p, const int4* seq, const long long* start, long long u, int (&at)[4]) {
@@ -232,8 +233,8 @@ struct Walk {
     const long long first = start[s], per = (start[s + 1] - first) / p.Hkv;
     const int h = (int)((u - first) / per), G = p.group.d;
     const long long in = u - first - h * per;
-    const int i = last_of(Tiles<M, KT>::rows(q.y, G), [&](int k) { return Tiles<M, KT>::before(G, q.z, k) <= in; });
-    if (lane == 0) at[0] = s, at[1] = h, at[2] = i, at[3] = (int)(in - Tiles<M, KT>::before(G, q.z, i));
+    const int i = last_of(Tiles<M, KT, E>::rows(q.y, G), [&](int k) { return Tiles<M, KT, E>::before(G, q.z, k) <= in; });
+    if (lane == 0) at[0] = s, at[1] = h, at[2] = i, at[3] = (int)(in - Tiles<M, KT, E>::before(G, q.z, i));
   }
   __device__ __forceinline__ void from(const int (&at)[4], long long u) {
     s = at[0];
@@ -241,11 +242,11 @@ struct Walk {
     h = at[1];
     i = at[2];
     j = at[3];
-    nt = Tiles<M, KT>::keys(p, n, ctx, i);
+    nt = Tiles<M, KT, E>::keys(p, n, ctx, i);
     task = u - j;
   }
   __device__ __forceinline__ void next_task() {
-    task += nt;
+    task += nt + E;
     j = 0;
     if (++i == rows) {
       i = 0;
@@ -257,7 +258,7 @@ struct Walk {
         load();
       }
     }
-    nt = Tiles<M, KT>::keys(p, n, ctx, i);
+    nt = Tiles<M, KT, E>::keys(p, n, ctx, i);
   }
 };
 

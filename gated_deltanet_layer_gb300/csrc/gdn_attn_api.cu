@@ -103,6 +103,7 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
   if (ldq % 8 || ldo % 8 || (gate && ldg % 8) || ldk % 8 || ldv % 8) return GDN_ERR_ARG;
   const long long slots = (long long)num_blocks * c.block_size;
   if (slots > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (ldk >= (1LL << 38) || ldv >= (1LL << 38)) return GDN_ERR_UNSUPPORTED;  // a tile map's largest stride
   const Layout l(c, h->grid);
   const Span o = matrix(out, tokens, ldo, cols);
   const Span in[] = {matrix(q, tokens, ldq, cols), matrix(gate, tokens, ldg, cols), matrix(k_cache, slots, ldk, kv),
@@ -146,7 +147,7 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
     p.start = reinterpret_cast<long long*>(h->ws + l.start);
   }
   // Rows of a request and key/value head: a tile of 16 has them all, or the tensor cores' tiles.
-  const bool few = (long long)p.max_len * p.group.d <= kAttnRowsM;
+  const bool few = (long long)p.max_len * p.group.d <= kAttnRowsM || num_blocks == 0;
   return cuda_status((few ? launch_attn_rows : launch_attn_tiles)(p, c.head_dim, h->grid, (cudaStream_t)stream));
 }
 

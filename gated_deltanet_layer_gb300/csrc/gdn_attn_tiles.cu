@@ -9,9 +9,9 @@
 // multiplied only when the maximum grows by more, so that weights are at most 2^8 and hardly a
 // tile is corrected; the sums divide it out again.
 //
-// Warps 0 - 7: the softmax, a row a thread, and the outputs. Warps 8 - 11: keys and values, 16 bytes
-// a lane by cp.async, from any slot to where the swizzled operand has it, zeros past the
-// last key. Warp 12: the products. With two row tiles the tensor cores work on one while
+// Warps 0 - 7: the softmax, a row a thread, and the outputs. Warps 8 - 11: keys and values by
+// TMA, four rows a copy from any four slots (so blocks of any size are alike, and rows past the last key
+// are zeros). Warp 12: the products. With two row tiles the tensor cores work on one while
 // the softmax works on the other; with one, S alternates between two buffers.
 #include <climits>
 
@@ -34,6 +34,7 @@ struct Cfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;        // row tiles of a task
   static constexpr int kM = 128 * kTiles;
   static constexpr int kKT = D == 256 ? 64 : 128;        // keys of a tile
+  static constexpr int kE = D == 256 ? 6 : 3;            // tiles' time that a task takes beside its tiles
   static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 5 : 4;
   static constexpr int kSlotBytes = kKT * D * 2;         // 32 KB, 16 KB with heads of 64
   static constexpr int kChunk = kKT * 128;               // bytes of 64 columns of a slot
@@ -47,7 +48,7 @@ struct alignas(1024) TileSmem {
   using C = Cfg<D>;
   unsigned char q[C::kTiles][128 * D * 2];
   unsigned char ring[C::kSlots][C::kSlotBytes];
-  uint64_t q_full, q_empty, full[C::kSlots], empty[C::kSlots], s_full[2], p_full[2], o_done[2], seg_done[2];
+  uint64_t q_full, q_empty, edge, full[C::kSlots], empty[C::kSlots], s_full[2], p_full[2], o_done[2], seg_done[2][2];
   uint32_t tmem;
   int failed;          // a wait has passed its limit
   unsigned last[2];
@@ -146,24 +147,25 @@ __device__ __forceinline__ void put32(const AttnParams& p, long long row, long l
 template <int D>
 struct Segments {
   using C = Cfg<D>;
-  Walk<C::kM, C::kKT> w;
+  Walk<C::kM, C::kKT, C::kE> w;
   long long u, u1;
   int j0, j1;  // key tiles of the segment
   __device__ __forceinline__ Segments(const AttnParams& p, const int4* seq, const long long* start, long long u0, long long u1,
                                       const int (&at)[4])
       : w(p, seq, start), u(u0), u1(u1) {
     w.from(at, u0);
-    cut();
-  }
-  __device__ __forceinline__ void cut() {
     j0 = w.j;
     j1 = (int)min((long long)w.nt, j0 + (u1 - u));
+    if (j0 >= w.nt) next();  // what the share begins with of a task has no tiles
   }
+  // Whether there is a segment.
+  __device__ __forceinline__ bool valid() const { return u < u1; }
   __device__ __forceinline__ bool next() {
-    u += j1 - j0;
+    u = w.task + w.nt + C::kE;
     if (u >= u1) return false;
     w.next_task();
-    cut();
+    j0 = 0;
+    j1 = (int)min((long long)w.nt, u1 - u);
     return true;
   }
   // end of row tile t's key tiles in the segment: its last row may see fewer than the task's
@@ -175,8 +177,23 @@ struct Segments {
   }
 };
 
+// The caches' rows as the copies want them: one at a time, and in boxes of `box` rows (0: no boxes).
+struct TileMaps {
+  CUtensorMap k, v, kb, vb;
+  int box;
+};
+// Four rows of 64 columns from column x on, each of its own, to 512 bytes of shared memory.
+__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, int x, const int (&row)[4], uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int D>
-__global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
+__global__ void __launch_bounds__(kNT, 1)
+    attn_tiles(const __grid_constant__ TileMaps maps, const AttnParams p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) unsigned char raw[];
   static_assert(sizeof(TileSmem<D>) <= 232448, "227 KB of shared memory a CTA");
@@ -186,6 +203,10 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
   if (tid == 0) {
     mbar_init(&s.q_full, 4);
     mbar_init(&s.q_empty, 1);
+    mbar_init(&s.edge, 4);
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+    if (maps.box) prefetch_tensormap(&maps.kb), prefetch_tensormap(&maps.vb);
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&s.full[i], 4);
       mbar_init(&s.empty[i], 1);
@@ -194,7 +215,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 4);
       mbar_init(&s.o_done[i], 1);
-      mbar_init(&s.seg_done[i], 4 * C::kTiles);
+      for (int t = 0; t < 2; ++t) mbar_init(&s.seg_done[t][i], 4);
     }
     s.failed = s.dirty[0] = s.dirty[1] = 0;
     fence_mbar_init();
@@ -209,18 +230,19 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
     seq = p.seq;
     start = p.start;
   } else {
-    attn_plan<C::kM, KT, kNT>(p, s.seq, s.start, s.scan, blockIdx.x == 0);
+    attn_plan<C::kM, KT, C::kE, kNT>(p, s.seq, s.start, s.scan, blockIdx.x == 0);
   }
   attn_zero_rows<kNT / 32>(p, seq, p.Hkv * p.group.d * D);
   const long long units = start[p.seqs];
-  const Shares shares(units, (int)max(1LL, min((long long)gridDim.x, (units + 1) / 2)));
+  const Shares shares(units, (int)max(1LL, min((long long)gridDim.x, (units + C::kE + 1) / (C::kE + 2))));
   const bool on = units > 0 && blockIdx.x < shares.ctas;
   const long long u0 = shares.first(blockIdx.x), u1 = shares.first(blockIdx.x + 1);
-  if (warp == 0 && on) Walk<C::kM, KT>::find(p, seq, start, u0, s.at);
+  if (warp == 0 && on) Walk<C::kM, KT, C::kE>::find(p, seq, start, u0, s.at);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
+  const int rows_end = p.num_blocks * (int)p.block.d;
   bool ok = on;
 
   if (warp < kLoad0) {
@@ -230,9 +252,9 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const int r = (warp & 3) * 32 + lane;
       Segments<D> g(p, seq, start, u0, u1, s.at);
-      int sn = 0, pv = 0;  // S tiles and PV products so far (of the row tile)
+      int sn = 0, pv = 0, ends = 0;  // S tiles, PV products and segments with any so far (of the row tile)
       int seg = 0;
-      do {
+      if (g.valid()) do {
         const int rows = g.w.n * (int)p.group.d, first = g.w.i * C::kM + t * 128, R = first + r;
         const bool live = R < rows, warp_live = first + (warp & 3) * 32 < rows;
         const int last_key = g.w.ctx + (int)p.group.div(min(R, rows - 1));
@@ -263,7 +285,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
               const float grown = fmaxf(m, tile_top), f = m == -INFINITY ? 0.f : ex2(m - grown);
               if (j > g.j0) {
                 if (C::kTiles == 1) {  // S came before the last PV
-                  ok = mbar_wait(&s.o_done[t], (pv - 1) & 1);
+                  ok = mbar_wait(&s.o_done[(pv - 1) & 1], ((pv - 1) >> 1) & 1);
                   ok = __all_sync(0xffffffffu, ok);
                   if (!ok) break;
                   tc_fence_after();
@@ -306,8 +328,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
         // ---- the task's end, or this CTA's
         const bool any = end > g.j0;
         if (any && ok) {
-          if (C::kTiles == 1 && end - g.j0 > 1) ok = mbar_wait(&s.o_done[t], (pv - 2) & 1);
-          ok = ok && mbar_wait(&s.o_done[t], (pv - 1) & 1);
+          ok = C::kTiles == 1 ? mbar_wait(&s.o_done[(pv - 1) & 1], ((pv - 1) >> 1) & 1) : mbar_wait(&s.o_done[t], ends++ & 1);
           tc_fence_after();
         }
         if (!(ok = named_all(1 + t, 128, ok))) break;
@@ -317,7 +338,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
         const uint32_t tok = p.group.div(live ? R : 0), hd = (live ? R : 0) - tok * p.group.d;
         const long long row = g.w.row0 + tok, col = ((long long)g.w.h * p.group.d + hd) * D;
         const int* poison = s.poison[seg & 1];
-        const bool flagged = s.dirty[seg & 1] != 0;
+        const bool flagged = any && s.dirty[seg & 1] != 0;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (warp_live) {
 #pragma unroll 1
@@ -345,7 +366,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
           if (!whole && live) p.part_ml[slot + r] = make_float2(m, l);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.seg_done[seg & 1]);
+        if (lane == 0 && any) mbar_arrive(&s.seg_done[t][seg & 1]);
         if (!whole && first < rows) {
           const int c0 = shares.owner(t0), c1 = shares.owner(t1 - 1);
           __threadfence();
@@ -359,34 +380,62 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
             // every part is there: the first CTA's second one, the others' first
             if (r == 0) p.done[2 * c0 + t] = 0;
             const auto at = [&](int c) { return (2LL * c + (c == c0)) * C::kM + t * 128; };
-            // eight lanes a row
-            for (int q = r >> 3; q < min(128, rows - first); q += 16) {
-              float top = -INFINITY, sum = 0.f;
-              for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.part_ml[at(c) + q]).x);
+            // A lane has its row's maximum and sum; the outputs go by rows, a row the warp's lanes wide.
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.part_ml[at(c) + r]).x);
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const float2 ml = __ldcg(&p.part_ml[at(c) + r]);
+              sum += ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - top));
+            }
+            const float in = sum == 0.f ? 0.f : 1.f / sum;
+            constexpr int kV = D / 32;  // columns of a lane
+            const int count = min(32, rows - first - (warp & 3) * 32);
+#pragma unroll 1
+            for (int q0 = 0; q0 < count; q0 += 4) {
+              float o[4][kV] = {};
+#pragma unroll 2
               for (int c = c0; c <= c1; ++c) {
-                const float2 ml = __ldcg(&p.part_ml[at(c) + q]);
-                sum += ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - top));
-              }
-              const float in = sum == 0.f ? 0.f : 1.f / sum;
-              const int RR = first + q;
-              const uint32_t tk = p.group.div(RR), hh = RR - tk * p.group.d;
-              for (int k = (r & 7) * 32; k < D; k += 256) {
-                float o[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-                for (int c = c0; c <= c1; ++c) {
-                  const float pm = __ldcg(&p.part_ml[at(c) + q]).x, e = pm == -INFINITY ? 0.f : ex2(pm - top);
-                  const float4* src = reinterpret_cast<const float4*>(p.part + (at(c) + q) * D + k);
+                for (int k = 0; k < 4; ++k) {
+                  const long long q = at(c) + (warp & 3) * 32 + q0 + k;  // a part has 128 rows, live or not
+                  const float pm = __ldcg(&p.part_ml[q]).x, tp = __shfl_sync(0xffffffffu, top, q0 + k);
+                  const float e = pm == -INFINITY ? 0.f : ex2(pm - tp);
+                  const float* src = p.part + q * D + lane * kV;
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const float4 v = __ldcg(src + i);
-                    o[4 * i] = fmaf(v.x, e, o[4 * i]);
-                    o[4 * i + 1] = fmaf(v.y, e, o[4 * i + 1]);
-                    o[4 * i + 2] = fmaf(v.z, e, o[4 * i + 2]);
-                    o[4 * i + 3] = fmaf(v.w, e, o[4 * i + 3]);
+                  for (int i = 0; i < kV; i += 2) {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src + i));
+                    o[k][i] = fmaf(v.x, e, o[k][i]);
+                    o[k][i + 1] = fmaf(v.y, e, o[k][i + 1]);
                   }
                 }
-                put32(p, g.w.row0 + tk, ((long long)g.w.h * p.group.d + hh) * D + k, o, in);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float f = __shfl_sync(0xffffffffu, in, q0 + k);
+                if (q0 + k >= count) break;
+                const int RR = first + (warp & 3) * 32 + q0 + k;
+                const uint32_t tk = p.group.div(RR), hh = RR - tk * p.group.d;
+                const long long rw = g.w.row0 + tk, cl = ((long long)g.w.h * p.group.d + hh) * D + lane * kV;
+                uint32_t w[kV / 2];
+#pragma unroll
+                for (int i = 0; i < kV; i += 2) {
+                  float a = o[k][i] * f, b = o[k][i + 1] * f;
+                  if (p.gate) {
+                    const uint32_t z = *reinterpret_cast<const uint32_t*>(p.gate + rw * p.ldg + cl + i);
+                    a = __fdividef(a, 1.f + __expf(-bf16_lo(z)));
+                    b = __fdividef(b, 1.f + __expf(-bf16_hi(z)));
+                  }
+                  w[i / 2] = pack2(a, b);
+                }
+                __nv_bfloat16* to = p.out + rw * p.ldo + cl;
+                if (kV == 2)
+                  *reinterpret_cast<uint32_t*>(to) = w[0];
+                else if (kV == 4)
+                  *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[kV / 2 - 1]);
+                else
+                  *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1 % (kV / 2)], w[2 % (kV / 2)], w[kV / 2 - 1]);
               }
             }
           }
@@ -399,42 +448,36 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
     if (warp < kMma) {
       // ---- keys, values and queries
       const int wl = warp - kLoad0, lt = tid - kLoad0 * 32;
-      constexpr int kPieces = D / 8;                    // 16-byte pieces of a row
-      constexpr int kPer = 32 / kPieces > 0 ? 32 / kPieces : 1;  // rows a warp copies at once
-      constexpr int kKeys = KT / 4;                     // keys of a warp
-      int n = 0;        // slots filled
-      int arrived = 0;  // slots whose copies are done and told
-      int qs = 0;       // tasks whose queries are loaded
-      // Slot i is told once its copies have landed, two slots later.
-      const auto tell = [&](int upto) {
-        while (arrived < upto) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.full[arrived % SLOTS]);
-          ++arrived;
-        }
-      };
-      const auto flush = [&] {
-        cp_async_wait_pending(0);
-        tell(n);
-      };
-      // A wait before which everything that has been filled is told.
-      const auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (!__all_sync(0xffffffffu, mbar_test(b, parity))) {
-          flush();
-          ok = __all_sync(0xffffffffu, mbar_wait(b, parity));
-        }
-        return ok;
-      };
+      constexpr int kKeys = KT / 4;           // keys of a warp
+      constexpr int kFours = kKeys / 4;       // of them four a copy, 64 columns wide: a lane each
+      constexpr uint32_t kShare = kKeys * D * 2;
+      static_assert(kFours * (D / 64) <= 32, "one copy a lane");
+      const int four = lane % kFours, chunk = lane / kFours;
+      const bool issues = chunk < D / 64;
+      const uint32_t place = chunk * C::kChunk + (wl * kKeys + four * 4) * 128;
+      // Where blocks are made of boxes of 8 rows or more, a whole tile comes as boxes: a copy of four
+      // rows takes an SM 22 cycles whatever its size.
+      const int boxes = min(maps.box, kKeys) > 0 ? kKeys / min(maps.box, kKeys) : 0;  // of a warp's keys, 64 columns wide
+      const int box_chunk = boxes ? lane / boxes : 0, box_row = boxes ? lane % boxes * (kKeys / boxes) : 0;
+      const bool box_issues = box_chunk < D / 64;
+      const uint32_t box_place = box_chunk * C::kChunk + (wl * kKeys + box_row) * 128;
+      int n = 0;                      // slots filled
+      uint32_t edges = 0;             // edge tiles so far
+      const auto wait = [&](uint64_t* b, uint32_t parity) { return ok = __all_sync(0xffffffffu, mbar_wait(b, parity)); };
       if (ok) {
         Segments<D> g(p, seq, start, u0, u1, s.at);
         int seg = 0;
-        const int c = lane % kPieces;
-        const uint32_t piece0 = (c >> 3) * C::kChunk;
-        do {
+        uint32_t waits[2] = {0, 0}, phases[2] = {0, 0};  // by row tile, a bit for even and odd tasks
+        if (g.valid()) do {
           if (seg >= 2) {
-            // the flags are the task's before last until it is through with them
-            wait(&s.seg_done[seg & 1], ((seg >> 1) - 1) & 1);
+            // The flags are the task's before last until its row tiles are through with them. (A row
+            // tile without keys in a segment says nothing: nothing would keep it from running ahead.)
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t)
+              if (waits[t] >> (seg & 1) & 1) {
+                ok = ok && wait(&s.seg_done[t][seg & 1], phases[t] >> (seg & 1) & 1);
+                phases[t] ^= 1u << (seg & 1);
+              }
             if (!(ok = named_all(3, 128, ok))) break;
             const bool flagged = s.dirty[seg & 1] != 0;
             named_sync(3, 128);
@@ -444,181 +487,204 @@ __global__ void __launch_bounds__(kNT, 1) attn_tiles(const AttnParams p) {
               named_sync(3, 128);
             }
           }
+#pragma unroll
+          for (int t = 0; t < C::kTiles; ++t)
+            waits[t] = (waits[t] & ~(1u << (seg & 1))) | (uint32_t)(g.end(t) > g.j0) << (seg & 1);
           const int keys = g.w.ctx + g.w.n, first_last = g.w.ctx + (int)p.group.div(g.w.i * C::kM);
-          const long long col = (long long)g.w.h * D + c * 8;
-          // of a warp's keys, a lane has the slot of one (heads of 256: of the first 16)
+          const int x = g.w.h * D + chunk * 64, box_x = g.w.h * D + box_chunk * 64;
+          // a lane has the slot of one of the warp's keys, a tile ahead
           KeyBlock kb = key_block(p, g.w.s, g.j0 * KT + wl * kKeys + lane % kKeys, keys);
+#pragma unroll 1
           for (int j = g.j0; j < g.j1 && ok; ++j) {
-            const int slot = key_slot(p, kb, g.w.s);
+            int at[4], box_at;
+            {
+              const int slot = key_slot(p, kb, g.w.s), row = slot < 0 ? rows_end : slot;  // past the last row: zeros
+#pragma unroll
+              for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, row, four * 4 + i);
+              box_at = __shfl_sync(0xffffffffu, row, box_row);
+            }
             if (j + 1 < g.j1) kb = key_block(p, g.w.s, (j + 1) * KT + wl * kKeys + lane % kKeys, keys);
 #pragma unroll 1
-            for (int which = 0; which < 2 && ok; ++which) {  // keys, values
+            for (int which = 0; which < 2; ++which, ++n) {  // keys, values
               if (!wait(&s.empty[n % SLOTS], (n / SLOTS & 1) ^ 1)) break;
-              const uint32_t dst = smem_u32(s.ring[n % SLOTS]) + piece0;
-              const __nv_bfloat16* src = (which ? p.v : p.k) + col;
-              const long long ld = which ? p.ldv : p.ldk;
-#pragma unroll
-              for (int r0 = 0; r0 < kKeys; r0 += kPer) {
-                const int rr = r0 + lane / kPieces, row = wl * kKeys + rr;
-                const int at = __shfl_sync(0xffffffffu, slot, rr);
-                cp_async16_or_zero(dst + row * 128 + (((c ^ row) & 7) << 4), src + max(at, 0) * ld, at >= 0);
+              unsigned char* to = s.ring[n % SLOTS];
+              // some row does not see some of these keys
+              const bool edge = which && j * KT + KT - 1 > first_last && g.w.n > 1;
+              uint64_t* bar = edge ? &s.edge : &s.full[n % SLOTS];
+              if (lane == 0) mbar_arrive_expect_tx(bar, kShare);
+              __syncwarp();
+              if (boxes && (j + 1) * KT <= keys) {
+                if (box_issues) tma_load_2d_plain(to + box_place, which ? &maps.vb : &maps.kb, box_x, box_at, bar);
+              } else if (issues) {
+                gather4(to + place, which ? &maps.v : &maps.k, x, at, bar);
               }
-              ++n;
-              if (which && j * KT + KT - 1 > first_last && g.w.n > 1) {
-                // some row does not see some of these keys: 0 x NaN. Values that are not finite are taken
-                // out, and the rows that do see them told by the column's first such key.
-                cp_async_commit();
-                cp_async_wait_pending(0);
+              if (edge) {
+                // 0 x NaN: values that are not finite are taken out, and the rows that do see them told
+                // by the column's first such key
+                if (!wait(&s.edge, edges++ & 1)) break;
+                bool found = false;
+                constexpr int kRow = D / 8;  // 16-byte pieces
+#pragma unroll 4
+                for (int i = lane; i < kKeys * kRow; i += 32) {
+                  const int row = wl * kKeys + i / kRow, c = i % kRow;
+                  const uint4 v = *reinterpret_cast<const uint4*>(to + (c >> 3) * C::kChunk + row * 128 + (((c ^ row) & 7) << 4));
+                  // an exponent of ones, and one, is a carry into the sign's place
+                  const auto not_finite = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                  found |= (not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) != 0;
+                }
+                found = __any_sync(0xffffffffu, found);
+                if (found) {
 #pragma unroll 1
-                for (int r0 = 0; r0 < kKeys; r0 += kPer) {
-                  const int row = wl * kKeys + r0 + lane / kPieces;
-                  unsigned char* at = s.ring[(n - 1) % SLOTS] + piece0 + row * 128 + (((c ^ row) & 7) << 4);
-                  uint4 v = *reinterpret_cast<const uint4*>(at);
-                  uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                  bool bad = false;
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    if ((u[i] & 0x7f80u) == 0x7f80u) {
-                      atomicMin(&s.poison[seg & 1][c * 8 + 2 * i], j * KT + row);
-                      u[i] &= 0xffff0000u;
-                      bad = true;
+                  for (int i = lane; i < kKeys * D; i += 32) {
+                    const int row = wl * kKeys + i / D, c = i % D;
+                    uint16_t* q = reinterpret_cast<uint16_t*>(to + (c >> 6) * C::kChunk + row * 128 + ((((c >> 3) ^ row) & 7) << 4)) + (c & 7);
+                    if ((*q & 0x7f80) == 0x7f80) {
+                      atomicMin(&s.poison[seg & 1][c], j * KT + row);
+                      *q = 0;
                     }
-                    if ((u[i] & 0x7f800000u) == 0x7f800000u) {
-                      atomicMin(&s.poison[seg & 1][c * 8 + 2 * i + 1], j * KT + row);
-                      u[i] &= 0xffffu;
-                      bad = true;
-                    }
-                  }
-                  if (bad) {
-                    s.dirty[seg & 1] = 1;
-                    *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
                   }
                 }
-                tell(n);
-              } else {
-                cp_async_commit();
-                cp_async_wait_pending(2);
-                tell(n - 2);
+                if (found) {
+                  s.dirty[seg & 1] = 1;
+                  fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.full[n % SLOTS]);
               }
               if (j == g.j0 && which == 0) {
                 // the task's queries, beside its first keys; rows past the last are zero
-                if (!wait(&s.q_empty, (qs & 1) ^ 1)) break;
+                if (!wait(&s.q_empty, (seg & 1) ^ 1)) break;
                 const int rows = g.w.n * (int)p.group.d;
-#pragma unroll 1
-                for (int x = lt; x < C::kM * kPieces; x += 128) {
-                  const int row = x / kPieces, cc = x % kPieces, R = g.w.i * C::kM + row, rr = row & 127;
-                  const bool live = R < rows;
-                  const uint32_t tok = p.group.div(live ? R : 0), hd = (live ? R : 0) - tok * p.group.d;
-                  cp_async16_or_zero(smem_u32(s.q[row >> 7]) + (cc >> 3) * (128 * 128) + rr * 128 + (((cc ^ rr) & 7) << 4),
-                                     p.q + (g.w.row0 + tok) * p.ldq + ((long long)g.w.h * p.group.d + hd) * D + cc * 8, live);
+                constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+                constexpr int kPer = 128 / kPieces;  // rows at once
+                const int cc = lt % kPieces, base = g.w.i * C::kM;
+                const uint32_t to_q = smem_u32(s.q[0]) + (cc >> 3) * (128 * 128);
+                const __nv_bfloat16* from = p.q + g.w.row0 * p.ldq + (long long)g.w.h * p.group.d * D + cc * 8;
+#pragma unroll 8
+                for (int r0 = 0; r0 < C::kM; r0 += kPer) {
+                  const int row = r0 + lt / kPieces, rr = row & 127;
+                  const bool live = base + row < rows;
+                  const uint32_t R = live ? base + row : 0, tok = p.group.div(R), hd = R - tok * p.group.d;
+                  cp_async16_or_zero(to_q + (row >> 7) * (128 * D * 2) + rr * 128 + (((cc ^ rr) & 7) << 4),
+                                     from + tok * p.ldq + hd * D, live);
                 }
-                cp_async_commit();
-                flush();
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.q_full);
-                ++qs;
               }
             }
           }
           ++seg;
           ok = named_all(3, 128, ok);
         } while (ok && g.next());
+        // No copy in flight when the CTA leaves: every slot that was filled is waited for. (A wait has
+        // failed: the last phases that were begun.)
+        for (int i = max(0, n - SLOTS); i < n; ++i) mbar_wait(&s.full[i % SLOTS], i / SLOTS & 1);
       }
-      flush();
     } else if (warp == kMma && ok) {
       // ---- the products
       Segments<D> g(p, seq, start, u0, u1, s.at);
       constexpr uint32_t is = idesc_bf16_f32(128, KT), io = idesc_bf16_f32(128, D) | kMnB;
-      int n = 0, seg = 0, sn[2] = {0, 0}, pn[2] = {0, 0};
+      int n = 0, seg = 0, sn = 0, pn[2] = {0, 0};  // slots, tasks, S tiles (with one row tile), weights' tiles
       const auto wait = [&](uint64_t* b, uint32_t parity) {
         ok = ok && mbar_wait(b, parity);
-        ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        return ok;
       };
+      // descriptors of the operands, as their low words change
+      const uint64_t qd = sdesc_k_sw128(smem_u32(s.q[0])), kd = sdesc_k_sw128(smem_u32(s.ring[0])),
+                     vd = sdesc_mn_sw128(smem_u32(s.ring[0]), C::kChunk);
       // S of row tile t (into buffer b) from the keys in ring slot k
       const auto scores = [&](int t, int b, int k) {
-        if (elect_one()) {
-          const uint32_t a = smem_u32(s.q[t]), kk = smem_u32(s.ring[k]);
+        const uint64_t a = qd + t * (128 * D * 2 >> 4), kk = kd + k * (C::kSlotBytes >> 4);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            mma_bf16(tmem + b * C::kS, sdesc_k_sw128(a + (i >> 2) * (128 * 128)) + 2 * (i & 3),
-                     sdesc_k_sw128(kk + (i >> 2) * C::kChunk) + 2 * (i & 3), is, i > 0);
-          mma_commit(&s.s_full[b]);
-        }
-        __syncwarp();
+        for (int i = 0; i < D / 16; ++i)
+          mma_bf16(tmem + b * C::kS, a + ((i >> 2) * (128 * 128) >> 4) + 2 * (i & 3), kk + ((i >> 2) * C::kChunk >> 4) + 2 * (i & 3),
+                   is, i > 0);
+        mma_commit(&s.s_full[b]);
       };
-      const auto values = [&](int t, int b, int k, bool first) {
-        if (elect_one()) {
-          const uint32_t v = smem_u32(s.ring[k]);
+      const auto values = [&](int t, int b, int k, bool first, bool tell) {
+        const uint64_t v = vd + k * (C::kSlotBytes >> 4);
 #pragma unroll
-          for (int i = 0; i < KT / 16; ++i)
-            mma_bf16_ts(tmem + C::kO + t * D, tmem + b * C::kS + 8 * i, sdesc_mn_sw128(v + i * 2048, C::kChunk), io,
-                        !(first && i == 0));
-          mma_commit(&s.o_done[t]);
-        }
-        __syncwarp();
+        for (int i = 0; i < KT / 16; ++i)
+          mma_bf16_ts(tmem + C::kO + t * D, tmem + b * C::kS + 8 * i, v + i * (2048 >> 4), io, !(first && i == 0));
+        if (tell) mma_commit(&s.o_done[C::kTiles == 2 ? t : b]);
       };
-      const auto release = [&](uint64_t* b) {
-        if (elect_one()) mma_commit(b);
-        __syncwarp();
-      };
-      const auto slot = [&](int i) { return i % SLOTS; };
-      const auto filled = [&](int i) { return wait(&s.full[i % SLOTS], i / SLOTS & 1); };
-      do {
+      const auto filled = [&](int slot, int i) { wait(&s.full[slot], i / SLOTS & 1); };
+      const auto after = [&](int slot, int d) { return slot + d >= SLOTS ? slot + d - SLOTS : slot + d; };
+      int ks = 0;  // ring slot n % SLOTS: step i's keys are slot n + 2 i, its values n + 2 i + 1
+      if (g.valid()) do {
         const int e[2] = {g.end(0), C::kTiles == 2 ? g.end(1) : g.j0};
-        if (!wait(&s.q_full, seg & 1) || !filled(n)) break;
         const int steps = g.j1 - g.j0;
-        if (C::kTiles == 2) {
-          // ring slots of step i: keys n + 2 i, values n + 2 i + 1
-          for (int t = 0; t < 2; ++t)
-            if (e[t] > g.j0) scores(t, t, slot(n));
-          release(&s.empty[slot(n)]);
-          if (steps == 1) release(&s.q_empty);
-          for (int i = 0; i < steps && ok; ++i) {
-            const int j = g.j0 + i;
-            for (int t = 0; t < 2 && ok; ++t) {
-              if (j < e[t]) {
-                if (!wait(&s.p_full[t], pn[t] & 1)) break;
-                ++pn[t];
-                if (!filled(n + 2 * i + 1)) break;
-                values(t, t, slot(n + 2 * i + 1), i == 0);
-              }
-              if (j + 1 < e[t]) {
-                if (!filled(n + 2 * i + 2)) break;
-                scores(t, t, slot(n + 2 * i + 2));
-              }
-            }
-            if (!ok || !filled(n + 2 * i + 1)) break;
-            release(&s.empty[slot(n + 2 * i + 1)]);
-            if (i + 1 < steps) {
-              if (!filled(n + 2 * i + 2)) break;
-              release(&s.empty[slot(n + 2 * i + 2)]);
-              if (i + 2 == steps) release(&s.q_empty);
-            }
+        wait(&s.q_full, seg & 1);
+        filled(ks, n);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (elect_one()) {
+          if (C::kTiles == 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (e[t] > g.j0) scores(t, t, ks);
+          } else {
+            scores(0, sn & 1, ks);
           }
-        } else {
-          // S's buffers alternate over the whole share
-          scores(0, sn[0]++ & 1, slot(n));
-          release(&s.empty[slot(n)]);
-          if (steps == 1) release(&s.q_empty);
-          for (int i = 0; i < steps && ok; ++i) {
-            if (i + 1 < steps) {
-              if (!filled(n + 2 * i + 2)) break;
-              scores(0, sn[0]++ & 1, slot(n + 2 * i + 2));
-              release(&s.empty[slot(n + 2 * i + 2)]);
-              if (i + 2 == steps) release(&s.q_empty);
+          mma_commit(&s.empty[ks]);
+          if (steps == 1) mma_commit(&s.q_empty);
+        }
+        __syncwarp();
+        ++sn;
+#pragma unroll 1
+        for (int i = 0; i < steps; ++i) {
+          const int vs = after(ks, 1), k2 = after(ks, 2), j = g.j0 + i;
+          const bool more = i + 1 < steps;
+          if (C::kTiles == 2) {
+            // a row tile's softmax runs while the other's products do
+            filled(vs, n + 1);
+            if (more) filled(k2, n + 2);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const bool pv = j < e[t], s_ = j + 1 < e[t];
+              if (pv) {
+                wait(&s.p_full[t], pn[t] & 1);
+                ++pn[t];
+              }
+              if (!(ok = __all_sync(0xffffffffu, ok))) break;
+              if (elect_one()) {
+                if (pv) values(t, t, vs, i == 0, !s_);
+                if (t == 1) mma_commit(&s.empty[vs]);
+                if (s_) scores(t, t, k2);
+                if (t == 1 && more) mma_commit(&s.empty[k2]);
+                if (t == 1 && i + 2 == steps) mma_commit(&s.q_empty);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          } else {
+            // S's buffers alternate over the whole share: the softmax of a tile runs beside the next one's S
+            if (more) {
+              filled(k2, n + 2);
+              if (!(ok = __all_sync(0xffffffffu, ok))) break;
+              if (elect_one()) {
+                scores(0, sn & 1, k2);
+                mma_commit(&s.empty[k2]);
+                if (i + 2 == steps) mma_commit(&s.q_empty);
+              }
+              __syncwarp();
+              ++sn;
             }
             const int b = pn[0] & 1;
-            if (!wait(&s.p_full[b], (pn[0] >> 1) & 1)) break;
+            filled(vs, n + 1);
+            wait(&s.p_full[b], (pn[0] >> 1) & 1);
             ++pn[0];
-            if (!filled(n + 2 * i + 1)) break;
-            values(0, b, slot(n + 2 * i + 1), i == 0);
-            release(&s.empty[slot(n + 2 * i + 1)]);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (elect_one()) {
+              values(0, b, vs, i == 0, true);
+              mma_commit(&s.empty[vs]);
+            }
+            __syncwarp();
           }
+          ks = k2;
+          n += 2;
         }
-        n += 2 * steps;
         ++seg;
       } while (ok && g.next());
     }
@@ -644,7 +710,29 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
   __shared__ PlanScratch<1024> x;
   griddep_wait();
   griddep_launch_dependents();
-  attn_plan<Cfg<D>::kM, Cfg<D>::kKT, 1024>(p, p.seq, p.start, x, true);
+  attn_plan<Cfg<D>::kM, Cfg<D>::kKT, Cfg<D>::kE, 1024>(p, p.seq, p.start, x, true);
+}
+
+// Tile map of a cache's rows: boxes of 64 columns, 128-byte swizzle, zeros past the last row.
+bool row_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
+  typedef CUresult (*Fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                         const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                         CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static Fn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (Fn)f;
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -652,6 +740,13 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   const size_t smem = sizeof(TileSmem<D>);
   cudaError_t e = opt_in<attn_tiles<D>>(smem);
   if (e != cudaSuccess) return e;
+  TileMaps m = {};
+  const long long rows = (long long)p.num_blocks * p.block.d, cols = (long long)p.Hkv * D;
+  // the largest power of two of rows that blocks are made of, up to a load warp's keys
+  for (int b = 8; b <= Cfg<D>::kKT / 4 && p.block.d % b == 0; b *= 2) m.box = b;
+  if (!row_map(&m.k, p.k, rows, cols, p.ldk, 1) || !row_map(&m.v, p.v, rows, cols, p.ldv, 1)) return cudaErrorInvalidValue;
+  if (m.box && (!row_map(&m.kb, p.k, rows, cols, p.ldk, m.box) || !row_map(&m.vb, p.v, rows, cols, p.ldv, m.box)))
+    return cudaErrorInvalidValue;
   if (p.seqs <= kAttnPlannedTiles) p.seq = nullptr;
   if (p.seq) {
     const Launch one(dim3(1), 1024, 0, true, s);
@@ -659,7 +754,7 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const Launch all(dim3(grid), kNT, smem, true, s);
-  return cudaLaunchKernelEx(&all.cfg, attn_tiles<D>, p);
+  return cudaLaunchKernelEx(&all.cfg, attn_tiles<D>, m, p);
 }
 
 }  // namespace
