@@ -52,10 +52,11 @@ struct AttnParams {
   long long ldg;
   __nv_bfloat16* out;
   long long ldo;
+  bool wide_out;              // rows of out are 32-byte aligned
   float scale_log2;           // scale times log2(e)
   unsigned int* error;        // sticky word
   unsigned int* done;         // [2 grid] parts finished of the task whose first part is the CTA's; zero between calls
-  float* part;                // [2 grid][M][D] sums of weights times values, relative to the part's maximum
+  float* part;                // [2 grid] sums of weights times values, M rows of D, relative to the part's maximum
   float2* part_ml;            // [2 grid][M] maximum (of scores times log2 e) and sum of weights
   int4* seq;                  // [seqs + 1] of the workspace: the plan, where a kernel before makes it
   long long* start;           // [seqs + 1]

@@ -137,6 +137,7 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
   p.ldg = ldg;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ldo = ldo;
+  p.wide_out = aligned(out, 32) && ldo % 16 == 0;
   p.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
   p.error = reinterpret_cast<unsigned int*>(h->ws);
   p.done = reinterpret_cast<unsigned int*>(h->ws + l.done);

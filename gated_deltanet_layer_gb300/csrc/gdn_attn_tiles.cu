@@ -81,6 +81,24 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two f32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -124,6 +142,7 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 // 32 columns of a done row: divided by the sum, gated, stored.
 __device__ __forceinline__ void put32(const AttnParams& p, long long row, long long col, const float (&v)[32], float inv) {
   __nv_bfloat16* o = p.out + row * p.ldo + col;
+  uint32_t w[16];
 #pragma unroll
   for (int c = 0; c < 32; c += 8) {
     float y[8];
@@ -138,7 +157,19 @@ __device__ __forceinline__ void put32(const AttnParams& p, long long row, long l
         y[2 * j + 1] = __fdividef(y[2 * j + 1], 1.f + __expf(-bf16_hi(u[j])));
       }
     }
-    *reinterpret_cast<uint4*>(o + c) = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[c / 2 + j] = pack2(y[2 * j], y[2 * j + 1]);
+  }
+  if (p.wide_out) {  // whole sectors: the lanes' rows are far from one another
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o + 16 * c), "r"(w[8 * c]), "r"(w[8 * c + 1]),
+                   "r"(w[8 * c + 2]), "r"(w[8 * c + 3]), "r"(w[8 * c + 4]), "r"(w[8 * c + 5]), "r"(w[8 * c + 6]), "r"(w[8 * c + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint4*>(o + 8 * c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   }
 }
 
@@ -279,7 +310,11 @@ __global__ void __launch_bounds__(kNT, 1)
             }
             float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 4; c < KT; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+            for (int c = 4; c < KT - 4; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[c + i], x[c + 4 + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[KT - 4 + i]);
             const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
             if (__any_sync(0xffffffffu, tile_top > m + kSlack || m == -INFINITY)) {
               const float grown = fmaxf(m, tile_top), f = m == -INFINITY ? 0.f : ex2(m - grown);
@@ -304,19 +339,23 @@ __global__ void __launch_bounds__(kNT, 1)
               m = grown;
             }
             const float base = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-base, -base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < KT; c += 64) {
               uint32_t w[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float a = ex2(fmaf(x[c + 2 * i], p.scale_log2, -base)), e = ex2(fmaf(x[c + 2 * i + 1], p.scale_log2, -base));
-                sum[i & 3] += a + e;
-                w[i] = pack2(a, e);
+                float2 y = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), by, less);
+                y.x = ex2(y.x);
+                y.y = ex2(y.y);
+                sum[i & 1] = add2(sum[i & 1], y);
+                w[i] = pack2(y.x, y.y);
               }
               tmem_st32(sc + c / 2, w);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            sum[0] = add2(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
             tmem_wait_st();
           }
           tc_fence_before();
@@ -357,9 +396,9 @@ __global__ void __launch_bounds__(kNT, 1)
               if (whole) {
                 put32(p, row, col + c, o, inv);
               } else {
-                float* part = p.part + (slot + r) * D + c;
+                float4* part = reinterpret_cast<float4*>(p.part + slot * D) + c / 4 * 128 + r;
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(part + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                for (int i = 0; i < 32; i += 4) part[i / 4 * 128] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
               }
             }
           }
@@ -380,62 +419,33 @@ __global__ void __launch_bounds__(kNT, 1)
             // every part is there: the first CTA's second one, the others' first
             if (r == 0) p.done[2 * c0 + t] = 0;
             const auto at = [&](int c) { return (2LL * c + (c == c0)) * C::kM + t * 128; };
-            // A lane has its row's maximum and sum; the outputs go by rows, a row the warp's lanes wide.
             float top = -INFINITY, sum = 0.f;
+            if (live) {
 #pragma unroll 4
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.part_ml[at(c) + r]).x);
+              for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.part_ml[at(c) + r]).x);
 #pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float2 ml = __ldcg(&p.part_ml[at(c) + r]);
-              sum += ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - top));
-            }
-            const float in = sum == 0.f ? 0.f : 1.f / sum;
-            constexpr int kV = D / 32;  // columns of a lane
-            const int count = min(32, rows - first - (warp & 3) * 32);
-#pragma unroll 1
-            for (int q0 = 0; q0 < count; q0 += 4) {
-              float o[4][kV] = {};
-#pragma unroll 2
               for (int c = c0; c <= c1; ++c) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const long long q = at(c) + (warp & 3) * 32 + q0 + k;  // a part has 128 rows, live or not
-                  const float pm = __ldcg(&p.part_ml[q]).x, tp = __shfl_sync(0xffffffffu, top, q0 + k);
-                  const float e = pm == -INFINITY ? 0.f : ex2(pm - tp);
-                  const float* src = p.part + q * D + lane * kV;
-#pragma unroll
-                  for (int i = 0; i < kV; i += 2) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src + i));
-                    o[k][i] = fmaf(v.x, e, o[k][i]);
-                    o[k][i + 1] = fmaf(v.y, e, o[k][i + 1]);
-                  }
-                }
+                const float2 ml = __ldcg(&p.part_ml[at(c) + r]);
+                sum += ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - top));
               }
+              const float in = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+              for (int k = 0; k < D; k += 32) {
+                float o[32] = {};
+#pragma unroll 2
+                for (int c = c0; c <= c1; ++c) {
+                  const float pm = __ldcg(&p.part_ml[at(c) + r]).x, e = pm == -INFINITY ? 0.f : ex2(pm - top);
+                  const float4* part = reinterpret_cast<const float4*>(p.part + at(c) * D) + k / 4 * 128 + r;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float f = __shfl_sync(0xffffffffu, in, q0 + k);
-                if (q0 + k >= count) break;
-                const int RR = first + (warp & 3) * 32 + q0 + k;
-                const uint32_t tk = p.group.div(RR), hh = RR - tk * p.group.d;
-                const long long rw = g.w.row0 + tk, cl = ((long long)g.w.h * p.group.d + hh) * D + lane * kV;
-                uint32_t w[kV / 2];
-#pragma unroll
-                for (int i = 0; i < kV; i += 2) {
-                  float a = o[k][i] * f, b = o[k][i + 1] * f;
-                  if (p.gate) {
-                    const uint32_t z = *reinterpret_cast<const uint32_t*>(p.gate + rw * p.ldg + cl + i);
-                    a = __fdividef(a, 1.f + __expf(-bf16_lo(z)));
-                    b = __fdividef(b, 1.f + __expf(-bf16_hi(z)));
+                  for (int i = 0; i < 8; ++i) {
+                    const float4 v = __ldcg(part + i * 128);
+                    o[4 * i] = fmaf(v.x, e, o[4 * i]);
+                    o[4 * i + 1] = fmaf(v.y, e, o[4 * i + 1]);
+                    o[4 * i + 2] = fmaf(v.z, e, o[4 * i + 2]);
+                    o[4 * i + 3] = fmaf(v.w, e, o[4 * i + 3]);
                   }
-                  w[i / 2] = pack2(a, b);
                 }
-                __nv_bfloat16* to = p.out + rw * p.ldo + cl;
-                if (kV == 2)
-                  *reinterpret_cast<uint32_t*>(to) = w[0];
-                else if (kV == 4)
-                  *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[kV / 2 - 1]);
-                else
-                  *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1 % (kV / 2)], w[2 % (kV / 2)], w[kV / 2 - 1]);
+                put32(p, row, col + k, o, in);
               }
             }
           }
@@ -572,6 +582,18 @@ __global__ void __launch_bounds__(kNT, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.q_full);
+                // the next ones on their way to L2
+                if (g.u + (g.w.nt - g.w.j) + C::kE < u1 && base + C::kM < rows) {
+#pragma unroll 2
+                  for (int i = lt; i < C::kM * (D / 64); i += 128) {
+                    const int R = base + C::kM + i / (D / 64);
+                    if (R < rows) {
+                      const uint32_t tok = p.group.div(R), hd = R - tok * p.group.d;
+                      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (g.w.row0 + tok) * p.ldq +
+                                                                    ((long long)g.w.h * p.group.d + hd) * D + i % (D / 64) * 64));
+                    }
+                  }
+                }
               }
             }
           }
