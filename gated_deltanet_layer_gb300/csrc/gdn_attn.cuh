@@ -1,8 +1,9 @@
 // Shared definitions of the paged attention (gdn_attn_paged): launch parameters,
 // the plan of its work, and the parts of rows that several CTAs work on.
 //
-// A task is (request, key/value head, tile of M query rows); query row r of a request
-// and key/value head is token r / G, query head r % G of the head's G = Hq / Hkv. A task's
+// A task is (request, key/value head, tile of query rows). A tile is M of the request's n G rows, of
+// which row r is token r / G, query head r % G of the head's G = Hq / Hkv; or, with G = 1, M tokens
+// with all their heads. A task's
 // units are the tiles of KT keys that its last row sees, and E more for what a task
 // takes beside its tiles (they come last, and nobody does anything in them). All tasks' units form one line, in
 // the order request, head, row tile, key tile, and every CTA takes an equal, contiguous
@@ -18,9 +19,9 @@ namespace gdn {
 // What of an index error (bits 23..16 of the error word).
 constexpr uint32_t kAttnBlock = 1, kAttnOffsets = 2, kAttnLength = 3, kAttnWait = 4, kAttnContext = 5;
 
-// Up to this many requests every CTA plans by itself, in shared memory (as far as it has
-// some left); with more of them a kernel before leaves the plan in the workspace.
-constexpr int kAttnPlanned = 256, kAttnPlannedTiles = 32;
+// Up to this many requests every CTA plans by itself, in shared memory; with more of
+// them a kernel before leaves the plan in the workspace.
+constexpr int kAttnPlanned = 256;
 
 // n / d for 0 <= n < 2^31.
 struct FastDiv {
@@ -41,6 +42,8 @@ struct AttnParams {
   int limit;         // most keys of a request
   FastDiv block;     // slots of a block
   FastDiv group;     // query heads of a key/value head
+  int tile_m;        // M and G of the tasks' tiles
+  FastDiv tile_g;
   int Hkv;
   const __nv_bfloat16* q;
   long long ldq;
@@ -55,7 +58,7 @@ struct AttnParams {
   bool wide_out;              // rows of out are 32-byte aligned
   float scale_log2;           // scale times log2(e)
   unsigned int* error;        // sticky word
-  unsigned int* done;         // [2 grid] parts finished of the task whose first part is the CTA's; zero between calls
+  unsigned int* done;         // [2 grid] parts finished of the tasks whose first part is a CTA's; zero between calls
   float* part;                // [2 grid] sums of weights times values, M rows of D, relative to the part's maximum
   float2* part_ml;            // [2 grid][M] maximum (of scores times log2 e) and sum of weights
   int4* seq;                  // [seqs + 1] of the workspace: the plan, where a kernel before makes it
@@ -87,22 +90,22 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 // Row tiles of a request and their key tiles. Tile i's last row is min((i + 1) M, n G) - 1, so
 // all but the last tile see ctx + ceil((i + 1) M / G) keys, which are
 // ceil((G ctx + (i + 1) M) / (G KT)) tiles.
-template <int M, int KT, int E>
+template <int KT, int E>
 struct Tiles {
-  __device__ __forceinline__ static int rows(int n, int G) { return (n * G + M - 1) / M; }
+  __device__ __forceinline__ static int rows(const AttnParams& p, int n) { return (n * (int)p.tile_g.d + p.tile_m - 1) / p.tile_m; }
   __device__ __forceinline__ static int keys(const AttnParams& p, int n, int ctx, int i) {
-    const uint32_t G = p.group.d, last = min((uint32_t)(i + 1) * M, n * G) - 1;
-    return ((uint32_t)ctx + p.group.div(last) + KT) / KT;
+    const uint32_t last = min((uint32_t)(i + 1) * p.tile_m, n * p.tile_g.d) - 1;
+    return ((uint32_t)ctx + p.tile_g.div(last) + KT) / KT;
   }
   // units before row tile i (at most the last one)
-  __device__ __forceinline__ static long long before(int G, int ctx, int i) {
+  __device__ __forceinline__ static long long before(const AttnParams& p, int ctx, int i) {
     if (i == 0) return 0;
-    const long long m = (long long)G * KT;
-    return floor_sum(i, m, M, (long long)G * ctx + M + m - 1) + (long long)i * E;
+    const long long G = p.tile_g.d, m = G * KT;
+    return floor_sum(i, m, p.tile_m, G * ctx + p.tile_m + m - 1) + (long long)i * E;
   }
   __device__ __forceinline__ static long long total(const AttnParams& p, int n, int ctx) {
-    const int t = rows(n, p.group.d);
-    return before(p.group.d, ctx, t - 1) + keys(p, n, ctx, t - 1) + E;
+    const int t = rows(p, n);
+    return before(p, ctx, t - 1) + keys(p, n, ctx, t - 1) + E;
   }
 };
 
@@ -116,7 +119,7 @@ struct PlanScratch {
 // before request s, seq[seqs].x the first pad row and start[seqs] all units. The offsets are the
 // caller's: row ends are the running maximum of the offsets that lie within the rows, and
 // a request whose offsets are not its row ends is padding. A block of NT threads.
-template <int M, int KT, int E, int NT>
+template <int KT, int E, int NT>
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long long* start, PlanScratch<NT>& x, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int top = 0;
@@ -150,7 +153,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long l
       if (far) attn_record(p.error, kAttnContext, s);
     }
     if (long_ || far) n = 0;
-    const long long mine = n > 0 ? p.Hkv * Tiles<M, KT, E>::total(p, n, c) : 0;
+    const long long mine = n > 0 ? p.Hkv * Tiles<KT, E>::total(p, n, c) : 0;
     long long u = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -194,7 +197,7 @@ struct Shares {
 };
 
 // A walk over the units, task by task.
-template <int M, int KT, int E>
+template <int KT, int E>
 struct Walk {
   const AttnParams& p;
   const int4* seq;
@@ -210,7 +213,7 @@ struct Walk {
     row0 = q.x;
     n = q.y;
     ctx = q.z;
-    rows = Tiles<M, KT, E>::rows(n, p.group.d);
+    rows = Tiles<KT, E>::rows(p, n);
   }
   // Where unit u, one of start[seqs], is: at = {s, h, i, j}. A converged warp.
   __device__ __forceinline__ static void find(const AttnParams& p, const int4* seq, const long long* start, long long u, int (&at)[4]) {
@@ -232,10 +235,10 @@ struct Walk {
     const int s = last_of(p.seqs, [&](int k) { return start[k] <= u; });
     const int4 q = seq[s];
     const long long first = start[s], per = (start[s + 1] - first) / p.Hkv;
-    const int h = (int)((u - first) / per), G = p.group.d;
+    const int h = (int)((u - first) / per);
     const long long in = u - first - h * per;
-    const int i = last_of(Tiles<M, KT, E>::rows(q.y, G), [&](int k) { return Tiles<M, KT, E>::before(G, q.z, k) <= in; });
-    if (lane == 0) at[0] = s, at[1] = h, at[2] = i, at[3] = (int)(in - Tiles<M, KT, E>::before(G, q.z, i));
+    const int i = last_of(Tiles<KT, E>::rows(p, q.y), [&](int k) { return Tiles<KT, E>::before(p, q.z, k) <= in; });
+    if (lane == 0) at[0] = s, at[1] = h, at[2] = i, at[3] = (int)(in - Tiles<KT, E>::before(p, q.z, i));
   }
   __device__ __forceinline__ void from(const int (&at)[4], long long u) {
     s = at[0];
@@ -243,7 +246,7 @@ struct Walk {
     h = at[1];
     i = at[2];
     j = at[3];
-    nt = Tiles<M, KT, E>::keys(p, n, ctx, i);
+    nt = Tiles<KT, E>::keys(p, n, ctx, i);
     task = u - j;
   }
   __device__ __forceinline__ void next_task() {
@@ -259,7 +262,7 @@ struct Walk {
         load();
       }
     }
-    nt = Tiles<M, KT, E>::keys(p, n, ctx, i);
+    nt = Tiles<KT, E>::keys(p, n, ctx, i);
   }
 };
 

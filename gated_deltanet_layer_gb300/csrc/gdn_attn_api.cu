@@ -27,7 +27,7 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 struct Layout {
   size_t done, seq, start, ml, part, end;
   Layout(const gdn_attn_config& c, int grid) {
-    const size_t n = c.max_seqs > kAttnPlannedTiles ? (size_t)c.max_seqs + 1 : 0;
+    const size_t n = c.max_seqs > kAttnPlanned ? (size_t)c.max_seqs + 1 : 0;
     done = kErrorBytes;
     seq = done + up((size_t)grid * 8);
     start = seq + up(n * 16);
@@ -143,12 +143,13 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
   p.done = reinterpret_cast<unsigned int*>(h->ws + l.done);
   p.part = reinterpret_cast<float*>(h->ws + l.part);
   p.part_ml = reinterpret_cast<float2*>(h->ws + l.ml);
-  if (c.max_seqs > kAttnPlannedTiles) {  // room for the plan; the launchers say whether it is made there
+  if (c.max_seqs > kAttnPlanned) {  // room for the plan; the launchers say whether it is made there
     p.seq = reinterpret_cast<int4*>(h->ws + l.seq);
     p.start = reinterpret_cast<long long*>(h->ws + l.start);
   }
-  // Rows of a request and key/value head: a tile of 16 has them all, or the tensor cores' tiles.
-  const bool few = (long long)p.max_len * p.group.d <= kAttnRowsM || num_blocks == 0;
+  // Rows of a request and key/value head: a tile of 16 has them all, or the tensor cores' tiles (which
+  // hold a token's heads together, and need a cache to map).
+  const bool few = (long long)p.max_len * p.group.d <= kAttnRowsM || p.group.d > 128 || num_blocks == 0;
   return cuda_status((few ? launch_attn_rows : launch_attn_tiles)(p, c.head_dim, h->grid, (cudaStream_t)stream));
 }
 

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const AttnParam
     seq = p.seq;
     start = p.start;
   } else {
-    attn_plan<kM, KT, 0, NT>(p, s.seq, s.start, s.scan, blockIdx.x == 0);
+    attn_plan<KT, 0, NT>(p, s.seq, s.start, s.scan, blockIdx.x == 0);
   }
   attn_zero_rows<W>(p, seq, p.Hkv * p.group.d * D);
   const long long units = start[p.seqs];
@@ -116,11 +116,11 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const AttnParam
   const long long u0 = shares.first(blockIdx.x), u1 = shares.first(blockIdx.x + 1);
   const int steps = (int)(u1 - u0);
 
-  if (warp == 0) Walk<kM, KT, 0>::find(p, seq, start, u0, s.at);
+  if (warp == 0) Walk<KT, 0>::find(p, seq, start, u0, s.at);
   __syncthreads();
 
   // The ring's loads: lanes 0 - 15 know the slots of the warp's 16 keys, a step ahead.
-  Walk<kM, KT, 0> ahead(p, seq, start);
+  Walk<KT, 0> ahead(p, seq, start);
   ahead.from(s.at, u0);
   const uint32_t ring = smem_u32(s.ring[warp]);
   KeyBlock kb = key_block(p, ahead.s, ahead.j * KT + warp * 16 + (lane & 15), ahead.ctx + ahead.n);
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const AttnParam
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) issue();
 
-  Walk<kM, KT, 0> w(p, seq, start);
+  Walk<KT, 0> w(p, seq, start);
   w.from(s.at, u0);
   float o[D / 8][4], m[2], l[2];
   int last_key[2], first_last = 0;  // last key that the thread's two rows see; the task's first row's
@@ -382,13 +382,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
   __shared__ PlanScratch<1024> x;
   griddep_wait();
   griddep_launch_dependents();
-  attn_plan<kM, Rows<D>::kKT, 0, 1024>(p, p.seq, p.start, x, true);
+  attn_plan<Rows<D>::kKT, 0, 1024>(p, p.seq, p.start, x, true);
 }
 
 template <int D>
 cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   const size_t smem = sizeof(RowsSmem<D>) + 128;
   if (p.seqs <= kAttnPlanned) p.seq = nullptr;
+  p.tile_m = kM;
+  p.tile_g = p.group;
   cudaError_t e = opt_in<attn_rows<D>>(smem);
   if (e != cudaSuccess) return e;
   if (p.seq) {

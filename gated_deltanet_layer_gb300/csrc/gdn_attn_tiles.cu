@@ -1,18 +1,22 @@
 // Paged attention (gdn_attn_paged) on the tensor cores (tcgen05): more query rows than
 // gdn_attn_rows.cu takes at a time.
 //
-// A task is up to two tiles of 128 query rows (one of heads of 256) of a request and
-// key/value head, the G query heads of a token next to one another, so that every key and value
-// that comes into shared memory serves 256 rows. For each tile of keys
+// Two CTAs work together (cta_group::2). A task is up to four tiles of 128 query rows (two with heads
+// of 256), half of them each CTA's, of a request and key/value head: a tile holds as many tokens
+// as fit with all their G heads. Every key and value that comes into the pair's shared memory,
+// half of it in each CTA, serves all of them. For each tile of 128 keys
 //   S = Q K^T (TMEM), P = 2^(scale log2(e) S - m) as bf16 (TMEM, over S), O += P V (TMEM),
 // with m a maximum that follows the running one at a distance of up to 8: a row's O and sum are
 // multiplied only when the maximum grows by more, so that weights are at most 2^8 and hardly a
 // tile is corrected; the sums divide it out again.
 //
-// Warps 0 - 7: the softmax, a row a thread, and the outputs. Warps 8 - 11: keys and values by
-// TMA, four rows a copy from any four slots (so blocks of any size are alike, and rows past the last key
-// are zeros). Warp 12: the products. With two row tiles the tensor cores work on one while
-// the softmax works on the other; with one, S alternates between two buffers.
+// Eight warps a row tile: the softmax, half a row a thread, and the outputs. Four warps: queries, keys and values by
+// TMA; the blocks' rows in boxes where a block is made of boxes of 8 or more, else four rows a copy
+// from any four slots, and rows past the last key are zeros. One warp of the first CTA: the
+// products of both. One warp: which part of which task comes next. With two row tiles a CTA
+// the tensor cores work on one while the softmax works on the other; with one, S alternates
+// between two buffers. A task whose rows fill one tile of each CTA alone has the keys of
+// every second tile in the place of the other tile's rows, and joins the two.
 #include <climits>
 
 #include "gdn_attn.cuh"
@@ -25,22 +29,37 @@ namespace {
 
 using namespace tc;
 
-constexpr int kNT = 512;
-constexpr int kLoad0 = 8, kMma = 12;  // first load warp; the warp of the products
-constexpr float kSlack = 8.f;         // log2 of the most that a weight is above 1
+constexpr float kSlack = 8.f;                      // log2 of the most that a weight is above 1
+constexpr int KT = 128;                            // keys of a tile
+constexpr int kSegs = 4;                           // parts of tasks that are known ahead
+constexpr int kSplit = 4;                          // key tiles from which on a task is split between a CTA's row tiles
 
 template <int D>
 struct Cfg {
-  static constexpr int kTiles = D == 256 ? 1 : 2;        // row tiles of a task
-  static constexpr int kM = 128 * kTiles;
-  static constexpr int kKT = D == 256 ? 64 : 128;        // keys of a tile
-  static constexpr int kE = D == 256 ? 6 : 3;            // tiles' time that a task takes beside its tiles
-  static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 5 : 4;
-  static constexpr int kSlotBytes = kKT * D * 2;         // 32 KB, 16 KB with heads of 64
-  static constexpr int kChunk = kKT * 128;               // bytes of 64 columns of a slot
-  // TMEM columns: S of the two row tiles, or S's two buffers; O
-  static constexpr int kS = D == 256 ? 64 : 128;
-  static constexpr int kO = 256;
+  static constexpr int kTiles = D == 256 ? 1 : 2;          // row tiles of a CTA
+  static constexpr int kRows = 256 * kTiles;               // rows of a task
+  static constexpr int kLoad0 = 8 * kTiles, kMma = kLoad0 + 4, kSched = kMma + 1;  // first load warp; the warp of the products; of the tasks
+  static constexpr int kNT = 32 * (kLoad0 + 8);
+  static constexpr int kSoftRegs = D == 256 ? 176 : 96, kOtherRegs = D == 256 ? 80 : 48;  // of what the launch has
+  static constexpr int kVCols = D == 256 ? 128 : 64;       // a CTA's columns of the values (heads of 64: 32, and 32 for nothing)
+  static constexpr int kSlotBytes = D == 256 ? 32768 : 16384;  // 64 keys, or kVCols columns of 128 values
+  static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 9 : 4;
+  static constexpr int kE = D == 256 ? 3 : 3;              // tiles' time that a task takes beside its tiles
+  static constexpr int kO = 256;                           // TMEM column of O; S of the two row tiles, or S's two buffers, before it
+};
+
+// A part of a task: what both CTAs of a pair, and all roles, work on next.
+struct Seg {
+  int s, h;        // request, key/value head
+  int row0, toks;  // first row of the task's tokens, and how many
+  int pos, keys;   // position of the first; the request's keys
+  int j0, j1;      // key tiles
+  int end[2];      // where those end that the row tiles of both CTAs see
+  int c0, c1;      // pairs that work on the task
+  int whole, slot; // nobody else does; which of the pair's two parts it is
+  int split;       // the keys are split between the CTA's row tiles
+  int on;          // 0: there is none
+  unsigned tag;    // numbers the segments
 };
 
 template <int D>
@@ -48,23 +67,29 @@ struct alignas(1024) TileSmem {
   using C = Cfg<D>;
   unsigned char q[C::kTiles][128 * D * 2];
   unsigned char ring[C::kSlots][C::kSlotBytes];
-  uint64_t q_full, q_empty, edge, full[C::kSlots], empty[C::kSlots], s_full[2], p_full[2], o_done[2], seg_done[2][2];
+  uint64_t q_full, q_empty, edge, full[C::kSlots], empty[C::kSlots], s_full[2], p_full[2], o_done[2], seg_full[kSegs],
+      seg_empty[kSegs];
   uint32_t tmem;
-  int failed;          // a wait has passed its limit
+  int failed;                   // a wait has passed its limit
   unsigned last[2];
-  int at[4];           // the first unit's request, head, row tile and key tile
-  int dirty[2];        // whether there are any of
-  int poison[2][D];    // by task: the first key, hidden from some row, whose value in the column is not finite
-  int4 seq[kAttnPlannedTiles + 1];
-  long long start[kAttnPlannedTiles + 1];
-  PlanScratch<kNT> scan;
+  int at[4];                    // the first unit's request, head, row tile and key tile
+  Seg seg[kSegs];
+  // By segment: the first key, hidden from some row, whose value in the column is not finite, as
+  // (tag << 12 | 4095 - the key's distance from pos), so that what is left of another segment is none; whether
+  // there are any: the tag.
+  unsigned poison[kSegs][D], flagged[kSegs];
+  int4 plan[kAttnPlanned + 1];
+  long long start[kAttnPlanned + 1];
+  PlanScratch<C::kNT> scan;
+  float half[2][2][128];  // what the two threads of a row tell one another, by S's buffer
 };
 
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// D[both CTAs' tmem] (+)= A[both CTAs' tmem] B, 256 rows; half of B in each CTA.
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
@@ -75,6 +100,34 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t next
          (uint64_t)2 << 61;
 }
 constexpr uint32_t kMnB = 1u << 16;  // idesc: B is N-major
+
+// On a barrier of either CTA (its cluster address). Not releases at cluster scope: those wait for all that the
+// thread has written, a thousand cycles with each tile; what these two tell of is in TMEM, behind
+// tcgen05's own fences, or on its way by TMA, or has been read.
+__device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void atomic_max_cluster(uint32_t at, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+// Four rows of 64 columns from column x on, each of its own, to 512 bytes of this CTA's shared memory; `bar` of either CTA.
+__device__ __forceinline__ void gather4_pair(void* dst, const CUtensorMap* map, int x, const int (&row)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -104,7 +157,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st32(uint32_t t, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
@@ -112,6 +168,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -173,166 +236,151 @@ __device__ __forceinline__ void put32(const AttnParams& p, long long row, long l
   }
 }
 
-// The CTA's share as a walk of segments: what is left of a task, or as much of it as is the
-// CTA's.
-template <int D>
-struct Segments {
-  using C = Cfg<D>;
-  Walk<C::kM, C::kKT, C::kE> w;
-  long long u, u1;
-  int j0, j1;  // key tiles of the segment
-  __device__ __forceinline__ Segments(const AttnParams& p, const int4* seq, const long long* start, long long u0, long long u1,
-                                      const int (&at)[4])
-      : w(p, seq, start), u(u0), u1(u1) {
-    w.from(at, u0);
-    j0 = w.j;
-    j1 = (int)min((long long)w.nt, j0 + (u1 - u));
-    if (j0 >= w.nt) next();  // what the share begins with of a task has no tiles
-  }
-  // Whether there is a segment.
-  __device__ __forceinline__ bool valid() const { return u < u1; }
-  __device__ __forceinline__ bool next() {
-    u = w.task + w.nt + C::kE;
-    if (u >= u1) return false;
-    w.next_task();
-    j0 = 0;
-    j1 = (int)min((long long)w.nt, u1 - u);
-    return true;
-  }
-  // end of row tile t's key tiles in the segment: its last row may see fewer than the task's
-  __device__ __forceinline__ int end(int t) const {
-    const int rows = w.n * (int)w.p.group.d, first = w.i * C::kM + t * 128;
-    if (first >= rows) return j0;
-    const int last = min(first + 128, rows) - 1;
-    return max(j0, min(j1, (w.ctx + (int)w.p.group.div(last) + C::kKT) / C::kKT));
-  }
-};
-
-// The caches' rows as the copies want them: one at a time, and in boxes of `box` rows (0: no boxes).
+// The caches' rows as the copies want them: one at a time, and in boxes of box_k and box_v rows (0: no
+// boxes); the queries' as a row tile's tokens with their heads.
 struct TileMaps {
-  CUtensorMap k, v, kb, vb;
-  int box;
+  CUtensorMap k, v, kb, vb, q;
+  int box_k, box_v;
+  int tokens;  // of a row tile
 };
-// Four rows of 64 columns from column x on, each of its own, to 512 bytes of shared memory.
-__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, int x, const int (&row)[4], uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(smem_u32(bar))
-      : "memory");
-}
 
 template <int D>
-__global__ void __launch_bounds__(kNT, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
     attn_tiles(const __grid_constant__ TileMaps maps, const AttnParams p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) unsigned char raw[];
   static_assert(sizeof(TileSmem<D>) <= 232448, "227 KB of shared memory a CTA");
   TileSmem<D>& s = *reinterpret_cast<TileSmem<D>*>(raw);
-  constexpr int KT = C::kKT, SLOTS = C::kSlots;
+  constexpr int SLOTS = C::kSlots, TILES = C::kTiles, kNT = C::kNT, kLoad0 = C::kLoad0, kMma = C::kMma, kSched = C::kSched;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
-    mbar_init(&s.q_full, 4);
+    mbar_init(&s.q_full, 2);
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.edge, 4);
-    prefetch_tensormap(&maps.k);
-    prefetch_tensormap(&maps.v);
-    if (maps.box) prefetch_tensormap(&maps.kb), prefetch_tensormap(&maps.vb);
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&s.full[i], 4);
+      mbar_init(&s.full[i], 8);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.p_full[i], 16);
       mbar_init(&s.o_done[i], 1);
-      for (int t = 0; t < 2; ++t) mbar_init(&s.seg_done[t][i], 4);
     }
-    s.failed = s.dirty[0] = s.dirty[1] = 0;
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&s.seg_full[i], 1);
+      mbar_init(&s.seg_empty[i], 16 * TILES + 4 + (rank == 0));  // both CTAs' softmax, the load warps, the products
+      s.flagged[i] = 0;
+    }
+    s.failed = 0;
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+    if (maps.box_k) prefetch_tensormap(&maps.kb), prefetch_tensormap(&maps.vb);
+    prefetch_tensormap(&maps.q);
     fence_mbar_init();
   }
-  for (int i = tid; i < 2 * D; i += kNT) (&s.poison[0][0])[i] = INT_MAX;
-  if (warp == kMma) tmem_alloc(&s.tmem, 512);
+  for (int i = tid; i < kSegs * D; i += kNT) (&s.poison[0][0])[i] = 0;
+  if (warp == kMma) tmem_alloc_pair(&s.tmem, 512);
   griddep_wait();
   griddep_launch_dependents();
-  const int4* seq = s.seq;
+  const int4* plan = s.plan;
   const long long* start = s.start;
   if (p.seq) {
-    seq = p.seq;
+    plan = p.seq;
     start = p.start;
   } else {
-    attn_plan<C::kM, KT, C::kE, kNT>(p, s.seq, s.start, s.scan, blockIdx.x == 0);
+    attn_plan<KT, C::kE, kNT>(p, s.plan, s.start, s.scan, blockIdx.x == 0);
   }
-  attn_zero_rows<kNT / 32>(p, seq, p.Hkv * p.group.d * D);
+  attn_zero_rows<kNT / 32>(p, plan, p.Hkv * p.group.d * D);
   const long long units = start[p.seqs];
-  const Shares shares(units, (int)max(1LL, min((long long)gridDim.x, (units + C::kE + 1) / (C::kE + 2))));
-  const bool on = units > 0 && blockIdx.x < shares.ctas;
-  const long long u0 = shares.first(blockIdx.x), u1 = shares.first(blockIdx.x + 1);
-  if (warp == 0 && on) Walk<C::kM, KT, C::kE>::find(p, seq, start, u0, s.at);
+  const Shares shares(units, (int)max(1LL, min((long long)pairs, (units + C::kE + 1) / (C::kE + 2))));
+  const bool on = units > 0 && pair < shares.ctas;
+  const long long u0 = shares.first(pair), u1 = shares.first(pair + 1);
+  if (warp == kSched && on) Walk<KT, C::kE>::find(p, plan, start, u0, s.at);
+  __syncthreads();
+  cluster_sync();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  const int rows_end = p.num_blocks * (int)p.block.d;
+  const int G = p.group.d, tile_toks = maps.tokens, rows_end = p.num_blocks * (int)p.block.d;
   bool ok = on;
+  // The next segment, by its number.
+  const auto take = [&](int n) {
+    ok = ok && mbar_wait(&s.seg_full[n % kSegs], n / kSegs & 1);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok && s.seg[n % kSegs].on;
+  };
 
   if (warp < kLoad0) {
-    more_regs<200>();
-    const int t = warp >> 2;  // row tile
-    if (ok && t < C::kTiles) {
+    more_regs<C::kSoftRegs>();
+    {
+      const int t = warp >> 3, hf = warp >> 2 & 1;  // row tile; half of the columns
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const int r = (warp & 3) * 32 + lane;
-      Segments<D> g(p, seq, start, u0, u1, s.at);
-      int sn = 0, pv = 0, ends = 0;  // S tiles, PV products and segments with any so far (of the row tile)
-      int seg = 0;
-      if (g.valid()) do {
-        const int rows = g.w.n * (int)p.group.d, first = g.w.i * C::kM + t * 128, R = first + r;
-        const bool live = R < rows, warp_live = first + (warp & 3) * 32 < rows;
-        const int last_key = g.w.ctx + (int)p.group.div(min(R, rows - 1));
-        const int end = g.end(t);
+      const bool in_tile = r < tile_toks * G, warp_in_tile = (warp & 3) * 32 < tile_toks * G;
+      const int r_tok = p.group.div(r), hd = r - r_tok * G, warp_tok = p.group.div((warp & 3) * 32);
+      int sn = 0, ends = 0;  // S tiles, and segments with any so far (of the row tile)
+      for (int n = 0;; ++n) {
+        const bool there = take(n);
+        if (!(ok = named_all(1 + t, 256, ok)) || !there) break;
+        const Seg& g = s.seg[n % kSegs];
+        const bool split = TILES == 2 && g.split;
+        const int j0 = g.j0 + (split ? t : 0), end = g.end[t], step = split ? 2 : 1, toks = g.toks, pos = g.pos;
+        const int first = ((split ? 0 : 2 * t) + rank) * tile_toks, tok = first + r_tok;  // the tile's first token, the row's
+        const bool live = in_tile && tok < toks, warp_live = warp_in_tile && first + warp_tok < toks;
+        const int last_key = pos + min(tok, toks - 1);
         float m = -INFINITY, l = 0.f;
-        for (int j = g.j0; j < end && ok; ++j, ++sn) {
-          const int b = C::kTiles == 2 ? t : sn & 1;
-          const uint32_t sc = tmem + lanes + b * C::kS;
-          ok = mbar_wait(&s.s_full[b], (C::kTiles == 2 ? sn : sn >> 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+#pragma unroll 1
+        for (int j = j0; j < end; j += step, ++sn) {
+          const int b = TILES == 2 ? t : sn & 1;
+          const uint32_t sc = tmem + lanes + b * 128;
+          ok = mbar_wait(&s.s_full[b], (TILES == 2 ? sn : sn >> 1) & 1);
           tc_fence_after();
-          if (warp_live) {
-            float x[KT];
+          float tile_top = -INFINITY;
+          // this half's S, 32 columns at a time, of which the keys 0 .. seen are seen
+          const int seen = last_key - j * KT - hf * (KT / 2);
+          const bool hides = __any_sync(0xffffffffu, seen < KT / 2 - 1);
+          const auto scores = [&](int c, float (&x)[32]) {
+            tmem_ld32(sc + hf * (KT / 2) + c, x);
+            if (hides) {
 #pragma unroll
-            for (int c = 0; c < KT; c += 32) tmem_ld32(sc + c, *reinterpret_cast<float(*)[32]>(x + c));
-            const int seen = last_key - j * KT;  // the tile's keys 0 .. seen
-            if (__any_sync(0xffffffffu, seen < KT - 1)) {
-#pragma unroll
-              for (int c = 0; c < KT; ++c)
-                if (c > seen) x[c] = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (c + i > seen) x[i] = -INFINITY;
             }
-            float top[4] = {x[0], x[1], x[2], x[3]};
+          };
+          if (warp_live && ok) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 4; c < KT - 4; c += 8)
+            for (int c = 0; c < KT / 2; c += 32) {
+              float x[32];
+              scores(c, x);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[c + i], x[c + 4 + i]);
+              for (int e = 0; e < 32; e += 8)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[KT - 4 + i]);
-            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+                for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[e + i], x[e + 4 + i]);
+            }
+            tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+            s.half[b][hf][r] = tile_top;
+          }
+          if (!(ok = named_all(1 + t, 256, ok))) break;
+          if (warp_live) {
+            tile_top = fmaxf(tile_top, s.half[b][hf ^ 1][r]);
             if (__any_sync(0xffffffffu, tile_top > m + kSlack || m == -INFINITY)) {
               const float grown = fmaxf(m, tile_top), f = m == -INFINITY ? 0.f : ex2(m - grown);
-              if (j > g.j0) {
-                if (C::kTiles == 1) {  // S came before the last PV
-                  ok = mbar_wait(&s.o_done[(pv - 1) & 1], ((pv - 1) >> 1) & 1);
-                  ok = __all_sync(0xffffffffu, ok);
-                  if (!ok) break;
+              if (j > j0) {
+                if (TILES == 1) {  // S came before the last PV
+                  ok = mbar_wait(&s.o_done[(sn - 1) & 1], ((sn - 1) >> 1) & 1);
                   tc_fence_after();
                 }
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
                   float o[32];
                   const uint32_t at = tmem + lanes + C::kO + t * D + c;
                   tmem_ld32(at, o);
 #pragma unroll
                   for (int i = 0; i < 32; ++i) o[i] *= f;
-                  tmem_st32(at, reinterpret_cast<const uint32_t*>(o));
+                  tmem_st32(at, o);
                 }
               }
               l *= f;
@@ -341,18 +389,21 @@ __global__ void __launch_bounds__(kNT, 1)
             const float base = m == -INFINITY ? 0.f : m;
             const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-base, -base);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            // P over the first half of the S that it comes from
 #pragma unroll
-            for (int c = 0; c < KT; c += 64) {
-              uint32_t w[32];
+            for (int c = 0; c < KT / 2; c += 32) {
+              float x[32];
+              uint32_t w[16];
+              scores(c, x);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float2 y = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), by, less);
+              for (int i = 0; i < 16; ++i) {
+                float2 y = fma2(make_float2(x[2 * i], x[2 * i + 1]), by, less);
                 y.x = ex2(y.x);
                 y.y = ex2(y.y);
                 sum[i & 1] = add2(sum[i & 1], y);
                 w[i] = pack2(y.x, y.y);
               }
-              tmem_st32(sc + c / 2, w);
+              tmem_st16(sc + hf * (KT / 2) + c / 2, w);
             }
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
@@ -360,28 +411,31 @@ __global__ void __launch_bounds__(kNT, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.p_full[b]);
-          ++pv;
+          if (lane == 0) arrive_cluster(map_rank(&s.p_full[b], 0));
         }
 
-        // ---- the task's end, or this CTA's
-        const bool any = end > g.j0;
+        // ---- the task's end, or this pair's
+        const bool any = end > j0;
         if (any && ok) {
-          ok = C::kTiles == 1 ? mbar_wait(&s.o_done[(pv - 1) & 1], ((pv - 1) >> 1) & 1) : mbar_wait(&s.o_done[t], ends++ & 1);
+          // with two row tiles O is told done once a segment, with one for every tile
+          ok = TILES == 1 ? mbar_wait(&s.o_done[(sn - 1) & 1], ((sn - 1) >> 1) & 1) : mbar_wait(&s.o_done[t], ends & 1);
+          ++ends;
           tc_fence_after();
         }
-        if (!(ok = named_all(1 + t, 128, ok))) break;
-        const long long t0 = g.w.task, t1 = t0 + g.w.nt;
-        const bool whole = t0 >= u0 && t1 <= u1;
-        const long long slot = (2LL * blockIdx.x + (t0 >= u0)) * C::kM + t * 128;  // the part's first row
-        const uint32_t tok = p.group.div(live ? R : 0), hd = (live ? R : 0) - tok * p.group.d;
-        const long long row = g.w.row0 + tok, col = ((long long)g.w.h * p.group.d + hd) * D;
-        const int* poison = s.poison[seg & 1];
-        const bool flagged = any && s.dirty[seg & 1] != 0;
+        s.half[t][hf][r] = l;
+        if (!(ok = named_all(1 + t, 256, ok))) break;
+        l += s.half[t][hf ^ 1][r];
+        const int c0 = g.c0, c1 = g.c1;
+        const bool whole = g.whole && !split;
+        const long long part_row = (2LL * pair + g.slot) * C::kRows + (2 * t + rank) * 128;  // the part's first row
+        const long long row = g.row0 + tok, col = ((long long)g.h * G + hd) * D;
+        const unsigned tag = g.tag;
+        const unsigned* poison = s.poison[n % kSegs];
+        const bool flagged = any && s.flagged[n % kSegs] == tag;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (warp_live) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
             float o[32];
             if (any) {
               tmem_ld32(tmem + lanes + C::kO + t * D + c, o);
@@ -389,53 +443,63 @@ __global__ void __launch_bounds__(kNT, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = 0.f;
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (flagged && poison[c + i] <= last_key) o[i] = NAN;
+            if (flagged) {
+#pragma unroll 4
+              for (int i = 0; i < 32; ++i) {
+                const unsigned q = poison[c + i];
+                if (q >> 12 == tag && (int)(4095 - (q & 4095)) <= last_key - pos + 1024) o[i] = NAN;
+              }
+            }
             if (live) {
               if (whole) {
                 put32(p, row, col + c, o, inv);
               } else {
-                float4* part = reinterpret_cast<float4*>(p.part + slot * D) + c / 4 * 128 + r;
+                float4* part = reinterpret_cast<float4*>(p.part + part_row * D) + c / 4 * 128 + r;
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) part[i / 4 * 128] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
               }
             }
           }
-          if (!whole && live) p.part_ml[slot + r] = make_float2(m, l);
+          if (!whole && live && hf == 0) p.part_ml[part_row + r] = make_float2(m, l);
         }
+        // the segment's entry and flags are free once both CTAs' softmax has read them
         __syncwarp();
-        if (lane == 0 && any) mbar_arrive(&s.seg_done[t][seg & 1]);
-        if (!whole && first < rows) {
-          const int c0 = shares.owner(t0), c1 = shares.owner(t1 - 1);
+        if (lane < 2) arrive_cluster(map_rank(&s.seg_empty[n % kSegs], lane));
+        if (!whole && first < toks) {
+          unsigned* done = p.done + 4 * c0 + (split ? 0 : 2 * t) + rank;
+          const int parts = (c1 - c0 + 1) << (split ? 1 : 0);
           __threadfence();
-          named_sync(1 + t, 128);
-          if (r == 0) {
-            s.last[t] = atomicAdd(p.done + 2 * c0 + t, 1u) == (unsigned)(c1 - c0);
+          named_sync(1 + t, 256);
+          if (r == 0 && hf == 0) {
+            s.last[t] = atomicAdd(done, 1u) == (unsigned)(parts - 1);
             __threadfence();
           }
-          named_sync(1 + t, 128);
+          named_sync(1 + t, 256);
           if (s.last[t]) {
-            // every part is there: the first CTA's second one, the others' first
-            if (r == 0) p.done[2 * c0 + t] = 0;
-            const auto at = [&](int c) { return (2LL * c + (c == c0)) * C::kM + t * 128; };
-            float top = -INFINITY, sum = 0.f;
+            // every part is there: the first pair's second one, the others' first, and where the keys
+            // are split both row tiles'
+            if (r == 0 && hf == 0) *done = 0;
+            const auto at = [&](int k) {
+              const int c = c0 + (split ? k >> 1 : k), u = split ? k & 1 : t;
+              return (2LL * c + (c == c0)) * C::kRows + (2 * u + rank) * 128;
+            };
             if (live) {
+              float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
-              for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.part_ml[at(c) + r]).x);
+              for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(&p.part_ml[at(k) + r]).x);
 #pragma unroll 4
-              for (int c = c0; c <= c1; ++c) {
-                const float2 ml = __ldcg(&p.part_ml[at(c) + r]);
+              for (int k = 0; k < parts; ++k) {
+                const float2 ml = __ldcg(&p.part_ml[at(k) + r]);
                 sum += ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - top));
               }
               const float in = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
-              for (int k = 0; k < D; k += 32) {
+              for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
                 float o[32] = {};
 #pragma unroll 2
-                for (int c = c0; c <= c1; ++c) {
-                  const float pm = __ldcg(&p.part_ml[at(c) + r]).x, e = pm == -INFINITY ? 0.f : ex2(pm - top);
-                  const float4* part = reinterpret_cast<const float4*>(p.part + at(c) * D) + k / 4 * 128 + r;
+                for (int k = 0; k < parts; ++k) {
+                  const float pm = __ldcg(&p.part_ml[at(k) + r]).x, e = pm == -INFINITY ? 0.f : ex2(pm - top);
+                  const float4* part = reinterpret_cast<const float4*>(p.part + at(k) * D) + c / 4 * 128 + r;
 #pragma unroll
                   for (int i = 0; i < 8; ++i) {
                     const float4 v = __ldcg(part + i * 128);
@@ -445,237 +509,257 @@ __global__ void __launch_bounds__(kNT, 1)
                     o[4 * i + 3] = fmaf(v.w, e, o[4 * i + 3]);
                   }
                 }
-                put32(p, row, col + k, o, in);
+                put32(p, row, col + c, o, in);
               }
             }
           }
         }
-        ++seg;
-      } while (g.next());
+      }
     }
   } else {
-    fewer_regs<56>();
+    fewer_regs<C::kOtherRegs>();
     if (warp < kMma) {
-      // ---- keys, values and queries
-      const int wl = warp - kLoad0, lt = tid - kLoad0 * 32;
-      constexpr int kKeys = KT / 4;           // keys of a warp
-      constexpr int kFours = kKeys / 4;       // of them four a copy, 64 columns wide: a lane each
-      constexpr uint32_t kShare = kKeys * D * 2;
-      static_assert(kFours * (D / 64) <= 32, "one copy a lane");
-      const int four = lane % kFours, chunk = lane / kFours;
-      const bool issues = chunk < D / 64;
-      const uint32_t place = chunk * C::kChunk + (wl * kKeys + four * 4) * 128;
-      // Where blocks are made of boxes of 8 rows or more, a whole tile comes as boxes: a copy of four
-      // rows takes an SM 22 cycles whatever its size.
-      const int boxes = min(maps.box, kKeys) > 0 ? kKeys / min(maps.box, kKeys) : 0;  // of a warp's keys, 64 columns wide
-      const int box_chunk = boxes ? lane / boxes : 0, box_row = boxes ? lane % boxes * (kKeys / boxes) : 0;
-      const bool box_issues = box_chunk < D / 64;
-      const uint32_t box_place = box_chunk * C::kChunk + (wl * kKeys + box_row) * 128;
-      int n = 0;                      // slots filled
-      uint32_t edges = 0;             // edge tiles so far
+      // ---- queries, keys and values: of a tile this CTA's 64 keys, and its columns of the 128 values
+      const int wl = warp - kLoad0;
+      constexpr int kK = 16, kV = 32, kVC = C::kVCols / 64;  // a warp's keys and values; their columns, by 64
+      constexpr uint32_t kKShare = kK * D * 2, kVShare = kV * C::kVCols * 2;
+      // lanes that copy, by four rows and 64 columns, or by boxes: where blocks are made of boxes of 8 rows or
+      // more, a whole tile comes as boxes (a copy of four rows takes an SM 22 cycles, a box not much more)
+      const int k4 = lane % 4, kc4 = lane / 4, v4 = lane % 8, vc4 = lane / 8;
+      const int bk = maps.box_k, bv = maps.box_v;
+      const int nk = bk ? kK / bk : 1, nv = bv ? kV / bv : 1;  // boxes of 64 columns
+      const int kb_c = lane / nk, kb_r = lane % nk * bk, vb_c = lane / nv, vb_r = lane % nv * bv;
+      const uint32_t full0 = map_rank(&s.full[0], 0);
+      int i = 0;           // slots filled
+      uint32_t edges = 0;  // edge tiles so far
       const auto wait = [&](uint64_t* b, uint32_t parity) { return ok = __all_sync(0xffffffffu, mbar_wait(b, parity)); };
-      if (ok) {
-        Segments<D> g(p, seq, start, u0, u1, s.at);
-        int seg = 0;
-        uint32_t waits[2] = {0, 0}, phases[2] = {0, 0};  // by row tile, a bit for even and odd tasks
-        if (g.valid()) do {
-          if (seg >= 2) {
-            // The flags are the task's before last until its row tiles are through with them. (A row
-            // tile without keys in a segment says nothing: nothing would keep it from running ahead.)
+      for (int n = 0; take(n); ++n) {
+        const Seg& g = s.seg[n % kSegs];
+        const int keys = g.keys, first_last = g.pos, req = g.s, j0 = g.j0, j1 = g.j1, h = g.h, toks = g.toks, row0 = g.row0;
+        const unsigned tag = g.tag;
+        const int kx = h * D, vx = D == 64 ? h * D + 32 * rank : h * D + C::kVCols * rank;
+        const auto blocks = [&](int j, KeyBlock& a, KeyBlock& b) {
+          a = key_block(p, req, j * KT + rank * 64 + wl * kK + lane % kK, keys);
+          b = key_block(p, req, j * KT + wl * kV + lane, keys);
+        };
+        KeyBlock kb, vb;
+        blocks(j0, kb, vb);
+#pragma unroll 1
+        for (int j = j0; j < j1; ++j) {
+          int k_row = key_slot(p, kb, req), v_row = key_slot(p, vb, req);
+          if (k_row < 0) k_row = rows_end;  // past the last row: zeros
+          if (v_row < 0) v_row = rows_end;
+          if (j + 1 < j1) blocks(j + 1, kb, vb);
+          const bool boxes = bk && (j + 1) * KT <= keys;
+
+          // keys
+          if (!wait(&s.empty[i % SLOTS], (i / SLOTS & 1) ^ 1)) break;
+          unsigned char* to = s.ring[i % SLOTS];
+          uint32_t bar = full0 + 8 * (i % SLOTS);
+          if (lane == 0) arrive_expect_cluster(bar, kKShare);
+          __syncwarp();
+          if (boxes) {
+            const int at = __shfl_sync(0xffffffffu, k_row, kb_r);
+            if (kb_c < D / 64) tma_load_2d_pair(to + kb_c * 8192 + (wl * kK + kb_r) * 128, &maps.kb, kx + kb_c * 64, at, bar);
+          } else {
+            int at[4];
 #pragma unroll
-            for (int t = 0; t < C::kTiles; ++t)
-              if (waits[t] >> (seg & 1) & 1) {
-                ok = ok && wait(&s.seg_done[t][seg & 1], phases[t] >> (seg & 1) & 1);
-                phases[t] ^= 1u << (seg & 1);
-              }
-            if (!(ok = named_all(3, 128, ok))) break;
-            const bool flagged = s.dirty[seg & 1] != 0;
-            named_sync(3, 128);
-            if (flagged) {
-              for (int i = lt; i < D; i += 128) s.poison[seg & 1][i] = INT_MAX;
-              if (lt == 0) s.dirty[seg & 1] = 0;
-              named_sync(3, 128);
-            }
+            for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(0xffffffffu, k_row, k4 * 4 + e);
+            if (kc4 < D / 64) gather4_pair(to + kc4 * 8192 + (wl * kK + k4 * 4) * 128, &maps.k, kx + kc4 * 64, at, bar);
           }
+          ++i;
+
+          if (j == j0 && wl == 0) {
+            // the task's queries, beside its first keys: whole tokens, whatever comes after the last
+            if (!wait(&s.q_empty, (n & 1) ^ 1)) break;
+            if (lane == 0) {
+              const uint32_t qbar = map_rank(&s.q_full, 0);
+              int tiles = 0;
 #pragma unroll
-          for (int t = 0; t < C::kTiles; ++t)
-            waits[t] = (waits[t] & ~(1u << (seg & 1))) | (uint32_t)(g.end(t) > g.j0) << (seg & 1);
-          const int keys = g.w.ctx + g.w.n, first_last = g.w.ctx + (int)p.group.div(g.w.i * C::kM);
-          const int x = g.w.h * D + chunk * 64, box_x = g.w.h * D + box_chunk * 64;
-          // a lane has the slot of one of the warp's keys, a tile ahead
-          KeyBlock kb = key_block(p, g.w.s, g.j0 * KT + wl * kKeys + lane % kKeys, keys);
-#pragma unroll 1
-          for (int j = g.j0; j < g.j1 && ok; ++j) {
-            int at[4], box_at;
-            {
-              const int slot = key_slot(p, kb, g.w.s), row = slot < 0 ? rows_end : slot;  // past the last row: zeros
+              for (int t = 0; t < TILES; ++t) tiles += (2 * t + rank) * tile_toks < toks;
+              arrive_expect_cluster(qbar, tiles * D * 2 * tile_toks * G);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, row, four * 4 + i);
-              box_at = __shfl_sync(0xffffffffu, row, box_row);
+              for (int t = 0; t < TILES; ++t)
+                if ((2 * t + rank) * tile_toks < toks)
+#pragma unroll
+                  for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d_pair(s.q[t] + c * 16384, &maps.q, c * 64, h * G, row0 + (2 * t + rank) * tile_toks, qbar);
             }
-            if (j + 1 < g.j1) kb = key_block(p, g.w.s, (j + 1) * KT + wl * kKeys + lane % kKeys, keys);
-#pragma unroll 1
-            for (int which = 0; which < 2; ++which, ++n) {  // keys, values
-              if (!wait(&s.empty[n % SLOTS], (n / SLOTS & 1) ^ 1)) break;
-              unsigned char* to = s.ring[n % SLOTS];
-              // some row does not see some of these keys
-              const bool edge = which && j * KT + KT - 1 > first_last && g.w.n > 1;
-              uint64_t* bar = edge ? &s.edge : &s.full[n % SLOTS];
-              if (lane == 0) mbar_arrive_expect_tx(bar, kShare);
-              __syncwarp();
-              if (boxes && (j + 1) * KT <= keys) {
-                if (box_issues) tma_load_2d_plain(to + box_place, which ? &maps.vb : &maps.kb, box_x, box_at, bar);
-              } else if (issues) {
-                gather4(to + place, which ? &maps.v : &maps.k, x, at, bar);
-              }
-              if (edge) {
-                // 0 x NaN: values that are not finite are taken out, and the rows that do see them told
-                // by the column's first such key
-                if (!wait(&s.edge, edges++ & 1)) break;
-                bool found = false;
-                constexpr int kRow = D / 8;  // 16-byte pieces
+            __syncwarp();
+          }
+
+          // values
+          if (!wait(&s.empty[i % SLOTS], (i / SLOTS & 1) ^ 1)) break;
+          to = s.ring[i % SLOTS];
+          bar = full0 + 8 * (i % SLOTS);
+          const bool edge = j * KT + KT - 1 > first_last && toks > 1;  // some row does not see some of these keys
+          const uint32_t to_bar = edge ? map_rank(&s.edge, rank) : bar;
+          if (lane == 0) arrive_expect_cluster(to_bar, kVShare);
+          __syncwarp();
+          if (boxes) {
+            const int at = __shfl_sync(0xffffffffu, v_row, vb_r);
+            if (vb_c < kVC) tma_load_2d_pair(to + vb_c * 16384 + (wl * kV + vb_r) * 128, &maps.vb, vx + vb_c * 64, at, to_bar);
+          } else {
+            int at[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(0xffffffffu, v_row, v4 * 4 + e);
+            if (vc4 < kVC) gather4_pair(to + vc4 * 16384 + (wl * kV + v4 * 4) * 128, &maps.v, vx + vc4 * 64, at, to_bar);
+          }
+          if (edge) {
+            // 0 x NaN: values that are not finite are taken out, and the rows that do see them told
+            // by the column's first such key, in both CTAs
+            if (!wait(&s.edge, edges++ & 1)) break;
+            bool found = false;
+            constexpr int kRow = C::kVCols / 8;  // 16-byte pieces
 #pragma unroll 4
-                for (int i = lane; i < kKeys * kRow; i += 32) {
-                  const int row = wl * kKeys + i / kRow, c = i % kRow;
-                  const uint4 v = *reinterpret_cast<const uint4*>(to + (c >> 3) * C::kChunk + row * 128 + (((c ^ row) & 7) << 4));
-                  // an exponent of ones, and one, is a carry into the sign's place
-                  const auto not_finite = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-                  found |= (not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) != 0;
-                }
-                found = __any_sync(0xffffffffu, found);
-                if (found) {
-#pragma unroll 1
-                  for (int i = lane; i < kKeys * D; i += 32) {
-                    const int row = wl * kKeys + i / D, c = i % D;
-                    uint16_t* q = reinterpret_cast<uint16_t*>(to + (c >> 6) * C::kChunk + row * 128 + ((((c >> 3) ^ row) & 7) << 4)) + (c & 7);
-                    if ((*q & 0x7f80) == 0x7f80) {
-                      atomicMin(&s.poison[seg & 1][c], j * KT + row);
-                      *q = 0;
-                    }
-                  }
-                }
-                if (found) {
-                  s.dirty[seg & 1] = 1;
-                  fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.full[n % SLOTS]);
-              }
-              if (j == g.j0 && which == 0) {
-                // the task's queries, beside its first keys; rows past the last are zero
-                if (!wait(&s.q_empty, (seg & 1) ^ 1)) break;
-                const int rows = g.w.n * (int)p.group.d;
-                constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-                constexpr int kPer = 128 / kPieces;  // rows at once
-                const int cc = lt % kPieces, base = g.w.i * C::kM;
-                const uint32_t to_q = smem_u32(s.q[0]) + (cc >> 3) * (128 * 128);
-                const __nv_bfloat16* from = p.q + g.w.row0 * p.ldq + (long long)g.w.h * p.group.d * D + cc * 8;
-#pragma unroll 8
-                for (int r0 = 0; r0 < C::kM; r0 += kPer) {
-                  const int row = r0 + lt / kPieces, rr = row & 127;
-                  const bool live = base + row < rows;
-                  const uint32_t R = live ? base + row : 0, tok = p.group.div(R), hd = R - tok * p.group.d;
-                  cp_async16_or_zero(to_q + (row >> 7) * (128 * D * 2) + rr * 128 + (((cc ^ rr) & 7) << 4),
-                                     from + tok * p.ldq + hd * D, live);
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.q_full);
-                // the next ones on their way to L2
-                if (g.u + (g.w.nt - g.w.j) + C::kE < u1 && base + C::kM < rows) {
-#pragma unroll 2
-                  for (int i = lt; i < C::kM * (D / 64); i += 128) {
-                    const int R = base + C::kM + i / (D / 64);
-                    if (R < rows) {
-                      const uint32_t tok = p.group.div(R), hd = R - tok * p.group.d;
-                      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (g.w.row0 + tok) * p.ldq +
-                                                                    ((long long)g.w.h * p.group.d + hd) * D + i % (D / 64) * 64));
-                    }
-                  }
-                }
-              }
+            for (int e = lane; e < kV * kRow; e += 32) {
+              const int row = wl * kV + e / kRow, c = e % kRow;
+              const uint4 v = *reinterpret_cast<const uint4*>(to + (c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
+              // an exponent of ones, and one, is a carry into the sign's place
+              const auto not_finite = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+              found |= (not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) != 0;
             }
+            found = __any_sync(0xffffffffu, found);
+            if (found) {
+              constexpr int kOwn = D == 64 ? 32 : C::kVCols;
+#pragma unroll 1
+              for (int e = lane; e < kV * C::kVCols; e += 32) {
+                const int row = wl * kV + e / C::kVCols, c = e % C::kVCols;
+                uint16_t* q = reinterpret_cast<uint16_t*>(to + (c >> 6) * 16384 + row * 128 + ((((c >> 3) ^ row) & 7) << 4)) + (c & 7);
+                if ((*q & 0x7f80) == 0x7f80) {
+                  if (c < kOwn) {
+                    const unsigned word = tag << 12 | (unsigned)(4095 - (j * KT + row - first_last + 1024));
+                    for (int a = 0; a < 2; ++a) atomic_max_cluster(map_rank(&s.poison[n % kSegs][kOwn * rank + c], a), word);
+                  }
+                  *q = 0;
+                }
+              }
+              if (lane < 2) atomic_max_cluster(map_rank(&s.flagged[n % kSegs], lane), tag);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(bar);
           }
-          ++seg;
-          ok = named_all(3, 128, ok);
-        } while (ok && g.next());
-        // No copy in flight when the CTA leaves: every slot that was filled is waited for. (A wait has
-        // failed: the last phases that were begun.)
-        for (int i = max(0, n - SLOTS); i < n; ++i) mbar_wait(&s.full[i % SLOTS], i / SLOTS & 1);
+          ++i;
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
       }
-    } else if (warp == kMma && ok) {
+      // No copy in flight when the CTA leaves: the first CTA waits for every slot that was filled. (Where a
+      // wait has failed, for the last phases that were begun.)
+      if (rank == 0)
+        for (int e = max(0, i - SLOTS); e < i; ++e) mbar_wait(&s.full[e % SLOTS], e / SLOTS & 1);
+    } else if (warp == kMma && rank == 0) {
       // ---- the products
-      Segments<D> g(p, seq, start, u0, u1, s.at);
-      constexpr uint32_t is = idesc_bf16_f32(128, KT), io = idesc_bf16_f32(128, D) | kMnB;
-      int n = 0, seg = 0, sn = 0, pn[2] = {0, 0};  // slots, tasks, S tiles (with one row tile), weights' tiles
+      constexpr uint32_t is = idesc_bf16_f32(256, KT), io = idesc_bf16_f32(256, D) | kMnB;
+      int i = 0, ks = 0, sn = 0, pn[2] = {0, 0};  // slots, the present one, S tiles (with one row tile), weights' tiles
       const auto wait = [&](uint64_t* b, uint32_t parity) {
         ok = ok && mbar_wait(b, parity);
         tc_fence_after();
       };
       // descriptors of the operands, as their low words change
       const uint64_t qd = sdesc_k_sw128(smem_u32(s.q[0])), kd = sdesc_k_sw128(smem_u32(s.ring[0])),
-                     vd = sdesc_mn_sw128(smem_u32(s.ring[0]), C::kChunk);
+                     vd = sdesc_mn_sw128(smem_u32(s.ring[0]), 16384);
       // S of row tile t (into buffer b) from the keys in ring slot k
       const auto scores = [&](int t, int b, int k) {
         const uint64_t a = qd + t * (128 * D * 2 >> 4), kk = kd + k * (C::kSlotBytes >> 4);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          mma_bf16(tmem + b * C::kS, a + ((i >> 2) * (128 * 128) >> 4) + 2 * (i & 3), kk + ((i >> 2) * C::kChunk >> 4) + 2 * (i & 3),
-                   is, i > 0);
-        mma_commit(&s.s_full[b]);
+        for (int e = 0; e < D / 16; ++e)
+          mma_bf16_pair(tmem + b * 128, a + ((e >> 2) * 16384 >> 4) + 2 * (e & 3), kk + ((e >> 2) * 8192 >> 4) + 2 * (e & 3), is, e > 0);
+        mma_commit_pair(&s.s_full[b]);
       };
       const auto values = [&](int t, int b, int k, bool first, bool tell) {
         const uint64_t v = vd + k * (C::kSlotBytes >> 4);
 #pragma unroll
-        for (int i = 0; i < KT / 16; ++i)
-          mma_bf16_ts(tmem + C::kO + t * D, tmem + b * C::kS + 8 * i, v + i * (2048 >> 4), io, !(first && i == 0));
-        if (tell) mma_commit(&s.o_done[C::kTiles == 2 ? t : b]);
+        for (int e = 0; e < KT / 16; ++e)
+          mma_bf16_ts_pair(tmem + C::kO + t * D, tmem + b * 128 + (e >> 2) * (KT / 2) + 8 * (e & 3), v + e * (2048 >> 4), io, !(first && e == 0));
+        if (tell) mma_commit_pair(&s.o_done[TILES == 2 ? t : b]);
       };
-      const auto filled = [&](int slot, int i) { wait(&s.full[slot], i / SLOTS & 1); };
+      const auto filled = [&](int slot, int e) { wait(&s.full[slot], e / SLOTS & 1); };
       const auto after = [&](int slot, int d) { return slot + d >= SLOTS ? slot + d - SLOTS : slot + d; };
-      int ks = 0;  // ring slot n % SLOTS: step i's keys are slot n + 2 i, its values n + 2 i + 1
-      if (g.valid()) do {
-        const int e[2] = {g.end(0), C::kTiles == 2 ? g.end(1) : g.j0};
-        const int steps = g.j1 - g.j0;
-        wait(&s.q_full, seg & 1);
-        filled(ks, n);
+      for (int n = 0; take(n); ++n) {
+        const Seg& g = s.seg[n % kSegs];
+        const int j0 = g.j0, steps = g.j1 - j0, end[2] = {g.end[0], g.end[1]};
+        const bool split = TILES == 2 && g.split;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
+        // the segment's slots: keys i + 2 e, values i + 2 e + 1
+        wait(&s.q_full, n & 1);
+        filled(ks, i);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         if (elect_one()) {
-          if (C::kTiles == 2) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (e[t] > g.j0) scores(t, t, ks);
+          if (TILES == 2) {
+#pragma unroll 1
+            for (int t = 0; t < (split ? 1 : 2); ++t)
+              if (end[t] > j0) scores(t, t, ks);
           } else {
             scores(0, sn & 1, ks);
           }
-          mma_commit(&s.empty[ks]);
-          if (steps == 1) mma_commit(&s.q_empty);
+          mma_commit_pair(&s.empty[ks]);
+          if (steps == 1) mma_commit_pair(&s.q_empty);
         }
         __syncwarp();
         ++sn;
+        if (split) {
+          // the CTAs' one row tile each, on every second tile of keys in the other one's place
+          if (steps > 1) {
+            const int k1 = after(ks, 2);
+            filled(k1, i + 2);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (elect_one()) {
+              scores(0, 1, k1);
+              mma_commit_pair(&s.empty[k1]);
+              if (steps == 2) mma_commit_pair(&s.q_empty);
+            }
+            __syncwarp();
+          }
 #pragma unroll 1
-        for (int i = 0; i < steps; ++i) {
-          const int vs = after(ks, 1), k2 = after(ks, 2), j = g.j0 + i;
-          const bool more = i + 1 < steps;
-          if (C::kTiles == 2) {
+          for (int e = 0; e < steps; ++e) {
+            const int t = e & 1, vs = after(ks, 1), k2 = after(after(ks, 2), 2);
+            const bool more = e + 2 < steps;
+            filled(vs, i + 1);
+            if (more) filled(k2, i + 4);
+            wait(&s.p_full[t], (t ? pn[1] : pn[0]) & 1);
+            ++(t ? pn[1] : pn[0]);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (elect_one()) {
+              values(t, t, vs, e < 2, !more);
+              mma_commit_pair(&s.empty[vs]);
+              if (more) {
+                scores(0, t, k2);
+                mma_commit_pair(&s.empty[k2]);
+                if (e + 3 == steps) mma_commit_pair(&s.q_empty);
+              }
+            }
+            __syncwarp();
+            ks = after(ks, 2);
+            i += 2;
+          }
+          if (!ok) break;
+          continue;
+        }
+#pragma unroll 1
+        for (int e = 0; e < steps; ++e) {
+          const int vs = after(ks, 1), k2 = after(ks, 2), j = j0 + e;
+          const bool more = e + 1 < steps;
+          if (TILES == 2) {
             // a row tile's softmax runs while the other's products do
-            filled(vs, n + 1);
-            if (more) filled(k2, n + 2);
-#pragma unroll
+            filled(vs, i + 1);
+            if (more) filled(k2, i + 2);
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-              const bool pv = j < e[t], s_ = j + 1 < e[t];
+              const bool pv = j < end[t], s_ = j + 1 < end[t];
               if (pv) {
                 wait(&s.p_full[t], pn[t] & 1);
                 ++pn[t];
               }
               if (!(ok = __all_sync(0xffffffffu, ok))) break;
               if (elect_one()) {
-                if (pv) values(t, t, vs, i == 0, !s_);
-                if (t == 1) mma_commit(&s.empty[vs]);
+                if (pv) values(t, t, vs, e == 0, !s_);
+                if (t == 1) mma_commit_pair(&s.empty[vs]);
                 if (s_) scores(t, t, k2);
-                if (t == 1 && more) mma_commit(&s.empty[k2]);
-                if (t == 1 && i + 2 == steps) mma_commit(&s.q_empty);
+                if (t == 1 && more) mma_commit_pair(&s.empty[k2]);
+                if (t == 1 && e + 2 == steps) mma_commit_pair(&s.q_empty);
               }
               __syncwarp();
             }
@@ -683,48 +767,97 @@ __global__ void __launch_bounds__(kNT, 1)
           } else {
             // S's buffers alternate over the whole share: the softmax of a tile runs beside the next one's S
             if (more) {
-              filled(k2, n + 2);
+              filled(k2, i + 2);
               if (!(ok = __all_sync(0xffffffffu, ok))) break;
               if (elect_one()) {
                 scores(0, sn & 1, k2);
-                mma_commit(&s.empty[k2]);
-                if (i + 2 == steps) mma_commit(&s.q_empty);
+                mma_commit_pair(&s.empty[k2]);
+                if (e + 2 == steps) mma_commit_pair(&s.q_empty);
               }
               __syncwarp();
               ++sn;
             }
             const int b = pn[0] & 1;
-            filled(vs, n + 1);
+            filled(vs, i + 1);
             wait(&s.p_full[b], (pn[0] >> 1) & 1);
             ++pn[0];
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             if (elect_one()) {
-              values(0, b, vs, i == 0, true);
-              mma_commit(&s.empty[vs]);
+              values(0, b, vs, e == 0, true);
+              mma_commit_pair(&s.empty[vs]);
             }
             __syncwarp();
           }
           ks = k2;
-          n += 2;
+          i += 2;
         }
-        ++seg;
-      } while (ok && g.next());
+        if (!ok) break;
+      }
+    } else if (warp == kSched && ok) {
+      // ---- the pair's share, a part of a task at a time
+      Walk<KT, C::kE> w(p, plan, start);
+      w.from(s.at, u0);
+      long long u = u0;
+      int j0 = w.j, n = 0;
+      unsigned tag = 0;
+      bool more = true;
+      while (true) {
+        // what the share begins with of a task, or ends with, may have no tiles
+        while (more && j0 >= w.nt) {
+          u = w.task + w.nt + C::kE;
+          more = u < u1;
+          if (more) w.next_task();
+          j0 = 0;
+        }
+        ok = mbar_wait(&s.seg_empty[n % kSegs], (n / kSegs & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          Seg& g = s.seg[n % kSegs];
+          g.on = more;
+          if (more) {
+            const int t0 = w.i * p.tile_m, j1 = (int)min((long long)w.nt, j0 + (u1 - u));
+            g.s = w.s;
+            g.h = w.h;
+            g.row0 = w.row0 + t0;
+            g.toks = min(p.tile_m, w.n - t0);
+            g.pos = w.ctx + t0;
+            g.keys = w.ctx + w.n;
+            g.j0 = j0;
+            g.j1 = j1;
+            for (int t = 0; t < 2; ++t) {
+              const int first = 2 * t * tile_toks, last = min(g.toks, first + 2 * tile_toks) - 1;
+              g.end[t] = t < TILES && first <= last ? max(j0, min(j1, (g.pos + last + KT) / KT)) : j0;
+            }
+            g.split = TILES == 2 && w.nt >= kSplit && g.toks <= 2 * tile_toks;
+            if (g.split) g.end[0] = g.end[1] = j1;
+            g.whole = w.task >= u0 && w.task + w.nt <= u1;
+            g.slot = w.task >= u0;
+            g.c0 = shares.owner(w.task);
+            g.c1 = shares.owner(w.task + w.nt - 1);
+            g.tag = ++tag;
+          }
+          mbar_arrive(&s.seg_full[n % kSegs]);
+        }
+        tag = __shfl_sync(0xffffffffu, tag, 0);
+        ++n;
+        if (!more) break;
+        j0 = w.nt;  // on to the next task
+      }
     }
   }
   if (on && !ok) {
     s.failed = 1;
-    atomicCAS(p.error, 0u, (kStatusDeadline << 24) | (kAttnWait << 16) | (blockIdx.x & 0xffff));
+    atomicCAS(p.error, 0u, (kStatusDeadline << 24) | (kAttnWait << 16) | (pair & 0xffff));
   }
+  // every role of both CTAs is through: the softmax has waited for the last products, or a wait has failed
   tc_fence_before();
-  // every role is through: the softmax has waited for the last products, or a wait has failed
   __syncthreads();
+  if (s.failed)  // the products in flight take microseconds
+    for (int i = 0; i < 8; ++i) __nanosleep(1000000);
+  cluster_sync();
   tc_fence_after();
-  if (warp == kMma) {
-    // a wait has failed somewhere: the products in flight take microseconds
-    if (on && s.failed)
-      for (int i = 0; i < 8; ++i) __nanosleep(1000000);
-    tmem_dealloc(tmem, 512);
-  }
+  if (warp == kMma) tmem_dealloc_pair(tmem, 512);
 }
 
 template <int D>
@@ -732,11 +865,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
   __shared__ PlanScratch<1024> x;
   griddep_wait();
   griddep_launch_dependents();
-  attn_plan<Cfg<D>::kM, Cfg<D>::kKT, Cfg<D>::kE, 1024>(p, p.seq, p.start, x, true);
+  attn_plan<KT, Cfg<D>::kE, 1024>(p, p.seq, p.start, x, true);
 }
 
-// Tile map of a cache's rows: boxes of 64 columns, 128-byte swizzle, zeros past the last row.
-bool row_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
+// Tile map of rows of 64-column boxes, 128-byte swizzle, zeros outside: {columns, rows} or {columns, heads, tokens}.
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   typedef CUresult (*Fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                          const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                          CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -748,13 +881,15 @@ bool row_map(CUtensorMap* m, const void* base, long long rows, long long cols, l
       f = nullptr;
     return (Fn)f;
   }();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool row_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return encode(m, base, 2, dims, strides, box);
 }
 
 template <int D>
@@ -763,19 +898,30 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   cudaError_t e = opt_in<attn_tiles<D>>(smem);
   if (e != cudaSuccess) return e;
   TileMaps m = {};
+  const int G = p.group.d;
+  m.tokens = 128 / G;
+  p.tile_m = Cfg<D>::kRows / 128 * m.tokens;
+  p.tile_g = FastDiv::of(1);
   const long long rows = (long long)p.num_blocks * p.block.d, cols = (long long)p.Hkv * D;
-  // the largest power of two of rows that blocks are made of, up to a load warp's keys
-  for (int b = 8; b <= Cfg<D>::kKT / 4 && p.block.d % b == 0; b *= 2) m.box = b;
+  // the largest power of two of rows that blocks are made of, up to a load warp's
+  for (int b = 8; b <= 32 && p.block.d % b == 0; b *= 2) {
+    m.box_v = b;
+    m.box_k = b <= 16 ? b : 16;
+  }
   if (!row_map(&m.k, p.k, rows, cols, p.ldk, 1) || !row_map(&m.v, p.v, rows, cols, p.ldv, 1)) return cudaErrorInvalidValue;
-  if (m.box && (!row_map(&m.kb, p.k, rows, cols, p.ldk, m.box) || !row_map(&m.vb, p.v, rows, cols, p.ldv, m.box)))
+  if (m.box_k && (!row_map(&m.kb, p.k, rows, cols, p.ldk, m.box_k) || !row_map(&m.vb, p.v, rows, cols, p.ldv, m.box_v)))
     return cudaErrorInvalidValue;
-  if (p.seqs <= kAttnPlannedTiles) p.seq = nullptr;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hkv * G, (cuuint64_t)p.tokens},
+                   strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.ldq * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)m.tokens};
+  if (!encode(&m.q, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  if (p.seqs <= kAttnPlanned) p.seq = nullptr;
   if (p.seq) {
     const Launch one(dim3(1), 1024, 0, true, s);
     e = cudaLaunchKernelEx(&one.cfg, plan_kernel<D>, p);
     if (e != cudaSuccess) return e;
   }
-  const Launch all(dim3(grid), kNT, smem, true, s);
+  const Launch all(dim3(grid / 2 * 2), Cfg<D>::kNT, smem, true, s);
   return cudaLaunchKernelEx(&all.cfg, attn_tiles<D>, m, p);
 }
 
