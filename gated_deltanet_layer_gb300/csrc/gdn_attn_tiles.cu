@@ -10,10 +10,10 @@
 // multiplied only when the maximum grows by more, so that weights are at most 2^8 and hardly a
 // tile is corrected; the sums divide it out again.
 //
-// Eight warps a row tile: the softmax, half a row a thread, and the outputs. Four warps: queries, keys and values by
+// Warps 0 - 7: the softmax, a row a thread, and the outputs. Warps 8 - 11: queries, keys and values by
 // TMA; the blocks' rows in boxes where a block is made of boxes of 8 or more, else four rows a copy
-// from any four slots, and rows past the last key are zeros. One warp of the first CTA: the
-// products of both. One warp: which part of which task comes next. With two row tiles a CTA
+// from any four slots, and rows past the last key are zeros. Warp 12 of the first CTA: the
+// products of both. Warp 13: which part of which task comes next. With two row tiles a CTA
 // the tensor cores work on one while the softmax works on the other; with one, S alternates
 // between two buffers. A task whose rows fill one tile of each CTA alone has the keys of
 // every second tile in the place of the other tile's rows, and joins the two.
@@ -29,6 +29,8 @@ namespace {
 
 using namespace tc;
 
+constexpr int kNT = 512;
+constexpr int kLoad0 = 8, kMma = 12, kSched = 13;  // first load warp; the warp of the products; of the tasks
 constexpr float kSlack = 8.f;                      // log2 of the most that a weight is above 1
 constexpr int KT = 128;                            // keys of a tile
 constexpr int kSegs = 4;                           // parts of tasks that are known ahead
@@ -38,9 +40,6 @@ template <int D>
 struct Cfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;          // row tiles of a CTA
   static constexpr int kRows = 256 * kTiles;               // rows of a task
-  static constexpr int kLoad0 = 8 * kTiles, kMma = kLoad0 + 4, kSched = kMma + 1;  // first load warp; the warp of the products; of the tasks
-  static constexpr int kNT = 32 * (kLoad0 + 8);
-  static constexpr int kSoftRegs = D == 256 ? 176 : 96, kOtherRegs = D == 256 ? 80 : 48;  // of what the launch has
   static constexpr int kVCols = D == 256 ? 128 : 64;       // a CTA's columns of the values (heads of 64: 32, and 32 for nothing)
   static constexpr int kSlotBytes = D == 256 ? 32768 : 16384;  // 64 keys, or kVCols columns of 128 values
   static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 9 : 4;
@@ -80,8 +79,7 @@ struct alignas(1024) TileSmem {
   unsigned poison[kSegs][D], flagged[kSegs];
   int4 plan[kAttnPlanned + 1];
   long long start[kAttnPlanned + 1];
-  PlanScratch<C::kNT> scan;
-  float half[2][2][128];  // what the two threads of a row tell one another, by S's buffer
+  PlanScratch<kNT> scan;
 };
 
 // D[both CTAs' tmem] (+)= A[both CTAs' tmem] B, 256 rows; half of B in each CTA.
@@ -157,10 +155,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
@@ -168,13 +163,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const float (&v)[32]) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -245,13 +233,13 @@ struct TileMaps {
 };
 
 template <int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     attn_tiles(const __grid_constant__ TileMaps maps, const AttnParams p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) unsigned char raw[];
   static_assert(sizeof(TileSmem<D>) <= 232448, "227 KB of shared memory a CTA");
   TileSmem<D>& s = *reinterpret_cast<TileSmem<D>*>(raw);
-  constexpr int SLOTS = C::kSlots, TILES = C::kTiles, kNT = C::kNT, kLoad0 = C::kLoad0, kMma = C::kMma, kSched = C::kSched;
+  constexpr int SLOTS = C::kSlots, TILES = C::kTiles;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
@@ -264,12 +252,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 16);
+      mbar_init(&s.p_full[i], 8);
       mbar_init(&s.o_done[i], 1);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&s.seg_full[i], 1);
-      mbar_init(&s.seg_empty[i], 16 * TILES + 4 + (rank == 0));  // both CTAs' softmax, the load warps, the products
+      mbar_init(&s.seg_empty[i], 8 * TILES + 4 + (rank == 0));  // both CTAs' softmax, the load warps, the products
       s.flagged[i] = 0;
     }
     s.failed = 0;
@@ -313,9 +301,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
   };
 
   if (warp < kLoad0) {
-    more_regs<C::kSoftRegs>();
-    {
-      const int t = warp >> 3, hf = warp >> 2 & 1;  // row tile; half of the columns
+    more_regs<192>();
+    const int t = warp >> 2;  // row tile
+    if (t < TILES) {
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const int r = (warp & 3) * 32 + lane;
       const bool in_tile = r < tile_toks * G, warp_in_tile = (warp & 3) * 32 < tile_toks * G;
@@ -323,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
       int sn = 0, ends = 0;  // S tiles, and segments with any so far (of the row tile)
       for (int n = 0;; ++n) {
         const bool there = take(n);
-        if (!(ok = named_all(1 + t, 256, ok)) || !there) break;
+        if (!(ok = named_all(1 + t, 128, ok)) || !there) break;
         const Seg& g = s.seg[n % kSegs];
         const bool split = TILES == 2 && g.split;
         const int j0 = g.j0 + (split ? t : 0), end = g.end[t], step = split ? 2 : 1, toks = g.toks, pos = g.pos;
@@ -337,50 +325,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
           const uint32_t sc = tmem + lanes + b * 128;
           ok = mbar_wait(&s.s_full[b], (TILES == 2 ? sn : sn >> 1) & 1);
           tc_fence_after();
-          float tile_top = -INFINITY;
-          // this half's S, 32 columns at a time, of which the keys 0 .. seen are seen
-          const int seen = last_key - j * KT - hf * (KT / 2);
-          const bool hides = __any_sync(0xffffffffu, seen < KT / 2 - 1);
-          const auto scores = [&](int c, float (&x)[32]) {
-            tmem_ld32(sc + hf * (KT / 2) + c, x);
-            if (hides) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c + i > seen) x[i] = -INFINITY;
-            }
-          };
-          if (warp_live && ok) {
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < KT / 2; c += 32) {
-              float x[32];
-              scores(c, x);
-#pragma unroll
-              for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[e + i], x[e + 4 + i]);
-            }
-            tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-            s.half[b][hf][r] = tile_top;
-          }
-          if (!(ok = named_all(1 + t, 256, ok))) break;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           if (warp_live) {
-            tile_top = fmaxf(tile_top, s.half[b][hf ^ 1][r]);
+            float x[KT];
+#pragma unroll
+            for (int c = 0; c < KT; c += 32) tmem_ld32(sc + c, *reinterpret_cast<float(*)[32]>(x + c));
+            const int seen = last_key - j * KT;  // the tile's keys 0 .. seen
+            if (__any_sync(0xffffffffu, seen < KT - 1)) {
+#pragma unroll
+              for (int c = 0; c < KT; ++c)
+                if (c > seen) x[c] = -INFINITY;
+            }
+            float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int c = 4; c < KT - 4; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[c + i], x[c + 4 + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[KT - 4 + i]);
+            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
             if (__any_sync(0xffffffffu, tile_top > m + kSlack || m == -INFINITY)) {
               const float grown = fmaxf(m, tile_top), f = m == -INFINITY ? 0.f : ex2(m - grown);
               if (j > j0) {
                 if (TILES == 1) {  // S came before the last PV
                   ok = mbar_wait(&s.o_done[(sn - 1) & 1], ((sn - 1) >> 1) & 1);
+                  ok = __all_sync(0xffffffffu, ok);
+                  if (!ok) break;
                   tc_fence_after();
                 }
 #pragma unroll 1
-                for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+                for (int c = 0; c < D; c += 32) {
                   float o[32];
                   const uint32_t at = tmem + lanes + C::kO + t * D + c;
                   tmem_ld32(at, o);
 #pragma unroll
                   for (int i = 0; i < 32; ++i) o[i] *= f;
-                  tmem_st32(at, o);
+                  uint32_t w[32];
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i]);
+                  tmem_st32(at, w);
                 }
               }
               l *= f;
@@ -389,21 +373,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
             const float base = m == -INFINITY ? 0.f : m;
             const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-base, -base);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            // P over the first half of the S that it comes from
 #pragma unroll
-            for (int c = 0; c < KT / 2; c += 32) {
-              float x[32];
-              uint32_t w[16];
-              scores(c, x);
+            for (int c = 0; c < KT; c += 64) {
+              uint32_t w[32];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float2 y = fma2(make_float2(x[2 * i], x[2 * i + 1]), by, less);
+              for (int i = 0; i < 32; ++i) {
+                float2 y = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), by, less);
                 y.x = ex2(y.x);
                 y.y = ex2(y.y);
                 sum[i & 1] = add2(sum[i & 1], y);
                 w[i] = pack2(y.x, y.y);
               }
-              tmem_st16(sc + hf * (KT / 2) + c / 2, w);
+              tmem_st32(sc + c / 2, w);
             }
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
@@ -422,9 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
           ++ends;
           tc_fence_after();
         }
-        s.half[t][hf][r] = l;
-        if (!(ok = named_all(1 + t, 256, ok))) break;
-        l += s.half[t][hf ^ 1][r];
+        if (!(ok = named_all(1 + t, 128, ok))) break;
         const int c0 = g.c0, c1 = g.c1;
         const bool whole = g.whole && !split;
         const long long part_row = (2LL * pair + g.slot) * C::kRows + (2 * t + rank) * 128;  // the part's first row
@@ -435,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (warp_live) {
 #pragma unroll 1
-          for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+          for (int c = 0; c < D; c += 32) {
             float o[32];
             if (any) {
               tmem_ld32(tmem + lanes + C::kO + t * D + c, o);
@@ -444,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
               for (int i = 0; i < 32; ++i) o[i] = 0.f;
             }
             if (flagged) {
-#pragma unroll 4
+#pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const unsigned q = poison[c + i];
                 if (q >> 12 == tag && (int)(4095 - (q & 4095)) <= last_key - pos + 1024) o[i] = NAN;
@@ -460,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
               }
             }
           }
-          if (!whole && live && hf == 0) p.part_ml[part_row + r] = make_float2(m, l);
+          if (!whole && live) p.part_ml[part_row + r] = make_float2(m, l);
         }
         // the segment's entry and flags are free once both CTAs' softmax has read them
         __syncwarp();
@@ -469,16 +448,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
           unsigned* done = p.done + 4 * c0 + (split ? 0 : 2 * t) + rank;
           const int parts = (c1 - c0 + 1) << (split ? 1 : 0);
           __threadfence();
-          named_sync(1 + t, 256);
-          if (r == 0 && hf == 0) {
+          named_sync(1 + t, 128);
+          if (r == 0) {
             s.last[t] = atomicAdd(done, 1u) == (unsigned)(parts - 1);
             __threadfence();
           }
-          named_sync(1 + t, 256);
+          named_sync(1 + t, 128);
           if (s.last[t]) {
             // every part is there: the first pair's second one, the others' first, and where the keys
             // are split both row tiles'
-            if (r == 0 && hf == 0) *done = 0;
+            if (r == 0) *done = 0;
             const auto at = [&](int k) {
               const int c = c0 + (split ? k >> 1 : k), u = split ? k & 1 : t;
               return (2LL * c + (c == c0)) * C::kRows + (2 * u + rank) * 128;
@@ -494,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
               }
               const float in = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
-              for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+              for (int c = 0; c < D; c += 32) {
                 float o[32] = {};
 #pragma unroll 2
                 for (int k = 0; k < parts; ++k) {
@@ -517,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
       }
     }
   } else {
-    fewer_regs<C::kOtherRegs>();
+    fewer_regs<64>();
     if (warp < kMma) {
       // ---- queries, keys and values: of a tile this CTA's 64 keys, and its columns of the 128 values
       const int wl = warp - kLoad0;
@@ -672,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::kNT, 1)
         const uint64_t v = vd + k * (C::kSlotBytes >> 4);
 #pragma unroll
         for (int e = 0; e < KT / 16; ++e)
-          mma_bf16_ts_pair(tmem + C::kO + t * D, tmem + b * 128 + (e >> 2) * (KT / 2) + 8 * (e & 3), v + e * (2048 >> 4), io, !(first && e == 0));
+          mma_bf16_ts_pair(tmem + C::kO + t * D, tmem + b * 128 + 8 * e, v + e * (2048 >> 4), io, !(first && e == 0));
         if (tell) mma_commit_pair(&s.o_done[TILES == 2 ? t : b]);
       };
       const auto filled = [&](int slot, int e) { wait(&s.full[slot], e / SLOTS & 1); };
@@ -921,7 +900,7 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
     e = cudaLaunchKernelEx(&one.cfg, plan_kernel<D>, p);
     if (e != cudaSuccess) return e;
   }
-  const Launch all(dim3(grid / 2 * 2), Cfg<D>::kNT, smem, true, s);
+  const Launch all(dim3(grid / 2 * 2), kNT, smem, true, s);
   return cudaLaunchKernelEx(&all.cfg, attn_tiles<D>, m, p);
 }
 
