@@ -1,76 +1,90 @@
 // act(x W^T + bias) + residual with W in 4 bits (gdn_linear_w4): a few rows of x, bound by
-// the bandwidth of the weights.
+// the bandwidth of the weights and the instructions that unpack them.
 //
-// y[m][n] = sum over groups of scale[n][g] (sum_k code[n][k] x[m][k] - zero[n][g] sum_k x[m][k]).
-// Products by mma.sync (16 weight rows x 8 rows of x x 16 columns) in f16 with f32 sums, a
-// group at a time, then scale times the group's sum in f32, so no weight is ever rounded.
+// y[m][n] = sum over groups of scale[n][g] sum_k value[n][k] x[m][k], value = code - zero or E2M1.
+// Products by mma.sync (16 weight rows x 8 rows of x x 16 columns) in bf16 with f32 sums, a
+// group at a time, then scale times the group's sum in f32: a value has at most 8 bits, so
+// no weight is rounded, and x is taken as it is.
 //
-// x as f16: every row times a power of two that takes its largest value to 2^14 .. 2^15, which
-// keeps bf16's 8 bits down to 2^-27 of that value.
-// Codes as f16. 4-bit whole numbers: 0x6400 | code is 1024 + code, and with the code four bits
-// further up 1024 + 16 code, so eight codes are four ANDs with an OR and one shift. The
-// columns of the second kind take x / 16, and what the 1024s add is known from sums of x: a group's
-// sum starts from minus that and minus zero times sum x. E2M1: a conversion of the hardware's, exact.
 // The order of the columns within a group of 32 is free as long as x has the same: a
-// lane's eight codes are one 32-bit word, and x is laid out in shared memory as the lanes want it.
+// lane's eight codes are one 32-bit word, its eight of x the 16 bytes beside them. Whole numbers: the
+// codes' bytes as bf16 are c 2^-133, one multiply-add makes (c - zero) 2^-6 of two. E2M1: the two
+// bytes of a bf16 from tables of eight, by permutes whose selectors are the codes themselves.
 //
-// A CTA takes 128 weight rows, 16 a warp, and a share of the columns; the CTAs of a cluster
-// share the columns and add their sums through distributed shared memory, in order.
-#include <cuda_fp16.h>
-
+// A CTA's warps are R x S: R groups of 16 weight rows, as many as give every SM one CTA, and S shares of
+// the columns, as many as there are warps left, whose sums are added up in shared memory at the end.
+// A warp's codes come through a ring of its own (cp.async), its scales and zeros four groups at
+// a time through registers, and x as a piece of all shares' columns at a time, two pieces deep;
+// from 17 rows on x comes to the lanes as it is, from L1: its pieces would be too short.
 #include <algorithm>
 
 #include "gdn_host.h"
 #include "gdn_prefill.cuh"
-#include "gdn_tc_pair.cuh"
+#include "gdn_tc_ptx.cuh"
 
 namespace gdn {
 namespace {
 
 using namespace tc;
 
-constexpr int kW = 8, kNT = kW * 32;
-constexpr int kRowsN = 16 * kW;     // weight rows of a CTA
-constexpr int kStep = 128;          // columns of a stage
-constexpr int kStages = 8;
-constexpr int kPitch = kStep / 2 + 16;  // bytes of a stage's row: its codes, and 16 against bank conflicts
+constexpr int kStep = 256;              // columns of a stage
+constexpr int kStages = 4;
+constexpr int kPitch = kStep / 2;       // bytes of a stage's row; its 16-byte pieces permuted, against bank conflicts
+constexpr int kStageBytes = 16 * kPitch, kRing = kStages * kStageBytes;  // of a warp
+constexpr int kXBytes = 32768;          // of x at a time, of all shares; twice
+constexpr bool x_in_smem(int mt) { return mt <= 2; }
 
-// Columns of x in shared memory at a time.
+// Warps of a CTA: what the registers allow.
 template <int MT>
-constexpr int chunk() { return MT <= 2 ? 1024 : MT == 4 ? 512 : 256; }
+constexpr int warps() { return MT <= 2 ? 20 : 16; }
 
-template <int MT>
-struct W4Smem {
-  unsigned char ring[kW][kStages][16 * kPitch];
-  uint4 x[chunk<MT>() / 32][MT][32];               // [group of 32][8 rows][lane]: 8 columns of a row as f16
-  float4 sums[chunk<MT>() / 32][MT][4];            // [group][8 rows][t]: what to start from, of rows 2 t and 2 t + 1: 1024s' part, sum x
-  float out[MT * 8][kRowsN];
-  float factor[MT * 8], unfactor[MT * 8];
-};
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// (v & mask) | 0x6400 in both halves.
-__device__ __forceinline__ uint32_t and_or_1024(uint32_t v, uint32_t mask) {
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(0x64006400u));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
-// Two E2M1 codes of a byte as f16.
-__device__ __forceinline__ uint32_t e2m1x2(uint32_t byte) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b, x, y, z;\n\tmov.b32 {b, x, y, z}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(byte));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-// Scales take 2^-15 with them, so that with x at up to 2^16 no sum is larger than what it stands
-// for; bf16's 8 bits and powers of two are exact at any size of theirs.
-constexpr float kDown = 0x1p-15f;
-__device__ __forceinline__ float e8m0(uint32_t e) {  // 2^(e - 127) of them
-  return __uint_as_float(e < 16 ? 0x80u << e : e == 255 ? 0x7fc00000u : (e - 15) << 23);
+// (v & mask) | w.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(w));
+  return r;
+}
+// Eight whole numbers (c - zero) 2^-6 as bf16; less: -zero 2^-6 twice.
+__device__ __forceinline__ void unpack_int(uint32_t w, uint32_t less, uint32_t (&o)[4]) {
+  const uint32_t ev = w & 0x0f0f0f0fu, od = (w >> 4) & 0x0f0f0f0fu;  // codes 0 2 4 6, 1 3 5 7
+  // a byte and its sign, which is 0, of each: bf16 subnormals
+  o[0] = fma_bf16x2(prmt(ev, od, 0xC480), 0x7f007f00u, less);
+  o[1] = fma_bf16x2(prmt(ev, od, 0xD591), 0x7f007f00u, less);
+  o[2] = fma_bf16x2(prmt(ev, od, 0xE6A2), 0x7f007f00u, less);
+  o[3] = fma_bf16x2(prmt(ev, od, 0xF7B3), 0x7f007f00u, less);
+}
+// Eight E2M1 values as bf16.
+__device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t (&o)[4]) {
+  const uint32_t up = w << 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    // 0, 1/2, 1, 3/2, 2, 3, 4, 6: 0000 3F00 3F80 3FC0 4000 4040 4080 40C0
+    const uint32_t sel = (h ? w >> 16 : w) & 0x7777u;
+    const uint32_t lo = prmt(0xC0800000u, 0xC0804000u, sel), hi = prmt(0x3F3F3F00u, 0x40404040u, sel);
+    // bit 7 of these bytes: the codes' signs
+    const uint32_t top = and_or(prmt(up, w, h ? 0x7362 : 0x5140), 0x80808080u, hi);
+    o[2 * h] = prmt(lo, top, 0x5140);
+    o[2 * h + 1] = prmt(lo, top, 0x7362);
+  }
+}
+__device__ __forceinline__ float e8m0(uint32_t e) {
+  return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : e << 23);
 }
 __device__ __forceinline__ float act_f(float y, int act) {
   if (act == 0) return y;
@@ -78,250 +92,233 @@ __device__ __forceinline__ float act_f(float y, int act) {
   return __fdividef(y, 1.0f + __expf(-s));
 }
 
-// FMT 0: whole numbers with zeros, 1: E2M1. GPS: scale groups of a stage (4, 2, 1).
-template <int FMT, int GPS, int MT>
-__global__ void __launch_bounds__(kNT) linear_w4(const W4Params p) {
-  extern __shared__ unsigned char raw[];
-  W4Smem<MT>& s = *reinterpret_cast<W4Smem<MT>*>(raw);
-  constexpr int KC = chunk<MT>();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
+// FMT 0: whole numbers with zeros, 1: E2M1. GPS: scale groups of a stage (8, 4, 2). MT: 8 rows of x. MR: rows
+// of x that are kept; with one, all of a product's columns are that row.
+template <int FMT, int GPS, int MT, int MR>
+__global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params p) {
+  static_assert(MR == MT * 8 || MR == 1, "");
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int kNT = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int R = p.row_groups, S = p.shares, rg = warp % R, sl = warp / R;
+  constexpr bool kStaged = x_in_smem(MT);
+  unsigned char* const ring = smem + (kStaged ? 2 * kXBytes : 0) + warp * kRing;
   const int m0 = blockIdx.y * MT * 8, M = min(MT * 8, p.M - m0);
   const int all = (p.K + kStep - 1) / kStep;
-  const int s0 = (int)((long long)all * rank / p.split), s1 = (int)((long long)all * (rank + 1) / p.split);
-  const int n0 = tile * kRowsN + warp * 16;
+  const int each = (all + S - 1) / S;  // stages of a share
+  const int s0 = min(sl * each, all), s1 = min(s0 + each, all);
+  const int piece = kStaged ? min(each, kXBytes / (2 * kStep * MR * S)) : each;  // stages of x at a time
+  const int n0 = (blockIdx.x * R + rg) * 16;
   const long long row0 = min(n0 + g, p.N - 1), row1 = min(n0 + g + 8, p.N - 1);
   const int groups = p.K / p.group;  // of a row
   griddep_wait();
   griddep_launch_dependents();
 
-  const auto issue = [&](int st) {
-    if (st < s1) {
+  // the lane's four 16-byte pieces of a stage's codes, of every fourth row
+  const unsigned char* from[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = (lane + 32 * i) >> 2, q = lane & 3, k = st * kStep + q * 32;
-        const unsigned char* src = p.codes + (long long)min(n0 + r, p.N - 1) * (p.K / 2) + k / 2;
-        const bool on = k < p.K;
+  for (int i = 0; i < 4; ++i)
+    from[i] = p.codes + (long long)min(n0 + (lane >> 3) + 4 * i, p.N - 1) * (p.K / 2) + (long long)s0 * (kStep / 2) + (lane & 7) * 16;
+  const uint32_t to = smem_u32(ring + (lane >> 3) * kPitch);
+  const auto codes_in = [&](int st) {
+    if (st < s1) {
+      const bool on = st * kStep + (lane & 7) * 32 < p.K;
+      const uint32_t at = to + (st & (kStages - 1)) * kStageBytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         smem_u32(s.ring[warp][(st - s0) % kStages] + r * kPitch + q * 16)),
-                     "l"(on ? src : p.codes), "r"(on ? 16 : 0)
+                         at + i * (4 * kPitch) + (((lane & 7) ^ ((lane >> 3) + 4 * i & 7)) << 4)),
+                     "l"(on ? from[i] : p.codes), "r"(on ? 16 : 0)
                      : "memory");
+        from[i] += kStep / 2;
       }
     }
     cp_async_commit();
   };
-#pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) issue(s0 + i);
-
-  // the rows' powers of two
-  for (int m = warp; m < MT * 8; m += kW) {
-    uint32_t top = 0;
-    if (m < M) {
-      const __nv_bfloat16* x = p.x + (long long)(m0 + m) * p.ldx;
-      for (int k = s0 * kStep + lane * 8; k < min(s1 * kStep, p.K); k += 256) {
-        const uint4 v = *reinterpret_cast<const uint4*>(x + k);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a = (u[j] >> 7) & 0xff, b = (u[j] >> 23) & 0xff;
-          if (a < 255) top = max(top, a);
-          if (b < 255) top = max(top, b);
-        }
+  // x of the shares' stages [c, c + piece): [share][group of 32][row][t], 8 columns each; zeros past the last
+  // column
+  const auto x_in = [&](int c, int buf) {
+    const uint32_t x = smem_u32(smem) + buf * kXBytes;
+    const int per_row = piece * (kStep / 8), rows = S * M;
+    for (int a = warp; a < rows; a += kNT >> 5) {
+      const int sh = a / M, m = a - sh * M, k0 = (sh * each + c) * kStep;
+      const __nv_bfloat16* src = p.x + (long long)(m0 + m) * p.ldx + k0;
+      const uint32_t dst = x + (sh * piece * (kStep / 32) * MR + m) * 64;
+      for (int i = lane; i < per_row; i += 32) {
+        const bool on = k0 + i * 8 < p.K;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (i >> 2) * (MR * 64) + (i & 3) * 16),
+                     "l"(on ? src + i * 8 : p.x), "r"(on ? 16 : 0)
+                     : "memory");
       }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) {
-      const int e = top == 0 ? 0 : max(-112, min(127, 141 - (int)top));
-      s.factor[m] = __uint_as_float((uint32_t)(e + 127) << 23);
-      s.unfactor[m] = __uint_as_float((uint32_t)(15 - e + 127) << 23);
+  };
+  // Scales (and zeros) of four groups of the two rows: a lane's t-th.
+  const auto scale_in = [&](int quad, uint32_t (&v)[2]) {
+    const int at = quad * 4 + t;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[e] = 0;
+      if (at < groups) {
+        const long long i = (e ? row1 : row0) * groups + at;
+        if (FMT == 1)
+          v[e] = __ldg(static_cast<const uint8_t*>(p.scales) + i);
+        else
+          v[e] = (uint32_t)__ldg(static_cast<const unsigned short*>(p.scales) + i) << 16 | (p.zeros ? __ldg(p.zeros + i) : 8u);
+      }
     }
-  }
+  };
+  constexpr int kQuad = GPS < 4 ? 4 / GPS : 1, kQuads = GPS > 4 ? GPS / 4 : 1;  // stages of four groups; fours of a stage
+  constexpr int kAhead = 2 * kQuads;  // fours that are on their way
+  if (kStaged) x_in(0, 0);
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) codes_in(s0 + i);
+  uint32_t sc[kAhead][2];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) scale_in(s0 / kQuad * kQuads + i, sc[i]);
+
   float acc[MT][4] = {};
-  __syncthreads();
-
-  int st = s0;
+  int buf = 0;
 #pragma unroll 1
-  for (int c0 = s0; c0 < s1; c0 += KC / kStep) {
-    const int c1 = min(c0 + KC / kStep, s1);
-    // x of the chunk
-    for (int i = tid; i < (c1 - c0) * 4 * MT * 32; i += kNT) {
-      const int l = i & 31, mt = (i >> 5) % MT, gr = (i >> 5) / MT, m = mt * 8 + (l >> 2), k = c0 * kStep + gr * 32 + (l & 3) * 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (m < M && k < p.K) v = *reinterpret_cast<const uint4*>(p.x + (long long)(m0 + m) * p.ldx + k);
-      const float f = s.factor[m];
-      const float y[8] = {bf16_lo(v.x) * f, bf16_hi(v.x) * f, bf16_lo(v.y) * f, bf16_hi(v.y) * f,
-                          bf16_lo(v.z) * f, bf16_hi(v.z) * f, bf16_lo(v.w) * f, bf16_hi(v.w) * f};
-      const auto h2 = [](float a, float b) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-      };
-      if (FMT == 1) {
-        s.x[gr][mt][l] = make_uint4(h2(y[0], y[1]), h2(y[2], y[3]), h2(y[4], y[5]), h2(y[6], y[7]));
-      } else {
-        constexpr float q = 0.0625f;
-        const uint4 o = make_uint4(h2(y[0], y[4]), h2(y[1] * q, y[5] * q), h2(y[2], y[6]), h2(y[3] * q, y[7] * q));
-        s.x[gr][mt][l] = o;
-        // the sums of what is multiplied: of the first kind's columns, and of the second's
-        const auto sum = [](uint32_t a, uint32_t b) {
-          const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a)), w = __half22float2(*reinterpret_cast<const __half2*>(&b));
-          return (u.x + u.y) + (w.x + w.y);
-        };
-        float one = sum(o.x, o.z), two = sum(o.y, o.w);
-        float start = (one + two) * 1024.f, x = one + 16.f * two;
-        start += __shfl_xor_sync(0xffffffffu, start, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        start += __shfl_xor_sync(0xffffffffu, start, 2);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if ((l & 3) == 0) reinterpret_cast<float2*>(&s.sums[gr][mt][0])[l >> 2] = make_float2(start, x);
-      }
+  for (int c = 0; c < each; c += piece, buf ^= 1) {
+    // x of these stages has come: with the codes that were asked for after it, or now
+    if (kStaged) {
+      if (c == 0 || piece < kStages) asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+      if (c + piece < each) x_in(c + piece, buf ^ 1);
     }
-    __syncthreads();
+    const unsigned char* x = smem + buf * kXBytes + sl * piece * (kStep / 32) * (MR * 64) + (MR == 1 ? t * 16 : g * 64 + t * 16);
 #pragma unroll 1
-    for (; st < c1; ++st) {
-      issue(st + kStages - 1);
-      float sc[GPS][2], zr[GPS][2];
-#pragma unroll
-      for (int q = 0; q < GPS; ++q) {
-        const int at = st * GPS + q;
-        const bool on = at < groups;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const long long i = (e ? row1 : row0) * groups + (on ? at : 0);
-          if (FMT == 1) {
-            sc[q][e] = on ? e8m0(static_cast<const uint8_t*>(p.scales)[i]) : 0.f;
-          } else {
-            sc[q][e] = on ? bf16_to_f(static_cast<const __nv_bfloat16*>(p.scales)[i]) * kDown : 0.f;
-            zr[q][e] = p.zeros ? (float)p.zeros[i] : 8.f;
-          }
-        }
-      }
+    for (int k = 0; k < piece; ++k, x += kStep / 32 * MR * 64) {  // all of them, for the waits, though the share may end before
+      const int st = s0 + c + k;
+      codes_in(st + kStages - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
-      const unsigned char* codes = s.ring[warp][(st - s0) % kStages];
-      float c[MT][4];
+      if (st >= s1) continue;
+      const unsigned char* codes = ring + (st & (kStages - 1)) * kStageBytes + g * kPitch + t * 4;
+      const int k0 = st * kStep + t * 8;  // the lane's first column
+      const int in_quad = kQuad > 1 ? (st % kQuad) * GPS : 0;  // the stage's first scale group, of the lanes' four
+      float z[MT][4], f[2];
+      uint32_t less[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        constexpr int PER = 4 / GPS;  // groups of 32 of a scale group
-        const int gr = (st - c0) * 4 + q, sg = q / PER;
+      for (int q = 0; q < kStep / 32; ++q) {
+        constexpr int PER = kStep / 32 / GPS;  // groups of 32 of a scale group
         if (q % PER == 0) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t v = __shfl_sync(0xffffffffu, sc[q / PER / 4][e], (lane & 28) + in_quad + q / PER % 4);
             if (FMT == 1) {
-              c[mt][0] = c[mt][1] = c[mt][2] = c[mt][3] = 0.f;
+              f[e] = e8m0(v);
             } else {
-              float4 z = s.sums[gr][mt][t];
-#pragma unroll
-              for (int i = 1; i < PER; ++i) {
-                const float4 y = s.sums[gr + i][mt][t];
-                z.x += y.x, z.y += y.y, z.z += y.z, z.w += y.w;
-              }
-              c[mt][0] = -fmaf(zr[sg][0], z.y, z.x);
-              c[mt][1] = -fmaf(zr[sg][0], z.w, z.z);
-              c[mt][2] = -fmaf(zr[sg][1], z.y, z.x);
-              c[mt][3] = -fmaf(zr[sg][1], z.w, z.z);
+              f[e] = __uint_as_float(v & 0xffff0000u);
+              const float u = (float)(v & 0xffff) * -0x1p-6f;
+              less[e] = pack_bf16x2(u, u);
             }
           }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) z[mt][0] = z[mt][1] = z[mt][2] = z[mt][3] = 0.f;
         }
-        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(codes + g * kPitch + q * 16 + t * 4);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + (g + 8) * kPitch + q * 16 + t * 4);
-        uint32_t a[4], b[4];
+        uint4 y[MT];
+        if (!kStaged) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            y[mt] = make_uint4(0, 0, 0, 0);
+            if (mt * 8 < M && k0 + q * 32 < p.K)
+              y[mt] = __ldg(reinterpret_cast<const uint4*>(p.x + (long long)(m0 + min(mt * 8 + g, M - 1)) * p.ldx + k0 + q * 32));
+          }
+        }
+        const int at = (q ^ g) << 4;
+        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(codes + at);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + 8 * kPitch + at);
+        uint32_t v0[4], v1[4];
         if (FMT == 1) {
-          a[0] = e2m1x2(w0), a[1] = e2m1x2(w1), a[2] = e2m1x2(w0 >> 8), a[3] = e2m1x2(w1 >> 8);
-          b[0] = e2m1x2(w0 >> 16), b[1] = e2m1x2(w1 >> 16), b[2] = e2m1x2(w0 >> 24), b[3] = e2m1x2(w1 >> 24);
+          unpack_e2m1(w0, v0);
+          unpack_e2m1(w1, v1);
         } else {
-          const uint32_t lo = 0x000f000fu, hi = 0x00f000f0u, v0 = w0 >> 8, v1 = w1 >> 8;
-          a[0] = and_or_1024(w0, lo), a[1] = and_or_1024(w1, lo), a[2] = and_or_1024(w0, hi), a[3] = and_or_1024(w1, hi);
-          b[0] = and_or_1024(v0, lo), b[1] = and_or_1024(v1, lo), b[2] = and_or_1024(v0, hi), b[3] = and_or_1024(v1, hi);
+          unpack_int(w0, less[0], v0);
+          unpack_int(w1, less[1], v1);
         }
+        const uint32_t a[4] = {v0[0], v1[0], v0[1], v1[1]}, b[4] = {v0[2], v1[2], v0[3], v1[3]};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const uint4 x = s.x[gr][mt][lane];
-          mma_f16(c[mt], a, x.x, x.y);
-          mma_f16(c[mt], b, x.z, x.w);
+          if (mt > 0 && mt * 8 >= M) break;  // no such rows
+          if (kStaged) y[mt] = *reinterpret_cast<const uint4*>(x + q * (MR * 64) + mt * 512);
+          mma_bf16_16816(z[mt], a, y[mt].x, y[mt].y);
+          mma_bf16_16816(z[mt], b, y[mt].z, y[mt].w);
         }
         if (q % PER == PER - 1) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            acc[mt][0] = fmaf(sc[sg][0], c[mt][0], acc[mt][0]);
-            acc[mt][1] = fmaf(sc[sg][0], c[mt][1], acc[mt][1]);
-            acc[mt][2] = fmaf(sc[sg][1], c[mt][2], acc[mt][2]);
-            acc[mt][3] = fmaf(sc[sg][1], c[mt][3], acc[mt][3]);
+            acc[mt][0] = fmaf(f[0], z[mt][0], acc[mt][0]);
+            acc[mt][1] = fmaf(f[0], z[mt][1], acc[mt][1]);
+            acc[mt][2] = fmaf(f[1], z[mt][2], acc[mt][2]);
+            acc[mt][3] = fmaf(f[1], z[mt][3], acc[mt][3]);
           }
         }
       }
+      if ((st + 1) % kQuad == 0) {
+#pragma unroll
+        for (int i = 0; i < kAhead - kQuads; ++i) sc[i][0] = sc[i + kQuads][0], sc[i][1] = sc[i + kQuads][1];
+#pragma unroll
+        for (int i = kAhead - kQuads; i < kAhead; ++i) scale_in((st + 1) / kQuad * kQuads + i, sc[i]);
+      }
       __syncwarp();
     }
-    __syncthreads();
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 
+  // the shares' sums, over x: [share][row of x][weight row]
+  const int W = R * 16;
+  float* out = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const int m = mt * 8 + 2 * t, n = warp * 16 + g;
-    s.out[m][n] = acc[mt][0] * s.unfactor[m];
-    s.out[m + 1][n] = acc[mt][1] * s.unfactor[m + 1];
-    s.out[m][n + 8] = acc[mt][2] * s.unfactor[m];
-    s.out[m + 1][n + 8] = acc[mt][3] * s.unfactor[m + 1];
-  }
-  if (p.split > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  // this CTA's share of the columns, over all of the cluster's sums
-  const int per = (kRowsN + p.split - 1) / p.split, b = rank * per, e = min(b + per, kRowsN);
-  for (int i = tid; i < M * per; i += kNT) {
-    const int m = i / per, n = b + i % per, col = tile * kRowsN + n;
-    if (n >= e || col >= p.N) continue;
-    float y = 0.f;
-    if (p.split > 1) {
-#pragma unroll 1
-      for (int r = 0; r < p.split; ++r) y += ld_cluster_f(map_rank(&s.out[m][n], r));
-    } else {
-      y = s.out[m][n];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = mt * 8 + 2 * t + (i & 1);
+      if (m < M) out[(sl * M + m) * W + rg * 16 + g + 8 * (i >> 1)] = FMT == 1 ? acc[mt][i] : acc[mt][i] * 64.f;
     }
+  }
+  __syncthreads();
+  for (int i = tid; i < M * W; i += kNT) {
+    const int m = i / W, n = i - m * W, col = blockIdx.x * W + n;
+    if (col >= p.N) continue;
+    float y = 0.f;
+    for (int sh = 0; sh < S; ++sh) y += out[(sh * M + m) * W + n];
     if (p.bias) y += bf16_to_f(p.bias[col]);
     y = act_f(y, p.act);
     const long long row = m0 + m;
     if (p.residual) y += bf16_to_f(p.residual[row * p.ldr + col]);
     p.out[row * p.ldo + col] = __float2bfloat16_rn(y);
   }
-  if (p.split > 1) cluster_sync();  // no CTA leaves while its part is read
 }
 
-template <int FMT, int GPS, int MT>
+template <int FMT, int GPS, int MT, int MR>
 cudaError_t launch(W4Params p, cudaStream_t s) {
-  const size_t smem = sizeof(W4Smem<MT>);
-  static_assert(sizeof(W4Smem<MT>) <= 232448, "227 KB of shared memory a CTA");
-  const cudaError_t e = opt_in<linear_w4<FMT, GPS, MT>>(smem);
+  constexpr int kMost = warps<MT>(), kX = x_in_smem(MT) ? 2 * kXBytes : 0;
+  static_assert(kX + kMost * kRing <= 232448, "227 KB of shared memory a CTA");
+  static_assert(kMost * 16 * MT * 8 * 4 <= kX + kMost * kRing, "the shares' sums");
+  const cudaError_t e = opt_in<linear_w4<FMT, GPS, MT, MR>>(kX + kMost * kRing);
   if (e != cudaSuccess) return e;
-  const int tiles = (p.N + kRowsN - 1) / kRowsN, passes = (p.M + MT * 8 - 1) / (MT * 8), steps = (p.K + kStep - 1) / kStep;
-  p.split = std::max(1, std::min({8, 2 * sm_count() / (tiles * passes), steps}));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.split * tiles, passes);
-  cfg.blockDim = dim3(kNT);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = p.split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_w4<FMT, GPS, MT>, p);
+  const int passes = (p.M + MT * 8 - 1) / (MT * 8), rows16 = (p.N + 15) / 16, steps = (p.K + kStep - 1) / kStep;
+  const int R = (int)std::min<long long>(kMost, ((long long)rows16 * passes + sm_count() - 1) / sm_count());
+  // a stage of x of all shares has room
+  const int S = std::max(1, std::min({kMost / R, x_in_smem(MT) ? kXBytes / (2 * kStep * MR) : kMost, steps}));
+  p.row_groups = R;
+  p.shares = S;
+  const Launch l(dim3((rows16 + R - 1) / R, passes), 32 * R * S, kX + R * S * kRing, true, s);
+  return cudaLaunchKernelEx(&l.cfg, linear_w4<FMT, GPS, MT, MR>, p);
 }
 template <int FMT, int GPS>
 cudaError_t by_rows(const W4Params& p, cudaStream_t s) {
-  return p.M <= 8 ? launch<FMT, GPS, 1>(p, s) : p.M <= 16 ? launch<FMT, GPS, 2>(p, s) : p.M <= 32 ? launch<FMT, GPS, 4>(p, s)
-                                                                                                : launch<FMT, GPS, 8>(p, s);
+  if (p.M == 1) return launch<FMT, GPS, 1, 1>(p, s);
+  return p.M <= 8 ? launch<FMT, GPS, 1, 8>(p, s) : p.M <= 16 ? launch<FMT, GPS, 2, 16>(p, s) : p.M <= 32 ? launch<FMT, GPS, 4, 32>(p, s)
+                                                                                                    : launch<FMT, GPS, 8, 64>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
-  if (p.mx) return by_rows<1, 4>(p, s);
-  return p.group == 32 ? by_rows<0, 4>(p, s) : p.group == 64 ? by_rows<0, 2>(p, s) : by_rows<0, 1>(p, s);
+  if (p.mx) return by_rows<1, 8>(p, s);
+  return p.group == 32 ? by_rows<0, 8>(p, s) : p.group == 64 ? by_rows<0, 4>(p, s) : by_rows<0, 2>(p, s);
 }
 
 }  // namespace gdn

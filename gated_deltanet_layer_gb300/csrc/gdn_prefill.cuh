@@ -208,7 +208,7 @@ struct W4Params {
   long long ldr;
   __nv_bfloat16* out;
   long long ldo;
-  int act, split;  // split: CTAs that share the columns
+  int act, row_groups, shares;  // of a CTA: 16 weight rows each, and of the columns
 };
 
 struct SlotParams {
