@@ -315,7 +315,7 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
 }
 
 struct AppendParams {
-  int tokens, Hq, Hkv, rotary, per;  // per: tokens of a CTA
+  int tokens, Hq, Hkv, rotary, parts;  // parts: warps that share a token
   const __nv_bfloat16* q;
   long long ldq;
   const __nv_bfloat16* k;

@@ -2,10 +2,10 @@
 // slots of a paged cache (gdn_kv_append).
 //
 // Bound by the bandwidth of its rows, each read and written once, and for few tokens by
-// latency. A CTA takes a few tokens: the cosines and sines of their positions go through
-// shared memory once for all heads; then every head's row is D / 8 lanes of 16 bytes, four rows
-// of a lane on their way at a time, and a lane has its pair's other half from the lane
-// r / 16 beside it.
+// latency. A warp takes a token, or a part of its heads where there are few tokens: a lane has the
+// same 8 columns of a head throughout, so the cosines and sines of its pairs stay in registers,
+// and four pieces of 256 columns are on their way at a time. A lane has its pairs' other
+// halves from the lane r / 16 beside it.
 //
 // Angles. pos f is wanted modulo a turn, to f32's accuracy at any position. f / (2 pi) is
 // a 64-bit binary fraction of a turn (in two double terms, so right to its last bits), and
@@ -21,7 +21,6 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads_ = 256, kDeep = 4;
-constexpr int kMaxTokens = 4;  // of a CTA
 
 __device__ __forceinline__ unsigned long long turns_of(float f) {
   const double x = f, hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
@@ -29,140 +28,137 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
   return (unsigned long long)(r * 18446744073709551616.0) + (unsigned long long)(long long)(b * 18446744073709551616.0);
 }
 
-template <int D, bool PAIRS>  // PAIRS: 2 i and 2 i + 1 turn together, else i and i + r / 2
-__global__ void __launch_bounds__(kThreads_) kv_append(const AppendParams p) {
-  constexpr int kL = D / 8, kGroups = kThreads_ / kL;
+template <int D, bool PAIRS, bool NORM>  // PAIRS: 2 i and 2 i + 1 turn together, else i and i + r / 2
+__global__ void __launch_bounds__(kThreads_, 4) kv_append(const AppendParams p) {
+  constexpr int kL = D / 8;  // lanes of a head
   __shared__ unsigned long long turn[D / 2];
-  __shared__ float2 cs[kMaxTokens][D / 2];
-  const int tid = threadIdx.x, half = p.rotary / 2;
+  const int tid = threadIdx.x, lane = tid & 31, c = lane % kL, half = p.rotary / 2;
   griddep_wait();
   griddep_launch_dependents();
-  const int t0 = blockIdx.x * p.per, count = min(p.per, p.tokens - t0);
   for (int i = tid; i < half; i += kThreads_) turn[i] = turns_of(p.freq[i]);
   __syncthreads();
-  for (int x = tid; x < count * half; x += kThreads_) {
-    const int t = x / half, i = x - t * half;
-    const unsigned long long a = (unsigned long long)(long long)p.pos[t0 + t] * turn[i];
-    float sn, cn;
-    sincospif((float)(int)(a >> 32) * 0x1p-31f, &sn, &cn);
-    cs[t][i] = make_float2(cn, sn);
-  }
-  __syncthreads();
 
-  const int lane = tid & 31, c = tid % kL, heads = p.Hq + 2 * p.Hkv, items = count * heads;
-  // the lane of the pairs' other halves, and the sign of the sine there
+  // the lane of the pairs' other halves
   const int shift = half / 8;
   const bool turned = c * 8 < p.rotary, second = c * 8 >= half;
   const int mate = PAIRS || !turned ? lane : second ? lane - shift : lane + shift;
-  const int mate_c = PAIRS || !turned ? c : second ? c - shift : c + shift;
-  float wq[8], wk[8];
-  const auto weights = [&](const __nv_bfloat16* w, float (&o)[8], int at) {
-    const uint4 v = w ? *reinterpret_cast<const uint4*>(w + at * 8) : make_uint4(0, 0, 0, 0);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[2 * j] = 1.f + bf16_lo(u[j]), o[2 * j + 1] = 1.f + bf16_hi(u[j]);
-  };
-  weights(p.qw, wq, c);
-  weights(p.kw, wk, c);
-  float mq[8], mk[8];
-  weights(p.qw, mq, mate_c);
-  weights(p.kw, mk, mate_c);
-
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (NORM && p.qw) wq = *reinterpret_cast<const uint4*>(p.qw + c * 8);
+  if (NORM && p.kw) wk = *reinterpret_cast<const uint4*>(p.kw + c * 8);
+  const int q_cols = p.Hq * D, k_cols = q_cols + p.Hkv * D, cols = k_cols + p.Hkv * D;
+  const int pieces = (cols + 255) / 256, part = (pieces + p.parts - 1) / p.parts;  // of a token; of a warp
+  const long long warps = (long long)gridDim.x * (kThreads_ / 32), units = (long long)p.tokens * p.parts;
 #pragma unroll 1
-  for (int base = 0; base < items; base += kGroups * kDeep) {
-    uint4 v[kDeep];
-    int tok[kDeep], head[kDeep];
-    long long slot[kDeep];
+  for (long long u = (long long)blockIdx.x * (kThreads_ / 32) + (tid >> 5); u < units; u += warps) {
+    const int t = (int)(u / p.parts), first = (int)(u - (long long)t * p.parts) * part, last = min(first + part, pieces);
+    long long slot = p.slots[t];
+    const long long pos = p.pos[t];
+    const __nv_bfloat16* q = p.q + t * p.ldq;
+    const __nv_bfloat16* k = p.k + t * p.ldk - q_cols;
+    const __nv_bfloat16* v = p.v + t * p.ldv - k_cols;
+    if (slot >= p.num_slots) {
+      if (first == 0 && lane == 0 && p.error) atomicCAS(p.error, 0u, (kStatusIndex << 24) | (1u << 16) | (uint32_t)(t & 0xffff));
+      slot = -1;
+    }
+    // a pad row: zero queries, nothing else
+    if (slot < 0) {
+      for (int col = first * 256 + lane * 8; col < min(last * 256, q_cols); col += 256)
+        *reinterpret_cast<uint4*>(p.q_out + t * p.ldqo + col) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    float cn[PAIRS ? 4 : 8], sn[PAIRS ? 4 : 8];
+    if (turned) {
+      const int i0 = PAIRS ? c * 4 : (second ? c * 8 - half : c * 8);
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-      const int item = base + k * kGroups + tid / kL;
-      tok[k] = item < items ? item / heads : -1;
-      v[k] = make_uint4(0, 0, 0, 0);
-      if (tok[k] >= 0) {
-        head[k] = item - tok[k] * heads;
-        const long long t = t0 + tok[k];
-        slot[k] = p.slots[t];
-        if (slot[k] >= p.num_slots) {
-          if (head[k] == 0 && c == 0 && p.error) atomicCAS(p.error, 0u, (kStatusIndex << 24) | (1u << 16) | (uint32_t)(t & 0xffff));
-          slot[k] = -1;
-        }
-        const __nv_bfloat16* row = head[k] < p.Hq           ? p.q + t * p.ldq + head[k] * D
-                                   : head[k] < p.Hq + p.Hkv ? p.k + t * p.ldk + (head[k] - p.Hq) * D
-                                                            : p.v + t * p.ldv + (head[k] - p.Hq - p.Hkv) * D;
-        if (slot[k] >= 0) v[k] = *reinterpret_cast<const uint4*>(row + c * 8);
+      for (int j = 0; j < (PAIRS ? 4 : 8); ++j) {
+        const unsigned long long a = (unsigned long long)pos * turn[i0 + j];
+        sincospif((float)(int)(a >> 32) * 0x1p-31f, &sn[j], &cn[j]);
+        if (!PAIRS && !second) sn[j] = -sn[j];
       }
     }
+#pragma unroll 1
+    for (int i0 = first; i0 < last; i0 += kDeep) {
+      uint4 x4[kDeep];
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-      const bool on = tok[k] >= 0, is_q = on && head[k] < p.Hq, is_k = on && !is_q && head[k] < p.Hq + p.Hkv;
-      uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, w[4];
-      float x[8], scale = 1.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(u[j]), x[2 * j + 1] = bf16_hi(u[j]);
-      const bool norm = is_q ? p.qw != nullptr : is_k && p.kw != nullptr;
-      if (p.qw || p.kw) {
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
-#pragma unroll
-        for (int o = kL / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (norm) scale = 1.f / sqrtf(sum * (1.f / D) + p.eps);
+      for (int d = 0; d < kDeep; ++d) {
+        const int col = (i0 + d) * 256 + lane * 8;
+        x4[d] = make_uint4(0, 0, 0, 0);
+        if (i0 + d < last && col < cols) x4[d] = *reinterpret_cast<const uint4*>((col < q_cols ? q : col < k_cols ? k : v) + col);
       }
-      if (!PAIRS) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __shfl_sync(0xffffffffu, u[j], mate);
-      }
-      if (!on) continue;
-      if (is_q || is_k) {
-        float y[8];
+      for (int d = 0; d < kDeep; ++d) {
+        if (i0 + d >= last) break;
+        const int col = (i0 + d) * 256 + lane * 8;
+        const bool is_q = col < q_cols, is_k = !is_q && col < k_cols;
+        uint32_t w[4] = {x4[d].x, x4[d].y, x4[d].z, x4[d].w};
+        // a piece of values alone, or of heads that neither turn nor are normalised, goes through as it is
+        if (__any_sync(0xffffffffu, is_q || is_k) && (NORM || half > 0)) {
+          float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = norm ? x[j] * scale * (is_q ? wq[j] : wk[j]) : x[j];
-        if (turned) {
-          const float2* a = cs[tok[k]];
+          for (int j = 0; j < 4; ++j) y[2 * j] = bf16_lo(w[j]), y[2 * j + 1] = bf16_hi(w[j]);
+          if (NORM) {
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+#pragma unroll
+            for (int o = kL / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (is_q ? p.qw != nullptr : p.kw != nullptr) {
+              const float scale = rsqrtf(sum * (1.f / D) + p.eps);
+              const uint32_t n[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y[2 * j] *= scale * (1.f + bf16_lo(n[j]));
+                y[2 * j + 1] *= scale * (1.f + bf16_hi(n[j]));
+              }
+            }
+          }
           if (PAIRS) {
+            if (turned) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = a[c * 4 + j];
-              const float e = y[2 * j], o = y[2 * j + 1];
-              y[2 * j] = e * f.x - o * f.y;
-              y[2 * j + 1] = o * f.x + e * f.y;
+              for (int j = 0; j < 4; ++j) {
+                const float a = y[2 * j], b = y[2 * j + 1];
+                y[2 * j] = a * cn[j] - b * sn[j];
+                y[2 * j + 1] = b * cn[j] + a * sn[j];
+              }
             }
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float2 f = a[(second ? mate_c : c) * 8 + j];
-              const float raw = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-              const float z = norm ? raw * scale * (is_q ? mq[j] : mk[j]) : raw;
-              y[j] = second ? y[j] * f.x + z * f.y : y[j] * f.x - z * f.y;
+              const float z = __shfl_sync(0xffffffffu, y[j], mate);
+              if (turned) y[j] = y[j] * cn[j] + z * sn[j];
             }
           }
-        }
+          if (is_q || is_k) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+            for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+          }
+        }
+        if (col < cols) {
+          __nv_bfloat16* to = is_q ? p.q_out + t * p.ldqo : is_k ? p.k_cache + slot * p.ldkc - q_cols : p.v_cache + slot * p.ldvc - k_cols;
+          *reinterpret_cast<uint4*>(to + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
-      const uint4 r = make_uint4(u[0], u[1], u[2], u[3]);
-      if (is_q)
-        *reinterpret_cast<uint4*>(p.q_out + (long long)(t0 + tok[k]) * p.ldqo + head[k] * D + c * 8) =
-            slot[k] >= 0 ? r : make_uint4(0, 0, 0, 0);
-      else if (slot[k] >= 0)
-        *reinterpret_cast<uint4*>(is_k ? p.k_cache + slot[k] * p.ldkc + (head[k] - p.Hq) * D + c * 8
-                                       : p.v_cache + slot[k] * p.ldvc + (head[k] - p.Hq - p.Hkv) * D + c * 8) = r;
     }
   }
 }
 
-template <int D>
-cudaError_t launch(const AppendParams& p, bool pairs, int grid, cudaStream_t s) {
+template <int D, bool PAIRS>
+cudaError_t launch(const AppendParams& p, int grid, cudaStream_t s) {
   const Launch l(dim3(grid), kThreads_, 0, true, s);
-  return pairs ? cudaLaunchKernelEx(&l.cfg, kv_append<D, true>, p) : cudaLaunchKernelEx(&l.cfg, kv_append<D, false>, p);
+  return p.qw || p.kw ? cudaLaunchKernelEx(&l.cfg, kv_append<D, PAIRS, true>, p) : cudaLaunchKernelEx(&l.cfg, kv_append<D, PAIRS, false>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(AppendParams p, int d, bool pairs, cudaStream_t s) {
-  p.per = std::max(1, std::min(kMaxTokens, p.tokens / (2 * sm_count())));
-  const int grid = (p.tokens + p.per - 1) / p.per;
-  return d == 64 ? launch<64>(p, pairs, grid, s) : d == 128 ? launch<128>(p, pairs, grid, s) : launch<256>(p, pairs, grid, s);
+  // as many warps as run at once; a token's pieces are split where there are fewer tokens
+  const long long most = 32LL * sm_count();
+  const int pieces = (int)(((long long)(p.Hq + 2 * p.Hkv) * d + 255) / 256);
+  p.parts = (int)std::max(1LL, std::min<long long>((pieces + kDeep - 1) / kDeep, most / p.tokens));
+  const int grid = (int)((std::min((long long)p.tokens * p.parts, most) + kThreads_ / 32 - 1) / (kThreads_ / 32));
+  if (d == 64) return pairs ? launch<64, true>(p, grid, s) : launch<64, false>(p, grid, s);
+  if (d == 128) return pairs ? launch<128, true>(p, grid, s) : launch<128, false>(p, grid, s);
+  return pairs ? launch<256, true>(p, grid, s) : launch<256, false>(p, grid, s);
 }
 
 }  // namespace gdn
