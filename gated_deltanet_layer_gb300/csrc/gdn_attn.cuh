@@ -339,9 +339,13 @@ struct AppendParams {
 };
 cudaError_t launch_kv_append(AppendParams p, int d, bool pairs, cudaStream_t s);
 
+// Tile maps: of the boxes of 64 columns of a matrix, and of a cache's rows.
+bool attn_encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box);
+bool attn_row_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows);
+
 // Launchers. grid: CTAs of the launch (the workspace has two parts a CTA).
-cudaError_t launch_attn_rows(const AttnParams& p, int d, int grid, cudaStream_t s);
-constexpr int kAttnRowsM = 16;
+// rows: the most of a request and key/value head.
+cudaError_t launch_attn_rows(const AttnParams& p, int d, int rows, int grid, cudaStream_t s);
 cudaError_t launch_attn_tiles(const AttnParams& p, int d, int grid, cudaStream_t s);
 
 }  // namespace gdn

@@ -60,6 +60,30 @@ const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*
 
 }  // namespace
 
+// Tile map of rows of 64-column boxes, 128-byte swizzle, zeros outside: {columns, rows} or {columns, heads, tokens}.
+bool gdn::attn_encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  typedef CUresult (*Fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                         const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                         CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static Fn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (Fn)f;
+  }();
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool gdn::attn_row_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return attn_encode(m, base, 2, dims, strides, box);
+}
+
 extern "C" size_t gdn_attn_workspace_bytes(const gdn_attn_config* cfg) {
   if (validate(cfg) != GDN_OK) return 0;
   return Layout(*cfg, sm_count()).end;
@@ -147,10 +171,12 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
     p.seq = reinterpret_cast<int4*>(h->ws + l.seq);
     p.start = reinterpret_cast<long long*>(h->ws + l.start);
   }
-  // Rows of a request and key/value head: a tile of 16 has them all, or the tensor cores' tiles (which
+  // Rows of a request and key/value head: a tile of 16, or 32, has them all, or the tensor cores' tiles (which
   // hold a token's heads together, and need a cache to map).
-  const bool few = (long long)p.max_len * p.group.d <= kAttnRowsM || p.group.d > 128 || num_blocks == 0;
-  return cuda_status((few ? launch_attn_rows : launch_attn_tiles)(p, c.head_dim, h->grid, (cudaStream_t)stream));
+  const int rows = (int)std::min<long long>((long long)p.max_len * p.group.d, 1 << 20);
+  const bool few = rows <= (c.head_dim == 256 ? 16 : 32) || p.group.d > 128 || num_blocks == 0;
+  return cuda_status(few ? launch_attn_rows(p, c.head_dim, rows, h->grid, (cudaStream_t)stream)
+                         : launch_attn_tiles(p, c.head_dim, h->grid, (cudaStream_t)stream));
 }
 
 extern "C" gdn_status gdn_attn_check(gdn_attn_t* h, void* stream, uint32_t* detail) {

@@ -847,30 +847,6 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
   attn_plan<KT, Cfg<D>::kE, 1024>(p, p.seq, p.start, x, true);
 }
 
-// Tile map of rows of 64-column boxes, 128-byte swizzle, zeros outside: {columns, rows} or {columns, heads, tokens}.
-bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-  typedef CUresult (*Fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                         const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                         CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static Fn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return (Fn)f;
-  }();
-  const cuuint32_t one[3] = {1, 1, 1};
-  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool row_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  return encode(m, base, 2, dims, strides, box);
-}
-
 template <int D>
 cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   const size_t smem = sizeof(TileSmem<D>);
@@ -887,13 +863,13 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
     m.box_v = b;
     m.box_k = b <= 16 ? b : 16;
   }
-  if (!row_map(&m.k, p.k, rows, cols, p.ldk, 1) || !row_map(&m.v, p.v, rows, cols, p.ldv, 1)) return cudaErrorInvalidValue;
-  if (m.box_k && (!row_map(&m.kb, p.k, rows, cols, p.ldk, m.box_k) || !row_map(&m.vb, p.v, rows, cols, p.ldv, m.box_v)))
+  if (!attn_row_map(&m.k, p.k, rows, cols, p.ldk, 1) || !attn_row_map(&m.v, p.v, rows, cols, p.ldv, 1)) return cudaErrorInvalidValue;
+  if (m.box_k && (!attn_row_map(&m.kb, p.k, rows, cols, p.ldk, m.box_k) || !attn_row_map(&m.vb, p.v, rows, cols, p.ldv, m.box_v)))
     return cudaErrorInvalidValue;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hkv * G, (cuuint64_t)p.tokens},
                    strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.ldq * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)m.tokens};
-  if (!encode(&m.q, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  if (!attn_encode(&m.q, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   if (p.seqs <= kAttnPlanned) p.seq = nullptr;
   if (p.seq) {
     const Launch one(dim3(1), 1024, 0, true, s);
