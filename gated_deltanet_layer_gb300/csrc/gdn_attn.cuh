@@ -21,7 +21,7 @@ constexpr uint32_t kAttnBlock = 1, kAttnOffsets = 2, kAttnLength = 3, kAttnWait 
 
 // Up to this many requests every CTA plans by itself, in shared memory; with more of
 // them a kernel before leaves the plan in the workspace.
-constexpr int kAttnPlanned = 256;
+constexpr int kAttnPlanned = 128;
 
 // n / d for 0 <= n < 2^31.
 struct FastDiv {
@@ -67,6 +67,14 @@ struct AttnParams {
 
 __device__ __forceinline__ void attn_record(unsigned int* error, uint32_t what, uint32_t who) {
   atomicCAS(error, 0u, (kStatusIndex << 24) | (what << 16) | (who & 0xffff));
+}
+
+// An add that comes after all that the thread has written, and, behind a barrier, that its CTA has, and
+// before all that it reads.
+__device__ __forceinline__ unsigned atom_add_acq_rel_u32(unsigned* p, unsigned v) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 // sum over i < n of floor((a i + b) / m), by the steps of Euclid's algorithm (a, b >= 0).

@@ -37,8 +37,11 @@ template <int D, int MT>
 struct alignas(1024) RowsSmem {
   using C = Rows<D, MT>;
   unsigned char ring[C::kW][C::kStages][2][16 * C::kRow];  // a warp's stages: keys, values
-  unsigned char q[C::kM * C::kRow];
-  float merge[C::kW][C::kM][C::kMergeStride];
+  unsigned char q[2][C::kM * C::kRow];  // of a task and the next
+  union {
+    float merge[C::kW][C::kM][C::kMergeStride];
+    float2 parts[16][C::kM];  // the joined parts' maxima and sums
+  };
   float2 ml[C::kW][C::kM];
   int poison[D];  // the first hidden-from-some key whose value in the column is not finite
   uint64_t full[C::kW][C::kStages];
@@ -149,11 +152,30 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
   KeyBlock kb = key_block(p, ahead.s, ahead.j * KT + warp * 16 + (lane & 15), ahead.ctx + ahead.n);
   int issued = 0;
   uint32_t boxed = 0;  // the stages that came as boxes
+  // The queries of a task: a share a warp; dead rows are zero. Those of the task after the present one come
+  // beside its first step's rows; there is room for no more, so a task of fewer steps than are ahead
+  // leaves the one after it to ask for its own.
+  int seen = 0, asked = 0, begun = 0;  // tasks: come across by the loads, whose queries are asked for, begun
+  const auto queries = [&](const Walk<KT, 0>& x) {
+    const uint32_t to = smem_u32(s.q[asked++ & 1]);
+    const int rows = x.n * (int)p.group.d;
+#pragma unroll 2
+    for (int e = tid; e < kM * D / 8; e += NT) {
+      const int r = e / (D / 8), c = e % (D / 8), R = x.i * kM + r;
+      const bool live = R < rows;
+      const uint32_t tok = p.group.div(live ? R : 0), hd = (live ? R : 0) - tok * p.group.d;
+      cp_async16_or_zero(to + (r >> 4) * (16 * C::kRow) + piece(r & 15, c),
+                         p.q + (x.row0 + tok) * p.ldq + ((long long)x.h * p.group.d + hd) * D + c * 8, live);
+    }
+  };
+  bool first = true;  // the next step to be asked for is its task's first here
   bool ok = true;
   const auto issue = [&] {
     if (issued < steps) {
       const int st = issued % ST, slot = key_slot(p, kb, ahead.s), h = ahead.h;
       const bool box = maps.boxes && ahead.j * KT + warp * 16 + 15 < ahead.ctx + ahead.n;
+      if (first && seen++ == asked && asked <= begun) queries(ahead);
+      first = ahead.j + 1 == ahead.nt;
       ++issued;
       if (issued < steps) {
         if (++ahead.j == ahead.nt) ahead.next_task();
@@ -193,22 +215,15 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
   int last_key[MT][2], first_last = 0;  // last key that the thread's rows see; the task's first row's
   bool fresh = true;
   uint32_t phases = 0;  // of the stages' barriers
+  int qbuf = 1;
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll 1
   for (int step = 0; step < steps; ++step) {
+    const bool starts = fresh;
     if (fresh) {
       fresh = false;
-      // the rows' queries; dead rows are zero
-      for (int x = tid; x < kM * D / 8; x += NT) {
-        const int r = x / (D / 8), c = x % (D / 8), R = w.i * kM + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (R < w.n * (int)p.group.d) {
-          const uint32_t tok = p.group.div(R), hd = R - tok * p.group.d;
-          v = *reinterpret_cast<const uint4*>(p.q + (w.row0 + tok) * p.ldq + ((long long)w.h * p.group.d + hd) * D + c * 8);
-        }
-        *reinterpret_cast<uint4*>(s.q + (r >> 4) * (16 * C::kRow) + piece(r & 15, c)) = v;
-      }
-      __syncthreads();
+      if (asked == begun) queries(w);
+      ++begun;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -224,14 +239,21 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
     }
     issue();
     const int st = step % ST;
-    if (boxed >> st & 1) {
+    const bool box = boxed >> st & 1;
+    if (starts)
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    else if (!box)
+      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
+    if (box) {
       ok = ok && mbar_wait(&s.full[warp][st], phases >> st & 1);
       phases ^= 1u << st;
-    } else {
-      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
+    }
+    if (starts) {
+      __syncthreads();  // the other warps' share of the queries
+      qbuf ^= 1;
     }
     __syncwarp();
-    const uint32_t ks = ring + st * (2 * 16 * C::kRow), vs = ks + 16 * C::kRow, qs = smem_u32(s.q);
+    const uint32_t ks = ring + st * (2 * 16 * C::kRow), vs = ks + 16 * C::kRow, qs = smem_u32(s.q[qbuf]);
     const int key0 = w.j * KT + warp * 16;
     if (key0 < w.ctx + w.n) {
       float x[MT][2][4] = {};
@@ -404,50 +426,35 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
         const int b = level == 0 ? mine * size : 0, by = level == 0 || groups == 1 ? 1 : size;
         const int count = level == 0 ? min(size, parts - b) : groups == 1 ? parts : groups;
         unsigned* done = p.done + (level == 0 ? gridDim.x + c0 + b : c0);
-        __threadfence();
         __syncthreads();
-        if (tid == 0) {
-          s.last = atomicAdd(done, 1u) == (unsigned)(count - 1);
-          __threadfence();
-        }
+        if (tid == 0) s.last = atom_add_acq_rel_u32(done, 1u) == (unsigned)(count - 1);
         __syncthreads();
         if (!s.last) break;
         if (tid == 0) *done = 0;
         const auto at = [&](int i) { return (long long)slot_of(b + i * by) * kM; };
-        for (int r = warp; r < live; r += W) {
-          float top = -INFINITY, sum = 0.f;
-          for (int i = lane; i < count; i += 32) top = fmaxf(top, __ldcg(&p.part_ml[at(i) + r]).x);
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          for (int i = lane; i < count; i += 32) {
-            const float2 ml = __ldcg(&p.part_ml[at(i) + r]);
-            sum += ml.y * (ml.x == -INFINITY ? 0.f : exp2f(ml.x - top));
-          }
-          sum = warp_sum(sum);
-          if (lane == 0) s.row_ml[r] = make_float2(top, sum);
-        }
+        for (int x = tid; x < live * count; x += NT) s.parts[x / live][x % live] = __ldcg(&p.part_ml[at(x / live) + x % live]);
         __syncthreads();
         for (int x = tid; x < live * D / 2; x += NT) {
           const int r = x / (D / 2), c = 2 * (x % (D / 2));
-          const float top = s.row_ml[r].x;
+          float top = -INFINITY, sum = 0.f;
+          for (int i = 0; i < count; ++i) top = fmaxf(top, s.parts[i][r].x);
           float2 v = make_float2(0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
           for (int i = 0; i < count; ++i) {
-            const long long q = at(i) + r;
-            const float pm = __ldcg(&p.part_ml[q]).x, e = pm == -INFINITY ? 0.f : exp2f(pm - top);
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part + q * D + c));
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part + (at(i) + r) * D + c)), ml = s.parts[i][r];
+            const float e = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+            sum = fmaf(ml.y, e, sum);
             v.x = fmaf(y.x, e, v.x);
             v.y = fmaf(y.y, e, v.y);
           }
-          if (level == 1)
-            put2<D>(p, w.row0, w.h, w.i * kM + r, c, v, s.row_ml[r].y);
-          else
+          if (level == 1) {
+            put2<D>(p, w.row0, w.h, w.i * kM + r, c, v, sum);
+          } else {
             *reinterpret_cast<float2*>(p.part + (at(0) + r) * D + c) = v;
+            if (c == 0) p.part_ml[at(0) + r] = make_float2(top, sum);
+          }
         }
-        if (level == 0) {
-          __syncthreads();  // the parts' maxima are read
-          if (tid < live) p.part_ml[at(0) + tid] = s.row_ml[tid];
-        }
+        __syncthreads();
       }
     }
     __syncthreads();

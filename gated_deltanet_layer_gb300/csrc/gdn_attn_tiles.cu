@@ -447,12 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         if (!whole && first < toks) {
           unsigned* done = p.done + 4 * c0 + (split ? 0 : 2 * t) + rank;
           const int parts = (c1 - c0 + 1) << (split ? 1 : 0);
-          __threadfence();
           named_sync(1 + t, 128);
-          if (r == 0) {
-            s.last[t] = atomicAdd(done, 1u) == (unsigned)(parts - 1);
-            __threadfence();
-          }
+          if (r == 0) s.last[t] = atom_add_acq_rel_u32(done, 1u) == (unsigned)(parts - 1);
           named_sync(1 + t, 128);
           if (s.last[t]) {
             // every part is there: the first pair's second one, the others' first, and where the keys
