@@ -352,8 +352,7 @@ bool attn_encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* d
 bool attn_row_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows);
 
 // Launchers. grid: CTAs of the launch (the workspace has two parts a CTA).
-// rows: the most of a request and key/value head.
-cudaError_t launch_attn_rows(const AttnParams& p, int d, int rows, int grid, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnParams& p, int d, int grid, cudaStream_t s);
 cudaError_t launch_attn_tiles(const AttnParams& p, int d, int grid, cudaStream_t s);
 
 }  // namespace gdn

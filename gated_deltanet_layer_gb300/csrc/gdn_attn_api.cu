@@ -171,12 +171,10 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
     p.seq = reinterpret_cast<int4*>(h->ws + l.seq);
     p.start = reinterpret_cast<long long*>(h->ws + l.start);
   }
-  // Rows of a request and key/value head: a tile of 16, or 32, has them all, or the tensor cores' tiles (which
+  // Rows of a request and key/value head: a tile of 16 has them all, or the tensor cores' tiles (which
   // hold a token's heads together, and need a cache to map).
-  const int rows = (int)std::min<long long>((long long)p.max_len * p.group.d, 1 << 20);
-  const bool few = rows <= (c.head_dim == 256 ? 16 : 32) || p.group.d > 128 || num_blocks == 0;
-  return cuda_status(few ? launch_attn_rows(p, c.head_dim, rows, h->grid, (cudaStream_t)stream)
-                         : launch_attn_tiles(p, c.head_dim, h->grid, (cudaStream_t)stream));
+  const bool few = (long long)p.max_len * p.group.d <= 16 || p.group.d > 128 || num_blocks == 0;
+  return cuda_status((few ? launch_attn_rows : launch_attn_tiles)(p, c.head_dim, h->grid, (cudaStream_t)stream));
 }
 
 extern "C" gdn_status gdn_attn_check(gdn_attn_t* h, void* stream, uint32_t* detail) {

@@ -1,4 +1,4 @@
-// Paged attention (gdn_attn_paged) on tiles of 16 or 32 query rows: one new token a request, or
+// Paged attention (gdn_attn_paged) on tiles of 16 query rows: one new token a request, or
 // a few.
 //
 // o = sum_p w_p v_p / sum_p w_p with w_p = 2^(x_p - m), x_p = scale log2(e) q . k_p and m
@@ -22,20 +22,20 @@ namespace {
 
 using namespace tc;
 
-template <int D, int MT>
+template <int D>
 struct Rows {
-  static constexpr int kM = 16 * MT;           // rows of a task
+  static constexpr int kM = 16;                // rows of a task
   static constexpr int kW = D == 256 ? 4 : 8;  // warps
   static constexpr int kKT = 16 * kW;          // keys of a tile
   static constexpr int kStages = D == 64 ? 5 : 3;
   static constexpr int kRow = 2 * D;           // bytes of a key row
   // columns merged at a time; floats of a row, against bank conflicts
-  static constexpr int kMergeCols = MT == 1 ? 32 : 8, kMergeStride = kMergeCols + 4;
+  static constexpr int kMergeCols = 32, kMergeStride = kMergeCols + 4;
 };
 
-template <int D, int MT>
+template <int D>
 struct alignas(1024) RowsSmem {
-  using C = Rows<D, MT>;
+  using C = Rows<D>;
   unsigned char ring[C::kW][C::kStages][2][16 * C::kRow];  // a warp's stages: keys, values
   unsigned char q[2][C::kM * C::kRow];  // of a task and the next
   union {
@@ -109,13 +109,13 @@ __device__ __forceinline__ void put2(const AttnParams& p, int row0, int h, int r
   *reinterpret_cast<uint32_t*>(p.out + row * p.ldo + c) = pack_bf16x2(v.x, v.y);
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __grid_constant__ RowMaps maps, const AttnParams p) {
-  using C = Rows<D, MT>;
+template <int D>
+__global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_constant__ RowMaps maps, const AttnParams p) {
+  using C = Rows<D>;
   constexpr int W = C::kW, KT = C::kKT, NT = W * 32, ST = C::kStages, kM = C::kM, kMergeCols = C::kMergeCols;
   extern __shared__ __align__(1024) unsigned char raw[];
-  static_assert(sizeof(RowsSmem<D, MT>) <= 232448, "227 KB of shared memory a CTA");
-  RowsSmem<D, MT>& s = *reinterpret_cast<RowsSmem<D, MT>*>(raw);
+  static_assert(sizeof(RowsSmem<D>) <= 232448, "227 KB of shared memory a CTA");
+  RowsSmem<D>& s = *reinterpret_cast<RowsSmem<D>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (lane == 0)
     for (int i = 0; i < ST; ++i) mbar_init(&s.full[warp][i], 1);
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
       const int r = e / (D / 8), c = e % (D / 8), R = x.i * kM + r;
       const bool live = R < rows;
       const uint32_t tok = p.group.div(live ? R : 0), hd = (live ? R : 0) - tok * p.group.d;
-      cp_async16_or_zero(to + (r >> 4) * (16 * C::kRow) + piece(r & 15, c),
+      cp_async16_or_zero(to + piece(r, c),
                          p.q + (x.row0 + tok) * p.ldq + ((long long)x.h * p.group.d + hd) * D + c * 8, live);
     }
   };
@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
 
   Walk<KT, 0> w(p, seq, start);
   w.from(s.at, u0);
-  float o[MT][D / 8][4], m[MT][2], l[MT][2];
-  int last_key[MT][2], first_last = 0;  // last key that the thread's rows see; the task's first row's
+  float o[D / 8][4], m[2], l[2];
+  int last_key[2], first_last = 0;  // last key that the thread's rows see; the task's first row's
   bool fresh = true;
   uint32_t phases = 0;  // of the stages' barriers
   int qbuf = 1;
@@ -225,15 +225,12 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
       if (asked == begun) queries(w);
       ++begun;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          m[mt][e] = -INFINITY;
-          l[mt][e] = 0.f;
-          last_key[mt][e] = w.ctx + min((int)p.group.div(w.i * kM + mt * 16 + g + 8 * e), w.n - 1);
-        }
+      for (int e = 0; e < 2; ++e) {
+        m[e] = -INFINITY;
+        l[e] = 0.f;
+        last_key[e] = w.ctx + min((int)p.group.div(w.i * kM + g + 8 * e), w.n - 1);
       }
       first_last = w.ctx + p.group.div(w.i * kM);
     }
@@ -256,65 +253,63 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
     const uint32_t ks = ring + st * (2 * 16 * C::kRow), vs = ks + 16 * C::kRow, qs = smem_u32(s.q[qbuf]);
     const int key0 = w.j * KT + warp * 16;
     if (key0 < w.ctx + w.n) {
-      float x[MT][2][4] = {};
+      // two sums of a score where the registers allow it: half as many products wait for one another
+      constexpr int kSums = D == 256 ? 1 : 2;
+      float sums[kSums][2][4] = {};
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        uint32_t b[4];
+        uint32_t a[4], b[4];
         ldmatrix4(ks + piece((lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1)), b);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t a[4];
-          ldmatrix4(qs + mt * (16 * C::kRow) + piece((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), a);
-          mma16816(x[mt][0], a, b[0], b[1]);
-          mma16816(x[mt][1], a, b[2], b[3]);
-        }
+        ldmatrix4(qs + piece((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), a);
+        mma16816(sums[k % kSums][0], a, b[0], b[1]);
+        mma16816(sums[k % kSums][1], a, b[2], b[3]);
       }
+      float x[2][4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] = kSums == 1 ? sums[0][e >> 2][e & 3] : sums[0][e >> 2][e & 3] + sums[kSums - 1][e >> 2][e & 3];
       const bool edge = key0 + 15 > first_last;  // some row does not see some key
-      uint32_t a[MT][4];
+      uint32_t a[4];
+      float top[2] = {m[0], m[1]};
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float top[2] = {m[mt][0], m[mt][1]};
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float y = x[mt][b][e] * p.scale_log2;
-            if (edge && key0 + b * 8 + 2 * t + (e & 1) > last_key[mt][e >> 1]) y = -INFINITY;
-            x[mt][b][e] = y;
-            top[e >> 1] = fmaxf(top[e >> 1], y);
-          }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+        for (int e = 0; e < 4; ++e) {
+          float y = x[b][e] * p.scale_log2;
+          if (edge && key0 + b * 8 + 2 * t + (e & 1) > last_key[e >> 1]) y = -INFINITY;
+          x[b][e] = y;
+          top[e >> 1] = fmaxf(top[e >> 1], y);
         }
-        if (__any_sync(0xffffffffu, top[0] > m[mt][0] || top[1] > m[mt][1])) {
-          const float f0 = m[mt][0] == -INFINITY ? 0.f : exp2f(m[mt][0] - top[0]), f1 = m[mt][1] == -INFINITY ? 0.f : exp2f(m[mt][1] - top[1]);
-          l[mt][0] *= f0;
-          l[mt][1] *= f1;
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            o[mt][n][0] *= f0;
-            o[mt][n][1] *= f0;
-            o[mt][n][2] *= f1;
-            o[mt][n][3] *= f1;
-          }
-          m[mt][0] = top[0];
-          m[mt][1] = top[1];
-        }
-        const float m0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0], m1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1];
+      for (int e = 0; e < 2; ++e) {
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+      }
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+        const float f0 = m[0] == -INFINITY ? 0.f : exp2f(m[0] - top[0]), f1 = m[1] == -INFINITY ? 0.f : exp2f(m[1] - top[1]);
+        l[0] *= f0;
+        l[1] *= f1;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float* y = x[mt][b];
-          y[0] = ex2(y[0] - m0);
-          y[1] = ex2(y[1] - m0);
-          y[2] = ex2(y[2] - m1);
-          y[3] = ex2(y[3] - m1);
-          l[mt][0] += y[0] + y[1];
-          l[mt][1] += y[2] + y[3];
-          a[mt][2 * b] = pack2(y[0], y[1]);
-          a[mt][2 * b + 1] = pack2(y[2], y[3]);
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][0] *= f0;
+          o[n][1] *= f0;
+          o[n][2] *= f1;
+          o[n][3] *= f1;
         }
+        m[0] = top[0];
+        m[1] = top[1];
+      }
+      const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float* y = x[b];
+        y[0] = ex2(y[0] - m0);
+        y[1] = ex2(y[1] - m0);
+        y[2] = ex2(y[2] - m1);
+        y[3] = ex2(y[3] - m1);
+        l[0] += y[0] + y[1];
+        l[1] += y[2] + y[3];
+        a[2 * b] = pack2(y[0], y[1]);
+        a[2 * b + 1] = pack2(y[2], y[3]);
       }
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) {
@@ -331,11 +326,8 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
             if ((b[e] & 0x7f800000u) == 0x7f800000u) atomicMin(to, key + 1), b[e] &= 0xffffu;
           }
         }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816(o[mt][2 * n], a[mt], b[0], b[1]);
-          mma16816(o[mt][2 * n + 1], a[mt], b[2], b[3]);
-        }
+        mma16816(o[2 * n], a, b[0], b[1]);
+        mma16816(o[2 * n + 1], a, b[2], b[3]);
       }
     }
     __syncwarp();
@@ -346,32 +338,26 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
 
     // ---- the task's end, or this CTA's: the warps' sums added up
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
-        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
-        if (t == 0) s.ml[warp][mt * 16 + g + 8 * e] = make_float2(m[mt][e], l[mt][e]);
-      }
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (t == 0) s.ml[warp][g + 8 * e] = make_float2(m[e], l[e]);
     }
     __syncthreads();
-    float f[MT][2];
+    float f[2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int e = 0; e < 2; ++e) {
+      const int r = g + 8 * e;
+      float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = mt * 16 + g + 8 * e;
-        float top = -INFINITY, sum = 0.f;
+      for (int x = 0; x < W; ++x) top = fmaxf(top, s.ml[x][r].x);
 #pragma unroll
-        for (int x = 0; x < W; ++x) top = fmaxf(top, s.ml[x][r].x);
-#pragma unroll
-        for (int x = 0; x < W; ++x) {
-          const float2 ml = s.ml[x][r];
-          sum += ml.y * (ml.x == -INFINITY ? 0.f : exp2f(ml.x - top));
-        }
-        f[mt][e] = m[mt][e] == -INFINITY ? 0.f : exp2f(m[mt][e] - top);
-        if (warp == 0 && t == 0) s.row_ml[r] = make_float2(top, sum);
+      for (int x = 0; x < W; ++x) {
+        const float2 ml = s.ml[x][r];
+        sum += ml.y * (ml.x == -INFINITY ? 0.f : exp2f(ml.x - top));
       }
+      f[e] = m[e] == -INFINITY ? 0.f : exp2f(m[e] - top);
+      if (warp == 0 && t == 0) s.row_ml[r] = make_float2(top, sum);
     }
     const long long t0 = w.task, t1 = t0 + w.nt;
     const bool whole = t0 >= u0 && t1 <= u1;
@@ -381,13 +367,10 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += kMergeCols) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int n = 0; n < kMergeCols / 8; ++n) {
-          const float* v = o[mt][c0 / 8 + n];
-          *reinterpret_cast<float2*>(&s.merge[warp][mt * 16 + g][n * 8 + 2 * t]) = make_float2(v[0] * f[mt][0], v[1] * f[mt][0]);
-          *reinterpret_cast<float2*>(&s.merge[warp][mt * 16 + g + 8][n * 8 + 2 * t]) = make_float2(v[2] * f[mt][1], v[3] * f[mt][1]);
-        }
+      for (int n = 0; n < kMergeCols / 8; ++n) {
+        const float* v = o[c0 / 8 + n];
+        *reinterpret_cast<float2*>(&s.merge[warp][g][n * 8 + 2 * t]) = make_float2(v[0] * f[0], v[1] * f[0]);
+        *reinterpret_cast<float2*>(&s.merge[warp][g + 8][n * 8 + 2 * t]) = make_float2(v[2] * f[1], v[3] * f[1]);
       }
       __syncthreads();
       for (int x = tid; x < kM * kMergeCols / 2; x += NT) {
@@ -434,24 +417,41 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
         const auto at = [&](int i) { return (long long)slot_of(b + i * by) * kM; };
         for (int x = tid; x < live * count; x += NT) s.parts[x / live][x % live] = __ldcg(&p.part_ml[at(x / live) + x % live]);
         __syncthreads();
-        for (int x = tid; x < live * D / 2; x += NT) {
-          const int r = x / (D / 2), c = 2 * (x % (D / 2));
-          float top = -INFINITY, sum = 0.f;
-          for (int i = 0; i < count; ++i) top = fmaxf(top, s.parts[i][r].x);
-          float2 v = make_float2(0.f, 0.f);
+        constexpr int kPer = kM * D / 2 / NT, kAt = kPer < 4 ? kPer : 4;  // pairs of columns of a thread; at a time
+#pragma unroll 1
+        for (int x0 = tid; x0 < live * D / 2; x0 += kAt * NT) {
+          float2 v[kAt];
+          float top[kAt], sum[kAt];
+#pragma unroll
+          for (int k = 0; k < kAt; ++k) {
+            v[k] = make_float2(0.f, 0.f);
+            top[k] = -INFINITY;
+            sum[k] = 0.f;
+            for (int i = 0; i < count; ++i) top[k] = fmaxf(top[k], s.parts[i][(x0 + k * NT) / (D / 2) % kM].x);
+          }
 #pragma unroll 4
           for (int i = 0; i < count; ++i) {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part + (at(i) + r) * D + c)), ml = s.parts[i][r];
-            const float e = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-            sum = fmaf(ml.y, e, sum);
-            v.x = fmaf(y.x, e, v.x);
-            v.y = fmaf(y.y, e, v.y);
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) {
+              // rows past the live ones are read, and nobody's
+              const int x = x0 + k * NT, r = x / (D / 2) % kM, c = 2 * (x % (D / 2));
+              const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part + (at(i) + r) * D + c)), ml = s.parts[i][r];
+              const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - top[k]);
+              sum[k] = fmaf(ml.y, e, sum[k]);
+              v[k].x = fmaf(y.x, e, v[k].x);
+              v[k].y = fmaf(y.y, e, v[k].y);
+            }
           }
-          if (level == 1) {
-            put2<D>(p, w.row0, w.h, w.i * kM + r, c, v, sum);
-          } else {
-            *reinterpret_cast<float2*>(p.part + (at(0) + r) * D + c) = v;
-            if (c == 0) p.part_ml[at(0) + r] = make_float2(top, sum);
+#pragma unroll
+          for (int k = 0; k < kAt; ++k) {
+            const int x = x0 + k * NT, r = x / (D / 2), c = 2 * (x % (D / 2));
+            if (r >= live) break;
+            if (level == 1) {
+              put2<D>(p, w.row0, w.h, w.i * kM + r, c, v[k], sum[k]);
+            } else {
+              *reinterpret_cast<float2*>(p.part + (at(0) + r) * D + c) = v[k];
+              if (c == 0) p.part_ml[at(0) + r] = make_float2(top[k], sum[k]);
+            }
           }
         }
         __syncthreads();
@@ -470,21 +470,21 @@ __global__ void __launch_bounds__(Rows<D, MT>::kW * 32, 1) attn_rows(const __gri
   }
 }
 
-template <int D, int MT>
+template <int D>
 __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
   __shared__ PlanScratch<1024> x;
   griddep_wait();
   griddep_launch_dependents();
-  attn_plan<Rows<D, MT>::kKT, 0, 1024>(p, p.seq, p.start, x, true);
+  attn_plan<Rows<D>::kKT, 0, 1024>(p, p.seq, p.start, x, true);
 }
 
-template <int D, int MT>
+template <int D>
 cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
-  const size_t smem = sizeof(RowsSmem<D, MT>);
-  cudaError_t e = opt_in<attn_rows<D, MT>>(smem);
+  const size_t smem = sizeof(RowsSmem<D>);
+  cudaError_t e = opt_in<attn_rows<D>>(smem);
   if (e != cudaSuccess) return e;
   if (p.seqs <= kAttnPlanned) p.seq = nullptr;
-  p.tile_m = 16 * MT;
+  p.tile_m = 16;
   p.tile_g = p.group;
   RowMaps m = {};
   const long long rows = (long long)p.num_blocks * p.block.d, cols = (long long)p.Hkv * D;
@@ -493,18 +493,17 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
     return cudaErrorInvalidValue;
   if (p.seq) {
     const Launch one(dim3(1), 1024, 0, true, s);
-    e = cudaLaunchKernelEx(&one.cfg, plan_kernel<D, MT>, p);
+    e = cudaLaunchKernelEx(&one.cfg, plan_kernel<D>, p);
     if (e != cudaSuccess) return e;
   }
-  const Launch all(dim3(grid), Rows<D, MT>::kW * 32, smem, true, s);
-  return cudaLaunchKernelEx(&all.cfg, attn_rows<D, MT>, m, p);
+  const Launch all(dim3(grid), Rows<D>::kW * 32, smem, true, s);
+  return cudaLaunchKernelEx(&all.cfg, attn_rows<D>, m, p);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const AttnParams& p, int d, int rows, int grid, cudaStream_t s) {
-  if (rows <= 16) return d == 64 ? launch<64, 1>(p, grid, s) : d == 128 ? launch<128, 1>(p, grid, s) : launch<256, 1>(p, grid, s);
-  return d == 64 ? launch<64, 2>(p, grid, s) : d == 128 ? launch<128, 2>(p, grid, s) : launch<256, 1>(p, grid, s);
+cudaError_t launch_attn_rows(const AttnParams& p, int d, int grid, cudaStream_t s) {
+  return d == 64 ? launch<64>(p, grid, s) : d == 128 ? launch<128>(p, grid, s) : launch<256>(p, grid, s);
 }
 
 }  // namespace gdn
