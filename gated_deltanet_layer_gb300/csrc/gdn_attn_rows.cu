@@ -4,9 +4,9 @@
 // o = sum_p w_p v_p / sum_p w_p with w_p = 2^(x_p - m), x_p = scale log2(e) q . k_p and m
 // the running maximum, over the keys once. A task's rows are the G query heads of a
 // key/value head times the request's tokens, so every key and value is read once for all of
-// them. A tile of keys is 16 for each warp; a warp has its own maximum, sums and
-// outputs, its own ring of key and value rows in shared memory, and waits for no other until the
-// task's end, where the warps' outputs are added up. The rows come as boxes of 16 by TMA where blocks
+// them. A tile of keys is 16 for each group of warps (one warp, or two with heads of 256); a
+// group has its own maximum, sums and outputs, its own ring of key and value rows in shared
+// memory, and waits for no other until the task's end, where the groups' outputs are added up. The rows come as boxes of 16 by TMA where blocks
 // are made of 16 slots, else, and past the last key, 16 bytes a lane. Products by mma.sync
 // (16 x 8 x 16), which leaves scores and outputs in registers; it has the time: bound by the
 // bandwidth of the keys and values.
@@ -25,26 +25,29 @@ using namespace tc;
 template <int D>
 struct Rows {
   static constexpr int kM = 16;                // rows of a task
-  static constexpr int kW = D == 256 ? 4 : 8;  // warps
-  static constexpr int kKT = 16 * kW;          // keys of a tile
+  // groups of 16 keys of a tile; warps of a group, which share its scores' work twice over and its columns:
+  // with heads of 256 four warps alone would not keep up with the rows
+  static constexpr int kG = D == 256 ? 4 : 8, kH = D == 256 ? 2 : 1, kW = kG * kH;
+  static constexpr int kKT = 16 * kG;          // keys of a tile
+  static constexpr int kCols = D / kH;         // a warp's columns of the outputs
   static constexpr int kStages = D == 64 ? 5 : 3;
   static constexpr int kRow = 2 * D;           // bytes of a key row
   // columns merged at a time; floats of a row, against bank conflicts
-  static constexpr int kMergeCols = 32, kMergeStride = kMergeCols + 4;
+  static constexpr int kMergeCols = D == 256 ? 16 : 32, kMergeStride = kMergeCols + 4;
 };
 
 template <int D>
 struct alignas(1024) RowsSmem {
   using C = Rows<D>;
-  unsigned char ring[C::kW][C::kStages][2][16 * C::kRow];  // a warp's stages: keys, values
+  unsigned char ring[C::kG][C::kStages][2][16 * C::kRow];  // a group's stages: keys, values
   unsigned char q[2][C::kM * C::kRow];  // of a task and the next
   union {
     float merge[C::kW][C::kM][C::kMergeStride];
     float2 parts[16][C::kM];  // the joined parts' maxima and sums
   };
-  float2 ml[C::kW][C::kM];
+  float2 ml[C::kG][C::kM];
   int poison[D];  // the first hidden-from-some key whose value in the column is not finite
-  uint64_t full[C::kW][C::kStages];
+  uint64_t full[C::kG][C::kStages];
   int4 seq[kAttnPlanned + 1];
   long long start[kAttnPlanned + 1];
   PlanScratch<C::kW * 32> scan;
@@ -116,9 +119,17 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
   extern __shared__ __align__(1024) unsigned char raw[];
   static_assert(sizeof(RowsSmem<D>) <= 232448, "227 KB of shared memory a CTA");
   RowsSmem<D>& s = *reinterpret_cast<RowsSmem<D>*>(raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (lane == 0)
-    for (int i = 0; i < ST; ++i) mbar_init(&s.full[warp][i], 1);
+  constexpr int GROUPS = C::kG, HALVES = C::kH;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = warp % GROUPS, hf = warp / GROUPS;
+  if (lane == 0 && hf == 0)
+    for (int i = 0; i < ST; ++i) mbar_init(&s.full[grp][i], 1);
+  // A group's warps wait for one another.
+  const auto group_sync = [&] {
+    if (HALVES == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * HALVES) : "memory");
+  };
   if (tid == 0) {
     if (maps.boxes) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v);
   }
@@ -147,9 +158,9 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
   // The ring's loads: lanes 0 - 15 know the slots of the warp's 16 keys, a step ahead.
   Walk<KT, 0> ahead(p, seq, start);
   ahead.from(s.at, u0);
-  const uint32_t ring = smem_u32(s.ring[warp]);
+  const uint32_t ring = smem_u32(s.ring[grp]);
   const int rows_end = p.num_blocks * (int)p.block.d;
-  KeyBlock kb = key_block(p, ahead.s, ahead.j * KT + warp * 16 + (lane & 15), ahead.ctx + ahead.n);
+  KeyBlock kb = key_block(p, ahead.s, ahead.j * KT + grp * 16 + (lane & 15), ahead.ctx + ahead.n);
   int issued = 0;
   uint32_t boxed = 0;  // the stages that came as boxes
   // The queries of a task: a share a warp; dead rows are zero. Those of the task after the present one come
@@ -173,29 +184,29 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
   const auto issue = [&] {
     if (issued < steps) {
       const int st = issued % ST, slot = key_slot(p, kb, ahead.s), h = ahead.h;
-      const bool box = maps.boxes && ahead.j * KT + warp * 16 + 15 < ahead.ctx + ahead.n;
+      const bool box = maps.boxes && ahead.j * KT + grp * 16 + 15 < ahead.ctx + ahead.n;
       if (first && seen++ == asked && asked <= begun) queries(ahead);
       first = ahead.j + 1 == ahead.nt;
       ++issued;
       if (issued < steps) {
         if (++ahead.j == ahead.nt) ahead.next_task();
-        kb = key_block(p, ahead.s, ahead.j * KT + warp * 16 + (lane & 15), ahead.ctx + ahead.n);
+        kb = key_block(p, ahead.s, ahead.j * KT + grp * 16 + (lane & 15), ahead.ctx + ahead.n);
       }
       boxed = box ? boxed | 1u << st : boxed & ~(1u << st);
       if (box) {
         const int row = __shfl_sync(0xffffffffu, slot < 0 ? rows_end : slot, 0);  // past the last row: zeros
-        if (lane == 0) mbar_arrive_expect_tx(&s.full[warp][st], 2 * 16 * C::kRow);
+        if (lane == 0 && hf == 0) mbar_arrive_expect_tx(&s.full[grp][st], 2 * 16 * C::kRow);
         __syncwarp();
-        if (lane < 2 * (D / 64)) {
+        if (lane < 2 * (D / 64) && hf == 0) {
           const int which = lane / (D / 64), c = lane % (D / 64);
-          tma_load_2d_plain(s.ring[warp][st][which] + c * 2048, which ? &maps.v : &maps.k, h * D + c * 64, row, &s.full[warp][st]);
+          tma_load_2d_plain(s.ring[grp][st][which] + c * 2048, which ? &maps.v : &maps.k, h * D + c * 64, row, &s.full[grp][st]);
         }
       } else {
         const long long col = (long long)h * D;
         const uint32_t dst = ring + st * (2 * 16 * C::kRow);
         constexpr int kPieces = D / 8, kPer = 32 / kPieces > 0 ? 32 / kPieces : 1;  // rows a warp copies at once
 #pragma unroll 2
-        for (int r0 = 0; r0 < 16; r0 += kPer) {
+        for (int r0 = hf * (16 / HALVES); r0 < (hf + 1) * (16 / HALVES); r0 += kPer) {
           const int r = r0 + lane / kPieces, c = lane % kPieces;
           const int at = __shfl_sync(0xffffffffu, slot, r);
           const long long row = max(at, 0);
@@ -211,7 +222,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
 
   Walk<KT, 0> w(p, seq, start);
   w.from(s.at, u0);
-  float o[D / 8][4], m[2], l[2];
+  float o[C::kCols / 8][4], m[2], l[2];
   int last_key[2], first_last = 0;  // last key that the thread's rows see; the task's first row's
   bool fresh = true;
   uint32_t phases = 0;  // of the stages' barriers
@@ -225,7 +236,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
       if (asked == begun) queries(w);
       ++begun;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      for (int n = 0; n < C::kCols / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[e] = -INFINITY;
@@ -242,16 +253,18 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
     else if (!box)
       asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
     if (box) {
-      ok = ok && mbar_wait(&s.full[warp][st], phases >> st & 1);
+      ok = ok && mbar_wait(&s.full[grp][st], phases >> st & 1);
       phases ^= 1u << st;
     }
     if (starts) {
       __syncthreads();  // the other warps' share of the queries
       qbuf ^= 1;
+    } else if (!box) {
+      group_sync();
     }
     __syncwarp();
     const uint32_t ks = ring + st * (2 * 16 * C::kRow), vs = ks + 16 * C::kRow, qs = smem_u32(s.q[qbuf]);
-    const int key0 = w.j * KT + warp * 16;
+    const int key0 = w.j * KT + grp * 16;
     if (key0 < w.ctx + w.n) {
       // two sums of a score where the registers allow it: half as many products wait for one another
       constexpr int kSums = D == 256 ? 1 : 2;
@@ -289,7 +302,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
         l[0] *= f0;
         l[1] *= f1;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
+        for (int n = 0; n < C::kCols / 8; ++n) {
           o[n][0] *= f0;
           o[n][1] *= f0;
           o[n][2] *= f1;
@@ -312,16 +325,16 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
         a[2 * b + 1] = pack2(y[2], y[3]);
       }
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
+      for (int n = 0; n < C::kCols / 16; ++n) {
         uint32_t b[4];
-        ldmatrix4_t(vs + piece((lane & 7) + ((lane >> 3) & 1) * 8, 2 * n + (lane >> 4)), b);
+        ldmatrix4_t(vs + hf * (C::kCols / 64 * 2048) + piece((lane & 7) + ((lane >> 3) & 1) * 8, 2 * n + (lane >> 4)), b);
         if (edge && w.n > 1) {
           // 0 x NaN: values that are not finite are taken out where a row does not see their key,
           // and the rows that do see it are told by the column's first such key
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + (e & 1) * 8 + 2 * t;
-            int* to = s.poison + n * 16 + (e >> 1) * 8 + g;
+            int* to = s.poison + hf * C::kCols + n * 16 + (e >> 1) * 8 + g;
             if ((b[e] & 0x7f80u) == 0x7f80u) atomicMin(to, key), b[e] &= 0xffff0000u;
             if ((b[e] & 0x7f800000u) == 0x7f800000u) atomicMin(to, key + 1), b[e] &= 0xffffu;
           }
@@ -330,7 +343,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
         mma16816(o[2 * n + 1], a, b[2], b[3]);
       }
     }
-    __syncwarp();
+    group_sync();  // the stage is read
     if (w.j + 1 < w.nt && step + 1 < steps) {
       ++w.j;
       continue;
@@ -341,7 +354,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      if (t == 0) s.ml[warp][g + 8 * e] = make_float2(m[e], l[e]);
+      if (t == 0 && hf == 0) s.ml[grp][g + 8 * e] = make_float2(m[e], l[e]);
     }
     __syncthreads();
     float f[2];
@@ -350,9 +363,9 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
       const int r = g + 8 * e;
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < W; ++x) top = fmaxf(top, s.ml[x][r].x);
+      for (int x = 0; x < GROUPS; ++x) top = fmaxf(top, s.ml[x][r].x);
 #pragma unroll
-      for (int x = 0; x < W; ++x) {
+      for (int x = 0; x < GROUPS; ++x) {
         const float2 ml = s.ml[x][r];
         sum += ml.y * (ml.x == -INFINITY ? 0.f : exp2f(ml.x - top));
       }
@@ -365,7 +378,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
     const int slot = 2 * blockIdx.x + (t0 >= u0);
     float* part = p.part + (long long)slot * kM * D;
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += kMergeCols) {
+    for (int c0 = 0; c0 < C::kCols; c0 += kMergeCols) {
 #pragma unroll
       for (int n = 0; n < kMergeCols / 8; ++n) {
         const float* v = o[c0 / 8 + n];
@@ -373,23 +386,23 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
         *reinterpret_cast<float2*>(&s.merge[warp][g + 8][n * 8 + 2 * t]) = make_float2(v[2] * f[1], v[3] * f[1]);
       }
       __syncthreads();
-      for (int x = tid; x < kM * kMergeCols / 2; x += NT) {
-        const int r = x / (kMergeCols / 2), c = 2 * (x % (kMergeCols / 2));
+      for (int x = tid; x < HALVES * kM * kMergeCols / 2; x += NT) {
+        const int h = x / (kM * kMergeCols / 2), r = x / (kMergeCols / 2) % kM, c = 2 * (x % (kMergeCols / 2)), col = h * C::kCols + c0 + c;
         if (r < live) {
           float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int y = 0; y < W; ++y) {
-            const float2 q = *reinterpret_cast<const float2*>(&s.merge[y][r][c]);
+          for (int y = 0; y < GROUPS; ++y) {
+            const float2 q = *reinterpret_cast<const float2*>(&s.merge[h * GROUPS + y][r][c]);
             v.x += q.x;
             v.y += q.y;
           }
           const int R = w.i * kM + r, seen = w.ctx + p.group.div(R);
-          if (s.poison[c0 + c] <= seen) v.x = NAN;
-          if (s.poison[c0 + c + 1] <= seen) v.y = NAN;
+          if (s.poison[col] <= seen) v.x = NAN;
+          if (s.poison[col + 1] <= seen) v.y = NAN;
           if (whole)
-            put2<D>(p, w.row0, w.h, R, c0 + c, v, s.row_ml[r].y);
+            put2<D>(p, w.row0, w.h, R, col, v, s.row_ml[r].y);
           else
-            *reinterpret_cast<float2*>(part + r * D + c0 + c) = v;
+            *reinterpret_cast<float2*>(part + r * D + col) = v;
         }
       }
       __syncthreads();
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
   if (!ok) {
     // A wait has passed its limit: the stages' last copies are waited for.
     for (int i = max(0, steps - ST); i < steps; ++i)
-      if (boxed >> (i % ST) & 1) mbar_wait(&s.full[warp][i % ST], ~phases >> (i % ST) & 1);
+      if (boxed >> (i % ST) & 1) mbar_wait(&s.full[grp][i % ST], ~phases >> (i % ST) & 1);
     if (lane == 0) atomicCAS(p.error, 0u, (kStatusDeadline << 24) | (kAttnWait << 16) | (blockIdx.x & 0xffff));
   }
 }
