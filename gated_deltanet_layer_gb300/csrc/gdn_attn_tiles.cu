@@ -627,7 +627,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     } else if (warp == kMma && rank == 0) {
       // ---- the products
       constexpr uint32_t is = idesc_bf16_f32(256, KT), io = idesc_bf16_f32(256, D) | kMnB;
-      int i = 0, ks = 0, sn = 0, pn[2] = {0, 0};  // slots, the present one, S tiles (with one row tile), weights' tiles
+      int i = 0, slot0 = 0;              // slots before the segment, and its first one
+      uint32_t sn = 0, pn0 = 0, pn1 = 0;  // S tiles, with one row tile; weights' tiles of each S
       const auto wait = [&](uint64_t* b, uint32_t parity) {
         ok = ok && mbar_wait(b, parity);
         tc_fence_after();
@@ -650,123 +651,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           mma_bf16_ts_pair(tmem + C::kO + t * D, tmem + b * 128 + 8 * e, v + e * (2048 >> 4), io, !(first && e == 0));
         if (tell) mma_commit_pair(&s.o_done[TILES == 2 ? t : b]);
       };
-      const auto filled = [&](int slot, int e) { wait(&s.full[slot], e / SLOTS & 1); };
-      const auto after = [&](int slot, int d) { return slot + d >= SLOTS ? slot + d - SLOTS : slot + d; };
       for (int n = 0; take(n); ++n) {
         const Seg& g = s.seg[n % kSegs];
-        const int j0 = g.j0, steps = g.j1 - j0, end[2] = {g.end[0], g.end[1]};
-        const bool split = TILES == 2 && g.split;
+        const int steps = g.j1 - g.j0, end0 = g.end[0] - g.j0, end1 = g.end[1] - g.j0;
+        const bool split = TILES == 1 || g.split;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
-        // the segment's slots: keys i + 2 e, values i + 2 e + 1
         wait(&s.q_full, n & 1);
-        filled(ks, i);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        if (elect_one()) {
-          if (TILES == 2) {
+        // The turns, PV of a tile and then an S, in the order that keeps the tensor cores busy while the
+        // softmax works on another S: with two row tiles PV(0, e), S(0, e + 1), PV(1, e), S(1, e + 1), the
+        // tile's softmax beside the other's products; where S alternates over the keys PV(e), S(e + 2).
+        // One copy of their instructions: those that a task's end or beginning had for itself would
+        // have to be fetched each time.
+        const int turns = split ? steps + 2 : 2 * steps + 2;
 #pragma unroll 1
-            for (int t = 0; t < (split ? 1 : 2); ++t)
-              if (end[t] > j0) scores(t, t, ks);
-          } else {
-            scores(0, sn & 1, ks);
+        for (int x = 0; x < turns; ++x) {
+          const int e = split ? x - 2 : (x >> 1) - 1, ahead = split ? e + 2 : e + 1;  // the tiles of PV and S
+          const int t = TILES == 1 ? 0 : x & 1;                                       // row tile of O
+          const int endt = split ? steps : t ? end1 : end0;
+          const bool pv = e >= 0 && e < endt, sc = ahead < endt, last = split || t == 1;
+          const int vb = TILES == 1 ? (sn + x) & 1 : t;  // the S of both: S(e + 2) comes where P(e) was
+          // the segment's slots: keys 2 e, values 2 e + 1
+          const int vi = 2 * e + 1, ki = 2 * ahead;
+          const int vs = (slot0 + max(vi, 0)) % SLOTS, k = (slot0 + ki) % SLOTS;
+          if (pv) {
+            wait(&s.full[vs], (i + vi) / SLOTS & 1);
+            wait(&s.p_full[vb], (vb ? pn1 : pn0) & 1);
+            ++(vb ? pn1 : pn0);
           }
-          mma_commit_pair(&s.empty[ks]);
-          if (steps == 1) mma_commit_pair(&s.q_empty);
-        }
-        __syncwarp();
-        ++sn;
-        if (split) {
-          // the CTAs' one row tile each, on every second tile of keys in the other one's place
-          if (steps > 1) {
-            const int k1 = after(ks, 2);
-            filled(k1, i + 2);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (e >= 0) {
             if (elect_one()) {
-              scores(0, 1, k1);
-              mma_commit_pair(&s.empty[k1]);
-              if (steps == 2) mma_commit_pair(&s.q_empty);
+              if (pv) values(t, vb, vs, e == 0 || (TILES == 2 && split && e == 1), TILES == 1 || !sc);
+              if (last) mma_commit_pair(&s.empty[vs]);
             }
             __syncwarp();
           }
-#pragma unroll 1
-          for (int e = 0; e < steps; ++e) {
-            const int t = e & 1, vs = after(ks, 1), k2 = after(after(ks, 2), 2);
-            const bool more = e + 2 < steps;
-            filled(vs, i + 1);
-            if (more) filled(k2, i + 4);
-            wait(&s.p_full[t], (t ? pn[1] : pn[0]) & 1);
-            ++(t ? pn[1] : pn[0]);
+          if (ahead < steps) {  // no PV waits for the keys of a later S
+            if (sc) wait(&s.full[k], (i + ki) / SLOTS & 1);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             if (elect_one()) {
-              values(t, t, vs, e < 2, !more);
-              mma_commit_pair(&s.empty[vs]);
-              if (more) {
-                scores(0, t, k2);
-                mma_commit_pair(&s.empty[k2]);
-                if (e + 3 == steps) mma_commit_pair(&s.q_empty);
-              }
-            }
-            __syncwarp();
-            ks = after(ks, 2);
-            i += 2;
-          }
-          if (!ok) break;
-          continue;
-        }
-#pragma unroll 1
-        for (int e = 0; e < steps; ++e) {
-          const int vs = after(ks, 1), k2 = after(ks, 2), j = j0 + e;
-          const bool more = e + 1 < steps;
-          if (TILES == 2) {
-            // a row tile's softmax runs while the other's products do
-            filled(vs, i + 1);
-            if (more) filled(k2, i + 2);
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-              const bool pv = j < end[t], s_ = j + 1 < end[t];
-              if (pv) {
-                wait(&s.p_full[t], pn[t] & 1);
-                ++pn[t];
-              }
-              if (!(ok = __all_sync(0xffffffffu, ok))) break;
-              if (elect_one()) {
-                if (pv) values(t, t, vs, e == 0, !s_);
-                if (t == 1) mma_commit_pair(&s.empty[vs]);
-                if (s_) scores(t, t, k2);
-                if (t == 1 && more) mma_commit_pair(&s.empty[k2]);
-                if (t == 1 && e + 2 == steps) mma_commit_pair(&s.q_empty);
-              }
-              __syncwarp();
-            }
-            if (!ok) break;
-          } else {
-            // S's buffers alternate over the whole share: the softmax of a tile runs beside the next one's S
-            if (more) {
-              filled(k2, i + 2);
-              if (!(ok = __all_sync(0xffffffffu, ok))) break;
-              if (elect_one()) {
-                scores(0, sn & 1, k2);
-                mma_commit_pair(&s.empty[k2]);
-                if (e + 2 == steps) mma_commit_pair(&s.q_empty);
-              }
-              __syncwarp();
-              ++sn;
-            }
-            const int b = pn[0] & 1;
-            filled(vs, i + 1);
-            wait(&s.p_full[b], (pn[0] >> 1) & 1);
-            ++pn[0];
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            if (elect_one()) {
-              values(0, b, vs, e == 0, true);
-              mma_commit_pair(&s.empty[vs]);
+              if (sc) scores(split ? 0 : t, vb, k);
+              if (last) mma_commit_pair(&s.empty[k]);
+              if (last && ahead == steps - 1) mma_commit_pair(&s.q_empty);
             }
             __syncwarp();
           }
-          ks = k2;
-          i += 2;
         }
         if (!ok) break;
+        sn += steps;
+        i += 2 * steps;
+        slot0 = i % SLOTS;
       }
     } else if (warp == kSched && ok) {
       // ---- the pair's share, a part of a task at a time
