@@ -20,16 +20,14 @@ from . import prefill as _p
 __all__ = ["PagedAttention", "kv_append"]
 
 
-def _cache(t, name, heads=None, d=None):
-    """A [slots, heads, head_dim] bf16 CUDA tensor whose slots' rows are packed; its slot stride."""
+def _cache(t, name):
+    """A [slots, heads, head_dim] bf16 CUDA tensor whose slots' rows are packed: its sizes and slot stride."""
     if t.dtype is not _bf16 or not t.is_cuda or t.dim() != 3 or (_p._several and t.get_device() != _p._device()):
         raise ValueError(f"{name} must be a [slots, heads, head_dim] bf16 CUDA tensor on the current device")
-    (n, h, w), (ld, a, b) = t.shape, t.stride()
-    if (heads is not None and (h != heads or w != d)) or n > _INT_MAX:
-        raise ValueError(f"{name} must be [slots, {heads}, {d}]")
-    if n and ((b != 1 and w > 1) or (a != w and h > 1) or (ld < h * w and n > 1)):
+    (n, h, d), (ld, a, b) = t.shape, t.stride()
+    if n > _INT_MAX or (n and ((b != 1 and d > 1) or (a != d and h > 1) or (ld < h * d and n > 1))):
         raise ValueError(f"the heads of a slot of {name} must be packed, and its slots must not overlap")
-    return ld if n > 1 else -(-h * w // 8) * 8
+    return n, h, d, ld if n > 1 else -(-h * d // 8) * 8
 
 
 def kv_append(q, k, v, token_pos, slots, inv_freq, k_cache, v_cache, *, q_norm_w=None, k_norm_w=None, norm_eps=1e-6,
@@ -40,39 +38,40 @@ def kv_append(q, k, v, token_pos, slots, inv_freq, k_cache, v_cache, *, q_norm_w
     inv_freq f32 [rotary_dim / 2] (None: no rotation); k_cache, v_cache [slots, Hkv, d],
     updated; norm weights bf16 [d] or None. q_out may be q; error: int32 [1], optional.
     Returns q_out."""
-    ldkc, heads, d = _cache(k_cache, "k_cache"), k_cache.shape[1], k_cache.shape[2]
-    ldvc = _cache(v_cache, "v_cache", heads, d)
+    n, heads, d, ldkc = _cache(k_cache, "k_cache")
+    nv, hv, dv, ldvc = _cache(v_cache, "v_cache")
     ldk, ldv = _rows(k, "k"), _rows(v, "v")
-    T = k.shape[0]
-    if v_cache.shape[0] != k_cache.shape[0]:
+    T, cols = k.shape
+    if nv != n or hv != heads or dv != d:
         raise ValueError("k_cache and v_cache have different sizes")
-    if k.shape[1] != heads * d or v.shape != k.shape:
+    if cols != heads * d or v.shape != (T, cols):
         raise ValueError(f"k and v must be [tokens, {heads * d}]")
     if T > _INT_MAX:
         raise GdnError("gdn_kv_append", _native.GDN_ERR_UNSUPPORTED)
     qp, ldq, qo, ldqo, hq = None, 0, None, 0, 0
     if q is not None:
         ldq, qp = _rows(q, "q"), q.data_ptr()
-        cols = q.shape[1]
-        if q.shape[0] != T or cols % d or cols == 0:
+        rows, cols = q.shape
+        hq = cols // d if d else 0
+        if rows != T or hq * d != cols or hq == 0:
             raise ValueError(f"q must be [tokens, heads * {d}]")
-        hq = cols // d
         if q_out is None:
             q_out, ldqo = _empty((T, cols), _bf16, q, stream), cols
         else:
             ldqo = _rows(q_out, "q_out")
-            if q_out.shape != q.shape:
+            if q_out.shape != (T, cols):
                 raise ValueError("q_out must have q's shape")
         qo = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     freq, rotary = None, 0
     if inv_freq is not None:
-        n = inv_freq.numel()
-        freq, rotary = _dense(inv_freq, "inv_freq", torch.float32, n), 2 * n
+        rotary = inv_freq.numel()
+        freq = _dense(inv_freq, "inv_freq", torch.float32, rotary)
+        rotary *= 2
     st = _native.lib().gdn_kv_append(
         T, hq, heads, d, qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, _dense(token_pos, "token_pos", _i32, T),
-        _dense(slots, "slots", torch.int64, T), k_cache.shape[0], freq, rotary, interleaved,
+        _dense(slots, "slots", torch.int64, T), n, freq, rotary, interleaved,
         None if q_norm_w is None else _dense(q_norm_w, "q_norm_w", _bf16, d),
         None if k_norm_w is None else _dense(k_norm_w, "k_norm_w", _bf16, d), norm_eps, qo, ldqo, k_cache.data_ptr(), ldkc,
         v_cache.data_ptr(), ldvc, None if error is None else _dense(error, "error", _i32, 1), _stream(stream))
@@ -130,12 +129,13 @@ class PagedAttention:
         [T, Hq * d], k_cache, v_cache [slots, Hkv, d] (slots a multiple of the block
         size), block_table int32 [S, blocks], cu_seqlens [S + 1], context_lens [S]. max_len:
         no request has more new tokens (None: no better bound than T). Returns out."""
-        T, cols = q.shape[0], self._columns
-        ldq = _rows(q, "q")
-        ldk, ldv = _cache(k_cache, "k_cache", self._heads, self._d), _cache(v_cache, "v_cache", self._heads, self._d)
-        n = k_cache.shape[0]
-        if q.shape[1] != cols or v_cache.shape[0] != n or n % self._block:
-            raise ValueError(f"q must be [tokens, {cols}], and the caches as many slots, whole blocks of {self._block}")
+        ldq, (T, cols) = _rows(q, "q"), q.shape
+        n, heads, d, ldk = _cache(k_cache, "k_cache")
+        nv, hv, dv, ldv = _cache(v_cache, "v_cache")
+        if heads != self._heads or d != self._d or hv != heads or dv != d or nv != n or n % self._block:
+            raise ValueError(f"k_cache and v_cache must be [slots, {self._heads}, {self._d}], whole blocks of {self._block} slots")
+        if cols != self._columns:
+            raise ValueError(f"q must be [tokens, {self._columns}]")
         S, wide = block_table.shape
         if max_len is None or max_len > T:
             max_len = T
