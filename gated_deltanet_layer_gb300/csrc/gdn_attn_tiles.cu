@@ -66,11 +66,12 @@ struct alignas(1024) TileSmem {
   using C = Cfg<D>;
   unsigned char q[C::kTiles][128 * D * 2];
   unsigned char ring[C::kSlots][C::kSlotBytes];
-  uint64_t q_full, q_empty, edge, full[C::kSlots], empty[C::kSlots], s_full[2], p_full[2], o_done[2], seg_full[kSegs],
+  uint64_t q_full, q_empty, edge, full[C::kSlots], empty[C::kSlots], s_full[2], p_full[2], o_done[2], joined, seg_full[kSegs],
       seg_empty[kSegs];
   uint32_t tmem;
   int failed;                   // a wait has passed its limit
   unsigned last[2];
+  unsigned split_done;          // row tiles that have finished their half of the keys of a task that is the pair's alone
   int at[4];                    // the first unit's request, head, row tile and key tile
   Seg seg[kSegs];
   // By segment: the first key, hidden from some row, whose value in the column is not finite, as
@@ -246,6 +247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     mbar_init(&s.q_full, 2);
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.edge, 4);
+    mbar_init(&s.joined, 8);
+    s.split_done = 0;
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&s.full[i], 8);
       mbar_init(&s.empty[i], 1);
@@ -308,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
       const int r = (warp & 3) * 32 + lane;
       const bool in_tile = r < tile_toks * G, warp_in_tile = (warp & 3) * 32 < tile_toks * G;
       const int r_tok = p.group.div(r), hd = r - r_tok * G, warp_tok = p.group.div((warp & 3) * 32);
-      int sn = 0, ends = 0;  // S tiles, and segments with any so far (of the row tile)
+      int sn = 0, ends = 0, joins = 0;  // S tiles, segments with any so far (of the row tile), split tasks that are the pair's alone
       for (int n = 0;; ++n) {
         const bool there = take(n);
         if (!(ok = named_all(1 + t, 128, ok)) || !there) break;
@@ -345,7 +348,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[KT - 4 + i]);
             const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-            if (__any_sync(0xffffffffu, tile_top > m + kSlack || m == -INFINITY)) {
+            // rows that are none have what was in their place: their maxima correct nothing
+            if (__any_sync(0xffffffffu, live && (tile_top > m + kSlack || m == -INFINITY))) {
               const float grown = fmaxf(m, tile_top), f = m == -INFINITY ? 0.f : ex2(m - grown);
               if (j > j0) {
                 if (TILES == 1) {  // S came before the last PV
@@ -405,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         }
         if (!(ok = named_all(1 + t, 128, ok))) break;
         const int c0 = g.c0, c1 = g.c1;
-        const bool whole = g.whole && !split;
+        const bool own = g.whole, whole = own && !split;
         const long long part_row = (2LL * pair + g.slot) * C::kRows + (2 * t + rank) * 128;  // the part's first row
         const long long row = g.row0 + tok, col = ((long long)g.h * G + hd) * D;
         const unsigned tag = g.tag;
@@ -445,15 +449,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         __syncwarp();
         if (lane < 2) arrive_cluster(map_rank(&s.seg_empty[n % kSegs], lane));
         if (!whole && first < toks) {
+          // A task that is the pair's alone, and split, is counted here: the counter in memory is that of the task
+          // that other pairs go on with, who may be there long before this one.
+          const bool alone = split && own;
           unsigned* done = p.done + 4 * c0 + (split ? 0 : 2 * t) + rank;
           const int parts = (c1 - c0 + 1) << (split ? 1 : 0);
           named_sync(1 + t, 128);
-          if (r == 0) s.last[t] = atom_add_acq_rel_u32(done, 1u) == (unsigned)(parts - 1);
+          if (r == 0) {
+            unsigned before;
+            if (alone) {
+              __threadfence();
+              before = atomicAdd(&s.split_done, 1u);
+              __threadfence();
+            } else {
+              before = atom_add_acq_rel_u32(done, 1u);
+            }
+            s.last[t] = before == (unsigned)(parts - 1);
+          }
           named_sync(1 + t, 128);
           if (s.last[t]) {
             // every part is there: the first pair's second one, the others' first, and where the keys
             // are split both row tiles'
-            if (r == 0) *done = 0;
+            if (r == 0) {
+              if (alone)
+                s.split_done = 0;
+              else
+                *done = 0;
+            }
             const auto at = [&](int k) {
               const int c = c0 + (split ? k >> 1 : k), u = split ? k & 1 : t;
               return (2LL * c + (c == c0)) * C::kRows + (2 * u + rank) * 128;
@@ -488,6 +510,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
               }
             }
           }
+        }
+        if (split && own) {
+          // the next such task has its parts in the same place: not before these are read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.joined);
+          ok = mbar_wait(&s.joined, joins++ & 1);
+          ok = __all_sync(0xffffffffu, ok);
         }
       }
     }

@@ -162,3 +162,33 @@ def test_refused_with_a_handle():
     with pytest.raises(GdnError):
         p.call(small)
     H.check(p.call(h), *p.reference())
+
+
+@pytest.mark.parametrize("heads,d,block,requests", [
+    ((40, 8), 128, 32, [(500 + 97 * i, 4) for i in range(24)]),
+    ((64, 8), 64, 16, [(0, 700), (600, 33), (0, 500), (900, 16), (1000, 32), (77, 300), (520, 40), (700, 9)]),
+    ((64, 8), 128, 16, [(0, 600), (640, 20), (0, 333), (800, 32), (515, 3), (33, 64), (1200, 17)]),
+    ((24, 4), 256, 64, [(300 + 41 * i, 3 + 2 * i) for i in range(24)]),
+    ((16, 16), 64, 16, [(512 + 64 * i, 30 + i) for i in range(12)])])
+def test_many_tasks(heads, d, block, requests):
+    """Many tasks a CTA, whole and in parts, some of them split between row tiles, right after one another."""
+    p = H.Pages(heads, d, block, requests, seed=d + len(requests))
+    h = p.handle()
+    outs = [p.call(h) for _ in range(4)]
+    assert h.check() == (0, 0)
+    H.check(outs[0], *p.reference())
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
+@pytest.mark.parametrize("heads,d", [((24, 4), 256), ((40, 8), 128), ((64, 8), 64)])
+def test_rows_that_are_none(heads, d):
+    """What stands in the place of a row tile's rows that are none changes no bit of the others: pad rows, and
+    what another call has left in shared memory."""
+    outs = []
+    for big in (0.0, 300.0):
+        other = H.Pages(heads, d, 16, [(0, 300)], seed=9, q_std=1.0 + big)
+        other.call(other.handle())
+        p = H.Pages(heads, d, 16, [(700, 37), (90, 301)], seed=d, extra=40)
+        p.q[int(p.cu[-1]):] = big
+        outs.append(p.call(p.handle())[:int(p.cu[-1])])
+    assert torch.equal(*outs)
