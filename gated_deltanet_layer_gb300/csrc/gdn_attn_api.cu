@@ -127,7 +127,7 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
   if (ldq % 8 || ldo % 8 || (gate && ldg % 8) || ldk % 8 || ldv % 8) return GDN_ERR_ARG;
   const long long slots = (long long)num_blocks * c.block_size;
   if (slots > INT32_MAX) return GDN_ERR_UNSUPPORTED;
-  if (ldk >= (1LL << 38) || ldv >= (1LL << 38)) return GDN_ERR_UNSUPPORTED;  // a tile map's largest stride
+  if (ldq >= (1LL << 38) || ldk >= (1LL << 38) || ldv >= (1LL << 38)) return GDN_ERR_UNSUPPORTED;  // a tile map's largest stride
   const Layout l(c, h->grid);
   const Span o = matrix(out, tokens, ldo, cols);
   const Span in[] = {matrix(q, tokens, ldq, cols), matrix(gate, tokens, ldg, cols), matrix(k_cache, slots, ldk, kv),

@@ -4,8 +4,11 @@
 // Bound by the bandwidth of its rows, each read and written once, and for few tokens by
 // latency. A warp takes a token, or a part of its heads where there are few tokens: a lane has the
 // same 8 columns of a head throughout, so the cosines and sines of its pairs stay in registers,
-// and four pieces of 256 columns are on their way at a time. A lane has its pairs' other
-// halves from the lane r / 16 beside it.
+// and two pieces of 256 columns are on their way while two are worked on, the first before the slot and
+// the angles are known. A lane has its pairs' other halves from the lane r / 16 beside it.
+// Three CTAs a SM: with four the angles' registers spill. Measured: 16384 tokens of 80 heads of 128, 671 MB, 111 us
+// (6.0 TB/s; four pieces that are not ahead of the work 122); 1777 of 32 heads of 256 with norms, 58 MB, 14.3 us
+// (20.5), a chain of 16 pieces a warp and 110 instructions a piece; 8 tokens 3.1 us.
 //
 // Angles. pos f is wanted modulo a turn, to f32's accuracy at any position. f / (2 pi) is
 // a 64-bit binary fraction of a turn (in two double terms, so right to its last bits), and
@@ -20,16 +23,18 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads_ = 256, kDeep = 4;
+constexpr int kThreads_ = 256, kDeep = 2;
 
 __device__ __forceinline__ unsigned long long turns_of(float f) {
-  const double x = f, hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
+  const double x = fabsf(f), hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
   const double a = x * hi, b = fma(x, hi, -a) + x * lo, r = a - floor(a);
-  return (unsigned long long)(r * 18446744073709551616.0) + (unsigned long long)(long long)(b * 18446744073709551616.0);
+  const unsigned long long u =
+      (unsigned long long)(r * 18446744073709551616.0) + (unsigned long long)(long long)(b * 18446744073709551616.0);
+  return f < 0.f ? 0ull - u : u;  // 1 - r would lose r's last bits
 }
 
 template <int D, bool PAIRS, bool NORM>  // PAIRS: 2 i and 2 i + 1 turn together, else i and i + r / 2
-__global__ void __launch_bounds__(kThreads_, 4) kv_append(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads_, 3) kv_append(const AppendParams p) {
   constexpr int kL = D / 8;  // lanes of a head
   __shared__ unsigned long long turn[D / 2];
   const int tid = threadIdx.x, lane = tid & 31, c = lane % kL, half = p.rotary / 2;
@@ -51,11 +56,21 @@ __global__ void __launch_bounds__(kThreads_, 4) kv_append(const AppendParams p) 
 #pragma unroll 1
   for (long long u = (long long)blockIdx.x * (kThreads_ / 32) + (tid >> 5); u < units; u += warps) {
     const int t = (int)(u / p.parts), first = (int)(u - (long long)t * p.parts) * part, last = min(first + part, pieces);
-    long long slot = p.slots[t];
-    const long long pos = p.pos[t];
     const __nv_bfloat16* q = p.q + t * p.ldq;
     const __nv_bfloat16* k = p.k + t * p.ldk - q_cols;
     const __nv_bfloat16* v = p.v + t * p.ldv - k_cols;
+    const auto rows_in = [&](int i0, uint4 (&x)[kDeep]) {
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        const int col = (i0 + d) * 256 + lane * 8;
+        x[d] = make_uint4(0, 0, 0, 0);
+        if (i0 + d < last && col < cols) x[d] = *reinterpret_cast<const uint4*>((col < q_cols ? q : col < k_cols ? k : v) + col);
+      }
+    };
+    uint4 next4[kDeep];
+    rows_in(first, next4);
+    long long slot = p.slots[t];
+    const long long pos = p.pos[t];
     if (slot >= p.num_slots) {
       if (first == 0 && lane == 0 && p.error) atomicCAS(p.error, 0u, (kStatusIndex << 24) | (1u << 16) | (uint32_t)(t & 0xffff));
       slot = -1;
@@ -80,11 +95,8 @@ __global__ void __launch_bounds__(kThreads_, 4) kv_append(const AppendParams p) 
     for (int i0 = first; i0 < last; i0 += kDeep) {
       uint4 x4[kDeep];
 #pragma unroll
-      for (int d = 0; d < kDeep; ++d) {
-        const int col = (i0 + d) * 256 + lane * 8;
-        x4[d] = make_uint4(0, 0, 0, 0);
-        if (i0 + d < last && col < cols) x4[d] = *reinterpret_cast<const uint4*>((col < q_cols ? q : col < k_cols ? k : v) + col);
-      }
+      for (int d = 0; d < kDeep; ++d) x4[d] = next4[d];
+      rows_in(i0 + kDeep, next4);
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
         if (i0 + d >= last) break;
@@ -152,7 +164,7 @@ cudaError_t launch(const AppendParams& p, int grid, cudaStream_t s) {
 
 cudaError_t launch_kv_append(AppendParams p, int d, bool pairs, cudaStream_t s) {
   // as many warps as run at once; a token's pieces are split where there are fewer tokens
-  const long long most = 32LL * sm_count();
+  const long long most = 24LL * sm_count();
   const int pieces = (int)(((long long)(p.Hq + 2 * p.Hkv) * d + 255) / 256);
   p.parts = (int)std::max(1LL, std::min<long long>((pieces + kDeep - 1) / kDeep, most / p.tokens));
   const int grid = (int)((std::min((long long)p.tokens * p.parts, most) + kThreads_ / 32 - 1) / (kThreads_ / 32));

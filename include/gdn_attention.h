@@ -50,7 +50,7 @@ extern "C" {
  * q [tokens][ldq >= num_q_heads * head_dim] and q_out, or both NULL (keys and
  * values alone; num_q_heads is then ignored), k, v [tokens][>= num_kv_heads *
  * head_dim] bf16; token_pos int32, slots int64 [tokens]; inv_freq f32
- * [rotary_dim / 2] (radians a position, finite; NULL with rotary_dim 0);
+ * [rotary_dim / 2] (radians a position, of less than 2^40; NULL with rotary_dim 0);
  * rotary_dim a multiple of 16, at most head_dim; head_dim 64, 128 or 256;
  * q_norm_w, k_norm_w bf16 [head_dim], each or both NULL: no norm. q_out may be q
  * itself (same pointer and stride); otherwise outputs overlap no input. */
@@ -102,7 +102,7 @@ gdn_status gdn_attn_create(const gdn_attn_config* cfg, void* workspace, size_t w
  * and is read as zeros. Pad rows and their outputs: not read, zero.
  * q, out [tokens][>= num_q_heads * head_dim], gate likewise or NULL; k_cache,
  * v_cache [num_blocks * block_size][>= num_kv_heads * head_dim] bf16 (fewer
- * than 2^31 slots); block_table int32 [seqs][max_blocks], cu_seqlens int32
+ * than 2^31 slots; ldq, ldk and ldv below 2^38); block_table int32 [seqs][max_blocks], cu_seqlens int32
  * [seqs + 1], context_lens int32 [seqs]. out must overlap no input.
  * One call at a time per handle (its calls share the workspace). */
 gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens, int32_t max_len, const void* q, int64_t ldq,

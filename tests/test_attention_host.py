@@ -99,6 +99,7 @@ PAGED = dict(seqs=2, tokens=6, max_len=3, q=A[0], ldq=1024, k=A[1], ldk=256, v=A
     (dict(ctx=A[5] + 1), ARG), (dict(table=A[3] + 2), ARG), (dict(q=A[0] + 8), ARG), (dict(out=A[7] + 2), ARG),
     (dict(gate=A[6] + 4), ARG), (dict(k=A[1] + 8), ARG), (dict(ldq=1016), ARG), (dict(ldq=1028), ARG), (dict(ldo=512), ARG),
     (dict(ldg=1000), ARG), (dict(ldk=248), ARG), (dict(ldv=257), ARG), (dict(num_blocks=1 << 27), UNSUPPORTED),
+    (dict(ldq=1 << 38), UNSUPPORTED), (dict(ldk=1 << 38), UNSUPPORTED), (dict(ldv=1 << 38), UNSUPPORTED),
     # overlaps
     (dict(out=A[0]), ARG), (dict(out=A[1] + 4096), ARG), (dict(out=A[2]), ARG), (dict(out=A[6] + 512), ARG),
     (dict(out=A[4] - 1024), ARG),

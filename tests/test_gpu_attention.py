@@ -242,7 +242,8 @@ def test_graph_and_stream(heads, d, block, requests):
 
 # ------------------------------------------------------------------- append
 
-def append_case(heads, d, rotary, T, block, seed, *, norms, interleaved, far=1000, pads=(), stride=0, in_place=False, q=True):
+def append_case(heads, d, rotary, T, block, seed, *, norms, interleaved, far=1000, pads=(), stride=0, in_place=False, q=True,
+                turn=1.0):
     from gated_deltanet_layer_gb300 import kv_append
     rng = np.random.default_rng(seed)
     hq, hkv = heads
@@ -253,7 +254,7 @@ def append_case(heads, d, rotary, T, block, seed, *, norms, interleaved, far=100
     n = T * 2 + 5
     slots = rng.permutation(n)[:T]
     slots[list(pads)] = -1 - np.arange(len(pads))
-    freq = torch.from_numpy((1e6 ** (-np.arange(0, rotary, 2) / rotary)).astype(np.float32)).cuda() if rotary else None
+    freq = torch.from_numpy((1e6 ** (-np.arange(0, rotary, 2) / rotary)).astype(np.float32)).cuda() * turn if rotary else None
     qw, kw = ((H.bf16(rng.standard_normal(d) * 0.2).cuda() for _ in range(2)) if norms else (None, None))
     kc, vc = (H.strided(H.bf16(rng.standard_normal((n, hkv, d))), stride) for _ in range(2))
     want, (wk, tk), wv = H.append_reference(H.f64(qs) if q else None, H.f64(ks), H.f64(vs), pos, slots,
@@ -300,3 +301,9 @@ def test_append_bad_slot():
     err.fill_(77)  # a word that is set stays
     kv_append(None, q[:, :64], q[:, 64:], H.ints([0, 1, 2]), H.ints([7, 8, 9], np.int64), None, kc, vc, error=err)
     assert err.item() == 77
+
+
+@pytest.mark.parametrize("turn,far", [(-1.0, 1 << 31), (-2.0 ** -30, 1 << 31), (2.0 ** -30, 1 << 31), (2.0 ** 38, 1000), (-2.0 ** 20, 1000)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_frequencies(turn, far, interleaved):
+    append_case((4, 2), 64, 64, 50, 16, 77, norms=True, interleaved=interleaved, far=far, turn=turn)
