@@ -14,8 +14,17 @@
 // A CTA's warps are R x S: R groups of 16 weight rows, as many as give every SM one CTA, and S shares of
 // the columns, as many as there are warps left, whose sums are added up in shared memory at the end.
 // A warp's codes come through a ring of its own (cp.async), its scales and zeros four groups at
-// a time through registers, and x as a piece of all shares' columns at a time, two pieces deep;
-// from 17 rows on x comes to the lanes as it is, from L1: its pieces would be too short.
+// a time through registers, and x to the lanes as it is, from L1. Through shared memory, pieces of all
+// shares at a time, its room was what bounded S: 16 rows of 1024 x 8192 33 us, 8 now; 8 rows of
+// 8192 x 8192 20.8 and 14.6.
+//
+// 8, 16 or 32 rows of x at a time. 32 in all read the weights once; fewer at a time where the groups are too few
+// for the SMs all the same (up to two a SM): 33 rows of 1037 x 1056 8.2 us with 32 at a time, 5.6 with 16. 64 at a
+// time leave too few registers: 64 rows of 8192 x 8192 77 us, 58 with two passes.
+//
+// Measured, codes and scales as bytes: 8 rows of 20480 x 8192 MXFP4 37.6 us (2.4 TB/s), 2560 x 8192 MXFP4, one
+// row 10.4, whole numbers 8.4: a SM's warps issue an instruction every other cycle, 49 for 512 weights (unpack 22,
+// the scales 8, loads and addresses 12), and 160 groups of rows are two for a CTA, which leaves 72 SMs idle.
 #include <algorithm>
 
 #include "gdn_host.h"
@@ -31,8 +40,6 @@ constexpr int kStep = 256;              // columns of a stage
 constexpr int kStages = 4;
 constexpr int kPitch = kStep / 2;       // bytes of a stage's row; its 16-byte pieces permuted, against bank conflicts
 constexpr int kStageBytes = 16 * kPitch, kRing = kStages * kStageBytes;  // of a warp
-constexpr int kXBytes = 32768;          // of x at a time, of all shares; twice
-constexpr bool x_in_smem(int mt) { return mt <= 2; }
 
 // Warps of a CTA: what the registers allow.
 template <int MT>
@@ -83,30 +90,25 @@ __device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t (&o)[4]) {
     o[2 * h + 1] = prmt(lo, top, 0x7362);
   }
 }
-__device__ __forceinline__ float e8m0(uint32_t e) {
-  return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : e << 23);
-}
+// 2^(e - 127), NaN for 255, as f32.
+__device__ __forceinline__ uint32_t e8m0(uint32_t e) { return max(e << 23, 0x00400000u) | (e == 255 ? 0x00400000u : 0u); }
 __device__ __forceinline__ float act_f(float y, int act) {
   if (act == 0) return y;
   const float s = act == 1 ? y : y * fmaf(0.07135481627f, y * y, 1.595769122f);
   return __fdividef(y, 1.0f + __expf(-s));
 }
 
-// FMT 0: whole numbers with zeros, 1: E2M1. GPS: scale groups of a stage (8, 4, 2). MT: 8 rows of x. MR: rows
-// of x that are kept; with one, all of a product's columns are that row.
-template <int FMT, int GPS, int MT, int MR>
+// FMT 0: whole numbers with zeros, 1: E2M1. GPS: scale groups of a stage (8, 4, 2). MT: 8 rows of x.
+template <int FMT, int GPS, int MT>
 __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params p) {
-  static_assert(MR == MT * 8 || MR == 1, "");
   extern __shared__ __align__(16) unsigned char smem[];
   const int kNT = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int R = p.row_groups, S = p.shares, rg = warp % R, sl = warp / R;
-  constexpr bool kStaged = x_in_smem(MT);
-  unsigned char* const ring = smem + (kStaged ? 2 * kXBytes : 0) + warp * kRing;
+  unsigned char* const ring = smem + warp * kRing;
   const int m0 = blockIdx.y * MT * 8, M = min(MT * 8, p.M - m0);
   const int all = (p.K + kStep - 1) / kStep;
   const int each = (all + S - 1) / S;  // stages of a share
   const int s0 = min(sl * each, all), s1 = min(s0 + each, all);
-  const int piece = kStaged ? min(each, kXBytes / (2 * kStep * MR * S)) : each;  // stages of x at a time
   const int n0 = (blockIdx.x * R + rg) * 16;
   const long long row0 = min(n0 + g, p.N - 1), row1 = min(n0 + g + 8, p.N - 1);
   const int groups = p.K / p.group;  // of a row
@@ -134,23 +136,6 @@ __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params 
     }
     cp_async_commit();
   };
-  // x of the shares' stages [c, c + piece): [share][group of 32][row][t], 8 columns each; zeros past the last
-  // column
-  const auto x_in = [&](int c, int buf) {
-    const uint32_t x = smem_u32(smem) + buf * kXBytes;
-    const int per_row = piece * (kStep / 8), rows = S * M;
-    for (int a = warp; a < rows; a += kNT >> 5) {
-      const int sh = a / M, m = a - sh * M, k0 = (sh * each + c) * kStep;
-      const __nv_bfloat16* src = p.x + (long long)(m0 + m) * p.ldx + k0;
-      const uint32_t dst = x + (sh * piece * (kStep / 32) * MR + m) * 64;
-      for (int i = lane; i < per_row; i += 32) {
-        const bool on = k0 + i * 8 < p.K;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (i >> 2) * (MR * 64) + (i & 3) * 16),
-                     "l"(on ? src + i * 8 : p.x), "r"(on ? 16 : 0)
-                     : "memory");
-      }
-    }
-  };
   // Scales (and zeros) of four groups of the two rows: a lane's t-th.
   const auto scale_in = [&](int quad, uint32_t (&v)[2]) {
     const int at = quad * 4 + t;
@@ -168,7 +153,6 @@ __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params 
   };
   constexpr int kQuad = GPS < 4 ? 4 / GPS : 1, kQuads = GPS > 4 ? GPS / 4 : 1;  // stages of four groups; fours of a stage
   constexpr int kAhead = 2 * kQuads;  // fours that are on their way
-  if (kStaged) x_in(0, 0);
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) codes_in(s0 + i);
   uint32_t sc[kAhead][2];
@@ -176,97 +160,81 @@ __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params 
   for (int i = 0; i < kAhead; ++i) scale_in(s0 / kQuad * kQuads + i, sc[i]);
 
   float acc[MT][4] = {};
-  int buf = 0;
 #pragma unroll 1
-  for (int c = 0; c < each; c += piece, buf ^= 1) {
-    // x of these stages has come: with the codes that were asked for after it, or now
-    if (kStaged) {
-      if (c == 0 || piece < kStages) asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncthreads();
-      if (c + piece < each) x_in(c + piece, buf ^ 1);
-    }
-    const unsigned char* x = smem + buf * kXBytes + sl * piece * (kStep / 32) * (MR * 64) + (MR == 1 ? t * 16 : g * 64 + t * 16);
-#pragma unroll 1
-    for (int k = 0; k < piece; ++k, x += kStep / 32 * MR * 64) {  // all of them, for the waits, though the share may end before
-      const int st = s0 + c + k;
-      codes_in(st + kStages - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncwarp();
-      if (st >= s1) continue;
-      const unsigned char* codes = ring + (st & (kStages - 1)) * kStageBytes + g * kPitch + t * 4;
-      const int k0 = st * kStep + t * 8;  // the lane's first column
-      const int in_quad = kQuad > 1 ? (st % kQuad) * GPS : 0;  // the stage's first scale group, of the lanes' four
-      float z[MT][4], f[2];
-      uint32_t less[2];
+  for (int st = s0; st < s1; ++st) {
+    codes_in(st + kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+    const unsigned char* codes = ring + (st & (kStages - 1)) * kStageBytes + g * kPitch + t * 4;
+    const int k0 = st * kStep + t * 8;  // the lane's first column
+    const int in_quad = kQuad > 1 ? (st % kQuad) * GPS : 0;  // the stage's first scale group, of the lanes' four
+    float z[MT][4], f[2];
+    uint32_t less[2];
 #pragma unroll
-      for (int q = 0; q < kStep / 32; ++q) {
-        constexpr int PER = kStep / 32 / GPS;  // groups of 32 of a scale group
-        if (q % PER == 0) {
+    for (int q = 0; q < kStep / 32; ++q) {
+      constexpr int PER = kStep / 32 / GPS;  // groups of 32 of a scale group
+      if (q % PER == 0) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t v = __shfl_sync(0xffffffffu, sc[q / PER / 4][e], (lane & 28) + in_quad + q / PER % 4);
-            if (FMT == 1) {
-              f[e] = e8m0(v);
-            } else {
-              f[e] = __uint_as_float(v & 0xffff0000u);
-              const float u = (float)(v & 0xffff) * -0x1p-6f;
-              less[e] = pack_bf16x2(u, u);
-            }
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) z[mt][0] = z[mt][1] = z[mt][2] = z[mt][3] = 0.f;
-        }
-        uint4 y[MT];
-        if (!kStaged) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            y[mt] = make_uint4(0, 0, 0, 0);
-            if (mt * 8 < M && k0 + q * 32 < p.K)
-              y[mt] = __ldg(reinterpret_cast<const uint4*>(p.x + (long long)(m0 + min(mt * 8 + g, M - 1)) * p.ldx + k0 + q * 32));
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t v = __shfl_sync(0xffffffffu, FMT == 1 ? e8m0(sc[q / PER / 4][e]) : sc[q / PER / 4][e], (lane & 28) + in_quad + q / PER % 4);
+          if (FMT == 1) {
+            f[e] = __uint_as_float(v);
+          } else {
+            f[e] = __uint_as_float(v & 0xffff0000u);
+            const float u = (float)(v & 0xffff) * -0x1p-6f;
+            less[e] = pack_bf16x2(u, u);
           }
         }
-        const int at = (q ^ g) << 4;
-        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(codes + at);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + 8 * kPitch + at);
-        uint32_t v0[4], v1[4];
-        if (FMT == 1) {
-          unpack_e2m1(w0, v0);
-          unpack_e2m1(w1, v1);
-        } else {
-          unpack_int(w0, less[0], v0);
-          unpack_int(w1, less[1], v1);
-        }
-        const uint32_t a[4] = {v0[0], v1[0], v0[1], v1[1]}, b[4] = {v0[2], v1[2], v0[3], v1[3]};
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) z[mt][0] = z[mt][1] = z[mt][2] = z[mt][3] = 0.f;
+      }
+      uint4 y[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        y[mt] = make_uint4(0, 0, 0, 0);
+        if (mt * 8 < M && k0 + q * 32 < p.K)
+          y[mt] = __ldg(reinterpret_cast<const uint4*>(p.x + (long long)(m0 + min(mt * 8 + g, M - 1)) * p.ldx + k0 + q * 32));
+      }
+      const int at = (q ^ g) << 4;
+      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(codes + at);
+      const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + 8 * kPitch + at);
+      uint32_t v0[4], v1[4];
+      if (FMT == 1) {
+        unpack_e2m1(w0, v0);
+        unpack_e2m1(w1, v1);
+      } else {
+        unpack_int(w0, less[0], v0);
+        unpack_int(w1, less[1], v1);
+      }
+      const uint32_t a[4] = {v0[0], v1[0], v0[1], v1[1]}, b[4] = {v0[2], v1[2], v0[3], v1[3]};
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (mt > 0 && mt * 8 >= M) break;  // no such rows
+        mma_bf16_16816(z[mt], a, y[mt].x, y[mt].y);
+        mma_bf16_16816(z[mt], b, y[mt].z, y[mt].w);
+      }
+      if (q % PER == PER - 1) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          if (mt > 0 && mt * 8 >= M) break;  // no such rows
-          if (kStaged) y[mt] = *reinterpret_cast<const uint4*>(x + q * (MR * 64) + mt * 512);
-          mma_bf16_16816(z[mt], a, y[mt].x, y[mt].y);
-          mma_bf16_16816(z[mt], b, y[mt].z, y[mt].w);
-        }
-        if (q % PER == PER - 1) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            acc[mt][0] = fmaf(f[0], z[mt][0], acc[mt][0]);
-            acc[mt][1] = fmaf(f[0], z[mt][1], acc[mt][1]);
-            acc[mt][2] = fmaf(f[1], z[mt][2], acc[mt][2]);
-            acc[mt][3] = fmaf(f[1], z[mt][3], acc[mt][3]);
-          }
+          acc[mt][0] = fmaf(f[0], z[mt][0], acc[mt][0]);
+          acc[mt][1] = fmaf(f[0], z[mt][1], acc[mt][1]);
+          acc[mt][2] = fmaf(f[1], z[mt][2], acc[mt][2]);
+          acc[mt][3] = fmaf(f[1], z[mt][3], acc[mt][3]);
         }
       }
-      if ((st + 1) % kQuad == 0) {
-#pragma unroll
-        for (int i = 0; i < kAhead - kQuads; ++i) sc[i][0] = sc[i + kQuads][0], sc[i][1] = sc[i + kQuads][1];
-#pragma unroll
-        for (int i = kAhead - kQuads; i < kAhead; ++i) scale_in((st + 1) / kQuad * kQuads + i, sc[i]);
-      }
-      __syncwarp();
     }
+    if ((st + 1) % kQuad == 0) {
+#pragma unroll
+      for (int i = 0; i < kAhead - kQuads; ++i) sc[i][0] = sc[i + kQuads][0], sc[i][1] = sc[i + kQuads][1];
+#pragma unroll
+      for (int i = kAhead - kQuads; i < kAhead; ++i) scale_in((st + 1) / kQuad * kQuads + i, sc[i]);
+    }
+    __syncwarp();
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 
-  // the shares' sums, over x: [share][row of x][weight row]
+  // the shares' sums, over the rings: [share][row of x][weight row]
   const int W = R * 16;
   float* out = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -291,27 +259,27 @@ __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params 
   }
 }
 
-template <int FMT, int GPS, int MT, int MR>
+template <int FMT, int GPS, int MT>
 cudaError_t launch(W4Params p, cudaStream_t s) {
-  constexpr int kMost = warps<MT>(), kX = x_in_smem(MT) ? 2 * kXBytes : 0;
-  static_assert(kX + kMost * kRing <= 232448, "227 KB of shared memory a CTA");
-  static_assert(kMost * 16 * MT * 8 * 4 <= kX + kMost * kRing, "the shares' sums");
-  const cudaError_t e = opt_in<linear_w4<FMT, GPS, MT, MR>>(kX + kMost * kRing);
+  constexpr int kMost = warps<MT>();
+  static_assert(kMost * kRing <= 232448, "227 KB of shared memory a CTA");
+  static_assert(16 * MT * 8 * 4 <= kRing, "the shares' sums");
+  const cudaError_t e = opt_in<linear_w4<FMT, GPS, MT>>(kMost * kRing);
   if (e != cudaSuccess) return e;
   const int passes = (p.M + MT * 8 - 1) / (MT * 8), rows16 = (p.N + 15) / 16, steps = (p.K + kStep - 1) / kStep;
   const int R = (int)std::min<long long>(kMost, ((long long)rows16 * passes + sm_count() - 1) / sm_count());
-  // a stage of x of all shares has room
-  const int S = std::max(1, std::min({kMost / R, x_in_smem(MT) ? kXBytes / (2 * kStep * MR) : kMost, steps}));
+  const int S = std::max(1, std::min(kMost / R, steps));
   p.row_groups = R;
   p.shares = S;
-  const Launch l(dim3((rows16 + R - 1) / R, passes), 32 * R * S, kX + R * S * kRing, true, s);
-  return cudaLaunchKernelEx(&l.cfg, linear_w4<FMT, GPS, MT, MR>, p);
+  const Launch l(dim3((rows16 + R - 1) / R, passes), 32 * R * S, R * S * kRing, true, s);
+  return cudaLaunchKernelEx(&l.cfg, linear_w4<FMT, GPS, MT>, p);
 }
 template <int FMT, int GPS>
 cudaError_t by_rows(const W4Params& p, cudaStream_t s) {
-  if (p.M == 1) return launch<FMT, GPS, 1, 1>(p, s);
-  return p.M <= 8 ? launch<FMT, GPS, 1, 8>(p, s) : p.M <= 16 ? launch<FMT, GPS, 2, 16>(p, s) : p.M <= 32 ? launch<FMT, GPS, 4, 32>(p, s)
-                                                                                                    : launch<FMT, GPS, 8, 64>(p, s);
+  // passes of fewer rows where there are SMs for them
+  const auto fits = [&](int rows) { return (p.N + 15LL) / 16 * ((p.M + rows - 1) / rows) <= 2 * sm_count(); };
+  if (p.M <= 8 || fits(8)) return launch<FMT, GPS, 1>(p, s);
+  return p.M <= 16 || fits(16) ? launch<FMT, GPS, 2>(p, s) : launch<FMT, GPS, 4>(p, s);
 }
 
 }  // namespace

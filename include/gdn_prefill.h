@@ -7,6 +7,7 @@
  *   gdn_slot_map       offsets, block tables and slots of a ragged batch from
  *                      its request lengths, on the device
  *   gdn_linear         act(x W^T + bias) + residual (in_proj, out_proj)
+ *   gdn_linear_w4      the same with the weights in 4 bits, for few rows
  *   gdn_prefill_conv   causal depthwise conv1d + SiLU, conv state in and out
  *   gdn_prefill_delta  L2-normalised q/k, gates, the gated delta rule and
  *                      optionally the gated RMSNorm x SiLU(z), SSM state in
@@ -166,9 +167,8 @@ typedef enum { GDN_W4_INT = 0, GDN_W4_MXFP4 = 1 } gdn_w4_format;
 /* gdn_linear with the weights in 4 bits, for few rows (decode and verify
  * steps): out[m][n] = bf16(act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]).
  * The activations stay bf16 (where gdn_decode_step quantises them to MXFP4). Weights
- * are taken as the codes and scales stand for them, without a rounding; sums
- * are f32. Within the columns that a CTA adds up, x keeps what is above 2^-31 of its row's
- * largest value there (exact above 2^-27). Up to 64 rows read the weights once; more
+ * and x are taken as they are, without a rounding; sums are f32, of a group's products first,
+ * which its scale then multiplies. Up to 64 rows read the weights once; more
  * are taken 64 at a time. inner is a multiple of `group`.
  * x [rows][ldx >= inner] (16-byte aligned, ldx a multiple of 8), codes
  * [cols][inner / 2] (16-byte aligned), scales and zeros [cols][inner / group];

@@ -14,10 +14,9 @@ Tolerances (set from the arithmetic, before any run; a rounding to bf16 is at mo
             of A; the exponentials and the gate 2^-20.
             All together, errors of roundings have no common sign: the 2-norm of a call's error is below
             2^-8 of the outputs' (each rounding's mean square is a third of its largest).
-  w4        2^-8 |y| for the rounding. Whole numbers: a group's sum holds 1024 + code and at
-            most 1040 |x| for a column: (G / 16 + 8) 2^-23 of 1056 sum |x| scale, of every
-            group; E2M1: (K / 16 + 16) 2^-23 of sum |x w|. The groups' sums in f32: (K / G +
-            16) 2^-23 of sum |x w|. Times 1.2 for the steepest activation.
+  w4        2^-8 |y| for the rounding. A weight without its scale has at most 8 bits, so products
+            are exact: (G / 16 + 16) 2^-23 of sum |x w| for the sums within the groups, (K / G +
+            16) 2^-23 for the groups' sums in f32. Times 1.2 for the steepest activation.
 """
 from __future__ import annotations
 
@@ -205,10 +204,7 @@ def w4_reference(x, codes, scales, zeros, bias, act, residual):
         y = x @ w.T
         size = np.abs(x) @ np.abs(w).T
         before = (groups + 16) * 2.0 ** -23 * size
-        if scales.dtype == torch.uint8:
-            before += (K / 16 + 16) * 2.0 ** -23 * size
-        else:
-            before += (G / 16 + 8) * 2.0 ** -23 * 1056 * (np.abs(x).reshape(-1, groups, G).sum(-1) @ np.abs(s).T)
+        before += (G / 16 + 16) * 2.0 ** -23 * size
     if bias is not None:
         y = y + f64(bias)
     if act == "silu":
