@@ -8,6 +8,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+from functools import partial
+from types import SimpleNamespace
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgdn_decode.so")
@@ -80,6 +82,22 @@ class Weights(ctypes.Structure):
 
 
 _lib = None
+_calls = None
+
+
+def calls() -> SimpleNamespace:
+    """The entry points that are marshalled in compiled code (csrc/gdn_binding.cpp)."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("_binding.so is not built; run `python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _calls = SimpleNamespace(**{
+            name: partial(getattr(_binding, name), ctypes.cast(getattr(L, entry), ctypes.c_void_p).value)
+            for name, entry in (("kv_append", "gdn_kv_append"), ("attend", "gdn_attn_paged"), ("linear_w4", "gdn_linear_w4"))})
+    return _calls
 
 
 def lib() -> ctypes.CDLL:

@@ -1,4 +1,5 @@
-"""Build the in-tree CUDA library (libgdn_decode.so) for sm_103a with nvcc.
+"""Build the in-tree CUDA library (libgdn_decode.so) for sm_103a with nvcc, and the
+compiled part of the Python binding (_binding.so) with the host's compiler.
 
 Each translation unit under csrc/ compiles in parallel; the objects link into
 one shared library next to this file. Nothing is installed anywhere.
@@ -18,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdn_decode.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE]
@@ -46,19 +48,37 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _build_binding(cuda_home: str) -> None:
+    """Against the installed torch's headers, whose libraries the process has loaded by then."""
+    import sysconfig
+
+    import torch
+    T = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "gdn_binding.cpp"), "-o", tmp, "-I", INCLUDE]
+    for d in (os.path.join(T, "include"), sysconfig.get_paths()["include"], os.path.join(cuda_home, "include")):
+        cmd += ["-isystem", d]
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-L", os.path.join(T, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(T, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding does not compile:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every translation unit and link libgdn_decode.so. Returns its path."""
+    """Compile every translation unit, link libgdn_decode.so and the binding. Returns the library's path."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
@@ -74,7 +94,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stdout + r.stderr
 
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_build_binding, os.path.dirname(os.path.dirname(nvcc)))
         results = list(ex.map(compile_one, _sources()))
+        binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():

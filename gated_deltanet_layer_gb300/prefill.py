@@ -120,38 +120,16 @@ def linear_w4(x, codes, scales, zeros=None, bias=None, activation=None, residual
     [N, K / 2], element 2 i in the low nibble of byte i. scales bf16 [N, K / group], group 32,
     64 or 128: (code - zero) * scale, zeros uint8 like scales or None (8). scales
     uint8 [N, K / 32]: MXFP4, E2M1 codes and e8m0 scales. The rest as for linear."""
-    ldx = _rows(x, "x")
-    M, K = x.shape
-    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[1] * 2 != K or scales.shape[0] != codes.shape[0]:
-        raise ValueError("codes must be [N, K / 2] and scales [N, K / group]")
-    N, groups = scales.shape
-    if groups == 0 or K % groups:
-        raise ValueError("the groups must divide K evenly")
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
-    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
-        raise GdnError("gdn_linear_w4", _native.GDN_ERR_UNSUPPORTED)
-    mx = scales.dtype is _u8
-    if out is None:
-        out, ldo = _empty((M, N), _bf16, x, stream), N
-    else:
-        ldo = _rows(out, "out")
-        if out.shape != (M, N):
-            raise ValueError("out must be [M, N]")
-    r, ldr = None, 0
-    if residual is not None:
-        r, ldr = residual.data_ptr(), _rows(residual, "residual")
-        if residual.shape != (M, N):
-            raise ValueError("residual must be [M, N]")
-    st = _native.lib().gdn_linear_w4(
-        M, N, K, x.data_ptr(), ldx, mx, K // groups, _dense(codes, "codes", _u8, N * (K // 2)),
-        _dense(scales, "scales", _u8 if mx else _bf16, N * groups),
-        None if zeros is None else _dense(zeros, "zeros", _u8, N * groups),
-        None if bias is None else _dense(bias, "bias", _bf16, N), ACTIVATIONS[activation], r, ldr, out.data_ptr(), ldo,
-        _stream(stream))
-    if st != GDN_OK:
-        raise GdnError("gdn_linear_w4", st)
-    return out
+    if stream is not None:
+        if out is None:
+            out = _empty((x.shape[0], scales.shape[0]), x.dtype, x, stream)
+        stream = _stream(stream)
+    r = _native.calls().linear_w4(stream, x, codes, scales, zeros, bias, ACTIVATIONS[activation], residual, out)
+    if r.__class__ is int:
+        raise GdnError("gdn_linear_w4", r)
+    return r
 
 
 def linear_check(stream=None):

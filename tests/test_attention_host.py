@@ -152,3 +152,20 @@ def test_python_refusals(lib):
         a.update(bad)
         with pytest.raises(GdnError):
             PagedAttention(a.pop("num_q_heads"), a.pop("num_kv_heads"), a.pop("head_dim"), a.pop("block_size"), **a)
+
+
+def test_calls_from_python_refused(lib):
+    """The compiled binding's own checks: types first, whatever comes after."""
+    x, f = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(4)
+    with pytest.raises(TypeError):
+        kv_append(x, x, x, f, f, None, [1], x)
+    with pytest.raises(ValueError):
+        kv_append(x, x, x, f, f, None, x.view(2, 1, 64), x.view(2, 1, 64))  # not on a device
+    with pytest.raises(TypeError):
+        linear_w4(None, f, f)
+    with pytest.raises(ValueError):
+        linear_w4(x, f, f)
+    with pytest.raises(ValueError):
+        linear_w4(x, f, f, activation="relu")
+    with pytest.raises(TypeError):
+        _native.calls().linear_w4(None, x)
