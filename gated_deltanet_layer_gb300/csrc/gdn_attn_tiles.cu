@@ -71,6 +71,7 @@ struct alignas(1024) TileSmem {
   uint32_t tmem;
   int failed;                   // a wait has passed its limit
   unsigned last[2];
+  float2 joint[C::kTiles][128];  // a joined row's maximum, and one over its sum
   unsigned split_done;          // row tiles that have finished their half of the keys of a task that is the pair's alone
   int at[4];                    // the first unit's request, head, row tile and key tile
   Seg seg[kSegs];
@@ -412,6 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         const bool own = g.whole, whole = own && !split;
         const long long part_row = (2LL * pair + g.slot) * C::kRows + (2 * t + rank) * 128;  // the part's first row
         const long long row = g.row0 + tok, col = ((long long)g.h * G + hd) * D;
+        const int g_row0 = g.row0, g_h = g.h;
         const unsigned tag = g.tag;
         const unsigned* poison = s.poison[n % kSegs];
         const bool flagged = any && s.flagged[n % kSegs] == tag;
@@ -480,34 +482,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
               const int c = c0 + (split ? k >> 1 : k), u = split ? k & 1 : t;
               return (2LL * c + (c == c0)) * C::kRows + (2 * u + rank) * 128;
             };
-            if (live) {
+            // a row a thread: the parts' maximum and sum; then 32 columns of a row a thread, whichever rows there are
+            const int rows = min(tile_toks, toks - first) * G;
+            if (r < rows) {
               float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-              for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(&p.part_ml[at(k) + r]).x);
-#pragma unroll 4
+#pragma unroll 8
               for (int k = 0; k < parts; ++k) {
                 const float2 ml = __ldcg(&p.part_ml[at(k) + r]);
-                sum += ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - top));
+                const float grown = fmaxf(top, ml.x);
+                sum = sum * (top == -INFINITY ? 0.f : ex2(top - grown)) + ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - grown));
+                top = grown;
               }
-              const float in = sum == 0.f ? 0.f : 1.f / sum;
+              s.joint[t][r] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+            }
+            named_sync(1 + t, 128);
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float o[32] = {};
+            for (int e = r; e < rows * (D / 32); e += 128) {
+              const int c = e / rows, i = e - c * rows, i_tok = p.group.div(i);
+              const float2 joint = s.joint[t][i];
+              float o[32] = {};
 #pragma unroll 2
-                for (int k = 0; k < parts; ++k) {
-                  const float pm = __ldcg(&p.part_ml[at(k) + r]).x, e = pm == -INFINITY ? 0.f : ex2(pm - top);
-                  const float4* part = reinterpret_cast<const float4*>(p.part + at(k) * D) + c / 4 * 128 + r;
+              for (int k = 0; k < parts; ++k) {
+                const float pm = __ldcg(&p.part_ml[at(k) + i]).x, w = pm == -INFINITY ? 0.f : ex2(pm - joint.x);
+                const float4* part = reinterpret_cast<const float4*>(p.part + at(k) * D) + c * 8 * 128 + i;
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const float4 v = __ldcg(part + i * 128);
-                    o[4 * i] = fmaf(v.x, e, o[4 * i]);
-                    o[4 * i + 1] = fmaf(v.y, e, o[4 * i + 1]);
-                    o[4 * i + 2] = fmaf(v.z, e, o[4 * i + 2]);
-                    o[4 * i + 3] = fmaf(v.w, e, o[4 * i + 3]);
-                  }
+                for (int q = 0; q < 8; ++q) {
+                  const float4 v = __ldcg(part + q * 128);
+                  o[4 * q] = fmaf(v.x, w, o[4 * q]);
+                  o[4 * q + 1] = fmaf(v.y, w, o[4 * q + 1]);
+                  o[4 * q + 2] = fmaf(v.z, w, o[4 * q + 2]);
+                  o[4 * q + 3] = fmaf(v.w, w, o[4 * q + 3]);
                 }
-                put32(p, row, col + c, o, in);
               }
+              put32(p, g_row0 + first + i_tok, ((long long)g_h * G + i - i_tok * G) * D + 32 * c, o, joint.y);
             }
           }
         }
@@ -656,24 +663,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     } else if (warp == kMma && rank == 0) {
       // ---- the products
       constexpr uint32_t is = idesc_bf16_f32(256, KT), io = idesc_bf16_f32(256, D) | kMnB;
-      int i = 0, slot0 = 0;              // slots before the segment, and its first one
-      uint32_t sn = 0, pn0 = 0, pn1 = 0;  // S tiles, with one row tile; weights' tiles of each S
-      const auto wait = [&](uint64_t* b, uint32_t parity) {
-        ok = ok && mbar_wait(b, parity);
-        tc_fence_after();
+      // the slots of the next keys and values, with their barriers' parities; those of the weights of each S
+      uint32_t ks = 0, k_parity = 0, vs = 1, v_parity = 0, p_parity = 0, sn = 0;  // sn: S tiles, with one row tile
+      const auto on_by_2 = [](uint32_t& slot, uint32_t& parity) {
+        slot += 2;
+        if (slot >= SLOTS) slot -= SLOTS, parity ^= 1;
       };
       // descriptors of the operands, as their low words change
       const uint64_t qd = sdesc_k_sw128(smem_u32(s.q[0])), kd = sdesc_k_sw128(smem_u32(s.ring[0])),
                      vd = sdesc_mn_sw128(smem_u32(s.ring[0]), 16384);
       // S of row tile t (into buffer b) from the keys in ring slot k
-      const auto scores = [&](int t, int b, int k) {
+      const auto scores = [&](int t, int b, uint32_t k) {
         const uint64_t a = qd + t * (128 * D * 2 >> 4), kk = kd + k * (C::kSlotBytes >> 4);
 #pragma unroll
         for (int e = 0; e < D / 16; ++e)
           mma_bf16_pair(tmem + b * 128, a + ((e >> 2) * 16384 >> 4) + 2 * (e & 3), kk + ((e >> 2) * 8192 >> 4) + 2 * (e & 3), is, e > 0);
         mma_commit_pair(&s.s_full[b]);
       };
-      const auto values = [&](int t, int b, int k, bool first, bool tell) {
+      const auto values = [&](int t, int b, uint32_t k, bool first, bool tell) {
         const uint64_t v = vd + k * (C::kSlotBytes >> 4);
 #pragma unroll
         for (int e = 0; e < KT / 16; ++e)
@@ -686,29 +693,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         const bool split = TILES == 1 || g.split;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
-        wait(&s.q_full, n & 1);
+        ok = ok && mbar_wait(&s.q_full, n & 1);
+        tc_fence_after();
         // The turns, PV of a tile and then an S, in the order that keeps the tensor cores busy while the
         // softmax works on another S: with two row tiles PV(0, e), S(0, e + 1), PV(1, e), S(1, e + 1), the
         // tile's softmax beside the other's products; where S alternates over the keys PV(e), S(e + 2).
         // One copy of their instructions: those that a task's end or beginning had for itself would
-        // have to be fetched each time.
+        // have to be fetched each time. One lane goes through a turn, waits and all: with the whole warp
+        // waiting, the tensor cores had done their products each time before it came back with the next.
         const int turns = split ? steps + 2 : 2 * steps + 2;
 #pragma unroll 1
         for (int x = 0; x < turns; ++x) {
           const int e = split ? x - 2 : (x >> 1) - 1, ahead = split ? e + 2 : e + 1;  // the tiles of PV and S
           const int t = TILES == 1 ? 0 : x & 1;                                       // row tile of O
           const int endt = split ? steps : t ? end1 : end0;
-          const bool pv = e >= 0 && e < endt, sc = ahead < endt, last = split || t == 1;
+          const bool pv = e >= 0 && e < endt, sc = ahead < endt, begun = split || t == 0, last = split || t == 1;
           const int vb = TILES == 1 ? (sn + x) & 1 : t;  // the S of both: S(e + 2) comes where P(e) was
-          // the segment's slots: keys 2 e, values 2 e + 1
-          const int vi = 2 * e + 1, ki = 2 * ahead;
-          const int vs = (slot0 + max(vi, 0)) % SLOTS, k = (slot0 + ki) % SLOTS;
-          if (pv) {
-            wait(&s.full[vs], (i + vi) / SLOTS & 1);
-            wait(&s.p_full[vb], (vb ? pn1 : pn0) & 1);
-            ++(vb ? pn1 : pn0);
-          }
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (e >= 0 && begun) ok = ok && mbar_wait(&s.full[vs], v_parity);
+          if (pv) ok = ok && mbar_wait(&s.p_full[vb], p_parity >> vb & 1);
+          tc_fence_after();
+          __syncwarp();
           if (e >= 0) {
             if (elect_one()) {
               if (pv) values(t, vb, vs, e == 0 || (TILES == 2 && split && e == 1), TILES == 1 || !sc);
@@ -716,21 +720,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             }
             __syncwarp();
           }
-          if (ahead < steps) {  // no PV waits for the keys of a later S
-            if (sc) wait(&s.full[k], (i + ki) / SLOTS & 1);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (ahead < steps) {
+            if (begun) ok = ok && mbar_wait(&s.full[ks], k_parity);
+            tc_fence_after();
+            __syncwarp();
             if (elect_one()) {
-              if (sc) scores(split ? 0 : t, vb, k);
-              if (last) mma_commit_pair(&s.empty[k]);
+              if (sc) scores(split ? 0 : t, vb, ks);
+              if (last) mma_commit_pair(&s.empty[ks]);
               if (last && ahead == steps - 1) mma_commit_pair(&s.q_empty);
             }
             __syncwarp();
           }
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (pv) p_parity ^= 1u << vb;
+          if (last) {
+            if (e >= 0) on_by_2(vs, v_parity);
+            if (ahead < steps) on_by_2(ks, k_parity);
+          }
         }
         if (!ok) break;
         sn += steps;
-        i += 2 * steps;
-        slot0 = i % SLOTS;
       }
     } else if (warp == kSched && ok) {
       // ---- the pair's share, a part of a task at a time
