@@ -17,6 +17,7 @@
 // the tensor cores work on one while the softmax works on the other; with one, S alternates
 // between two buffers. A task whose rows fill one tile of each CTA alone has the keys of
 // every second tile in the place of the other tile's rows, and joins the two.
+#include <algorithm>
 #include <climits>
 
 #include "gdn_attn.cuh"
@@ -247,11 +248,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
   if (tid == 0) {
     mbar_init(&s.q_full, 2);
     mbar_init(&s.q_empty, 1);
-    mbar_init(&s.edge, 4);
+    mbar_init(&s.edge, 2);
     mbar_init(&s.joined, 8);
     s.split_done = 0;
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&s.full[i], 8);
+      mbar_init(&s.full[i], 4);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -530,136 +531,159 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
   } else {
     fewer_regs<64>();
     if (warp < kMma) {
-      // ---- queries, keys and values: of a tile this CTA's 64 keys, and its columns of the 128 values
-      const int wl = warp - kLoad0;
-      constexpr int kK = 16, kV = 32, kVC = C::kVCols / 64;  // a warp's keys and values; their columns, by 64
+      // ---- queries and keys by two warps, values by two: of a tile this CTA's 64 keys, and its columns of the 128
+      // values. (Each warp a quarter of both took 2000 cycles a tile, one instruction after the other.)
+      const int half = warp & 1;
+      constexpr int kK = 32, kV = 64, kVC = C::kVCols / 64;  // a warp's keys and values; their columns, by 64
       constexpr uint32_t kKShare = kK * D * 2, kVShare = kV * C::kVCols * 2;
       // lanes that copy, by four rows and 64 columns, or by boxes: where blocks are made of boxes of 8 rows or
       // more, a whole tile comes as boxes (a copy of four rows takes an SM 22 cycles, a box not much more)
-      const int k4 = lane % 4, kc4 = lane / 4, v4 = lane % 8, vc4 = lane / 8;
-      const int bk = maps.box_k, bv = maps.box_v;
-      const int nk = bk ? kK / bk : 1, nv = bv ? kV / bv : 1;  // boxes of 64 columns
-      const int kb_c = lane / nk, kb_r = lane % nk * bk, vb_c = lane / nv, vb_r = lane % nv * bv;
       const uint32_t full0 = map_rank(&s.full[0], 0);
-      int i = 0;           // slots filled
-      uint32_t edges = 0;  // edge tiles so far
+      const bool of_keys = warp < kLoad0 + 2;
+      uint32_t slot = of_keys ? 0 : 1, parity = 1;  // the warp's next, and the parity of its emptying
+      int filled = 0;                               // slots, of keys and values
       const auto wait = [&](uint64_t* b, uint32_t parity) { return ok = __all_sync(0xffffffffu, mbar_wait(b, parity)); };
-      for (int n = 0; take(n); ++n) {
-        const Seg& g = s.seg[n % kSegs];
-        const int keys = g.keys, first_last = g.pos, req = g.s, j0 = g.j0, j1 = g.j1, h = g.h, toks = g.toks, row0 = g.row0;
-        const unsigned tag = g.tag;
-        const int kx = h * D, vx = D == 64 ? h * D + 32 * rank : h * D + C::kVCols * rank;
-        const auto blocks = [&](int j, KeyBlock& a, KeyBlock& b) {
-          a = key_block(p, req, j * KT + rank * 64 + wl * kK + lane % kK, keys);
-          b = key_block(p, req, j * KT + wl * kV + lane, keys);
-        };
-        KeyBlock kb, vb;
-        blocks(j0, kb, vb);
+      const auto next = [&] {
+        slot += 2;
+        if (slot >= SLOTS) slot -= SLOTS, parity ^= 1;
+        filled += 2;
+      };
+      const auto row_of = [&](const KeyBlock& b, int req) {
+        const int row = key_slot(p, b, req);
+        return row < 0 ? rows_end : row;  // past the last row: zeros
+      };
+      if (of_keys) {
+        const int b = maps.box_k, k4 = lane % 8, kc4 = lane / 8;  // by fours: which, and of which columns
+        const int nb = b ? kK / b : 1, c_b = lane / nb, r_b = lane % nb * b;
+        for (int n = 0; take(n); ++n) {
+          const Seg& g = s.seg[n % kSegs];
+          const int keys = g.keys, req = g.s, j0 = g.j0, j1 = g.j1, h = g.h, toks = g.toks, row0 = g.row0;
+          const int key0 = rank * 64 + half * kK + lane;
+          KeyBlock kb = key_block(p, req, j0 * KT + key0, keys);
 #pragma unroll 1
-        for (int j = j0; j < j1; ++j) {
-          int k_row = key_slot(p, kb, req), v_row = key_slot(p, vb, req);
-          if (k_row < 0) k_row = rows_end;  // past the last row: zeros
-          if (v_row < 0) v_row = rows_end;
-          if (j + 1 < j1) blocks(j + 1, kb, vb);
-          const bool boxes = bk && (j + 1) * KT <= keys;
-
-          // keys
-          if (!wait(&s.empty[i % SLOTS], (i / SLOTS & 1) ^ 1)) break;
-          unsigned char* to = s.ring[i % SLOTS];
-          uint32_t bar = full0 + 8 * (i % SLOTS);
-          if (lane == 0) arrive_expect_cluster(bar, kKShare);
-          __syncwarp();
-          if (boxes) {
-            const int at = __shfl_sync(0xffffffffu, k_row, kb_r);
-            if (kb_c < D / 64) tma_load_2d_pair(to + kb_c * 8192 + (wl * kK + kb_r) * 128, &maps.kb, kx + kb_c * 64, at, bar);
-          } else {
-            int at[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(0xffffffffu, k_row, k4 * 4 + e);
-            if (kc4 < D / 64) gather4_pair(to + kc4 * 8192 + (wl * kK + k4 * 4) * 128, &maps.k, kx + kc4 * 64, at, bar);
-          }
-          ++i;
-
-          if (j == j0 && wl == 0) {
-            // the task's queries, beside its first keys: whole tokens, whatever comes after the last
-            if (!wait(&s.q_empty, (n & 1) ^ 1)) break;
-            if (lane == 0) {
-              const uint32_t qbar = map_rank(&s.q_full, 0);
-              int tiles = 0;
-#pragma unroll
-              for (int t = 0; t < TILES; ++t) tiles += (2 * t + rank) * tile_toks < toks;
-              arrive_expect_cluster(qbar, tiles * D * 2 * tile_toks * G);
-#pragma unroll
-              for (int t = 0; t < TILES; ++t)
-                if ((2 * t + rank) * tile_toks < toks)
-#pragma unroll
-                  for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d_pair(s.q[t] + c * 16384, &maps.q, c * 64, h * G, row0 + (2 * t + rank) * tile_toks, qbar);
-            }
+          for (int j = j0; j < j1; ++j) {
+            const int row = row_of(kb, req);
+            if (j + 1 < j1) kb = key_block(p, req, (j + 1) * KT + key0, keys);
+            if (!wait(&s.empty[slot], parity)) break;
+            unsigned char* to = s.ring[slot] + half * kK * 128;
+            const uint32_t bar = full0 + 8 * slot;
+            if (lane == 0) arrive_expect_cluster(bar, kKShare);
             __syncwarp();
-          }
-
-          // values
-          if (!wait(&s.empty[i % SLOTS], (i / SLOTS & 1) ^ 1)) break;
-          to = s.ring[i % SLOTS];
-          bar = full0 + 8 * (i % SLOTS);
-          const bool edge = j * KT + KT - 1 > first_last && toks > 1;  // some row does not see some of these keys
-          const uint32_t to_bar = edge ? map_rank(&s.edge, rank) : bar;
-          if (lane == 0) arrive_expect_cluster(to_bar, kVShare);
-          __syncwarp();
-          if (boxes) {
-            const int at = __shfl_sync(0xffffffffu, v_row, vb_r);
-            if (vb_c < kVC) tma_load_2d_pair(to + vb_c * 16384 + (wl * kV + vb_r) * 128, &maps.vb, vx + vb_c * 64, at, to_bar);
-          } else {
-            int at[4];
+            if (b && (j + 1) * KT <= keys) {
+              const int at = __shfl_sync(0xffffffffu, row, r_b);
+              if (c_b < D / 64) tma_load_2d_pair(to + c_b * 8192 + r_b * 128, &maps.kb, h * D + c_b * 64, at, bar);
+            } else {
+              int at[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(0xffffffffu, v_row, v4 * 4 + e);
-            if (vc4 < kVC) gather4_pair(to + vc4 * 16384 + (wl * kV + v4 * 4) * 128, &maps.v, vx + vc4 * 64, at, to_bar);
-          }
-          if (edge) {
-            // 0 x NaN: values that are not finite are taken out, and the rows that do see them told
-            // by the column's first such key, in both CTAs
-            if (!wait(&s.edge, edges++ & 1)) break;
-            bool found = false;
-            constexpr int kRow = C::kVCols / 8;  // 16-byte pieces
-#pragma unroll 4
-            for (int e = lane; e < kV * kRow; e += 32) {
-              const int row = wl * kV + e / kRow, c = e % kRow;
-              const uint4 v = *reinterpret_cast<const uint4*>(to + (c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
-              // an exponent of ones, and one, is a carry into the sign's place
-              const auto not_finite = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-              found |= (not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) != 0;
+              for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(0xffffffffu, row, k4 * 4 + e);
+              if (kc4 < D / 64) gather4_pair(to + kc4 * 8192 + k4 * 512, &maps.k, h * D + kc4 * 64, at, bar);
             }
-            found = __any_sync(0xffffffffu, found);
-            if (found) {
-              constexpr int kOwn = D == 64 ? 32 : C::kVCols;
-#pragma unroll 1
-              for (int e = lane; e < kV * C::kVCols; e += 32) {
-                const int row = wl * kV + e / C::kVCols, c = e % C::kVCols;
-                uint16_t* q = reinterpret_cast<uint16_t*>(to + (c >> 6) * 16384 + row * 128 + ((((c >> 3) ^ row) & 7) << 4)) + (c & 7);
-                if ((*q & 0x7f80) == 0x7f80) {
-                  if (c < kOwn) {
-                    const unsigned word = tag << 12 | (unsigned)(4095 - (j * KT + row - first_last + 1024));
-                    for (int a = 0; a < 2; ++a) atomic_max_cluster(map_rank(&s.poison[n % kSegs][kOwn * rank + c], a), word);
-                  }
-                  *q = 0;
-                }
+            next();
+            if (j == j0 && half == 0) {
+              // the task's queries, beside its first keys: whole tokens, whatever comes after the last
+              if (!wait(&s.q_empty, (n & 1) ^ 1)) break;
+              if (lane == 0) {
+                const uint32_t qbar = map_rank(&s.q_full, 0);
+                int tiles = 0;
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) tiles += (2 * t + rank) * tile_toks < toks;
+                arrive_expect_cluster(qbar, tiles * D * 2 * tile_toks * G);
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+                  if ((2 * t + rank) * tile_toks < toks)
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                      tma_load_3d_pair(s.q[t] + c * 16384, &maps.q, c * 64, h * G, row0 + (2 * t + rank) * tile_toks, qbar);
               }
-              if (lane < 2) atomic_max_cluster(map_rank(&s.flagged[n % kSegs], lane), tag);
-              fence_proxy_async_smem();
+              __syncwarp();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(bar);
           }
-          ++i;
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
+      } else {
+        const int b = maps.box_v, v4 = lane % 16, vc4 = lane / 16;
+        const int nb = b ? kV / b : 1, c_b = lane / nb, r_b = lane % nb * b;
+        uint32_t edges = 0;  // edge tiles so far
+        for (int n = 0; take(n); ++n) {
+          const Seg& g = s.seg[n % kSegs];
+          const int keys = g.keys, first_last = g.pos, req = g.s, j0 = g.j0, j1 = g.j1, toks = g.toks;
+          const unsigned tag = g.tag;
+          const int x0 = g.h * D + (D == 64 ? 32 : C::kVCols) * rank, key0 = half * kV + lane;
+          KeyBlock lo = key_block(p, req, j0 * KT + key0, keys), hi = key_block(p, req, j0 * KT + key0 + 32, keys);
+#pragma unroll 1
+          for (int j = j0; j < j1; ++j) {
+            const int row_lo = row_of(lo, req), row_hi = row_of(hi, req);
+            if (j + 1 < j1) {
+              lo = key_block(p, req, (j + 1) * KT + key0, keys);
+              hi = key_block(p, req, (j + 1) * KT + key0 + 32, keys);
+            }
+            if (!wait(&s.empty[slot], parity)) break;
+            unsigned char* to = s.ring[slot];
+            const uint32_t bar = full0 + 8 * slot;
+            const bool edge = j * KT + KT - 1 > first_last && toks > 1;  // some row does not see some of these keys
+            const uint32_t to_bar = edge ? map_rank(&s.edge, rank) : bar;
+            if (lane == 0) arrive_expect_cluster(to_bar, kVShare);
+            __syncwarp();
+            if (b && (j + 1) * KT <= keys) {
+              const int a = __shfl_sync(0xffffffffu, row_lo, r_b & 31), c = __shfl_sync(0xffffffffu, row_hi, r_b & 31);
+              if (c_b < kVC)
+                tma_load_2d_pair(to + c_b * 16384 + (half * kV + r_b) * 128, &maps.vb, x0 + c_b * 64, r_b < 32 ? a : c, to_bar);
+            } else {
+              int at[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int from = v4 * 4 + e & 31;
+                const int a = __shfl_sync(0xffffffffu, row_lo, from), c = __shfl_sync(0xffffffffu, row_hi, from);
+                at[e] = v4 < 8 ? a : c;
+              }
+              if (vc4 < kVC) gather4_pair(to + vc4 * 16384 + half * kV * 128 + v4 * 512, &maps.v, x0 + vc4 * 64, at, to_bar);
+            }
+            if (edge) {
+              // 0 x NaN: values that are not finite are taken out, and the rows that do see them told
+              // by the column's first such key, in both CTAs
+              if (!wait(&s.edge, edges++ & 1)) break;
+              bool found = false;
+              constexpr int kRow = C::kVCols / 8;  // 16-byte pieces
+  #pragma unroll 8
+              for (int e = lane; e < kV * kRow; e += 32) {
+                const int row = half * kV + e / kRow, c = e % kRow;
+                const uint4 v = *reinterpret_cast<const uint4*>(to + (c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
+                // an exponent of ones, and one, is a carry into the sign's place
+                const auto not_finite = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                found |= (not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) != 0;
+              }
+              found = __any_sync(0xffffffffu, found);
+              if (found) {
+                constexpr int kOwn = D == 64 ? 32 : C::kVCols;
+  #pragma unroll 1
+                for (int e = lane; e < kV * C::kVCols; e += 32) {
+                  const int row = half * kV + e / C::kVCols, c = e % C::kVCols;
+                  uint16_t* q = reinterpret_cast<uint16_t*>(to + (c >> 6) * 16384 + row * 128 + ((((c >> 3) ^ row) & 7) << 4)) + (c & 7);
+                  if ((*q & 0x7f80) == 0x7f80) {
+                    if (c < kOwn) {
+                      const unsigned word = tag << 12 | (unsigned)(4095 - (j * KT + row - first_last + 1024));
+                      for (int a = 0; a < 2; ++a) atomic_max_cluster(map_rank(&s.poison[n % kSegs][kOwn * rank + c], a), word);
+                    }
+                    *q = 0;
+                  }
+                }
+                if (lane < 2) atomic_max_cluster(map_rank(&s.flagged[n % kSegs], lane), tag);
+                fence_proxy_async_smem();
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(bar);
+            }
+            next();
+          }
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
+        }
       }
       // No copy in flight when the CTA leaves: the first CTA waits for every slot that was filled. (Where a
       // wait has failed, for the last phases that were begun.)
       if (rank == 0)
-        for (int e = max(0, i - SLOTS); e < i; ++e) mbar_wait(&s.full[e % SLOTS], e / SLOTS & 1);
+        for (int e = max(0, filled - SLOTS); e < filled; ++e) mbar_wait(&s.full[e % SLOTS], e / SLOTS & 1);
     } else if (warp == kMma && rank == 0) {
       // ---- the products
       constexpr uint32_t is = idesc_bf16_f32(256, KT), io = idesc_bf16_f32(256, D) | kMnB;
@@ -828,9 +852,9 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   p.tile_g = FastDiv::of(1);
   const long long rows = (long long)p.num_blocks * p.block.d, cols = (long long)p.Hkv * D;
   // the largest power of two of rows that blocks are made of, up to a load warp's
-  for (int b = 8; b <= 32 && p.block.d % b == 0; b *= 2) {
+  for (int b = 8; b <= 64 && p.block.d % b == 0; b *= 2) {
     m.box_v = b;
-    m.box_k = b <= 16 ? b : 16;
+    m.box_k = std::min(b, 32);
   }
   if (!attn_row_map(&m.k, p.k, rows, cols, p.ldk, 1) || !attn_row_map(&m.v, p.v, rows, cols, p.ldv, 1)) return cudaErrorInvalidValue;
   if (m.box_k && (!attn_row_map(&m.kb, p.k, rows, cols, p.ldk, m.box_k) || !attn_row_map(&m.vb, p.v, rows, cols, p.ldv, m.box_v)))
