@@ -6,10 +6,17 @@
 // key/value head times the request's tokens, so every key and value is read once for all of
 // them. A tile of keys is 16 for each group of warps (one warp, or two with heads of 256); a
 // group has its own maximum, sums and outputs, its own ring of key and value rows in shared
-// memory, and waits for no other until the task's end, where the groups' outputs are added up. The rows come as boxes of 16 by TMA where blocks
-// are made of 16 slots, else, and past the last key, 16 bytes a lane. Products by mma.sync
-// (16 x 8 x 16), which leaves scores and outputs in registers; it has the time: bound by the
-// bandwidth of the keys and values.
+// memory, and waits for no other until the task's end, where the groups' outputs are added up. The rows
+// come as boxes of 16 by TMA where blocks are made of 16 slots, else, and past the last key, 16 bytes a
+// lane (64 requests over blocks of 24: 107 us for 71 of bandwidth, where boxes take four fifths of it). Products by
+// mma.sync (16 x 8 x 16), which leaves scores and outputs in registers; it has the time: the tensor cores are
+// busy for a fifth, the issue slots for a quarter.
+//
+// Bound by the bandwidth of the keys and values. Measured: 64 requests of one token over up to 8192,
+// 64 heads of 128 on 8, 926 MB, 165 us (5.6 TB/s, 82% of the measured copy); two over up to 131072, 24 heads of 256 on
+// 4, 742 MB, 128 us (5.8 TB/s, 85%; one warp a group of keys 153); one over 100000 of a shard's single key head 23, of
+// which 15 are the plan, the first rows and the joins of 150 parts, in two levels. Rows of several tiles: 20 rows a request and
+// key head over up to 6000 read everything twice, 125 us; as a tile of the tensor cores 81.
 #include <climits>
 
 #include "gdn_attn.cuh"

@@ -17,6 +17,13 @@
 // the tensor cores work on one while the softmax works on the other; with one, S alternates
 // between two buffers. A task whose rows fill one tile of each CTA alone has the keys of
 // every second tile in the place of the other tile's rows, and joins the two.
+//
+// Measured: chunks of 2048 tokens in all of two requests over up to 30000, 24 heads of 256 on 4, 757 - 795 us (1.6 - 1.7
+// PFLOP/s, 84 - 88% of the measured rate; one CTA by itself, keys and values for 128 rows, 1460): the tensor cores. 8192 fresh
+// tokens of 5 requests, 64 heads of 128 on 8, 275 us (64%): a turn's products take 1080 cycles, but the chain S, softmax, PV of
+// a row tile 3900, in which two turns run, as S and O fill TMEM. 24 requests of 4 tokens over up to 6000, 40 heads of
+// 128 on 8, 81 us (51% of the bandwidth): 20 of a tile's 128 rows are there, each tile of keys is a turn all
+// the same, and a task has 8 us of queries, first tile and join.
 #include <algorithm>
 #include <climits>
 
