@@ -22,10 +22,11 @@
 // for the SMs all the same (up to two a SM): 33 rows of 1037 x 1056 8.2 us with 32 at a time, 5.6 with 16. 64 at a
 // time leave too few registers: 64 rows of 8192 x 8192 77 us, 58 with two passes.
 //
-// Measured, codes and scales as bytes: 8 rows of 20480 x 8192 MXFP4 37.6 us (2.4 TB/s), 2560 x 8192 MXFP4, one
-// row 10.4, whole numbers 8.4: a SM's warps issue an instruction every other cycle, 49 for 512 weights (unpack 22,
-// the scales 8, loads and addresses 12), and 160 groups of rows are two for a CTA, which leaves 72 SMs idle.
+// Measured, codes and scales as bytes: 8 rows of 20480 x 8192 whole numbers 25.0 us (3.5 TB/s), MXFP4 35.2; 2560 x 8192,
+// one row, MXFP4 9.7, whole numbers 8.2: a SM's warps issue an instruction every other cycle, 45 for 512 weights (unpack 22,
+// the scales 8, loads and addresses 8), and 160 groups of rows are two for a CTA, which leaves 72 SMs idle.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_host.h"
 #include "gdn_prefill.cuh"
@@ -160,8 +161,8 @@ __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params 
   for (int i = 0; i < kAhead; ++i) scale_in(s0 / kQuad * kQuads + i, sc[i]);
 
   float acc[MT][4] = {};
-#pragma unroll 1
-  for (int st = s0; st < s1; ++st) {
+  // full: all its columns are there
+  const auto stage = [&](int st, auto full) {
     codes_in(st + kStages - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params 
       uint4 y[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        y[mt] = make_uint4(0, 0, 0, 0);
-        if (mt * 8 < M && k0 + q * 32 < p.K)
+        if (!full) y[mt] = make_uint4(0, 0, 0, 0);
+        if (full || (mt * 8 < M && k0 + q * 32 < p.K))
           y[mt] = __ldg(reinterpret_cast<const uint4*>(p.x + (long long)(m0 + min(mt * 8 + g, M - 1)) * p.ldx + k0 + q * 32));
       }
       const int at = (q ^ g) << 4;
@@ -230,7 +231,16 @@ __global__ void __launch_bounds__(32 * warps<MT>(), 1) linear_w4(const W4Params 
       for (int i = kAhead - kQuads; i < kAhead; ++i) scale_in((st + 1) / kQuad * kQuads + i, sc[i]);
     }
     __syncwarp();
-  }
+  };
+  // With 32 rows a test before each load pays: without one they are all asked for at once, and the registers that
+  // they come to are missing elsewhere (64 rows of 8192 x 8192 58 us, 86 without). With fewer it costs 5 to 8%.
+  const int whole = MT <= 2 ? min(s1, p.K / kStep) : s0;
+  int st = s0;
+  if (MT <= 2)
+#pragma unroll 1
+    for (; st < whole; ++st) stage(st, std::true_type());
+#pragma unroll 1
+  for (; st < s1; ++st) stage(st, std::false_type());
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 

@@ -54,7 +54,7 @@ def test_epilogue(act, bias, residual):
 
 
 def test_wide():
-    """Columns enough that a CTA has several pieces of x in shared memory, one after the other."""
+    """Columns enough that a CTA has many groups of them and few shares of the inner size."""
     case(4, 20000, 2304, 128, 1, zeros=True)
     case(30, 6000, 2304, 32, 2)
 
@@ -121,3 +121,11 @@ def test_residual_in_place_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, base)
+
+
+@pytest.mark.parametrize("group", ["mx", 32, 128])
+@pytest.mark.parametrize("M,N,K", [(12, 2500, 1408), (16, 5000, 256), (20, 4000, 640), (33, 2500, 1152), (64, 4900, 384),
+                                   (1, 30000, 512), (40, 5000, 128)])
+def test_passes(group, M, N, K):
+    """Enough columns that rows are taken 16 or 32 at a time, and CTAs have several groups of them."""
+    case(M, N, K, group, M + K, zeros=True)
