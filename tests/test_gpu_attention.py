@@ -307,3 +307,20 @@ def test_append_bad_slot():
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_append_frequencies(turn, far, interleaved):
     append_case((4, 2), 64, 64, 50, 16, 77, norms=True, interleaved=interleaved, far=far, turn=turn)
+
+
+def test_append_on_a_stream():
+    from gated_deltanet_layer_gb300 import kv_append
+    rng = np.random.default_rng(4)
+    q, k, v = (H.bf16(rng.standard_normal((9, c))).cuda() for c in (512, 128, 128))
+    pos, slots = H.ints(np.arange(9)), H.ints(np.arange(9)[::-1].copy(), np.int64)
+    freq = torch.full((32,), 0.5, device="cuda")
+    outs = []
+    for st in (None, torch.cuda.Stream()):
+        kc, vc = torch.zeros(10, 1, 128, dtype=torch.bfloat16, device="cuda"), torch.ones(10, 1, 128, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        out = kv_append(q, k, v, pos, slots, freq, kc, vc, interleaved=True, stream=st)
+        torch.cuda.synchronize()
+        outs.append((out, kc, vc))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[0][0].shape == q.shape
+    assert kv_append(None, k, v, pos, slots, freq, *outs[0][1:]) is None
