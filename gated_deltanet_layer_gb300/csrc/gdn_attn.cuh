@@ -4,7 +4,7 @@
 // A task is (request, key/value head, tile of query rows). A tile is M of the request's n G rows, of
 // which row r is token r / G, query head r % G of the head's G = Hq / Hkv; or, with G = 1, M tokens
 // with all their heads. A task's
-// units are the tiles of KT keys that its last row sees, and E more for what a task
+// units are the tiles of KT keys that its last row sees, and tile_e more for what a task
 // takes beside its tiles (they come last, and nobody does anything in them). All tasks' units form one line, in
 // the order request, head, row tile, key tile, and every CTA takes an equal, contiguous
 // share of it, whatever the lengths: a CTA has whole tasks, and at its two ends
@@ -43,6 +43,7 @@ struct AttnParams {
   FastDiv block;     // slots of a block
   FastDiv group;     // query heads of a key/value head
   int tile_m;        // M and G of the tasks' tiles
+  int tile_e;        // units that a task takes beside its tiles
   FastDiv tile_g;
   int Hkv;
   const __nv_bfloat16* q;
@@ -98,7 +99,7 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 // Row tiles of a request and their key tiles. Tile i's last row is min((i + 1) M, n G) - 1, so
 // all but the last tile see ctx + ceil((i + 1) M / G) keys, which are
 // ceil((G ctx + (i + 1) M) / (G KT)) tiles.
-template <int KT, int E>
+template <int KT>
 struct Tiles {
   __device__ __forceinline__ static int rows(const AttnParams& p, int n) { return (n * (int)p.tile_g.d + p.tile_m - 1) / p.tile_m; }
   __device__ __forceinline__ static int keys(const AttnParams& p, int n, int ctx, int i) {
@@ -109,11 +110,11 @@ struct Tiles {
   __device__ __forceinline__ static long long before(const AttnParams& p, int ctx, int i) {
     if (i == 0) return 0;
     const long long G = p.tile_g.d, m = G * KT;
-    return floor_sum(i, m, p.tile_m, G * ctx + p.tile_m + m - 1) + (long long)i * E;
+    return floor_sum(i, m, p.tile_m, G * ctx + p.tile_m + m - 1) + (long long)i * p.tile_e;
   }
   __device__ __forceinline__ static long long total(const AttnParams& p, int n, int ctx) {
     const int t = rows(p, n);
-    return before(p, ctx, t - 1) + keys(p, n, ctx, t - 1) + E;
+    return before(p, ctx, t - 1) + keys(p, n, ctx, t - 1) + p.tile_e;
   }
 };
 
@@ -127,7 +128,7 @@ struct PlanScratch {
 // before request s, seq[seqs].x the first pad row and start[seqs] all units. The offsets are the
 // caller's: row ends are the running maximum of the offsets that lie within the rows, and
 // a request whose offsets are not its row ends is padding. A block of NT threads.
-template <int KT, int E, int NT>
+template <int KT, int NT>
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long long* start, PlanScratch<NT>& x, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int top = 0;
@@ -161,7 +162,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long l
       if (far) attn_record(p.error, kAttnContext, s);
     }
     if (long_ || far) n = 0;
-    const long long mine = n > 0 ? p.Hkv * Tiles<KT, E>::total(p, n, c) : 0;
+    const long long mine = n > 0 ? p.Hkv * Tiles<KT>::total(p, n, c) : 0;
     long long u = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -205,7 +206,7 @@ struct Shares {
 };
 
 // A walk over the units, task by task.
-template <int KT, int E>
+template <int KT>
 struct Walk {
   const AttnParams& p;
   const int4* seq;
@@ -221,7 +222,7 @@ struct Walk {
     row0 = q.x;
     n = q.y;
     ctx = q.z;
-    rows = Tiles<KT, E>::rows(p, n);
+    rows = Tiles<KT>::rows(p, n);
   }
   // Where unit u, one of start[seqs], is: at = {s, h, i, j}. A converged warp.
   __device__ __forceinline__ static void find(const AttnParams& p, const int4* seq, const long long* start, long long u, int (&at)[4]) {
@@ -245,8 +246,8 @@ struct Walk {
     const long long first = start[s], per = (start[s + 1] - first) / p.Hkv;
     const int h = (int)((u - first) / per);
     const long long in = u - first - h * per;
-    const int i = last_of(Tiles<KT, E>::rows(p, q.y), [&](int k) { return Tiles<KT, E>::before(p, q.z, k) <= in; });
-    if (lane == 0) at[0] = s, at[1] = h, at[2] = i, at[3] = (int)(in - Tiles<KT, E>::before(p, q.z, i));
+    const int i = last_of(Tiles<KT>::rows(p, q.y), [&](int k) { return Tiles<KT>::before(p, q.z, k) <= in; });
+    if (lane == 0) at[0] = s, at[1] = h, at[2] = i, at[3] = (int)(in - Tiles<KT>::before(p, q.z, i));
   }
   __device__ __forceinline__ void from(const int (&at)[4], long long u) {
     s = at[0];
@@ -254,11 +255,11 @@ struct Walk {
     h = at[1];
     i = at[2];
     j = at[3];
-    nt = Tiles<KT, E>::keys(p, n, ctx, i);
+    nt = Tiles<KT>::keys(p, n, ctx, i);
     task = u - j;
   }
   __device__ __forceinline__ void next_task() {
-    task += nt + E;
+    task += nt + p.tile_e;
     j = 0;
     if (++i == rows) {
       i = 0;
@@ -270,7 +271,7 @@ struct Walk {
         load();
       }
     }
-    nt = Tiles<KT, E>::keys(p, n, ctx, i);
+    nt = Tiles<KT>::keys(p, n, ctx, i);
   }
 };
 

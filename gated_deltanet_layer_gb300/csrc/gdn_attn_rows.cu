@@ -16,7 +16,7 @@
 // 64 heads of 128 on 8, 926 MB, 165 us (5.6 TB/s, 82% of the measured copy); two over up to 131072, 24 heads of 256 on
 // 4, 742 MB, 128 us (5.8 TB/s, 85%; one warp a group of keys 153); one over 100000 of a shard's single key head 23, of
 // which 15 are the plan, the first rows and the joins of 150 parts, in two levels. Rows of several tiles: 20 rows a request and
-// key head over up to 6000 read everything twice, 125 us; as a tile of the tensor cores 81.
+// key head over up to 6000 read everything twice, 125 us; as a tile of the tensor cores 73.
 #include <climits>
 
 #include "gdn_attn.cuh"
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
     seq = p.seq;
     start = p.start;
   } else {
-    attn_plan<KT, 0, NT>(p, s.seq, s.start, s.scan, blockIdx.x == 0);
+    attn_plan<KT, NT>(p, s.seq, s.start, s.scan, blockIdx.x == 0);
   }
   attn_zero_rows<W>(p, seq, p.Hkv * p.group.d * D);
   const long long units = start[p.seqs];
@@ -159,11 +159,11 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
   const long long u0 = shares.first(blockIdx.x), u1 = shares.first(blockIdx.x + 1);
   const int steps = (int)(u1 - u0);
 
-  if (warp == 0) Walk<KT, 0>::find(p, seq, start, u0, s.at);
+  if (warp == 0) Walk<KT>::find(p, seq, start, u0, s.at);
   __syncthreads();
 
   // The ring's loads: lanes 0 - 15 know the slots of the warp's 16 keys, a step ahead.
-  Walk<KT, 0> ahead(p, seq, start);
+  Walk<KT> ahead(p, seq, start);
   ahead.from(s.at, u0);
   const uint32_t ring = smem_u32(s.ring[grp]);
   const int rows_end = p.num_blocks * (int)p.block.d;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
   // beside its first step's rows; there is room for no more, so a task of fewer steps than are ahead
   // leaves the one after it to ask for its own.
   int seen = 0, asked = 0, begun = 0;  // tasks: come across by the loads, whose queries are asked for, begun
-  const auto queries = [&](const Walk<KT, 0>& x) {
+  const auto queries = [&](const Walk<KT>& x) {
     const uint32_t to = smem_u32(s.q[asked++ & 1]);
     const int rows = x.n * (int)p.group.d;
 #pragma unroll 2
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) issue();
 
-  Walk<KT, 0> w(p, seq, start);
+  Walk<KT> w(p, seq, start);
   w.from(s.at, u0);
   float o[C::kCols / 8][4], m[2], l[2];
   int last_key[2], first_last = 0;  // last key that the thread's rows see; the task's first row's
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
   __shared__ PlanScratch<1024> x;
   griddep_wait();
   griddep_launch_dependents();
-  attn_plan<Rows<D>::kKT, 0, 1024>(p, p.seq, p.start, x, true);
+  attn_plan<Rows<D>::kKT, 1024>(p, p.seq, p.start, x, true);
 }
 
 template <int D>

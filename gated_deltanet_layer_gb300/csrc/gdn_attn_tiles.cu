@@ -22,7 +22,7 @@
 // PFLOP/s, 84 - 88% of the measured rate; one CTA by itself, keys and values for 128 rows, 1460): the tensor cores. 8192 fresh
 // tokens of 5 requests, 64 heads of 128 on 8, 275 us (64%): a turn's products take 1080 cycles, but the chain S, softmax, PV of
 // a row tile 3900, in which two turns run, as S and O fill TMEM. 24 requests of 4 tokens over up to 6000, 40 heads of
-// 128 on 8, 81 us (51% of the bandwidth): 20 of a tile's 128 rows are there, each tile of keys is a turn all
+// 128 on 8, 73 us (57% of the bandwidth): 20 of a tile's 128 rows are there, each tile of keys is a turn all
 // the same, and a task has 8 us of queries, first tile and join.
 #include <algorithm>
 #include <climits>
@@ -51,7 +51,6 @@ struct Cfg {
   static constexpr int kVCols = D == 256 ? 128 : 64;       // a CTA's columns of the values (heads of 64: 32, and 32 for nothing)
   static constexpr int kSlotBytes = D == 256 ? 32768 : 16384;  // 64 keys, or kVCols columns of 128 values
   static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 9 : 4;
-  static constexpr int kE = D == 256 ? 3 : 3;              // tiles' time that a task takes beside its tiles
   static constexpr int kO = 256;                           // TMEM column of O; S of the two row tiles, or S's two buffers, before it
 };
 
@@ -289,14 +288,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     plan = p.seq;
     start = p.start;
   } else {
-    attn_plan<KT, C::kE, kNT>(p, s.plan, s.start, s.scan, blockIdx.x == 0);
+    attn_plan<KT, kNT>(p, s.plan, s.start, s.scan, blockIdx.x == 0);
   }
   attn_zero_rows<kNT / 32>(p, plan, p.Hkv * p.group.d * D);
   const long long units = start[p.seqs];
-  const Shares shares(units, (int)max(1LL, min((long long)pairs, (units + C::kE + 1) / (C::kE + 2))));
+  const Shares shares(units, (int)max(1LL, min((long long)pairs, (units + p.tile_e + 1) / (p.tile_e + 2))));
   const bool on = units > 0 && pair < shares.ctas;
   const long long u0 = shares.first(pair), u1 = shares.first(pair + 1);
-  if (warp == kSched && on) Walk<KT, C::kE>::find(p, plan, start, u0, s.at);
+  if (warp == kSched && on) Walk<KT>::find(p, plan, start, u0, s.at);
   __syncthreads();
   cluster_sync();
   tc_fence_before();
@@ -774,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
       }
     } else if (warp == kSched && ok) {
       // ---- the pair's share, a part of a task at a time
-      Walk<KT, C::kE> w(p, plan, start);
+      Walk<KT> w(p, plan, start);
       w.from(s.at, u0);
       long long u = u0;
       int j0 = w.j, n = 0;
@@ -783,7 +782,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
       while (true) {
         // what the share begins with of a task, or ends with, may have no tiles
         while (more && j0 >= w.nt) {
-          u = w.task + w.nt + C::kE;
+          u = w.task + w.nt + p.tile_e;
           more = u < u1;
           if (more) w.next_task();
           j0 = 0;
@@ -844,7 +843,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p) {
   __shared__ PlanScratch<1024> x;
   griddep_wait();
   griddep_launch_dependents();
-  attn_plan<KT, Cfg<D>::kE, 1024>(p, p.seq, p.start, x, true);
+  attn_plan<KT, 1024>(p, p.seq, p.start, x, true);
 }
 
 template <int D>
@@ -856,6 +855,10 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   const int G = p.group.d;
   m.tokens = 128 / G;
   p.tile_m = Cfg<D>::kRows / 128 * m.tokens;
+  // A task's own time (queries, first tile, join) in tiles of keys. More where all tasks have their keys split between
+  // the row tiles, as a tile is one turn there and not two: 24 requests of 4 tokens over up to 6000, heads of
+  // 128, 82 us with 3, 75 with 6, 72 with 8; fresh prompts 276 with 3, 286 with 4, 297 with 5.
+  p.tile_e = Cfg<D>::kTiles == 2 && p.max_len <= 2 * m.tokens ? 8 : 3;
   p.tile_g = FastDiv::of(1);
   const long long rows = (long long)p.num_blocks * p.block.d, cols = (long long)p.Hkv * D;
   // the largest power of two of rows that blocks are made of, up to a load warp's
