@@ -12,6 +12,7 @@
 // the CTA that finishes last joins them, in order.
 #pragma once
 
+#include "gdn_attn_shares.h"
 #include "gdn_common.cuh"
 
 namespace gdn {
@@ -189,21 +190,6 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int4* seq, long l
   }
   __syncthreads();
 }
-
-// The CTAs' shares of the units.
-struct Shares {
-  long long each, more, units;  // the first `more` CTAs have one unit more
-  int ctas;
-  __device__ __forceinline__ Shares(long long units, int ctas) : units(units), ctas(ctas) {
-    each = units / ctas;
-    more = units - each * ctas;
-  }
-  __device__ __forceinline__ long long first(int c) const { return c * each + min((long long)c, more); }
-  __device__ __forceinline__ int owner(long long u) const {
-    const long long wide = more * (each + 1);
-    return u < wide ? (int)(u / (each + 1)) : (int)(more + (u - wide) / each);
-  }
-};
 
 // A walk over the units, task by task.
 template <int KT>

@@ -418,17 +418,15 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
     if (!whole) {
       if (tid < live) p.part_ml[slot * kM + tid] = s.row_ml[tid];
       // The parts: slot 1 of the first CTA, slot 0 of the others (a CTA's part is its second one
-      // where the task begins in it). Who finishes last of a group of about sqrt(parts) joins the group's
-      // into its first one, and the last of those all groups': no CTA has many to read.
-      const int c0 = shares.owner(t0), c1 = shares.owner(t1 - 1), parts = c1 - c0 + 1;
-      const int size = parts <= 16 ? parts : (int)ceilf(sqrtf((float)parts)), groups = (parts + size - 1) / size;
+      // where the task begins in it), counted and joined as Join has it.
+      const Join join(shares.owner(t0), shares.owner(t1 - 1));
+      const int c0 = join.c0;
       const auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0); };
-      const int mine = ((int)blockIdx.x - c0) / size;
+      const int mine = join.group(blockIdx.x);
 #pragma unroll 1
-      for (int level = groups > 1 ? 0 : 1; level < 2; ++level) {
-        const int b = level == 0 ? mine * size : 0, by = level == 0 || groups == 1 ? 1 : size;
-        const int count = level == 0 ? min(size, parts - b) : groups == 1 ? parts : groups;
-        unsigned* done = p.done + (level == 0 ? gridDim.x + c0 + b : c0);
+      for (int level = join.first_level(); level < 2; ++level) {
+        const int b = join.begin(level, mine), by = join.step(level), count = join.count(level, mine);
+        unsigned* done = p.done + join.word(level, mine, gridDim.x);
         __syncthreads();
         if (tid == 0) s.last = atom_add_acq_rel_u32(done, 1u) == (unsigned)(count - 1);
         __syncthreads();
