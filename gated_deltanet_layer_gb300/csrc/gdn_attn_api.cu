@@ -1,6 +1,7 @@
 // Host side of the C ABI in include/gdn_attention.h: config validation,
 // argument checks and launches.
 #include <algorithm>
+#include <cmath>
 #include <new>
 
 #include "gdn_attention.h"
@@ -37,12 +38,14 @@ struct Layout {
   }
 };
 
+float scale_log2(const gdn_attn_config& c) { return (float)((double)c.scale * 1.4426950408889634); }
+
 gdn_status validate(const gdn_attn_config* c) {
   if (!c) return GDN_ERR_ARG;
   if (c->num_q_heads <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0 || c->block_size <= 0 || c->max_tokens < 1 ||
       c->max_seqs < 1)
     return GDN_ERR_ARG;
-  if (!(c->scale == c->scale)) return GDN_ERR_ARG;
+  if (!std::isfinite(scale_log2(*c))) return GDN_ERR_ARG;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return GDN_ERR_UNSUPPORTED;
   if (c->num_q_heads % c->num_kv_heads != 0 || c->num_q_heads > 1024) return GDN_ERR_UNSUPPORTED;
   if (c->max_tokens > (1 << 24) || c->max_seqs > 65535) return GDN_ERR_UNSUPPORTED;
@@ -162,7 +165,7 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ldo = ldo;
   p.wide_out = aligned(out, 32) && ldo % 16 == 0;
-  p.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2(c);
   p.error = reinterpret_cast<unsigned int*>(h->ws);
   p.done = reinterpret_cast<unsigned int*>(h->ws + l.done);
   p.part = reinterpret_cast<float*>(h->ws + l.part);
@@ -172,8 +175,9 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
     p.start = reinterpret_cast<long long*>(h->ws + l.start);
   }
   // Rows of a request and key/value head: a tile of 16 has them all, or the tensor cores' tiles (which
-  // hold a token's heads together, and need a cache to map).
-  const bool few = (long long)p.max_len * p.group.d <= 16 || p.group.d > 128 || num_blocks == 0;
+  // hold a token's heads together, and need a cache to map). These take a row's maximum and hide keys before they scale,
+  // which is right for scales above zero alone; the few rows' form scales first.
+  const bool few = (long long)p.max_len * p.group.d <= 16 || p.group.d > 128 || num_blocks == 0 || !(p.scale_log2 > 0.f);
   return cuda_status((few ? launch_attn_rows : launch_attn_tiles)(p, c.head_dim, h->grid, (cudaStream_t)stream));
 }
 

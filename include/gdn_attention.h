@@ -68,7 +68,7 @@ typedef struct {
   int32_t block_size;    /* slots of a block, any number >= 1 */
   int32_t max_tokens;    /* most rows of one call */
   int32_t max_seqs;      /* most requests of one call */
-  float scale;           /* multiplies q . k */
+  float scale;           /* multiplies q . k; any finite number (chunks take longer with one of 0 or below) */
 } gdn_attn_config;
 
 typedef struct gdn_attn gdn_attn_t;

@@ -169,3 +169,16 @@ def test_calls_from_python_refused(lib):
         linear_w4(x, f, f, activation="relu")
     with pytest.raises(TypeError):
         _native.calls().linear_w4(None, x)
+
+
+@pytest.mark.parametrize("scale", [float("inf"), -float("inf"), 3e38])
+def test_scale_that_is_not_finite_refused(lib, scale):
+    """3e38 is not, once it has taken up the logarithm's base."""
+    c, h = config(scale=scale), ctypes.c_void_p()
+    assert lib.gdn_attn_workspace_bytes(ctypes.byref(c)) == 0
+    assert lib.gdn_attn_create(ctypes.byref(c), 4096, 1 << 40, None, ctypes.byref(h)) == ARG
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, -3e37, 1e-45])
+def test_finite_scales_taken(lib, scale):
+    assert lib.gdn_attn_workspace_bytes(ctypes.byref(config(scale=scale))) > 0
