@@ -110,7 +110,7 @@ constexpr uint32_t kMnB = 1u << 16;  // idesc: B is N-major
 
 // On a barrier of either CTA (its cluster address). Not releases at cluster scope: those wait for all that the
 // thread has written, a thousand cycles with each tile; what these two tell of is in TMEM, behind
-// tcgen05's own fences, or on its way by TMA, or has been read.
+// tcgen05's own fences, or on its way by TMA.
 __device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -423,7 +423,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         const int g_row0 = g.row0, g_h = g.h;
         const unsigned tag = g.tag;
         const unsigned* poison = s.poison[n % kSegs];
-        const bool flagged = any && s.flagged[n % kSegs] == tag;
+        const bool flagged = __any_sync(0xffffffffu, any && s.flagged[n % kSegs] == tag);
+        // The segment's entry and flags are free once both CTAs' softmax has read them: this CTA writes the next one's entry
+        // over them, either its flags. Where there are no flags the other CTA need not wait for a read, as whatever
+        // it writes is not this tag; a release at cluster scope costs half a microsecond a segment.
+        if (!flagged) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.seg_empty[n % kSegs]);
+          if (lane == 1) arrive_cluster(map_rank(&s.seg_empty[n % kSegs], rank ^ 1));
+        }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (warp_live) {
 #pragma unroll 1
@@ -454,9 +462,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           }
           if (!whole && live) p.part_ml[part_row + r] = make_float2(m, l);
         }
-        // the segment's entry and flags are free once both CTAs' softmax has read them
-        __syncwarp();
-        if (lane < 2) arrive_cluster(map_rank(&s.seg_empty[n % kSegs], lane));
+        if (flagged) {
+          __syncwarp();
+          if (lane < 2) mbar_arrive_cluster(map_rank(&s.seg_empty[n % kSegs], lane));
+        }
         if (!whole && first < toks) {
           // A task that is the pair's alone, and split, is counted here: the counter in memory is that of the task
           // that other pairs go on with, who may be there long before this one.
@@ -787,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           if (more) w.next_task();
           j0 = 0;
         }
-        ok = mbar_wait(&s.seg_empty[n % kSegs], (n / kSegs & 1) ^ 1);
+        ok = mbar_wait_cluster(&s.seg_empty[n % kSegs], (n / kSegs & 1) ^ 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {

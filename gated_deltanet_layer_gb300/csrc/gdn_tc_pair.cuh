@@ -23,6 +23,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return ok;
 }
 
+// The same where threads of either CTA of a pair have arrived (release at cluster scope): what they had read and
+// written before comes before what follows here.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  const auto passed = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  const unsigned long long t0 = globaltimer_ns();
+  bool ok;
+#pragma unroll 1
+  do {
+    ok = passed();
+  } while (!ok && globaltimer_ns() - t0 < kWaitNs);
+  return ok;
+}
+
 // One lane of a converged warp. What it issues under such a branch has its operands in
 // uniform registers; under a test of the lane's number each tcgen05.mma took twice the
 // time to issue.

@@ -1,5 +1,6 @@
 """Paged attention where neighbouring tasks are each shared by more CTAs than are joined at once, on
 the GPU, against a 64-bit implementation."""
+import numpy as np
 import pytest
 import torch
 
@@ -42,3 +43,30 @@ def test_long_neighbours(heads, d, block, requests):
     assert all(torch.equal(o, outs[0]) for o in outs[1:])
     short = H.Pages(heads, d, block, [(40 + i, 1) for i in range(len(requests))], seed=5)
     H.check(short.call(h), *short.reference())
+
+
+@pytest.mark.parametrize("heads,d,requests", [((16, 4), 64, [(60 * i, 150 + 7 * i) for i in range(10)]),
+                                              ((12, 6), 128, [(200 - 20 * i, 90 + 31 * i) for i in range(8)]),
+                                              ((20, 4), 128, [(500 + 90 * i, 4) for i in range(16)]),
+                                              ((24, 4), 256, [(30 * i, 40 + 13 * i) for i in range(10)])])
+def test_hidden_values_in_many_parts(heads, d, requests):
+    """Values that are not finite and that later tokens alone see, in about half of many parts of tasks, one right after the
+    other in each pair of CTAs: no part has another's."""
+    p = H.Pages(heads, d, 16, requests, seed=d)
+    rng = np.random.default_rng(d)
+    for s in range(p.S):
+        at, n = p.slots(s), int(p.new[s])
+        for head in range(p.Hkv):
+            for row in rng.integers(1, n, 2):
+                if rng.random() < 0.5:
+                    p.v[int(at[len(at) - int(row)]), head, int(rng.integers(0, d))] = float(rng.choice([np.nan, np.inf, -np.inf]))
+    want, tol = p.reference()
+    ok = np.isfinite(want)
+    assert ok.any() and not ok.all()
+    h = p.handle()
+    outs = [p.call(h) for _ in range(12)]
+    assert h.check() == (0, 0)
+    got = H.f64(outs[0])
+    assert not np.isfinite(got[~ok]).any()
+    assert np.isfinite(got[ok]).all() and (np.abs(got[ok] - want[ok]) <= tol[ok]).all()
+    assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs[1:])
