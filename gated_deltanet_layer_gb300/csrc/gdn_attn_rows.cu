@@ -154,8 +154,9 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
   }
   attn_zero_rows<W>(p, seq, p.Hkv * p.group.d * D);
   const long long units = start[p.seqs];
+  if (units == 0) return;
   const Shares shares(units, (int)min((long long)gridDim.x, (units + 1) / 2));
-  if (units == 0 || blockIdx.x >= shares.ctas) return;
+  if (blockIdx.x >= shares.ctas) return;
   const long long u0 = shares.first(blockIdx.x), u1 = shares.first(blockIdx.x + 1);
   const int steps = (int)(u1 - u0);
 
