@@ -358,6 +358,8 @@ __global__ void __launch_bounds__(Rows<D>::kW * 32, 1) attn_rows(const __grid_co
     }
 
     // ---- the task's end, or this CTA's: the warps' sums added up
+    // its last keys are where copies by lanes stand among boxes, and a box may come next in their place
+    if (maps.boxes) fence_proxy_async_smem();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);

@@ -21,3 +21,16 @@ def test_pad_rows_alone(requests, max_len):
         out = h.attend(q, kv, kv.clone(), ints(requests, 4), ints(requests + 1), ints(requests), max_len=max_len)
         assert (out == 0).all()
     assert h.check() == (0, 0)
+
+
+@pytest.mark.parametrize("heads,d,block", [((8, 2), 64, 16), ((8, 2), 128, 32), ((12, 3), 256, 16)])
+def test_pieces_and_boxes_in_turn(heads, d, block):
+    """Many short requests a CTA, whose last keys come in pieces and the others in boxes: each place of the ring has both in
+    turn. Every call has the first one's bits."""
+    rng = np.random.default_rng(d)
+    p = H.Pages(heads, d, block, [(int(c), 1) for c in rng.integers(0, 700, 400)], seed=d)
+    h = p.handle()
+    outs = [p.call(h) for _ in range(10)]
+    assert h.check() == (0, 0)
+    H.check(outs[0], *p.reference())
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
