@@ -59,6 +59,7 @@ struct AttnParams {
   long long ldo;
   bool wide_out;              // rows of out are 32-byte aligned
   float scale_log2;           // scale times log2(e)
+  float scale_pow2;           // the largest power of two that is not above it
   unsigned int* error;        // sticky word
   unsigned int* done;         // [2 grid] parts finished of the tasks whose first part is a CTA's; zero between calls
   float* part;                // [2 grid] sums of weights times values, M rows of D, relative to the part's maximum

@@ -166,6 +166,7 @@ extern "C" gdn_status gdn_attn_paged(gdn_attn_t* h, int32_t seqs, int32_t tokens
   p.ldo = ldo;
   p.wide_out = aligned(out, 32) && ldo % 16 == 0;
   p.scale_log2 = scale_log2(c);
+  p.scale_pow2 = p.scale_log2 > 0.f ? std::ldexp(1.f, std::ilogb(p.scale_log2)) : 0.f;
   p.error = reinterpret_cast<unsigned int*>(h->ws);
   p.done = reinterpret_cast<unsigned int*>(h->ws + l.done);
   p.part = reinterpret_cast<float*>(h->ws + l.part);

@@ -329,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         const int first = ((split ? 0 : 2 * t) + rank) * tile_toks, tok = first + r_tok;  // the tile's first token, the row's
         const bool live = in_tile && tok < toks, warp_live = warp_in_tile && first + warp_tok < toks;
         const int last_key = pos + min(tok, toks - 1);
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, by1 = p.scale_log2, less1 = 0.f;  // weights are 2^(x by1 + less1)
 #pragma unroll 1
         for (int j = j0; j < end; j += step, ++sn) {
           const int b = TILES == 2 ? t : sn & 1;
@@ -355,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
               for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[c + i], x[c + 4 + i]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[KT - 4 + i]);
-            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+            const float largest = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), tile_top = largest * p.scale_log2;
             // rows that are none have what was in their place: their maxima correct nothing
             if (__any_sync(0xffffffffu, live && (tile_top > m + kSlack || m == -INFINITY))) {
               const float grown = fmaxf(m, tile_top), f = m == -INFINITY ? 0.f : ex2(m - grown);
@@ -380,10 +380,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
                 }
               }
               l *= f;
+              // x scale - m in one rounding is off by what m was rounded by: a factor of all weights, which their sum has too, but
+              // from scores of 2^31 on one that passes f32's range. There the next smaller score is at least 64 below, and
+              // a power of two for the scale, which rounds nothing, tells the largest one from all others as well.
+              if (tile_top > m) {
+                const bool far = fabsf(tile_top) >= 0x1p30f;
+                by1 = far ? p.scale_pow2 : p.scale_log2;
+                less1 = far ? -(largest * by1) - (tile_top - tile_top) : -tile_top;
+              }
               m = grown;
             }
-            const float base = m == -INFINITY ? 0.f : m;
-            const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-base, -base);
+            const float2 by = make_float2(by1, by1), less = make_float2(less1, less1);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < KT; c += 64) {

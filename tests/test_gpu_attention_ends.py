@@ -34,3 +34,36 @@ def test_pieces_and_boxes_in_turn(heads, d, block):
     assert h.check() == (0, 0)
     H.check(outs[0], *p.reference())
     assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [16, 33, 60, 100])
+@pytest.mark.parametrize("heads,d,requests", [((8, 2), 64, [(130, 1), (700, 1)]), ((8, 2), 64, [(100, 60), (0, 130)]),
+                                              ((8, 2), 128, [(100, 60), (0, 130)]), ((10, 2), 128, [(900, 5), (33, 5)]),
+                                              ((6, 1), 256, [(300, 1), (600, 2)]), ((6, 1), 256, [(70, 90), (300, 20)])])
+def test_scores_of_any_size(heads, d, requests, size, sign):
+    """Scores of 2^size times a whole number from 1 to 100, or of minus that, times the scale: the largest one's keys have all the
+    weight, in equal parts. They are exact in f32 but for the scale's rounding, which equal ones have alike, and what is
+    between two of them leaves the smaller no weight; so a row's error is the roundings of weights (1, or what the sum
+    divides out again) and of the output, and the sums'."""
+    p = H.Pages(heads, d, 16, requests, seed=d + size)
+    rng = np.random.default_rng(size)
+    q = np.zeros((p.T, p.Hq, d))
+    q[:, :, 1] = 2.0 ** (size // 2)
+    k = H.f64(p.k)
+    k[:, :, 1] = sign * rng.integers(1, 101, k.shape[:2]) * 2.0 ** (size - size // 2)
+    p.q, p.k = H.bf16(q.reshape(p.T, -1)).cuda(), H.bf16(k).cuda()
+    k, v = H.f64(p.k), H.f64(p.v)
+    h = p.handle()
+    got = H.f64(p.call(h)).reshape(p.T, p.Hq, d)
+    assert h.check() == (0, 0)
+    for s in range(p.S):
+        at = p.slots(s)
+        for t in range(int(p.new[s])):
+            seen = at[:int(p.ctx[s]) + t + 1]
+            for head in range(p.Hkv):
+                best = k[seen, head, 1] == k[seen, head, 1].max()
+                o, a = v[seen[best], head].mean(0), np.abs(v[seen[best], head]).mean(0)
+                tol = 2.0 ** -8 * np.abs(o) * 1.01 + (2.0 ** -8 + (len(at) / 16 + 64) * 2.0 ** -23 + 2.0 ** -20) * a
+                rows = got[int(p.cu[s]) + t, head * p.G:(head + 1) * p.G]
+                assert (np.abs(rows - o) <= tol).all()
