@@ -7,7 +7,7 @@
 // and two pieces of 256 columns are on their way while two are worked on, the first before the slot and
 // the angles are known. A lane has its pairs' other halves from the lane r / 16 beside it.
 // Three CTAs a SM: with four the angles' registers spill. Measured: 16384 tokens of 80 heads of 128, 671 MB, 111 us
-// (6.0 TB/s; four pieces that are not ahead of the work 122); 1777 of 32 heads of 256 with norms, 58 MB, 14.3 us
+// (6.0 TB/s; four pieces that are not ahead of the work 122); 1777 of 32 heads of 256 with norms, 58 MB, 14.7 us
 // (20.5), a chain of 16 pieces a warp and 110 instructions a piece; 8 tokens 3.1 us.
 //
 // Angles. pos f is wanted modulo a turn, to f32's accuracy at any position. f / (2 pi) is
@@ -109,13 +109,27 @@ __global__ void __launch_bounds__(kThreads_, 3) kv_append(const AppendParams p) 
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[2 * j] = bf16_lo(w[j]), y[2 * j + 1] = bf16_hi(w[j]);
           if (NORM) {
-            float sum = 0.f;
+            const auto squares = [&] {
+              float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+              for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
 #pragma unroll
-            for (int o = kL / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (is_q ? p.qw != nullptr : p.kw != nullptr) {
-              const float scale = rsqrtf(sum * (1.f / D) + p.eps);
+              for (int o = kL / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              return sum * (1.f / D);
+            };
+            const bool normed = is_q ? p.qw != nullptr : p.kw != nullptr;
+            float mean = squares() + p.eps;
+            // A head whose squares pass f32's range, or are lost below it, is scaled first. One test for the means from
+            // 2^-80 up to 2^120 (1777 tokens of 32 heads of 256 14.7 us; 14.9 with a test for each end and side, 14.4 without).
+            constexpr uint32_t kLow = (127 - 80) << 23, kHigh = (127 + 120) << 23;
+            if (__any_sync(0xffffffffu, __float_as_uint(mean) - kLow >= kHigh - kLow)) {
+              const float by = !normed ? 1.f : !(mean < 0x1p120f) ? 0x1p-100f : mean < 0x1p-80f ? 0x1p80f : 1.f;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] *= by;
+              mean = squares() + p.eps * by * by;
+            }
+            if (normed) {
+              const float scale = rsqrtf(mean);
               const uint32_t n[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {

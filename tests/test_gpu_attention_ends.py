@@ -67,3 +67,37 @@ def test_scores_of_any_size(heads, d, requests, size, sign):
                 tol = 2.0 ** -8 * np.abs(o) * 1.01 + (2.0 ** -8 + (len(at) / 16 + 64) * 2.0 ** -23 + 2.0 ** -20) * a
                 rows = got[int(p.cu[s]) + t, head * p.G:(head + 1) * p.G]
                 assert (np.abs(rows - o) <= tol).all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
+@pytest.mark.parametrize("size", [126, 70, 62, 20, -20, -38, -45, -60, -126, -133])
+@pytest.mark.parametrize("heads,d,rotary", [((4, 2), 64, 64), ((6, 1), 128, 48), ((3, 3), 256, 64)])
+def test_norms_of_any_size(heads, d, rotary, size, eps):
+    """Heads of values about 2^size, beside ordinary ones, through the norms, all of which are defined (no head is zero)."""
+    from gated_deltanet_layer_gb300 import kv_append
+    rng = np.random.default_rng(d)
+    (hq, hkv), T = heads, 21
+    x = rng.standard_normal((T, hq + 2 * hkv, d)).clip(-2.9, 2.9)
+    x[rng.random(x.shape[:2]) < 0.5] *= 2.0 ** size
+    x[:, :, 0] = np.where(x[:, :, 0] == 0, 1, x[:, :, 0])
+    rows = H.bf16(x.reshape(T, -1))
+    zero = (rows.view(T, -1, d) == 0).all(-1).any()
+    assert not zero
+    rows = rows.cuda()
+    a, b = hq * d, hkv * d
+    qs, ks, vs = rows[:, :a], rows[:, a:a + b], rows[:, a + b:]
+    pos, slots = rng.integers(0, 1000, T), rng.permutation(T + 3)[:T]
+    freq = torch.from_numpy((1e4 ** (-np.arange(0, rotary, 2) / rotary)).astype(np.float32)).cuda()
+    qw, kw = (H.bf16(rng.standard_normal(d) * 0.2).cuda() for _ in range(2))
+    for q_norm, k_norm in ((qw, kw), (None, kw), (qw, None)):
+        kc, vc = (torch.zeros(T + 3, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        # each side by itself: the other is taken as it is
+        want = [H.append_reference(H.f64(qs), H.f64(ks), H.f64(vs), pos, slots, H.f64(freq), H.f64(kc), H.f64(vc), n, n, float(np.float32(eps)), False, d)
+                for n in (None if q_norm is None else H.f64(qw), None if k_norm is None else H.f64(kw))]
+        got = kv_append(qs, ks, vs, H.ints(pos), H.ints(slots, np.int64), freq, kc, vc, q_norm_w=q_norm, k_norm_w=k_norm,
+                        norm_eps=eps)
+        for y, (w, tol) in ((got, want[0][0]), (kc, want[1][1])):
+            # turned as they are, the largest may pass bf16's range; the smallest are rounded to whole subnormals
+            ok = np.abs(w) < 3.3e38
+            assert (np.abs(H.f64(y)[ok] - w[ok]) <= tol[ok] + 2.0 ** -134).all()
+        assert torch.equal(vc[H.ints(slots).long()].reshape(T, -1), vs)
