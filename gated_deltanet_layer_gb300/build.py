@@ -20,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdn_decode.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_ABI = os.path.join(OBJDIR, "binding.abi")  # what _binding.so was built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE]
@@ -52,9 +53,18 @@ def _deps():
             + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _abi() -> str:
+    """The torch and the Python that _binding.so belongs to: its C++ ABI is theirs."""
+    import torch
+    return " ".join((torch.__version__, str(torch.version.git_version), os.path.dirname(torch.__file__), sys.implementation.cache_tag))
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(BINDING_ABI)):
         return False
+    with open(BINDING_ABI) as f:
+        if f.read() != _abi():
+            return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
@@ -75,6 +85,8 @@ def _build_binding(cuda_home: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"the binding does not compile:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_ABI, "w") as f:
+        f.write(_abi())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

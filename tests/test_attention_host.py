@@ -182,3 +182,15 @@ def test_scale_that_is_not_finite_refused(lib, scale):
 @pytest.mark.parametrize("scale", [0.0, -0.1, -3e37, 1e-45])
 def test_finite_scales_taken(lib, scale):
     assert lib.gdn_attn_workspace_bytes(ctypes.byref(config(scale=scale))) > 0
+
+
+def test_built_again_for_another_torch(lib, monkeypatch):
+    """The binding is bound to the torch that it was built against, whatever the sources' times."""
+    assert B.up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        assert not B.up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch.version, "git_version", "0")
+        assert not B.up_to_date()
+    assert B.up_to_date()
