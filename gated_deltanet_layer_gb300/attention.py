@@ -41,7 +41,8 @@ def kv_append(q, k, v, token_pos, slots, inv_freq, k_cache, v_cache, *, q_norm_w
 
 class PagedAttention:
     """Causal attention over a paged cache, bound to one workspace on one device.
-    max_tokens and max_seqs bound one call; scale None: head_dim ** -0.5. The handle may be
+    max_tokens and max_seqs bound one call; scale None: head_dim ** -0.5. Making it waits for
+    its stream, so that calls on other streams find the workspace cleared. The handle may be
     dropped while its calls run; a graph that captured them needs it for as long as it is
     replayed."""
 
@@ -66,6 +67,8 @@ class PagedAttention:
         if st != GDN_OK:
             raise GdnError("gdn_attn_create", st)
         self._h = h
+        if not torch.cuda.is_current_stream_capturing():
+            (stream if stream is not None else torch.cuda.current_stream()).synchronize()
 
     def __del__(self):
         h = getattr(self, "_h", None)

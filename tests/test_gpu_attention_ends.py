@@ -101,3 +101,22 @@ def test_norms_of_any_size(heads, d, rotary, size, eps):
             ok = np.abs(w) < 3.3e38
             assert (np.abs(H.f64(y)[ok] - w[ok]) <= tol[ok] + 2.0 ** -134).all()
         assert torch.equal(vc[H.ints(slots).long()].reshape(T, -1), vs)
+
+
+@pytest.mark.parametrize("heads,d,requests", [((8, 2), 128, [(3000, 1), (9000, 1)]), ((8, 2), 64, [(2000, 60)])])
+def test_made_on_a_busy_stream(heads, d, requests):
+    """A handle made on a stream that is busy, in memory that held something else, and called on another stream at once."""
+    p = H.Pages(heads, d, 16, requests, seed=3)
+    want = p.reference()
+    first = p.handle()
+    size = first.workspace.numel()
+    del first
+    busy, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(busy):
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(200_000_000)
+        h = p.handle()
+    out = p.call(h, stream=other)
+    other.synchronize()
+    assert h.check(other) == (0, 0)
+    H.check(out, *want)
