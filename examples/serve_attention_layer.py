@@ -9,6 +9,10 @@ A step, whether it brings prompts or one token a request:
   PagedAttention.attend    the step's queries over their requests' pages, gated
   linear_w4                out projection, added to the residual stream
 
+The prompts here are short. A server keeps bf16 weights beside the codes for long ones, whose
+projections `linear` does in one pass, where linear_w4 reads the weights again for each 32 rows
+at most.
+
     python examples/serve_attention_layer.py [decode steps]
 """
 from __future__ import annotations

@@ -90,7 +90,8 @@ class PagedAttention:
         themselves, times sigmoid(gate) if given (gdn_attn_paged). q, gate, out
         [T, Hq * d], k_cache, v_cache [slots, Hkv, d] (slots a multiple of the block
         size), block_table int32 [S, blocks], cu_seqlens [S + 1], context_lens [S]. max_len:
-        no request has more new tokens (None: no better bound than T). Returns out."""
+        no request has more new tokens (None: no better bound than T, with which single tokens
+        take the chunks' form, up to half as long again). Returns out."""
         if stream is not None:
             if out is None:
                 out = _empty(q.shape, q.dtype, q, stream)

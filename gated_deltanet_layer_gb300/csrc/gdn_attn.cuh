@@ -24,7 +24,8 @@ constexpr uint32_t kAttnBlock = 1, kAttnOffsets = 2, kAttnLength = 3, kAttnWait 
 // them a kernel before leaves the plan in the workspace.
 constexpr int kAttnPlanned = 128;
 
-// n / d for 0 <= n < 2^31.
+// n / d for 0 <= n < 2^31: division by an invariant integer as Granlund and Montgomery (1994) have it, by the
+// high half of a product and a shift.
 struct FastDiv {
   uint32_t d, mul, shift;
   __host__ static FastDiv of(uint32_t d) {
@@ -80,7 +81,9 @@ __device__ __forceinline__ unsigned atom_add_acq_rel_u32(unsigned* p, unsigned v
   return old;
 }
 
-// sum over i < n of floor((a i + b) / m), by the steps of Euclid's algorithm (a, b >= 0).
+// sum over i < n of floor((a i + b) / m) (a, b >= 0), by the steps of Euclid's algorithm: whole multiples of m are taken
+// out, then the points below the line are counted along the other axis (Graham, Knuth and Patashnik, Concrete
+// Mathematics, 3.5).
 __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   long long sum = 0;
 #pragma unroll 1

@@ -14,7 +14,8 @@
 //
 // Bound by the bandwidth of the keys and values. Measured: 64 requests of one token over up to 8192,
 // 64 heads of 128 on 8, 926 MB, 165 us (5.6 TB/s, 82% of the measured copy); two over up to 131072, 24 heads of 256 on
-// 4, 742 MB, 128 us (5.8 TB/s, 85%; one warp a group of keys 153); one over 100000 of a shard's single key head 23, of
+// 4, 742 MB, 128 us (5.8 TB/s, 85%; one warp a group of keys 153); one over 100000 of a shard's single key head 23
+// (27 with keys and values from memory, of 7.5), of
 // which 15 are the plan, the first rows and the joins of 150 parts, in two levels. Rows of several tiles: 20 rows a request and
 // key head over up to 6000 read everything twice, 125 us; as a tile of the tensor cores 73.
 #include <climits>

@@ -18,9 +18,11 @@
 // between two buffers. A task whose rows fill one tile of each CTA alone has the keys of
 // every second tile in the place of the other tile's rows, and joins the two.
 //
-// Measured: chunks of 2048 tokens in all of two requests over up to 30000, 24 heads of 256 on 4, 757 - 795 us (1.6 - 1.7
-// PFLOP/s, 84 - 88% of the measured rate; one CTA by itself, keys and values for 128 rows, 1460): the tensor cores. 8192 fresh
-// tokens of 5 requests, 64 heads of 128 on 8, 275 us (64%): a turn's products take 1080 cycles, but the chain S, softmax, PV of
+// Measured: chunks of 2048 tokens in all of two requests over up to 30000, 24 heads of 256 on 4, 757 - 795 us in bursts of ten
+// (1.6 - 1.7 PFLOP/s, 84 - 88% of the measured burst rate; one CTA by itself, keys and values for 128 rows, 1460), 887 - 938 in
+// a row of calls at the power limit (1.37 - 1.45 PFLOP/s, 79 - 84% of the measured sustained rate): the tensor cores. 8192 fresh
+// tokens of 5 requests, 64 heads of 128 on 8, 275 us (64% of the burst rate; up to 394 right after such a row of chunks): a
+// turn's products take 1080 cycles, but the chain S, softmax, PV of
 // a row tile 3900, in which two turns run, as S and O fill TMEM. 24 requests of 4 tokens over up to 6000, 40 heads of
 // 128 on 8, 73 us (57% of the bandwidth): 20 of a tile's 128 rows are there, each tile of keys is a turn all
 // the same, and a task has 8 us of queries, first tile and join.
@@ -42,7 +44,11 @@ constexpr int kLoad0 = 8, kMma = 12, kSched = 13;  // first load warp; the warp 
 constexpr float kSlack = 8.f;                      // log2 of the most that a weight is above 1
 constexpr int KT = 128;                            // keys of a tile
 constexpr int kSegs = 4;                           // parts of tasks that are known ahead
-constexpr int kSplit = 4;                          // key tiles from which on a task is split between a CTA's row tiles
+// Key tiles from which on a task is split between a CTA's row tiles. With 4, 16, never (us; 2 and 8 as 4): 24 requests of 4
+// tokens over up to 6000, 40 heads of 128 on 8, 68, 82, 100; 48 of 3 over up to 3000, 64 on 8, 88, 110, 120; 96 of 4 over up
+// to 1000, 40 on 8, 102, 107, 108; 12 of 8 over up to 12000, 32 heads of 64 on 4, 37, 38, 52; but 8 of 16 over up to 30000, 8 on
+// 1, 65, 66, 52.
+constexpr int kSplit = 4;
 
 template <int D>
 struct Cfg {
@@ -872,8 +878,11 @@ cudaError_t launch(AttnParams p, int grid, cudaStream_t s) {
   m.tokens = 128 / G;
   p.tile_m = Cfg<D>::kRows / 128 * m.tokens;
   // A task's own time (queries, first tile, join) in tiles of keys. More where all tasks have their keys split between
-  // the row tiles, as a tile is one turn there and not two: 24 requests of 4 tokens over up to 6000, heads of
-  // 128, 82 us with 3, 75 with 6, 72 with 8; fresh prompts 276 with 3, 286 with 4, 297 with 5.
+  // the row tiles, as a tile is one turn there and not two. With 3, 5, 8, 12 (us): 24 requests of 4 tokens over up to 6000, 40
+  // heads of 128 on 8, 74, 71, 68, 69; 48 of 3 over up to 3000, 64 on 8, 99, 92, 88, 91; 4 of 32 over up to 2000, 64 on 8, 27, 26,
+  // 25, 25; 12 of 8 over up to 12000, heads of 64, 38, 36, 37, 39; 96 of 4 over up to 1000 98, 97, 102, 105. Where they have not:
+  // fresh prompts of 3000 tokens, heads of 64, 112, 116, 117, 127; 4 prompts of 1000, heads of 256, 77, 81, 83, 84; 24 of 8 over
+  // up to 4000, heads of 256, 47, 47, 49, 49; with 1 these three 110, 84, 50.
   p.tile_e = Cfg<D>::kTiles == 2 && p.max_len <= 2 * m.tokens ? 8 : 3;
   p.tile_g = FastDiv::of(1);
   const long long rows = (long long)p.num_blocks * p.block.d, cols = (long long)p.Hkv * D;

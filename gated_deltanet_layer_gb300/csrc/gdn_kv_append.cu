@@ -7,8 +7,8 @@
 // and two pieces of 256 columns are on their way while two are worked on, the first before the slot and
 // the angles are known. A lane has its pairs' other halves from the lane r / 16 beside it.
 // Three CTAs a SM: with four the angles' registers spill. Measured: 16384 tokens of 80 heads of 128, 671 MB, 111 us
-// (6.0 TB/s; four pieces that are not ahead of the work 122); 1777 of 32 heads of 256 with norms, 58 MB, 14.7 us
-// (20.5), a chain of 16 pieces a warp and 110 instructions a piece; 8 tokens 3.1 us.
+// (6.0 TB/s; four pieces that are not ahead of the work 122); 1777 of 32 heads of 256 with norms, 58 MB, 14.7 us,
+// 15.0 with rows and slots that are not in L2, a chain of 16 pieces a warp and 110 instructions a piece; 8 tokens 3.1 us.
 //
 // Angles. pos f is wanted modulo a turn, to f32's accuracy at any position. f / (2 pi) is
 // a 64-bit binary fraction of a turn (in two double terms, so right to its last bits), and

@@ -15,15 +15,17 @@
 // the columns, as many as there are warps left, whose sums are added up in shared memory at the end.
 // A warp's codes come through a ring of its own (cp.async), its scales and zeros four groups at
 // a time through registers, and x to the lanes as it is, from L1. Through shared memory, pieces of all
-// shares at a time, its room was what bounded S: 16 rows of 1024 x 8192 33 us, 8 now; 8 rows of
-// 8192 x 8192 20.8 and 14.6.
+// shares at a time, its room was what bounded S: 16 rows of 1024 x 8192 33 us, 6.4 now; 8 rows of
+// 8192 x 8192 20.8 and 14.7.
 //
-// 8, 16 or 32 rows of x at a time. 32 in all read the weights once; fewer at a time where the groups are too few
+// 8, 16 or 32 rows of x at a time, the weights once for each: as many as there are, fewer at a time where the groups are too few
 // for the SMs all the same (up to two a SM): 33 rows of 1037 x 1056 8.2 us with 32 at a time, 5.6 with 16. 64 at a
 // time leave too few registers: 64 rows of 8192 x 8192 77 us, 58 with two passes.
 //
-// Measured, codes and scales as bytes: 8 rows of 20480 x 8192 whole numbers 25.0 us (3.5 TB/s), MXFP4 35.2; 2560 x 8192,
-// one row, MXFP4 9.7, whole numbers 8.2: a SM's warps issue an instruction every other cycle, 45 for 512 weights (unpack 22,
+// Measured with the weights from memory, as a server has them (and with the same weights over and over, part of them in L2):
+// 8 rows of 20480 x 8192 whole numbers 31.4 us (25.0), 2.8 TB/s; MXFP4 37.4 (35.1); 16 of 5120 x 5120 14.0 (10.7); 64 of
+// 8192 x 8192 91 (58.6); 2560 x 8192, one row, MXFP4 10.4 (9.8), whole numbers 9.7 (8.4). Figures above are the latter. A SM's
+// warps issue an instruction every other cycle, 45 for 512 weights (unpack 22,
 // the scales 8, loads and addresses 8), and 160 groups of rows are two for a CTA, which leaves 72 SMs idle.
 #include <algorithm>
 #include <type_traits>

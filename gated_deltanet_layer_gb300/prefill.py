@@ -119,7 +119,8 @@ def linear_w4(x, codes, scales, zeros=None, bias=None, activation=None, residual
     """linear with the weights in 4 bits, for few rows (gdn_linear_w4): codes uint8
     [N, K / 2], element 2 i in the low nibble of byte i. scales bf16 [N, K / group], group 32,
     64 or 128: (code - zero) * scale, zeros uint8 like scales or None (8). scales
-    uint8 [N, K / 32]: MXFP4, E2M1 codes and e8m0 scales. The rest as for linear."""
+    uint8 [N, K / 32]: MXFP4, E2M1 codes and e8m0 scales. More than 8 rows may read the
+    weights again for each 8, 16 or 32. The rest as for linear."""
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
     if stream is not None:

@@ -41,8 +41,8 @@ extern "C" {
  *   with a, b the values i and i + rotary_dim / 2 of the head, or with
  *   `interleaved` 2 i and 2 i + 1;
  *   q_out[t] = q', k_cache[slots[t]] = k', v_cache[slots[t]] = v.
- * f32 throughout, one rounding to bf16; v is copied. The angles' fractions of a
- * turn are exact to 2^-30 at any position (64-bit fixed point). A token with a
+ * f32 throughout, one rounding to bf16; v is copied. An angle is within 2^-25 of a
+ * turn at any position (its fraction in 64-bit fixed point, rounded to f32). A token with a
  * negative slot is a pad row: its q_out row is zero and nothing is appended. A
  * slot >= num_slots does the same and sets *error (a device word, optional) to
  * GDN_ERR_INDEX in bits 31..24, 1 in 23..16 and the token in 15..0, if it was
@@ -91,16 +91,21 @@ gdn_status gdn_attn_create(const gdn_attn_config* cfg, void* workspace, size_t w
  * gdn_kv_append has put into the cache before):
  *   o = sum_p softmax_p(scale q . k_p) v_p,  and with gate: o * sigmoid(gate).
  * Scores, maxima, sums and outputs are f32; the weights of the values are
- * rounded to bf16 before they are multiplied. Keys a token does not see have no
+ * rounded to bf16 before they are multiplied. Sums of weights (of 2^8 at most, or for scores past 2^20
+ * of 2^40) times values have to stay within f32's range. Keys a token does not see have no
  * part in its row, whatever they hold; a value that is not finite and is seen makes its
  * column of the row NaN or infinite; a row whose every score is minus infinity is zero.
  * max_len is an upper bound of the requests' new tokens known to the host
- * (tokens if nothing better is known); it chooses the form.
+ * (tokens if nothing better is known); it chooses the form: where it times the query heads
+ * of a key/value head is at most 16, that of few rows. A bound that is too high makes
+ * single tokens take the chunks' form, which is up to half as long again.
  * A request longer than max_len, with a negative context, or with more keys
  * than max_blocks blocks hold records GDN_ERR_INDEX and is padding: zero rows.
  * A block outside 0 .. num_blocks - 1 that a request needs records GDN_ERR_INDEX
  * and is read as zeros. Pad rows and their outputs: not read, zero.
- * q, out [tokens][>= num_q_heads * head_dim], gate likewise or NULL; k_cache,
+ * q, out [tokens][>= num_q_heads * head_dim], gate likewise or NULL, a row's query heads one
+ * after another (where a projection has a head's query and gate side by side, its weights' rows are
+ * put in this order once); k_cache,
  * v_cache [num_blocks * block_size][>= num_kv_heads * head_dim] bf16 (fewer
  * than 2^31 slots; ldq, ldk and ldv below 2^38); block_table int32 [seqs][max_blocks], cu_seqlens int32
  * [seqs + 1], context_lens int32 [seqs]. out must overlap no input.

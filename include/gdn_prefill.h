@@ -168,8 +168,9 @@ typedef enum { GDN_W4_INT = 0, GDN_W4_MXFP4 = 1 } gdn_w4_format;
  * steps): out[m][n] = bf16(act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]).
  * The activations stay bf16 (where gdn_decode_step quantises them to MXFP4). Weights
  * and x are taken as they are, without a rounding; sums are f32, of a group's products first,
- * which its scale then multiplies. Up to 32 rows read the weights once; more are taken 32 at a
- * time (fewer where the matrix is small). inner is a multiple of `group`.
+ * which its scale then multiplies. Up to 8 rows read the weights once; more are taken 8, 16 or 32 at a
+ * time, the fewer the smaller the matrix is, and the weights are read again each time: a prompt's
+ * rows are better off with bf16 weights and gdn_linear. inner is a multiple of `group`.
  * x [rows][ldx >= inner] (16-byte aligned, ldx a multiple of 8), codes
  * [cols][inner / 2] (16-byte aligned), scales and zeros [cols][inner / group];
  * the rest as for gdn_linear. A value of x that is not finite makes its row of out NaN
