@@ -67,8 +67,9 @@ class PagedAttention:
         if st != GDN_OK:
             raise GdnError("gdn_attn_create", st)
         self._h = h
-        if not torch.cuda.is_current_stream_capturing():
-            (stream if stream is not None else torch.cuda.current_stream()).synchronize()
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     def __del__(self):
         h = getattr(self, "_h", None)

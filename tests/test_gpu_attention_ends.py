@@ -120,3 +120,65 @@ def test_made_on_a_busy_stream(heads, d, requests):
     other.synchronize()
     assert h.check(other) == (0, 0)
     H.check(out, *want)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_made_within_a_capture(given):
+    """Making a handle while its stream captures waits for nothing; its clearing is a part of the graph."""
+    p = H.Pages((8, 2), 128, 16, [(3000, 1), (200, 1)], seed=4)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    p.call(p.handle())  # what a first call loads is there
+    torch.cuda.synchronize()
+    out = torch.empty_like(p.q)
+    with torch.cuda.graph(g, stream=side):
+        if given:
+            with torch.cuda.stream(torch.cuda.Stream()):  # another one is current, and does not capture
+                h = p.handle(stream=side)
+        else:
+            h = p.handle()
+        p.call(h, out=out)
+    for _ in range(3):
+        out.fill_(5)
+        g.replay()
+        torch.cuda.synchronize()
+        H.check(out, *p.reference())
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_captured(interleaved):
+    """An append in a graph, replayed with other rows, positions and slots in the same memory, pad rows among them."""
+    from gated_deltanet_layer_gb300 import kv_append
+    rng, (hq, hkv, d), T = np.random.default_rng(5), (6, 2, 128), 19
+    freq = torch.from_numpy((1e4 ** (-np.arange(0, d, 2) / d)).astype(np.float32)).cuda()
+    qw, kw = (H.bf16(rng.standard_normal(d) * 0.2).cuda() for _ in range(2))
+    rows = torch.empty(T, (hq + 2 * hkv) * d, dtype=torch.bfloat16, device="cuda")
+    pos, slots = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int64, device="cuda")
+    kc, vc = (torch.zeros(40, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    err, out = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(T, hq * d, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        q, k, v = rows.split([hq * d, hkv * d, hkv * d], 1)
+        return kv_append(q, k, v, pos, slots, freq, kc, vc, q_norm_w=qw, k_norm_w=kw, interleaved=interleaved, q_out=out, error=err)
+
+    def fill():
+        rows.copy_(H.bf16(rng.standard_normal(tuple(rows.shape))))
+        pos.copy_(torch.from_numpy(rng.integers(0, 2**31 - 1, T).astype(np.int32)))
+        at = rng.permutation(40)[:T]
+        at[rng.integers(0, T, 3)] = -1
+        slots.copy_(torch.from_numpy(at))
+    fill()
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(4):
+        fill()
+        q, k, v = (H.f64(t) for t in rows.split([hq * d, hkv * d, hkv * d], 1))
+        want, (wk, tk), wv = H.append_reference(q, k, v, pos.cpu().numpy(), slots.cpu().numpy(), H.f64(freq), H.f64(kc), H.f64(vc),
+                                                H.f64(qw), H.f64(kw), 1e-6, interleaved, d)
+        g.replay()
+        torch.cuda.synchronize()
+        H.check(out, *want)
+        H.check(kc, wk, tk)
+        assert np.array_equal(H.f64(vc), wv) and err.item() == 0
