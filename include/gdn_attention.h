@@ -81,7 +81,8 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_config* cfg);
 /* Validate the config, bind the caller's workspace (256-byte aligned device
  * memory that outlives the handle) and clear its error word and counters on
  * `stream`. The handle holds host state only. It belongs to the device that is
- * current here; calls with another one current are GDN_ERR_ARG. */
+ * current here; calls with another one current are GDN_ERR_ARG. Calls on another stream
+ * are ordered after the clearing by the caller. */
 gdn_status gdn_attn_create(const gdn_attn_config* cfg, void* workspace, size_t workspace_bytes, void* stream,
                            gdn_attn_t** out);
 
